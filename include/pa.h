@@ -5,8 +5,10 @@
  * with a log-sum-exp merge, and a sparse selected-page variant; with the two steps next
  * to it: the per-token FP8 quantise-and-write that fills the cache
  * (pa_kv_quantize_write) and the indexer's page scores and top-k that choose the sparse
- * variant's pages (pa_index_topk); and the log-sum-exp merge that combines the parts of a
- * context split across GPUs (pa_lse_merge).  sm_103a (GB300).
+ * variant's pages (pa_index_topk); the log-sum-exp merge that combines the parts of a
+ * context split across GPUs (pa_lse_merge); and what happens to the cache between two
+ * decode steps: eviction by accumulated attention weight (pa_attn_mass, pa_evict_select,
+ * pa_kv_compact) and beam search (pa_beam_select, pa_beam_reorder).  sm_103a (GB300).
  *
  * Sources of the operation (the pages are pull-request threads):
  *  - ROCm/ATOM PR 2614, "Change": dense max-q-len-1 per-token FP8 decode and sparse
@@ -352,6 +354,228 @@ typedef struct pa_lse_merge_args {
  * pointer, PA_ERR_UNSUPPORTED for head_dim other than 128 or more than 64 parts,
  * PA_ERR_CUDA when the launch fails. */
 pa_status_t pa_lse_merge(const pa_lse_merge_args_t *args, void *stream);
+
+/* ---- attention mass: what each cached token has been worth to the queries so far ---- */
+
+/* Arguments of pa_attn_mass.  All pointers are device pointers. */
+typedef struct pa_attn_mass_args {
+  const void *q;                 /* bf16 [num_rows, num_kv_heads * group_size, head_dim], 16-B aligned */
+  const void *k_cache;           /* [num_pages, num_kv_heads, page_size, head_dim], e4m3 or bf16; 16-B aligned */
+  const float *k_scale;          /* fp32 [num_pages, num_kv_heads, page_size]; PER_TOKEN only, 16-B aligned */
+  const int32_t *block_table;    /* [num_seqs, block_table_stride] */
+  const int32_t *context_lens;   /* [num_seqs]: tokens in each request's cache, own q_len included */
+  const int32_t *cu_seqlens_q;   /* [num_seqs + 1]: rows of request r are [cu[r], cu[r+1]) */
+  const float *lse;              /* fp32 [num_rows, num_kv_heads * group_size]: pa_decode's lse of the same step
+                                    (natural log; a row of -inf gives no weight) */
+  const float *mass;             /* fp32 [num_seqs, num_kv_heads, mass_stride]; may be NULL when decay is 0 */
+  float *mass_out;               /* same shape; may be `mass` itself (any other overlap is refused) */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_PAGE, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_QLEN,
+                                    PA_DEV_TIMEOUT are OR-ed in */
+  int64_t num_pages;
+  int32_t num_seqs;              /* 0 .. 4096; 0 enqueues nothing */
+  int32_t num_rows;
+  int32_t num_kv_heads;          /* 1 .. 64 */
+  int32_t group_size;            /* 16 */
+  int32_t head_dim;              /* 128 */
+  int32_t page_size;             /* 16, 32, 64 or 128 */
+  int32_t kv_dtype;              /* PA_KV_* */
+  int32_t scale_mode;            /* FP8: SCALAR or PER_TOKEN; BF16: NONE */
+  int32_t block_table_stride;
+  int32_t mass_stride;           /* positions per (request, KV head) row of the mass */
+  int32_t max_q_len;             /* bound on any request's q_len, 1 .. 64 */
+  float k_scale_scalar;          /* SCALAR only */
+  float sm_scale;                /* > 0 */
+  float decay;                   /* 0 .. 1: what the mass so far is multiplied by */
+  int32_t reserved;              /* 0 */
+} pa_attn_mass_args_t;
+
+/* Adds one decode step's attention weights to the mass of the cached tokens, the quantity
+ * by which pa_evict_select keeps them.  For request r with context L, q_len rows and KV head
+ * h, and every position p < L:
+ *   w[p] = sum over its rows t and the 16 query heads g of h, where p < L - q_len + t + 1,
+ *          of exp(sm_scale * q[t][g] . k[p] * k_scale[p] - lse[t][g]),
+ *   mass_out[r][h][p] = (p < L - q_len ? decay * mass[r][h][p] : 0) + w[p].
+ * The step's own tokens start from zero, so a slot's earlier owner leaves nothing behind, and
+ * with decay 0 `mass` is not read.  Positions >= L, and requests without rows, are left as they are
+ * (in mass_out).  A position on a bad page gets w = 0.  A request with a bad length is skipped.
+ * The mass belongs to the request, not to the page: requests may share pages (a common prefix,
+ * beams).  Sums and exponentials are fp32 and always in the same order.  Inputs other than lse's
+ * -inf must be finite.  One kernel launch on `stream`; no host synchronisation, no allocation.
+ * PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap of mass and
+ * mass_out other than equality, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for
+ * a shape or mode outside the limits above, PA_ERR_CAPACITY when num_pages * num_kv_heads *
+ * page_size passes 2^31 - 1, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_attn_mass(const pa_attn_mass_args_t *args, void *stream);
+
+/* ---- eviction: which tokens a bounded cache keeps, and their move to the front ---- */
+
+#define PA_DEV_BAD_KEEP 0x400u /* pa_kv_compact: new_lens outside [0, keep_stride] or past the tables, or a keep row
+                                  that is not ascending positions of the request's cache */
+
+/* Arguments of pa_evict_select.  All pointers are device pointers. */
+typedef struct pa_evict_select_args {
+  const float *mass;             /* fp32 [num_seqs, num_kv_heads, mass_stride] */
+  const int32_t *context_lens;   /* [num_seqs] */
+  int32_t *keep;                 /* out: [num_seqs, num_kv_heads, budget] kept positions, ascending, -1 after */
+  int32_t *new_lens;             /* out: [num_seqs] min(context_len, budget); must not be context_lens */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT is OR-ed in */
+  int32_t num_seqs;              /* 0 .. 65535; 0 enqueues nothing */
+  int32_t num_kv_heads;          /* 1 .. 64 */
+  int32_t mass_stride;           /* >= 1 */
+  int32_t budget;                /* >= 1: most tokens kept per (request, KV head) */
+  int32_t keep_first;            /* >= 0: positions [0, keep_first) always stay */
+  int32_t keep_recent;           /* >= 0: the last keep_recent positions always stay;
+                                    keep_first + keep_recent <= budget */
+  int32_t reserved;              /* 0 */
+} pa_evict_select_args_t;
+
+/* Chooses, for every (request, KV head), the positions that stay when its cache is cut to
+ * `budget` tokens.  With context L <= budget all of them stay.  Else the first keep_first, the
+ * last keep_recent, and of those between the ones with the largest mass until there are budget
+ * of them; equal masses (0 and -0 are equal) stay lowest position first, and a NaN counts as less
+ * than any number.  The result is exact, whatever the values.  A request whose context is negative
+ * or beyond mass_stride is flagged: its keep rows are all -1 and its new_lens 0.  One kernel
+ * launch on `stream`; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing
+ * pointer or a value out of range, PA_ERR_ALIGN for a pointer not aligned to 4 bytes,
+ * PA_ERR_UNSUPPORTED for more than 64 KV heads or 65535 requests, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_evict_select(const pa_evict_select_args_t *args, void *stream);
+
+/* Arguments of pa_kv_compact.  All pointers are device pointers. */
+typedef struct pa_kv_compact_args {
+  const int32_t *keep;           /* [num_seqs, num_kv_heads, keep_stride] positions, strictly ascending per row */
+  const int32_t *new_lens;       /* [num_seqs]: entries of every keep row of the request */
+  const int32_t *block_table;    /* [num_seqs, block_table_stride]: where the cache is */
+  const int32_t *dst_block_table;/* [num_seqs, dst_block_table_stride]: where it goes; NULL moves it in place, to
+                                    the front of its own pages */
+  void *k_cache;                 /* [num_pages, num_kv_heads, page_size, head_dim], e4m3 or bf16; 16-B aligned */
+  void *v_cache;
+  float *k_scale;                /* fp32 [num_pages, num_kv_heads, page_size]; PER_TOKEN only, 4-B aligned */
+  float *v_scale;
+  const float *mass;             /* nullable: fp32 [num_seqs, num_kv_heads, mass_stride] */
+  float *mass_out;               /* where the kept tokens' mass goes: [num_seqs, num_kv_heads, mass_out_stride]; in place
+                                    `mass` itself with the same stride, with dst_block_table not overlapping it */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_KEEP, PA_DEV_BAD_PAGE are OR-ed in */
+  int64_t num_pages;
+  int32_t num_seqs;              /* 0 .. 65535; 0 enqueues nothing */
+  int32_t num_kv_heads;          /* 1 .. 64 */
+  int32_t head_dim;              /* 128 */
+  int32_t page_size;             /* 16, 32, 64 or 128 */
+  int32_t kv_dtype;              /* PA_KV_* */
+  int32_t scale_mode;            /* FP8: SCALAR or PER_TOKEN; BF16: NONE */
+  int32_t keep_stride;           /* >= 1 */
+  int32_t block_table_stride;
+  int32_t dst_block_table_stride;
+  int32_t mass_stride;
+  int32_t mass_out_stride;
+  int32_t reserved;              /* 0 */
+} pa_kv_compact_args_t;
+
+/* Moves the kept tokens to the front: for every (request r, KV head h) and i < new_lens[r],
+ * slot i of r's destination pages takes the K and V rows, the scales and the mass of position
+ * keep[r][h][i], bit for bit; afterwards new_lens is the request's context_lens.  Positions
+ * keep their order, so causal cutoffs, recency and the indexer's last page stay meaningful.
+ * In place nothing but the request's own first pages is written, and tokens that do not move are
+ * not touched; slots past new_lens are left as they are.  Pages that another request reads
+ * as well (a common prefix, beams) must not be compacted in place: give dst_block_table, whose pages
+ * are then written and must be nobody else's (not the source's either).  An entry that is not above the one before it
+ * or lies past the tables, and a bad page, are flagged and that token is not moved.  One kernel launch
+ * on `stream`; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer,
+ * a value out of range, or mass_out against the rule above, PA_ERR_ALIGN for a misaligned pointer,
+ * PA_ERR_UNSUPPORTED for a shape or mode outside the limits above, PA_ERR_CAPACITY when num_pages *
+ * num_kv_heads * page_size passes 2^31 - 1, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_kv_compact(const pa_kv_compact_args_t *args, void *stream);
+
+/* ---- beam search over the paged cache ---- */
+
+#define PA_DEV_BAD_BEAM 0x800u /* pa_beam_reorder: a parent outside [0, num_beams), or beams of one request with
+                                  different lengths (the request's rows are carried over as they are) */
+
+enum { PA_LOGITS_BF16 = 0, PA_LOGITS_F32 = 1 };
+
+/* Arguments of pa_beam_select.  All pointers are device pointers; beams of request n are
+ * [n * num_beams, (n + 1) * num_beams). */
+typedef struct pa_beam_select_args {
+  const void *logits;            /* [num_reqs * num_beams, logits_stride], the first `vocab` of each row; aligned to
+                                    its element (rows need no 16-byte alignment) */
+  const float *scores;           /* fp32 [num_reqs, num_beams]: sum of log-probabilities so far (-inf: no such beam yet) */
+  const uint8_t *finished;       /* nullable [num_reqs, num_beams]: non-zero for a beam that has ended */
+  const int32_t *lengths;        /* nullable [num_reqs, num_beams]: tokens of each beam; needed when
+                                    length_penalty is not 0 */
+  int32_t *tokens;               /* out: [num_reqs, num_beams] token that continues each new beam */
+  int32_t *parents;              /* out: [num_reqs, num_beams] beam (of the same request) that it continues */
+  float *scores_out;             /* out: its sum of log-probabilities; may be `scores` */
+  uint8_t *finished_out;         /* nullable out: may be `finished` */
+  int32_t *lengths_out;          /* nullable out: may be `lengths`; needs lengths */
+  int64_t logits_stride;         /* elements between rows, >= vocab */
+  int32_t num_reqs;              /* 0 .. 65535; 0 enqueues nothing */
+  int32_t num_beams;             /* 1 .. 32 */
+  int32_t vocab;                 /* 1 .. 2^24 */
+  int32_t logits_dtype;          /* PA_LOGITS_* */
+  int32_t eos_token;             /* the token that ends a beam, or -1: none; needed (>= 0) with finished */
+  float length_penalty;          /* >= 0 */
+  int32_t reserved;              /* 0 */
+} pa_beam_select_args_t;
+
+/* One step of beam search: the num_beams best continuations of each request's beams, best first.
+ * A live beam b continues with every token v at total = scores[b] + logits[b][v] - logsumexp(logits[b])
+ * and length lengths[b] + 1; a finished one only with eos_token, at its own score and length.
+ * Candidates are ranked by total / max(length, 1)^length_penalty, equal ranks by the lower beam,
+ * then the lower token.  A candidate that does not exist or whose total is NaN (a row of -inf
+ * logits, a NaN or +inf among them) counts as -inf and is taken, lowest beam and token first, only
+ * where nothing better is left; its scores_out is -inf.  finished_out is set where the parent
+ * had ended or the token is eos_token.  Totals and ranks are fp64 (the sum of exponentials is
+ * accumulated in fp32 over short runs and joined in fp64); scores_out is rounded once.  One kernel launch on `stream`;
+ * no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer or a value out
+ * of range, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for more than 32 beams,
+ * 65535 requests or 2^24 tokens, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_beam_select(const pa_beam_select_args_t *args, void *stream);
+
+#define PA_MAX_BEAM_STATES 4
+
+/* Arguments of pa_beam_reorder.  All pointers but state_in and state_out themselves are device pointers. */
+typedef struct pa_beam_reorder_args {
+  const int32_t *parents;        /* [num_reqs, num_beams]: pa_beam_select's */
+  const int32_t *context_lens;   /* [num_reqs * num_beams]: tokens in each beam's cache, equal within a request */
+  const int32_t *block_table;    /* [num_reqs * num_beams, block_table_stride] */
+  int32_t *block_table_out;      /* same shape; must not overlap block_table */
+  void *k_cache;                 /* [num_pages, num_kv_heads, page_size, head_dim], e4m3 or bf16; 16-B aligned */
+  void *v_cache;
+  float *k_scale;                /* fp32 [num_pages, num_kv_heads, page_size]; PER_TOKEN only, 4-B aligned */
+  float *v_scale;
+  uint32_t *status;              /* nullable: PA_DEV_BAD_BEAM, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_PAGE are OR-ed in */
+  const void *state_in[PA_MAX_BEAM_STATES];  /* num_states device arrays of num_reqs * num_beams rows of */
+  void *state_out[PA_MAX_BEAM_STATES];       /*   state_bytes bytes each; in and out must not overlap */
+  int64_t state_bytes[PA_MAX_BEAM_STATES];   /* > 0 */
+  int64_t num_pages;
+  int32_t num_states;            /* 0 .. 4 */
+  int32_t num_reqs;              /* 0 .. 65535; 0 enqueues nothing */
+  int32_t num_beams;             /* 1 .. 32; num_reqs * num_beams <= 65535 */
+  int32_t num_kv_heads;          /* 1 .. 64 */
+  int32_t head_dim;              /* 128 */
+  int32_t page_size;             /* 16, 32, 64 or 128 */
+  int32_t kv_dtype;              /* PA_KV_* */
+  int32_t scale_mode;            /* FP8: SCALAR or PER_TOKEN; BF16: NONE */
+  int32_t block_table_stride;
+  int32_t reserved;              /* 0 */
+} pa_beam_reorder_args_t;
+
+/* Lets every beam's history follow its parent without copying whole caches.  With L = the
+ * request's context length and f = L / page_size full pages, row j of block_table_out holds the
+ * parent's first f entries, shared by reference; then, if L is not a multiple of page_size, the page
+ * that the beam's next token goes to; then row j's own later entries as they were.  That
+ * partial page is never shared: the first child (lowest j) of a parent takes the parent's, and every further
+ * child takes the partial page of a beam that has no children (there are as many of those as
+ * further children, in ascending order), into which the L % page_size tokens of the parent's page are
+ * copied (K, V and scales of all KV heads).  So the partial pages of a request's beams must be its own
+ * and distinct before the call, and are afterwards; nothing is allocated.  With parents all 0
+ * the call also spreads a prompt, cached once in beam 0's pages, over all beams.  Each state's row j becomes
+ * its parent's row (mass, token history).  A flagged request keeps its rows, as if each beam were its
+ * own parent.  One kernel launch on `stream`; no host synchronisation, no allocation.
+ * PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for
+ * a misaligned pointer, PA_ERR_UNSUPPORTED for a shape or mode outside the limits above,
+ * PA_ERR_CAPACITY when num_pages * num_kv_heads * page_size passes 2^31 - 1, PA_ERR_CUDA when the
+ * launch fails. */
+pa_status_t pa_beam_reorder(const pa_beam_reorder_args_t *args, void *stream);
 
 /* ---- test hooks: exact integer / byte outputs of the row map and the page gather ---- */
 

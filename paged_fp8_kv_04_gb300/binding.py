@@ -77,6 +77,10 @@ class KvWriteArgs(ctypes.Structure):
 
 DEV_BAD_SLOT = 0x100
 DEV_BAD_INDEX_ROW = 0x200
+DEV_BAD_KEEP = 0x400
+DEV_BAD_BEAM = 0x800
+LOGITS_BF16, LOGITS_F32 = 0, 1
+MAX_BEAM_STATES = 4
 
 
 class IndexArgs(ctypes.Structure):
@@ -97,6 +101,42 @@ class LseMergeArgs(ctypes.Structure):
                 ("num_parts", ctypes.c_int32), ("num_rows", ctypes.c_int32),
                 ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def _struct(name, pointers, i64="", i32="", f32=""):
+    """A ctypes structure of pointers, then int64, int32 and float fields, then a reserved word."""
+    fields = [(n, ctypes.c_void_p) for n in pointers.split()]
+    fields += [(n, ctypes.c_int64) for n in i64.split()]
+    fields += [(n, ctypes.c_int32) for n in i32.split()]
+    fields += [(n, ctypes.c_float) for n in f32.split()]
+    return type(name, (ctypes.Structure,), {"_fields_": fields + [("reserved", ctypes.c_int32)]})
+
+
+AttnMassArgs = _struct(
+    "AttnMassArgs", "q k_cache k_scale block_table context_lens cu_seqlens_q lse mass mass_out status",
+    "num_pages", "num_seqs num_rows num_kv_heads group_size head_dim page_size kv_dtype scale_mode "
+    "block_table_stride mass_stride max_q_len", "k_scale_scalar sm_scale decay")
+EvictSelectArgs = _struct(
+    "EvictSelectArgs", "mass context_lens keep new_lens status", "",
+    "num_seqs num_kv_heads mass_stride budget keep_first keep_recent")
+KvCompactArgs = _struct(
+    "KvCompactArgs", "keep new_lens block_table dst_block_table k_cache v_cache k_scale v_scale mass mass_out "
+    "status", "num_pages", "num_seqs num_kv_heads head_dim page_size kv_dtype scale_mode keep_stride "
+    "block_table_stride dst_block_table_stride mass_stride mass_out_stride")
+BeamSelectArgs = _struct(
+    "BeamSelectArgs", "logits scores finished lengths tokens parents scores_out finished_out lengths_out",
+    "logits_stride", "num_reqs num_beams vocab logits_dtype eos_token", "length_penalty")
+
+
+class BeamReorderArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "parents", "context_lens", "block_table", "block_table_out", "k_cache", "v_cache", "k_scale",
+        "v_scale", "status")] + [
+        ("state_in", ctypes.c_void_p * MAX_BEAM_STATES), ("state_out", ctypes.c_void_p * MAX_BEAM_STATES),
+        ("state_bytes", ctypes.c_int64 * MAX_BEAM_STATES), ("num_pages", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in (
+            "num_states", "num_reqs", "num_beams", "num_kv_heads", "head_dim", "page_size", "kv_dtype",
+            "scale_mode", "block_table_stride", "reserved")]
 
 
 _lib = None
@@ -152,6 +192,12 @@ def lib(path: Optional[str] = None):
     L.pa_index_topk.restype = ctypes.c_int
     L.pa_lse_merge.argtypes = [ctypes.POINTER(LseMergeArgs), P]
     L.pa_lse_merge.restype = ctypes.c_int
+    for name, args in (("pa_attn_mass", AttnMassArgs), ("pa_evict_select", EvictSelectArgs),
+                       ("pa_kv_compact", KvCompactArgs), ("pa_beam_select", BeamSelectArgs),
+                       ("pa_beam_reorder", BeamReorderArgs)):
+        f = getattr(L, name)
+        f.argtypes = [ctypes.POINTER(args), P]
+        f.restype = ctypes.c_int
     L.pa_debug_trace.argtypes = [P, ctypes.c_size_t]
     L.pa_debug_trace.restype = ctypes.c_int
     if path is None:
@@ -412,3 +458,252 @@ def lse_merge(part_out, part_lse, out, lse=None, stream=None, args: Optional[Lse
     if st != 0:
         raise PaError(st, "pa_lse_merge")
     return out
+
+
+# ----------------------------------------------- the cache between two decode steps
+#
+# These calls take tensors, check types, shapes and layout (the library sees only
+# pointers), allocate the outputs that are not given on the launching stream, and run on
+# the device of their tensors whatever the current device is.
+
+def _need(name, t, dtype, shape):
+    """t is a dense tensor of this dtype and shape (None in the shape: any size)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    s = t.shape
+    if len(s) != len(shape) or any(w is not None and w != n for w, n in zip(shape, s)):
+        raise ValueError(f"{name}: shape {tuple(s)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _status_ptr(status):
+    if status is None:
+        return None
+    if status.element_size() != 4 or status.numel() < 1:
+        raise TypeError("status: one 4-byte device word")
+    return status.data_ptr()
+
+
+def _kv_mode(k_cache, k_scale):
+    """(KV_*, SCALE_*, row dtype) of a cache tensor [num_pages, Hkv, page_size, D]."""
+    import torch
+    if k_cache.dtype is torch.bfloat16:
+        if k_scale is not None:
+            raise ValueError("k_scale: a bf16 cache has no scales")
+        return KV_BF16, SCALE_NONE
+    if k_cache.dtype is not torch.uint8 and k_cache.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"k_cache: {k_cache.dtype}, expected uint8, float8_e4m3fn or bfloat16")
+    return KV_FP8_E4M3, SCALE_PER_TOKEN if k_scale is not None else SCALE_SCALAR
+
+
+def _cache_ptrs(k_cache, v_cache, k_scale, v_scale):
+    """Pointers, mode and shape of a K and V cache pair with optional per-token scales."""
+    import torch
+    kv, sm = _kv_mode(k_cache, k_scale)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected [num_pages, Hkv, page_size, D]")
+    pages, heads, ps, d = k_cache.shape
+    shape = (pages, heads, ps, d)
+    kp, vp = _need("k_cache", k_cache, k_cache.dtype, shape), _need("v_cache", v_cache, k_cache.dtype, shape)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale: both or neither")
+    ksp = vsp = None
+    if k_scale is not None:
+        ksp = _need("k_scale", k_scale, torch.float32, shape[:3])
+        vsp = _need("v_scale", v_scale, torch.float32, shape[:3])
+    return kp, vp, ksp, vsp, kv, sm, shape
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device per call")
+
+
+def _enqueue(name, args, device, stream):
+    """Calls the C entry `name` on `device` and `stream` (default: torch's current stream there)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors on {device}, expected a CUDA device")
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        st = f(ctypes.byref(args), s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(ctypes.byref(args), s.cuda_stream)
+    if st != 0:
+        raise PaError(st, name)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output allocated for use on the launching stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *, max_q_len,
+              sm_scale=None, decay=1.0, out=None, k_scale=None, k_scale_scalar=1.0, status=None,
+              stream=None):
+    """Adds a decode step's attention weights to the cached tokens' mass (pa_attn_mass).
+
+    q bf16 [rows, Hq, D], k_cache as pa_decode's, lse fp32 [rows, Hq] of the same pa_decode,
+    mass fp32 [B, Hkv, stride]; updated in place, or into `out` when given (positions past a
+    request's context are not written).  max_q_len bounds every request's rows.  Returns
+    the updated tensor."""
+    import torch
+    i32 = torch.int32
+    kv, sm = _kv_mode(k_cache, k_scale)
+    if k_cache.dim() != 4 or mass.dim() != 3 or q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("expected q [rows, Hq, D], k_cache [num_pages, Hkv, page_size, D], "
+                         "block_table [B, stride] and mass [B, Hkv, stride]")
+    pages, heads, ps, d = k_cache.shape
+    B, rows, Hq = context_lens.shape[0], q.shape[0], q.shape[1]
+    if Hq % heads:
+        raise ValueError(f"q: {Hq} query heads over {heads} KV heads")
+    out = mass if out is None else out
+    width = mass.shape[2]
+    _same_device(k_cache.device, q, block_table, context_lens, cu_seqlens_q, lse, mass, out, k_scale, status)
+    a = AttnMassArgs(
+        _need("q", q, torch.bfloat16, (rows, Hq, d)), _need("k_cache", k_cache, k_cache.dtype, (pages, heads, ps, d)),
+        None if k_scale is None else _need("k_scale", k_scale, torch.float32, (pages, heads, ps)),
+        _need("block_table", block_table, i32, (B, None)), _need("context_lens", context_lens, i32, (B,)),
+        _need("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,)), _need("lse", lse, torch.float32, (rows, Hq)),
+        _need("mass", mass, torch.float32, (B, heads, width)), _need("out", out, torch.float32, (B, heads, width)),
+        _status_ptr(status), pages, B, rows, heads, Hq // heads, d, ps, kv, sm, block_table.shape[1], width,
+        max_q_len, k_scale_scalar, sm_scale if sm_scale is not None else d ** -0.5, decay, 0)
+    _enqueue("pa_attn_mass", a, k_cache.device, stream)
+    return out
+
+
+def evict_select(mass, context_lens, *, budget, first=0, recent=0, keep=None, new_lens=None,
+                 status=None, stream=None):
+    """The positions that stay when every cache is cut to `budget` tokens (pa_evict_select):
+    the first `first`, the last `recent` and the largest mass between.  mass fp32
+    [B, Hkv, stride], context_lens int32 [B].  Returns (keep int32 [B, Hkv, budget], ascending,
+    -1 after; new_lens int32 [B])."""
+    import torch
+    if mass.dim() != 3:
+        raise ValueError("mass: expected [B, Hkv, stride]")
+    B, heads, width = mass.shape
+    dev = mass.device
+    if keep is None:
+        keep = _empty((B, heads, max(int(budget), 1)), torch.int32, dev, stream)
+    if new_lens is None:
+        new_lens = _empty((B,), torch.int32, dev, stream)
+    _same_device(dev, context_lens, keep, new_lens, status)
+    a = EvictSelectArgs(
+        _need("mass", mass, torch.float32, (B, heads, width)), _need("context_lens", context_lens, torch.int32, (B,)),
+        _need("keep", keep, torch.int32, (B, heads, max(int(budget), 1))), _need("new_lens", new_lens, torch.int32, (B,)),
+        _status_ptr(status), B, heads, width, budget, first, recent, 0)
+    _enqueue("pa_evict_select", a, dev, stream)
+    return keep, new_lens
+
+
+def kv_compact(keep, new_lens, block_table, k_cache, v_cache, *, dst_block_table=None, k_scale=None,
+               v_scale=None, mass=None, mass_out=None, status=None, stream=None) -> None:
+    """Moves the kept tokens to the front of their own pages, or of dst_block_table's
+    (pa_kv_compact).  keep int32 [B, Hkv, n] and new_lens int32 [B] as evict_select gives
+    them; mass fp32 [B, Hkv, stride] moves along, in place or, with dst_block_table, into
+    mass_out.  Afterwards new_lens are the context lengths."""
+    import torch
+    if keep.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("expected keep [B, Hkv, n] and block_table [B, stride]")
+    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale)
+    B, dev = keep.shape[0], k_cache.device
+    if mass_out is None and dst_block_table is None:
+        mass_out = mass
+    if mass is None and mass_out is not None:
+        raise ValueError("mass_out without mass")
+    mp = mop = None
+    if mass is not None:
+        mp = _need("mass", mass, torch.float32, (B, heads, None))
+        if mass_out is None:
+            raise ValueError("mass_out: needed with mass and dst_block_table")
+        mop = _need("mass_out", mass_out, torch.float32, (B, heads, None))
+    dp = None if dst_block_table is None else _need("dst_block_table", dst_block_table, torch.int32, (B, None))
+    _same_device(dev, keep, new_lens, block_table, dst_block_table, v_cache, k_scale, v_scale, mass, mass_out, status)
+    a = KvCompactArgs(
+        _need("keep", keep, torch.int32, (B, heads, None)), _need("new_lens", new_lens, torch.int32, (B,)),
+        _need("block_table", block_table, torch.int32, (B, None)), dp, kp, vp, ksp, vsp, mp, mop, _status_ptr(status),
+        pages, B, heads, d, ps, kv, sm, keep.shape[2], block_table.shape[1],
+        0 if dst_block_table is None else dst_block_table.shape[1], 0 if mass is None else mass.shape[2],
+        0 if mass is None else mass_out.shape[2], 0)
+    _enqueue("pa_kv_compact", a, dev, stream)
+
+
+def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_penalty=0.0, tokens=None,
+                parents=None, scores_out=None, finished_out=None, lengths_out=None, stream=None):
+    """One step of beam search (pa_beam_select): the W best continuations of each request's W
+    beams.  logits bf16 or fp32 [N, W, V] or [N * W, V] (rows may be strided: a padded
+    vocabulary), scores fp32 [N, W] (-inf: no such beam yet), finished uint8 and lengths int32
+    [N, W], both optional.  Returns (tokens, parents, scores, finished, lengths), each [N, W];
+    the last two are None where their input is and no output is given."""
+    import torch
+    if scores.dim() != 2 or logits.dim() not in (2, 3):
+        raise ValueError("expected logits [N, W, V] or [N * W, V] and scores [N, W]")
+    N, W = scores.shape
+    V, dev = logits.shape[-1], logits.device
+    if logits.dtype is not torch.bfloat16 and logits.dtype is not torch.float32:
+        raise TypeError(f"logits: {logits.dtype}, expected bfloat16 or float32")
+    if logits.numel() != N * W * V or (logits.dim() == 3 and logits.shape[1] != W):
+        raise ValueError(f"logits: shape {tuple(logits.shape)} for {N} x {W} beams")
+    stride = logits.stride(-2) if N * W > 1 else V
+    if logits.dim() == 3 and W == 1:
+        stride = logits.stride(0) if N > 1 else V
+    if (V > 1 and logits.stride(-1) != 1) or stride < V or \
+            (logits.dim() == 3 and N > 1 and logits.stride(0) != W * stride):
+        raise ValueError("logits: rows must be dense and evenly spaced")
+    mk = lambda t, dtype: _empty((N, W), dtype, dev, stream) if t is None else t
+    tokens, parents, scores_out = mk(tokens, torch.int32), mk(parents, torch.int32), mk(scores_out, torch.float32)
+    if finished is not None:
+        finished_out = mk(finished_out, torch.uint8)
+    if lengths is not None:
+        lengths_out = mk(lengths_out, torch.int32)
+    _same_device(dev, scores, finished, lengths, tokens, parents, scores_out, finished_out, lengths_out)
+    need = lambda name, t, dtype: None if t is None else _need(name, t, dtype, (N, W))
+    a = BeamSelectArgs(
+        logits.data_ptr(), need("scores", scores, torch.float32), need("finished", finished, torch.uint8),
+        need("lengths", lengths, torch.int32), need("tokens", tokens, torch.int32),
+        need("parents", parents, torch.int32), need("scores_out", scores_out, torch.float32),
+        need("finished_out", finished_out, torch.uint8), need("lengths_out", lengths_out, torch.int32),
+        stride, N, W, V, LOGITS_F32 if logits.dtype is torch.float32 else LOGITS_BF16, eos, length_penalty, 0)
+    _enqueue("pa_beam_select", a, dev, stream)
+    return tokens, parents, scores_out, finished_out, lengths_out
+
+
+def beam_reorder(parents, context_lens, block_table, block_table_out, k_cache, v_cache, *, k_scale=None,
+                 v_scale=None, states=(), status=None, stream=None) -> None:
+    """Lets the beams' histories follow their parents (pa_beam_reorder).  parents int32 [N, W],
+    context_lens int32 [N * W], block tables int32 [N * W, stride]; states: up to four
+    (in, out) pairs of tensors with N * W rows, gathered by parent."""
+    import torch
+    if parents.dim() != 2:
+        raise ValueError("parents: expected [N, W]")
+    N, W = parents.shape
+    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    if len(states) > MAX_BEAM_STATES:
+        raise ValueError(f"states: at most {MAX_BEAM_STATES}")
+    a = BeamReorderArgs(
+        _need("parents", parents, torch.int32, (N, W)), _need("context_lens", context_lens, torch.int32, (N * W,)),
+        _need("block_table", block_table, torch.int32, (N * W, None)),
+        _need("block_table_out", block_table_out, torch.int32, (N * W, block_table.shape[1])), kp, vp, ksp, vsp,
+        _status_ptr(status))
+    for i, (x, y) in enumerate(states):
+        if x.dim() < 1 or x.shape[0] != N * W:
+            raise ValueError(f"states[{i}]: expected {N * W} rows")
+        a.state_in[i] = _need(f"states[{i}] in", x, x.dtype, x.shape)
+        a.state_out[i] = _need(f"states[{i}] out", y, x.dtype, x.shape)
+        a.state_bytes[i] = x.numel() // max(N * W, 1) * x.element_size()
+        _same_device(dev, x, y)
+    a.num_pages, a.num_states, a.num_reqs, a.num_beams = pages, len(states), N, W
+    a.num_kv_heads, a.head_dim, a.page_size, a.kv_dtype, a.scale_mode = heads, d, ps, kv, sm
+    a.block_table_stride = block_table.shape[1]
+    _same_device(dev, parents, context_lens, block_table, block_table_out, v_cache, k_scale, v_scale, status)
+    _enqueue("pa_beam_reorder", a, dev, stream)
