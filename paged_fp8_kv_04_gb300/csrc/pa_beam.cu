@@ -6,6 +6,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "pa.h"
 #include "pa_host.cuh"
@@ -22,6 +23,16 @@ constexpr int kMaxReqs = 65535;
 
 // --------------------------------------------------------------------------- selection
 
+// The beams of one request are handled by a cluster of C CTAs: rows are dealt out, and a row is cut
+// into parts where there are more CTAs than beams.  Each part is read once: a thread keeps the
+// running maximum and sum of exponentials of its elements, and the vector its maximum came from.
+//   lse = m + log sum exp(x - m),  total = score + (x - lse).
+// Within a row the order of the totals is the order of the logits, so the W best of a part are
+// found without its lse: of the threads' best elements the W-th, tau, bounds them from below, and
+// elements at or above tau lie with the at most W threads whose best does.  Only those threads'
+// elements are looked at again (from L2), whatever the values: keys are (value, index) pairs,
+// all different.  Every CTA leaves its list, maximum and sum in the shared memory of the
+// cluster's first CTA, one cluster barrier follows, and a warp there joins parts and beams.
 struct BeamParams {
   const void *logits;
   const float *scores;
@@ -32,142 +43,376 @@ struct BeamParams {
   uint8_t *finished_out;
   int32_t *lengths_out;
   int64_t stride;
-  int32_t W, V, f32, eos;
+  int32_t W, V, eos, parts;
   float penalty;
 };
 
-__device__ __forceinline__ float logit(const BeamParams &p, int64_t row, int v) {
-  const int64_t i = row * p.stride + v;
-  if (p.f32) return static_cast<const float *>(p.logits)[i];
-  return __uint_as_float((uint32_t) static_cast<const uint16_t *>(p.logits)[i] << 16);
-}
+typedef unsigned long long u64;
 
 // Keys that order (value, index) pairs: larger value first, then lower index; NaN is -inf.  The
-// largest key is the best pair.
-__device__ __forceinline__ unsigned long long pair_key(float x, int v) {
+// largest key is the best pair; no pair has key 0.
+__device__ __forceinline__ u64 pair_key(float x, int v) {
   const float y = x != x ? -INFINITY : x + 0.f;  // -0 = +0
   const uint32_t u = __float_as_uint(y);
   const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return ((unsigned long long)o << 32) | (0xFFFFFFFFu - (uint32_t)v);
+  return ((u64)o << 32) | (0xFFFFFFFFu - (uint32_t)v);
 }
-__device__ __forceinline__ float key_value(unsigned long long k) {
+__device__ __forceinline__ float key_value(u64 k) {
   const uint32_t o = (uint32_t)(k >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
-__device__ __forceinline__ int key_index(unsigned long long k) {
-  return (int)(0xFFFFFFFFu - (uint32_t)(k & 0xFFFFFFFFull));
-}
+__device__ __forceinline__ int key_index(u64 k) { return (int)(0xFFFFFFFFu - (uint32_t)(k & 0xFFFFFFFFull)); }
 // Ordered bits of a double that is not NaN; greater than 0 for every such double.
-__device__ __forceinline__ unsigned long long rank_key(double x) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+__device__ __forceinline__ u64 rank_key(double x) {
+  const u64 u = (u64)__double_as_longlong(x + 0.0);
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
-constexpr int kBeamThreads = 1024;
+// 32 keys, one per lane, in descending order over the lanes: bitonic networks on shuffles.
+__device__ __forceinline__ u64 exchange(u64 k, int lane, int j, bool up) {
+  const u64 y = __shfl_xor_sync(~0u, k, j);
+  const bool larger = ((lane & j) == 0) == up;
+  return larger ? (k > y ? k : y) : (k < y ? k : y);
+}
+__device__ __forceinline__ u64 sort32(u64 k, int lane) {
+#pragma unroll
+  for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+    for (int j = n >> 1; j >= 1; j >>= 1) k = exchange(k, lane, j, (lane & n) == 0);
+  return k;
+}
+// The 32 best of two descending lists, the other's given from its end.
+__device__ __forceinline__ u64 merge32(u64 k, u64 other_reversed, int lane) {
+  k = k > other_reversed ? k : other_reversed;
+#pragma unroll
+  for (int j = 16; j >= 1; j >>= 1) k = exchange(k, lane, j, true);
+  return k;
+}
 
-__device__ unsigned long long block_max(unsigned long long k, unsigned long long *buf) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const unsigned long long y = __shfl_xor_sync(~0u, k, o);
-    k = k > y ? k : y;
+constexpr int kBeamThreads = 512;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kUnroll = 4;  // 16-byte loads in flight per thread: 32 KB per CTA, two CTAs per SM
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ float get(const uint4 &v, int e) {
+    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
+    return (e & 1) ? pa::bf16hi(w) : pa::bf16lo(w);
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = k;
-  __syncthreads();
-  k = buf[threadIdx.x & 31];
+};
+template <>
+struct Vec<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ float get(const uint4 &v, int e) {
+    return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+  }
+};
+
+// A row seen as 16-byte vectors on 16-byte boundaries: vector j holds the elements
+// E j - e0 .. E j - e0 + E - 1, of which the first and last vector may have fewer.
+template <typename T>
+struct RowView {
+  static constexpr int E = Vec<T>::E;
+  const T *x;
+  int V, e0, nv;
+  __device__ RowView(const T *row, int vocab) : x(row), V(vocab) {
+    e0 = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    nv = (e0 + V + E - 1) / E;
+  }
+  __device__ __forceinline__ int first(int j) const { return E * j - e0; }  // may be negative
+  __device__ __forceinline__ uint4 load(int j) const {
+    const int f = first(j);
+    if (f >= 0 && f + E <= V) return __ldg(reinterpret_cast<const uint4 *>(x + f));
+    uint32_t w[4];  // a ragged end: what is missing is -inf
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const unsigned long long y = __shfl_xor_sync(~0u, k, o);
-    k = k > y ? k : y;
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(T) == 4) {
+        w[i] = f + i >= 0 && f + i < V ? ((const uint32_t *)x)[f + i] : 0xFF800000u;
+      } else {
+        const int a = f + 2 * i;
+        const uint32_t lo = a >= 0 && a < V ? ((const uint16_t *)x)[a] : 0xFF80u;
+        const uint32_t hi = a + 1 >= 0 && a + 1 < V ? ((const uint16_t *)x)[a + 1] : 0xFF80u;
+        w[i] = lo | (hi << 16);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxLists = kMaxBeams;  // rows * parts <= 32
+
+struct BeamShared {
+  u64 buf[kBeamWarps][32];
+  u64 list[kMaxLists][kMaxBeams];  // the first CTA's: each (row, part)'s best, descending
+  long long sum[kMaxLists];        // sum of exp(x - m) in units of 2^-36, or -1: NaN
+  float max[kMaxLists];
+  long long wsum[kBeamWarps];
+  double lse[kMaxBeams];
+  double norm[kMaxBeams];          // max(new length, 1) ^ length_penalty
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// This shared-memory address in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(const void *p) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(pa::smem_u32(p)));
+  return a;
+}
+__device__ __forceinline__ void store_cluster(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// Joins the warps' descending lists (one key per lane); the result is in warp 0.
+__device__ __forceinline__ u64 join_warps(u64 k, BeamShared &sm, int warp, int lane, int lists) {
+  sm.buf[warp][lane] = k;
+  for (int n = lists >> 1; n >= 1; n >>= 1) {
+    __syncthreads();
+    if (warp < n) {
+      k = merge32(k, sm.buf[warp + n][31 - lane], lane);
+      sm.buf[warp][lane] = k;
+    }
   }
   return k;
 }
 
-// A CTA per request.  For every beam: the row's log-sum-exp, then its W best tokens, one
-// reduction over the row each; then one warp merges the beams' lists, a lane per beam.
-__global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamParams p) {
-  __shared__ unsigned long long buf[32];
-  __shared__ double dbuf[32];
-  __shared__ unsigned long long list[kMaxBeams][kMaxBeams];  // [beam][k]: the k-th best (logit, token)
-  __shared__ double lse[kMaxBeams];
-  const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int b = 0; b < p.W; ++b) {
-    const int64_t row = (int64_t)n * p.W + b;
-    unsigned long long best = 0;
-    for (int v = tid; v < p.V; v += kBeamThreads) {
-      const unsigned long long k = pair_key(logit(p, row, v), v);
-      best = k > best ? k : best;
-    }
-    best = block_max(best, buf);
-    const float m = key_value(best);
-    double s = 0.0;
-    for (int v = tid; v < p.V; v += kBeamThreads)
-      s += pa::fast_exp2((logit(p, row, v) - m) * 1.4426950408889634f);  // NaN for NaN, and for +-inf - itself
+// One part of one row: its list, maximum and sum go to slot `slot` of the first CTA.
+template <typename T>
+__device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int part, int slot, bool wait) {
+  constexpr int E = Vec<T>::E;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const RowView<T> r(static_cast<const T *>(p.logits) + row * p.stride, p.V);
+  const int lo = (int)((int64_t)r.nv * part / p.parts), hi = (int)((int64_t)r.nv * (part + 1) / p.parts);
+
+  // ---- one pass: maximum, sum of 2^((x - m) log2 e), and the vector of the maximum
+  float m = -INFINITY, s = 0.f;
+  int best = lo + tid;
+  uint4 bv = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  bool nan = false;
+  for (int j0 = lo + tid; j0 < hi; j0 += kUnroll * kBeamThreads) {
+    uint4 v[kUnroll];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    __syncthreads();
-    if (lane == 0) dbuf[warp] = s;
-    __syncthreads();
-    s = dbuf[lane];
+    for (int u = 0; u < kUnroll; ++u)
+      if (j0 + u * kBeamThreads < hi) v[u] = r.load(j0 + u * kBeamThreads);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    if (tid == 0) lse[b] = (double)m + log(s);
-    for (int k = 0; k < p.W; ++k) {
-      if (tid == 0) list[b][k] = best;
-      if (k + 1 == p.W) break;
-      unsigned long long next = 0;
-      for (int v = tid; v < p.V; v += kBeamThreads) {
-        const unsigned long long key = pair_key(logit(p, row, v), v);
-        if (key < best && key > next) next = key;
+    for (int u = 0; u < kUnroll; ++u) {
+      if (j0 + u * kBeamThreads >= hi) break;
+      float mx = Vec<T>::get(v[u], 0);
+#pragma unroll
+      for (int e = 1; e < E; ++e) mx = fmaxf(mx, Vec<T>::get(v[u], e));
+      if (mx > m) {
+        s *= pa::fast_exp2((m - mx) * kLog2e);
+        m = mx;
+        bv = v[u];
+        best = j0 + u * kBeamThreads;
       }
-      best = block_max(next, buf);  // 0 once the vocabulary is used up
+      // the difference first: exact near the maximum, and in range at the types' lowest values
+      const float ref = m == -INFINITY ? 0.f : m;
+      float t[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) t[e] = pa::fast_exp2((Vec<T>::get(v[u], e) - ref) * kLog2e);
+#pragma unroll
+      for (int n = E / 2; n >= 1; n >>= 1)
+#pragma unroll
+        for (int e = 0; e < n; ++e) t[e] += t[e + n];
+      s += t[0];
     }
+  }
+  nan = s != s;  // a NaN or +inf among the elements
+  u64 key = 0;
+  if (lo + tid < hi) {
+    int at = max(r.first(lo + tid), 0);  // nothing above -inf: the first element
+    if (m > -INFINITY) {
+      at = r.first(best);
+      bool found = false;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (!found) {
+          if (Vec<T>::get(bv, e) == m) found = true;
+          else ++at;
+        }
+    }
+    key = pair_key(m, at);
+  }
+
+  // ---- the W-th of the threads' best elements
+  __syncthreads();  // the buffers' readers of an earlier part are done
+  u64 k = join_warps(sort32(key, lane), sm, warp, lane, kBeamWarps);
+  // the part's sum: every thread's relative to the part's maximum, in fixed point (2^-36), so that
+  // joining 512 of them loses nothing
+  __syncthreads();
+  const float top = key_value(sm.buf[0][0]);
+  const float scaled = m == -INFINITY ? 0.f : s * pa::fast_exp2((m - top) * kLog2e);
+  long long fixed = nan ? 0 : __float2ll_rn(scaled * 68719476736.f);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) fixed += __shfl_xor_sync(~0u, fixed, o);
+  const bool wnan = __any_sync(~0u, nan);
+  if (lane == 0) sm.wsum[warp] = wnan ? -1 : fixed;
+
+  // ---- the elements at or above tau, from the threads whose best is one of the W: a warp for each
+  const u64 tau = sm.buf[0][p.W - 1];
+  u64 mine = 0;
+  for (int i = warp; i < p.W; i += kBeamWarps) {
+    const u64 owner = sm.buf[0][i];
+    if (owner == 0) break;
+    const int oj = (key_index(owner) + r.e0) / E;
+    for (int j0 = lo + (oj - lo) % kBeamThreads; j0 < hi; j0 += 32 * kBeamThreads) {
+      const int64_t j = (int64_t)j0 + (int64_t)lane * kBeamThreads;
+      uint4 v;
+      if (j < hi) v = r.load((int)j);
+      unsigned left = 0;  // this lane's elements at or above tau
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int at = r.first((int)j) + e;
+        if (j < hi && at >= 0 && at < p.V && pair_key(Vec<T>::get(v, e), at) >= tau) left |= 1u << e;
+      }
+      while (__any_sync(~0u, left != 0)) {
+        const unsigned who = __ballot_sync(~0u, left != 0);
+        const int src = __ffs(who) - 1;
+        u64 c = 0;
+        if (lane == src) {
+          const int e = __ffs(left) - 1;
+          left &= left - 1;
+          float x = 0.f;
+#pragma unroll
+          for (int q = 0; q < E; ++q)
+            if (q == e) x = Vec<T>::get(v, q);
+          c = pair_key(x, r.first((int)j) + e);
+        }
+        c = __shfl_sync(~0u, c, src);
+        // insert: lanes above it keep theirs, the others shift down by one
+        const int pos = __popc(__ballot_sync(~0u, mine > c));
+        const u64 up = __shfl_up_sync(~0u, mine, 1);
+        if (lane == pos) mine = c;
+        if (lane > pos) mine = up;
+      }
+    }
+  }
+  if (wait) cluster_wait();  // the first CTA runs: its shared memory can be written
+  __syncthreads();
+  int lists = 1;
+  while (lists < kBeamWarps && lists < p.W) lists <<= 1;
+  k = join_warps(mine, sm, warp, lane, lists);
+  if (warp == 0) {
+    long long t = lane < kBeamWarps ? sm.wsum[lane] : 0;
+    const bool bad = __any_sync(~0u, t < 0);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+    store_cluster(in_first_cta(&sm.list[slot][lane]), k);
+    if (lane == 0) {
+      store_cluster(in_first_cta(&sm.max[slot]), top);
+      store_cluster(in_first_cta(&sm.sum[slot]), (u64)(bad ? -1 : t));
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const BeamParams p) {
+  __shared__ BeamShared sm;
+  cluster_arrive();
+  uint32_t C;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+  const uint32_t rank = cluster_rank();
+  const int n = blockIdx.x / C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t base = (int64_t)n * p.W, me = base + lane;
+  const bool mine = lane < p.W;
+  bool done = false;
+  int len = 0;
+  if (rank == 0 && warp == 0) {
+    // lane b: beam b's length and its power, while the others' loads are on their way
+    done = mine && p.finished != nullptr && p.finished[me] != 0;
+    len = mine && p.lengths != nullptr ? p.lengths[me] : 0;
+    if (!done && len < INT_MAX) ++len;
+    sm.norm[lane] = p.penalty == 0.f ? 1.0 : pow((double)max(len, 1), (double)p.penalty);
+  }
+  const int units = p.W * p.parts;
+  bool waited = false;
+  for (int u = rank; u < units; u += C) {
+    beam_part<T>(p, sm, base + u / p.parts, u % p.parts, u, !waited);
+    waited = true;
+  }
+  if (!waited) cluster_wait();
+  cluster_arrive();
+  if (rank != 0) return;
+  cluster_wait();
+
+  // ---- the first CTA: a warp joins the parts of a row
+  for (int b = warp; b < p.W; b += kBeamWarps) {
+    const int s0 = b * p.parts;
+    u64 k = sm.list[s0][lane];
+    for (int q = 1; q < p.parts; ++q) k = merge32(k, sm.list[s0 + q][31 - lane], lane);
+    const float m = lane < p.parts ? sm.max[s0 + lane] : -INFINITY;
+    const long long t = lane < p.parts ? sm.sum[s0 + lane] : 0;
+    float M = m;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    double sum = (double)t * (1.0 / 68719476736.0);
+    if (p.parts > 1) {
+      sum = m == -INFINITY ? 0.0 : sum * exp((double)m - (double)M);
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    }
+    const bool bad = __any_sync(~0u, t < 0);
+    __syncwarp();
+    if (lane == 0) sm.lse[b] = bad ? (double)NAN : (double)M + log(sum);
+    sm.list[s0][lane] = k;
   }
   __syncthreads();
   if (warp != 0) return;
   // Lane b walks beam b's candidates in order: `at` counts those taken.
-  const bool mine = lane < p.W;
-  const int64_t me = (int64_t)n * p.W + lane;
   const float cum = mine ? p.scores[me] : -INFINITY;
-  const bool done = mine && p.finished != nullptr && p.finished[me] != 0;
-  const int len = mine && p.lengths != nullptr ? p.lengths[me] : 0;
-  const int newlen = done ? len : (len == INT_MAX ? len : len + 1);
-  const double norm = p.penalty == 0.f ? 1.0 : pow((double)max(newlen, 1), (double)p.penalty);
+  const double lse = mine ? sm.lse[lane] : 0.0, norm = sm.norm[lane];
+  const u64 *list = sm.list[mine ? lane * p.parts : 0];
   // no continuation at a number: every candidate counts as -inf
-  const bool dead = mine && (cum != cum || cum == -INFINITY || (!done && !(fabs(lse[mine ? lane : 0]) < INFINITY)));
-  int at = 0;
-  for (int j = 0; j < p.W; ++j) {
-    unsigned long long key = 0;
-    int tok = -1;
-    double total = -INFINITY;
-    if (mine && at < p.V) {
-      if (dead) {
-        tok = at;
-      } else if (done) {
-        tok = at == 0 ? p.eos : (at <= p.eos ? at - 1 : at);
-        if (at == 0) total = (double)cum;
-      } else {
-        tok = key_index(list[lane][at]);
-        total = (double)cum + ((double)key_value(list[lane][at]) - lse[lane]);
-        if (total != total) total = -INFINITY;
-      }
-      key = rank_key(total / norm);
+  const bool dead = mine && (cum != cum || cum == -INFINITY || (!done && !(fabs(lse) < INFINITY)));
+  int at = 0, tok = -1;
+  double total = -INFINITY;
+  u64 key = 0;
+  auto next = [&]() {
+    key = 0;
+    total = -INFINITY;
+    if (!mine || at >= p.V) return;
+    if (dead) {
+      tok = at;
+    } else if (done) {
+      tok = at == 0 ? p.eos : (at <= p.eos ? at - 1 : at);
+      if (at == 0) total = (double)cum;
+    } else {
+      tok = key_index(list[at]);
+      total = (double)cum + ((double)key_value(list[at]) - lse);
+      if (total != total) total = -INFINITY;
     }
-    unsigned long long top = key;
+    key = rank_key(p.penalty == 0.f ? total : total / norm);
+  };
+  next();
+  for (int j = 0; j < p.W; ++j) {
+    u64 top = key;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
-      const unsigned long long y = __shfl_xor_sync(~0u, top, o);
+      const u64 y = __shfl_xor_sync(~0u, top, o);
       top = top > y ? top : y;
     }
     const int win = __ffs(__ballot_sync(~0u, key == top)) - 1;  // equal ranks: the lower beam
     if (lane == win) {
-      const int64_t o = (int64_t)n * p.W + j;
-      p.tokens[o] = tok;
-      p.parents[o] = lane;
-      p.scores_out[o] = (float)total;
-      if (p.finished_out != nullptr) p.finished_out[o] = done || (p.eos >= 0 && tok == p.eos);
-      if (p.lengths_out != nullptr) p.lengths_out[o] = newlen;
+      p.tokens[base + j] = tok;
+      p.parents[base + j] = lane;
+      p.scores_out[base + j] = (float)total;
+      if (p.finished_out != nullptr) p.finished_out[base + j] = done || (p.eos >= 0 && tok == p.eos);
+      if (p.lengths_out != nullptr) p.lengths_out[base + j] = len;
       ++at;
+      if (at < p.W) next();
     }
   }
 }
@@ -269,6 +514,27 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const Reo
   }
 }
 
+constexpr int kMaxCluster = 16;  // more than 8 needs the kernel's opt-in
+
+// The current device's SM count, and its kernels' opt-in to clusters of 16, once per device; 0 for
+// a device beyond those tracked, -1 when a call fails.
+int beam_device() {
+  static std::once_flag once[pa_host::kMaxDevices];
+  static int sms[pa_host::kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev < 0 || dev >= pa_host::kMaxDevices) return 0;
+  std::call_once(once[dev], [dev]() {
+    int n = 0;
+    const bool ok =
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        cudaFuncSetAttribute(beam_select_kernel<float>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaFuncSetAttribute(beam_select_kernel<uint16_t>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    sms[dev] = ok ? n : -1;
+  });
+  return sms[dev];
+}
+
 }  // namespace
 
 extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stream) {
@@ -300,12 +566,29 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   p.stride = a->logits_stride;
   p.W = a->num_beams;
   p.V = a->vocab;
-  p.f32 = a->logits_dtype == PA_LOGITS_F32;
   p.eos = a->eos_token;
   p.penalty = a->length_penalty;
-  (void)cudaGetLastError();  // drop an earlier, unrelated launch error
-  beam_select_kernel<<<a->num_reqs, kBeamThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const bool f32 = a->logits_dtype == PA_LOGITS_F32;
+  const int sms = beam_device();
+  if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+  // CTAs per request: as many as keep one wave (two CTAs per SM) and 16 KB of logits each
+  const int64_t bytes = (int64_t)a->num_beams * a->vocab * (f32 ? 4 : 2);
+  int C = 1;
+  while (C < kMaxCluster && (int64_t)a->num_reqs * C <= sms && bytes / (2 * C) >= 16384) C *= 2;
+  p.parts = C > a->num_beams ? C / a->num_beams : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a->num_reqs * C);
+  cfg.blockDim = dim3(kBeamThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, beam_select_kernel<float>, p)
+                            : cudaLaunchKernelEx(&cfg, beam_select_kernel<uint16_t>, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 extern "C" pa_status_t pa_beam_reorder(const pa_beam_reorder_args_t *a, void *stream) {
