@@ -419,9 +419,9 @@ typedef struct pa_evict_select_args {
   int32_t *keep;                 /* out: [num_seqs, num_kv_heads, budget] kept positions, ascending, -1 after */
   int32_t *new_lens;             /* out: [num_seqs] min(context_len, budget); must not be context_lens */
   uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT is OR-ed in */
-  int32_t num_seqs;              /* 0 .. 65535; 0 enqueues nothing */
+  int32_t num_seqs;              /* >= 0, num_seqs * num_kv_heads <= 65535; 0 enqueues nothing */
   int32_t num_kv_heads;          /* 1 .. 64 */
-  int32_t mass_stride;           /* >= 1 */
+  int32_t mass_stride;           /* 1 .. 2^30 */
   int32_t budget;                /* >= 1: most tokens kept per (request, KV head) */
   int32_t keep_first;            /* >= 0: positions [0, keep_first) always stay */
   int32_t keep_recent;           /* >= 0: the last keep_recent positions always stay;
@@ -437,7 +437,7 @@ typedef struct pa_evict_select_args {
  * or beyond mass_stride is flagged: its keep rows are all -1 and its new_lens 0.  One kernel
  * launch on `stream`; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing
  * pointer or a value out of range, PA_ERR_ALIGN for a pointer not aligned to 4 bytes,
- * PA_ERR_UNSUPPORTED for more than 64 KV heads or 65535 requests, PA_ERR_CUDA when the launch fails. */
+ * PA_ERR_UNSUPPORTED for a shape beyond the limits above, PA_ERR_CUDA when the launch fails. */
 pa_status_t pa_evict_select(const pa_evict_select_args_t *args, void *stream);
 
 /* Arguments of pa_kv_compact.  All pointers are device pointers. */
@@ -456,7 +456,7 @@ typedef struct pa_kv_compact_args {
                                     `mass` itself with the same stride, with dst_block_table not overlapping it */
   uint32_t *status;              /* nullable: PA_DEV_BAD_KEEP, PA_DEV_BAD_PAGE are OR-ed in */
   int64_t num_pages;
-  int32_t num_seqs;              /* 0 .. 65535; 0 enqueues nothing */
+  int32_t num_seqs;              /* >= 0, num_seqs * num_kv_heads <= 65535; 0 enqueues nothing */
   int32_t num_kv_heads;          /* 1 .. 64 */
   int32_t head_dim;              /* 128 */
   int32_t page_size;             /* 16, 32, 64 or 128 */

@@ -466,85 +466,91 @@ def lse_merge(part_out, part_lse, out, lse=None, stream=None, args: Optional[Lse
 # pointers), allocate the outputs that are not given on the launching stream, and run on
 # the device of their tensors whatever the current device is.
 
-def _need(name, t, dtype, shape):
-    """t is a dense tensor of this dtype and shape (None in the shape: any size)."""
+def _need(name, t, dtype, shape, dev):
+    """Pointer of a dense tensor of this dtype and shape on CUDA device number dev."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    s = t.shape
-    if len(s) != len(shape) or any(w is not None and w != n for w, n in zip(shape, s)):
-        raise ValueError(f"{name}: shape {tuple(s)}, expected {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{dev} like the rest of the call")
 
 
-def _status_ptr(status):
+def _rank(name, t, dims):
+    if t.dim() != dims:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dims}")
+    return t.shape
+
+
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"tensors on {t.device}, expected a CUDA device")
+    return dev
+
+
+def _status_ptr(status, dev):
     if status is None:
         return None
-    if status.element_size() != 4 or status.numel() < 1:
-        raise TypeError("status: one 4-byte device word")
+    if status.element_size() != 4 or status.numel() < 1 or status.get_device() != dev:
+        raise ValueError("status: a 4-byte word on the call's device")
     return status.data_ptr()
 
 
 def _kv_mode(k_cache, k_scale):
-    """(KV_*, SCALE_*, row dtype) of a cache tensor [num_pages, Hkv, page_size, D]."""
+    """(KV_*, SCALE_*) of a cache tensor."""
     import torch
-    if k_cache.dtype is torch.bfloat16:
-        if k_scale is not None:
-            raise ValueError("k_scale: a bf16 cache has no scales")
-        return KV_BF16, SCALE_NONE
-    if k_cache.dtype is not torch.uint8 and k_cache.dtype is not torch.float8_e4m3fn:
-        raise TypeError(f"k_cache: {k_cache.dtype}, expected uint8, float8_e4m3fn or bfloat16")
-    return KV_FP8_E4M3, SCALE_PER_TOKEN if k_scale is not None else SCALE_SCALAR
+    dt = k_cache.dtype
+    if dt is torch.uint8 or dt is torch.float8_e4m3fn:
+        return KV_FP8_E4M3, SCALE_SCALAR if k_scale is None else SCALE_PER_TOKEN
+    if dt is not torch.bfloat16:
+        raise TypeError(f"k_cache: {dt}, expected uint8, float8_e4m3fn or bfloat16")
+    if k_scale is not None:
+        raise ValueError("k_scale: a bf16 cache has no scales")
+    return KV_BF16, SCALE_NONE
 
 
-def _cache_ptrs(k_cache, v_cache, k_scale, v_scale):
+def _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev):
     """Pointers, mode and shape of a K and V cache pair with optional per-token scales."""
     import torch
     kv, sm = _kv_mode(k_cache, k_scale)
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: expected [num_pages, Hkv, page_size, D]")
-    pages, heads, ps, d = k_cache.shape
-    shape = (pages, heads, ps, d)
-    kp, vp = _need("k_cache", k_cache, k_cache.dtype, shape), _need("v_cache", v_cache, k_cache.dtype, shape)
-    if (k_scale is None) != (v_scale is None):
+    shape = _rank("k_cache", k_cache, 4)
+    kp = _need("k_cache", k_cache, k_cache.dtype, shape, dev)
+    vp = _need("v_cache", v_cache, k_cache.dtype, shape, dev)
+    if k_scale is None:
+        if v_scale is not None:
+            raise ValueError("k_scale and v_scale: both or neither")
+        return kp, vp, None, None, kv, sm, shape
+    if v_scale is None:
         raise ValueError("k_scale and v_scale: both or neither")
-    ksp = vsp = None
-    if k_scale is not None:
-        ksp = _need("k_scale", k_scale, torch.float32, shape[:3])
-        vsp = _need("v_scale", v_scale, torch.float32, shape[:3])
-    return kp, vp, ksp, vsp, kv, sm, shape
+    return (kp, vp, _need("k_scale", k_scale, torch.float32, shape[:3], dev),
+            _need("v_scale", v_scale, torch.float32, shape[:3], dev), kv, sm, shape)
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device per call")
-
-
-def _enqueue(name, args, device, stream):
-    """Calls the C entry `name` on `device` and `stream` (default: torch's current stream there)."""
+def _enqueue(name, entry, args, dev, stream):
+    """Calls a C entry on device number dev and `stream` (default: torch's current stream there)."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"{name}: tensors on {device}, expected a CUDA device")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = f(ctypes.byref(args), s.cuda_stream)
+    # the raw handle of torch's current stream: its Stream object costs as much as the launch
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = entry(ctypes.byref(args), s)
     else:
-        with torch.cuda.device(device):
-            st = f(ctypes.byref(args), s.cuda_stream)
+        with torch.cuda.device(dev):
+            st = entry(ctypes.byref(args), s)
     if st != 0:
         raise PaError(st, name)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, dev, stream):
     """An output allocated for use on the launching stream."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *, max_q_len,
@@ -557,27 +563,26 @@ def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *,
     request's context are not written).  max_q_len bounds every request's rows.  Returns
     the updated tensor."""
     import torch
-    i32 = torch.int32
+    i32, f32, dev = torch.int32, torch.float32, _device_of(k_cache)
     kv, sm = _kv_mode(k_cache, k_scale)
-    if k_cache.dim() != 4 or mass.dim() != 3 or q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("expected q [rows, Hq, D], k_cache [num_pages, Hkv, page_size, D], "
-                         "block_table [B, stride] and mass [B, Hkv, stride]")
-    pages, heads, ps, d = k_cache.shape
-    B, rows, Hq = context_lens.shape[0], q.shape[0], q.shape[1]
-    if Hq % heads:
-        raise ValueError(f"q: {Hq} query heads over {heads} KV heads")
-    out = mass if out is None else out
-    width = mass.shape[2]
-    _same_device(k_cache.device, q, block_table, context_lens, cu_seqlens_q, lse, mass, out, k_scale, status)
+    cache = _rank("k_cache", k_cache, 4)
+    pages, heads, ps, d = cache
+    rows, Hq, _ = _rank("q", q, 3)
+    B, _, width = shape = _rank("mass", mass, 3)
+    table = _rank("block_table", block_table, 2)
+    if Hq % heads or shape[1] != heads or table[0] != B:
+        raise ValueError(f"q {tuple(q.shape)}, mass {tuple(shape)} and block_table {tuple(table)} for {heads} KV heads")
+    if out is None:
+        out = mass
     a = AttnMassArgs(
-        _need("q", q, torch.bfloat16, (rows, Hq, d)), _need("k_cache", k_cache, k_cache.dtype, (pages, heads, ps, d)),
-        None if k_scale is None else _need("k_scale", k_scale, torch.float32, (pages, heads, ps)),
-        _need("block_table", block_table, i32, (B, None)), _need("context_lens", context_lens, i32, (B,)),
-        _need("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,)), _need("lse", lse, torch.float32, (rows, Hq)),
-        _need("mass", mass, torch.float32, (B, heads, width)), _need("out", out, torch.float32, (B, heads, width)),
-        _status_ptr(status), pages, B, rows, heads, Hq // heads, d, ps, kv, sm, block_table.shape[1], width,
-        max_q_len, k_scale_scalar, sm_scale if sm_scale is not None else d ** -0.5, decay, 0)
-    _enqueue("pa_attn_mass", a, k_cache.device, stream)
+        _need("q", q, torch.bfloat16, (rows, Hq, d), dev), _need("k_cache", k_cache, k_cache.dtype, cache, dev),
+        None if k_scale is None else _need("k_scale", k_scale, f32, cache[:3], dev),
+        _need("block_table", block_table, i32, table, dev), _need("context_lens", context_lens, i32, (B,), dev),
+        _need("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev), _need("lse", lse, f32, (rows, Hq), dev),
+        _need("mass", mass, f32, shape, dev), _need("out", out, f32, shape, dev), _status_ptr(status, dev),
+        pages, B, rows, heads, Hq // heads, d, ps, kv, sm, table[1], width, max_q_len, k_scale_scalar,
+        sm_scale if sm_scale is not None else d ** -0.5, decay, 0)
+    _enqueue("pa_attn_mass", lib().pa_attn_mass, a, dev, stream)
     return out
 
 
@@ -588,20 +593,18 @@ def evict_select(mass, context_lens, *, budget, first=0, recent=0, keep=None, ne
     [B, Hkv, stride], context_lens int32 [B].  Returns (keep int32 [B, Hkv, budget], ascending,
     -1 after; new_lens int32 [B])."""
     import torch
-    if mass.dim() != 3:
-        raise ValueError("mass: expected [B, Hkv, stride]")
-    B, heads, width = mass.shape
-    dev = mass.device
+    i32, dev = torch.int32, _device_of(mass)
+    B, heads, width = shape = _rank("mass", mass, 3)
+    kept = (B, heads, budget if budget > 0 else 1)  # the library refuses a budget below 1
     if keep is None:
-        keep = _empty((B, heads, max(int(budget), 1)), torch.int32, dev, stream)
+        keep = _empty(kept, i32, dev, stream)
     if new_lens is None:
-        new_lens = _empty((B,), torch.int32, dev, stream)
-    _same_device(dev, context_lens, keep, new_lens, status)
+        new_lens = _empty((B,), i32, dev, stream)
     a = EvictSelectArgs(
-        _need("mass", mass, torch.float32, (B, heads, width)), _need("context_lens", context_lens, torch.int32, (B,)),
-        _need("keep", keep, torch.int32, (B, heads, max(int(budget), 1))), _need("new_lens", new_lens, torch.int32, (B,)),
-        _status_ptr(status), B, heads, width, budget, first, recent, 0)
-    _enqueue("pa_evict_select", a, dev, stream)
+        _need("mass", mass, torch.float32, shape, dev), _need("context_lens", context_lens, i32, (B,), dev),
+        _need("keep", keep, i32, kept, dev), _need("new_lens", new_lens, i32, (B,), dev),
+        _status_ptr(status, dev), B, heads, width, budget, first, recent, 0)
+    _enqueue("pa_evict_select", lib().pa_evict_select, a, dev, stream)
     return keep, new_lens
 
 
@@ -612,29 +615,28 @@ def kv_compact(keep, new_lens, block_table, k_cache, v_cache, *, dst_block_table
     them; mass fp32 [B, Hkv, stride] moves along, in place or, with dst_block_table, into
     mass_out.  Afterwards new_lens are the context lengths."""
     import torch
-    if keep.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("expected keep [B, Hkv, n] and block_table [B, stride]")
-    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale)
-    B, dev = keep.shape[0], k_cache.device
-    if mass_out is None and dst_block_table is None:
+    i32, f32, dev = torch.int32, torch.float32, _device_of(k_cache)
+    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev)
+    B, _, n = _rank("keep", keep, 3)
+    width = _rank("block_table", block_table, 2)[1]
+    dp = mp = mop = None
+    dst_width = mass_width = out_width = 0
+    if dst_block_table is not None:
+        dst_width = _rank("dst_block_table", dst_block_table, 2)[1]
+        dp = _need("dst_block_table", dst_block_table, i32, (B, dst_width), dev)
+    elif mass_out is None:
         mass_out = mass
-    if mass is None and mass_out is not None:
-        raise ValueError("mass_out without mass")
-    mp = mop = None
+    if (mass is None) != (mass_out is None):
+        raise ValueError("mass and mass_out: both or neither (in place mass alone)")
     if mass is not None:
-        mp = _need("mass", mass, torch.float32, (B, heads, None))
-        if mass_out is None:
-            raise ValueError("mass_out: needed with mass and dst_block_table")
-        mop = _need("mass_out", mass_out, torch.float32, (B, heads, None))
-    dp = None if dst_block_table is None else _need("dst_block_table", dst_block_table, torch.int32, (B, None))
-    _same_device(dev, keep, new_lens, block_table, dst_block_table, v_cache, k_scale, v_scale, mass, mass_out, status)
+        mass_width, out_width = _rank("mass", mass, 3)[2], _rank("mass_out", mass_out, 3)[2]
+        mp = _need("mass", mass, f32, (B, heads, mass_width), dev)
+        mop = _need("mass_out", mass_out, f32, (B, heads, out_width), dev)
     a = KvCompactArgs(
-        _need("keep", keep, torch.int32, (B, heads, None)), _need("new_lens", new_lens, torch.int32, (B,)),
-        _need("block_table", block_table, torch.int32, (B, None)), dp, kp, vp, ksp, vsp, mp, mop, _status_ptr(status),
-        pages, B, heads, d, ps, kv, sm, keep.shape[2], block_table.shape[1],
-        0 if dst_block_table is None else dst_block_table.shape[1], 0 if mass is None else mass.shape[2],
-        0 if mass is None else mass_out.shape[2], 0)
-    _enqueue("pa_kv_compact", a, dev, stream)
+        _need("keep", keep, i32, (B, heads, n), dev), _need("new_lens", new_lens, i32, (B,), dev),
+        _need("block_table", block_table, i32, (B, width), dev), dp, kp, vp, ksp, vsp, mp, mop,
+        _status_ptr(status, dev), pages, B, heads, d, ps, kv, sm, n, width, dst_width, mass_width, out_width, 0)
+    _enqueue("pa_kv_compact", lib().pa_kv_compact, a, dev, stream)
 
 
 def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_penalty=0.0, tokens=None,
@@ -645,35 +647,48 @@ def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_p
     [N, W], both optional.  Returns (tokens, parents, scores, finished, lengths), each [N, W];
     the last two are None where their input is and no output is given."""
     import torch
-    if scores.dim() != 2 or logits.dim() not in (2, 3):
-        raise ValueError("expected logits [N, W, V] or [N * W, V] and scores [N, W]")
-    N, W = scores.shape
-    V, dev = logits.shape[-1], logits.device
-    if logits.dtype is not torch.bfloat16 and logits.dtype is not torch.float32:
+    i32, u8, f32, dev = torch.int32, torch.uint8, torch.float32, _device_of(logits)
+    N, W = shape = _rank("scores", scores, 2)
+    if logits.dtype is not torch.bfloat16 and logits.dtype is not f32:
         raise TypeError(f"logits: {logits.dtype}, expected bfloat16 or float32")
-    if logits.numel() != N * W * V or (logits.dim() == 3 and logits.shape[1] != W):
-        raise ValueError(f"logits: shape {tuple(logits.shape)} for {N} x {W} beams")
-    stride = logits.stride(-2) if N * W > 1 else V
-    if logits.dim() == 3 and W == 1:
-        stride = logits.stride(0) if N > 1 else V
-    if (V > 1 and logits.stride(-1) != 1) or stride < V or \
-            (logits.dim() == 3 and N > 1 and logits.stride(0) != W * stride):
-        raise ValueError("logits: rows must be dense and evenly spaced")
-    mk = lambda t, dtype: _empty((N, W), dtype, dev, stream) if t is None else t
-    tokens, parents, scores_out = mk(tokens, torch.int32), mk(parents, torch.int32), mk(scores_out, torch.float32)
+    full = logits.shape
+    V = full[-1]
+    if full != (N, W, V) and full != (N * W, V):
+        raise ValueError(f"logits: shape {tuple(full)} for {N} x {W} beams")
+    stride = V
+    if not logits.is_contiguous():
+        st = logits.stride()
+        if len(full) == 3:  # the stride of a dimension of size 1 means nothing
+            stride = st[1] if W > 1 else st[0] if N > 1 else V
+            even = N == 1 or st[0] == W * stride
+        else:
+            stride, even = st[0] if N * W > 1 else V, True
+        if (V > 1 and st[-1] != 1) or stride < V or not even:
+            raise ValueError("logits: rows must be dense and evenly spaced")
+    if tokens is None:
+        tokens = _empty(shape, i32, dev, stream)
+    if parents is None:
+        parents = _empty(shape, i32, dev, stream)
+    if scores_out is None:
+        scores_out = _empty(shape, f32, dev, stream)
+    fp = fop = lp = lop = None
     if finished is not None:
-        finished_out = mk(finished_out, torch.uint8)
+        fp = _need("finished", finished, u8, shape, dev)
+        if finished_out is None:
+            finished_out = _empty(shape, u8, dev, stream)
+    if finished_out is not None:
+        fop = _need("finished_out", finished_out, u8, shape, dev)
     if lengths is not None:
-        lengths_out = mk(lengths_out, torch.int32)
-    _same_device(dev, scores, finished, lengths, tokens, parents, scores_out, finished_out, lengths_out)
-    need = lambda name, t, dtype: None if t is None else _need(name, t, dtype, (N, W))
+        lp = _need("lengths", lengths, i32, shape, dev)
+        if lengths_out is None:
+            lengths_out = _empty(shape, i32, dev, stream)
+    if lengths_out is not None:
+        lop = _need("lengths_out", lengths_out, i32, shape, dev)
     a = BeamSelectArgs(
-        logits.data_ptr(), need("scores", scores, torch.float32), need("finished", finished, torch.uint8),
-        need("lengths", lengths, torch.int32), need("tokens", tokens, torch.int32),
-        need("parents", parents, torch.int32), need("scores_out", scores_out, torch.float32),
-        need("finished_out", finished_out, torch.uint8), need("lengths_out", lengths_out, torch.int32),
-        stride, N, W, V, LOGITS_F32 if logits.dtype is torch.float32 else LOGITS_BF16, eos, length_penalty, 0)
-    _enqueue("pa_beam_select", a, dev, stream)
+        logits.data_ptr(), _need("scores", scores, f32, shape, dev), fp, lp, _need("tokens", tokens, i32, shape, dev),
+        _need("parents", parents, i32, shape, dev), _need("scores_out", scores_out, f32, shape, dev), fop, lop,
+        stride, N, W, V, LOGITS_F32 if logits.dtype is f32 else LOGITS_BF16, eos, length_penalty, 0)
+    _enqueue("pa_beam_select", lib().pa_beam_select, a, dev, stream)
     return tokens, parents, scores_out, finished_out, lengths_out
 
 
@@ -683,27 +698,23 @@ def beam_reorder(parents, context_lens, block_table, block_table_out, k_cache, v
     context_lens int32 [N * W], block tables int32 [N * W, stride]; states: up to four
     (in, out) pairs of tensors with N * W rows, gathered by parent."""
     import torch
-    if parents.dim() != 2:
-        raise ValueError("parents: expected [N, W]")
-    N, W = parents.shape
-    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
+    i32, dev = torch.int32, _device_of(k_cache)
+    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev)
+    N, W = shape = _rank("parents", parents, 2)
+    R = N * W
+    table = (R, _rank("block_table", block_table, 2)[1])
     if len(states) > MAX_BEAM_STATES:
         raise ValueError(f"states: at most {MAX_BEAM_STATES}")
+    sin, sout, size = [], [], []
+    for x, y in states:
+        if x.dim() < 1 or x.shape[0] != R:
+            raise ValueError(f"states: shape {tuple(x.shape)}, expected {R} rows")
+        sin.append(_need("states' input", x, x.dtype, x.shape, dev))
+        sout.append(_need("states' output", y, x.dtype, x.shape, dev))
+        size.append(x.numel() // max(R, 1) * x.element_size())
     a = BeamReorderArgs(
-        _need("parents", parents, torch.int32, (N, W)), _need("context_lens", context_lens, torch.int32, (N * W,)),
-        _need("block_table", block_table, torch.int32, (N * W, None)),
-        _need("block_table_out", block_table_out, torch.int32, (N * W, block_table.shape[1])), kp, vp, ksp, vsp,
-        _status_ptr(status))
-    for i, (x, y) in enumerate(states):
-        if x.dim() < 1 or x.shape[0] != N * W:
-            raise ValueError(f"states[{i}]: expected {N * W} rows")
-        a.state_in[i] = _need(f"states[{i}] in", x, x.dtype, x.shape)
-        a.state_out[i] = _need(f"states[{i}] out", y, x.dtype, x.shape)
-        a.state_bytes[i] = x.numel() // max(N * W, 1) * x.element_size()
-        _same_device(dev, x, y)
-    a.num_pages, a.num_states, a.num_reqs, a.num_beams = pages, len(states), N, W
-    a.num_kv_heads, a.head_dim, a.page_size, a.kv_dtype, a.scale_mode = heads, d, ps, kv, sm
-    a.block_table_stride = block_table.shape[1]
-    _same_device(dev, parents, context_lens, block_table, block_table_out, v_cache, k_scale, v_scale, status)
-    _enqueue("pa_beam_reorder", a, dev, stream)
+        _need("parents", parents, i32, shape, dev), _need("context_lens", context_lens, i32, (R,), dev),
+        _need("block_table", block_table, i32, table, dev), _need("block_table_out", block_table_out, i32, table, dev),
+        kp, vp, ksp, vsp, _status_ptr(status, dev), tuple(sin), tuple(sout), tuple(size), pages, len(states), N, W, heads,
+        d, ps, kv, sm, table[1], 0)
+    _enqueue("pa_beam_reorder", lib().pa_beam_reorder, a, dev, stream)

@@ -155,13 +155,6 @@ struct BeamShared {
   double norm[kMaxBeams];          // max(new length, 1) ^ length_penalty
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // This shared-memory address in the cluster's first CTA.
 __device__ __forceinline__ uint32_t in_first_cta(const void *p) {
   uint32_t a;
@@ -300,7 +293,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
       }
     }
   }
-  if (wait) cluster_wait();  // the first CTA runs: its shared memory can be written
+  if (wait) pa::cluster_wait();  // the first CTA runs: its shared memory can be written
   __syncthreads();
   int lists = 1;
   while (lists < kBeamWarps && lists < p.W) lists <<= 1;
@@ -321,10 +314,8 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
 template <typename T>
 __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const BeamParams p) {
   __shared__ BeamShared sm;
-  cluster_arrive();
-  uint32_t C;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
-  const uint32_t rank = cluster_rank();
+  pa::cluster_arrive();
+  const uint32_t C = pa::cluster_ctas(), rank = pa::cluster_rank();
   const int n = blockIdx.x / C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t base = (int64_t)n * p.W, me = base + lane;
   const bool mine = lane < p.W;
@@ -343,10 +334,10 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
     beam_part<T>(p, sm, base + u / p.parts, u % p.parts, u, !waited);
     waited = true;
   }
-  if (!waited) cluster_wait();
-  cluster_arrive();
+  if (!waited) pa::cluster_wait();
+  pa::cluster_arrive();
   if (rank != 0) return;
-  cluster_wait();
+  pa::cluster_wait();
 
   // ---- the first CTA: a warp joins the parts of a row
   for (int b = warp; b < p.W; b += kBeamWarps) {

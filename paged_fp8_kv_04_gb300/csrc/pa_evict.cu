@@ -4,16 +4,18 @@
 
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "pa.h"
 #include "pa_host.cuh"
+#include "pa_ptx.cuh"
 
 namespace {
 
 using pa_host::aligned;
 
-constexpr int kD = pa_host::kD;
-constexpr int kMaxSeqs = 65535;
+constexpr int kMaxRows = 65535;         // (request, KV head) pairs of a call
+constexpr int kMaxPositions = 1 << 30;  // per (request, KV head) row
 
 // --------------------------------------------------------------------------- selection
 
@@ -33,84 +35,217 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 }
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kStageKeys = 49152;  // keys a CTA can hold in shared memory (192 KB)
 
-// Sum of v over the CTA, known to every thread.
-__device__ int block_sum(int v, int *buf) {
-  const int s = __reduce_add_sync(~0u, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
-  __syncthreads();
-  return __reduce_add_sync(~0u, buf[threadIdx.x & 31]);
+// A cluster of C CTAs per (request, KV head), each with one stretch of the positions.  The masses
+// are read once, as keys into shared memory (rows beyond C * kStageKeys are read again instead).
+// The key T of the last middle token taken is found by counting keys in 2048 bins of the
+// range that still holds it: at first the range of the middle's keys (so the bins are as fine as the
+// data allow, and shared-memory counters rarely collide), then one bin of the step before; three
+// steps narrow 2^32 to a single key.  The CTAs' counts meet through distributed shared memory,
+// one cluster barrier per step.  Then the kept positions are written in order: those above T and
+// the first `need` equal to it, at offsets from the counts of the warps and CTAs before.
+struct SelectShared {
+  uint32_t hist[2][kBins];
+  uint32_t range[2];             // this CTA's smallest and largest middle key
+  int total[2];                  // this CTA's keys equal to T, and certain ones
+  uint32_t wlo[kSelWarps], whi[kSelWarps];
+  int weq[kSelWarps], wsure[kSelWarps], scan[kSelWarps];
+  int pick[3];                   // the chosen bin, keys above it, keys in it
+};
+
+// 8 bytes at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint2 load_cluster(const void *p, uint32_t rank) {
+  uint32_t a;
+  uint2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
 
-// Exclusive prefix sum of v over the CTA's threads; total in *total.
-__device__ int block_scan(int v, int *buf, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += y;
   }
-  __syncthreads();
-  if (lane == 31) buf[warp] = x;
-  __syncthreads();
-  int w = buf[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, w, o);
-    if (lane >= o) w += y;
-  }
-  *total = __shfl_sync(~0u, w, 31);
-  const int before = warp == 0 ? 0 : __shfl_sync(~0u, w, warp == 0 ? 0 : warp - 1);
-  return before + x - v;
+  return v;
 }
 
-// A CTA per (request, KV head).  The key of the last token taken from the middle is found bit by
-// bit: the largest key T with at least `want` middle keys >= T.  Then the positions are written in
-// order: those above T, and the first ones equal to it.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
-  __shared__ int buf[32];
-  const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+// The number of `eq` equal keys that stay when `before` of them come earlier.
+__device__ __forceinline__ int ties_taken(int need, int before, int eq) { return min(max(need - before, 0), eq); }
+
+template <bool STAGED>
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ __align__(16) SelectShared sm;
+  const int C = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
+  const int row = blockIdx.x / C, r = row / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = p.L[r];
-  int32_t *keep = p.keep + ((int64_t)r * p.Hkv + h) * p.budget;
+  int32_t *keep = p.keep + (int64_t)row * p.budget;
   const bool bad = L < 0 || L > p.stride;
   const int n = bad ? 0 : min(L, p.budget);
-  if (h == 0 && tid == 0) {
+  if (row == r * p.Hkv && rank == 0 && tid == 0) {
     p.new_lens[r] = n;
     if (bad && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_CONTEXT);
   }
-  for (int64_t i = n + tid; i < p.budget; i += kSelThreads) keep[i] = -1;
-  if (n == L || bad) {
-    for (int i = tid; i < n; i += kSelThreads) keep[i] = i;
+  const int gid = rank * kSelThreads + tid, gsz = C * kSelThreads;
+  if (bad || n == L) {  // the same for the whole cluster
+    for (int64_t i = gid; i < p.budget; i += gsz) keep[i] = i < n ? (int)i : -1;
     return;
   }
-  const float *m = p.mass + ((int64_t)r * p.Hkv + h) * p.stride;
-  const int lo = p.first, hi = L - p.recent, want = p.budget - p.first - p.recent;
-  uint32_t T = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t cand = T | (1u << bit);
-    int c = 0;
-    for (int64_t i = (int64_t)lo + tid; i < hi; i += kSelThreads) c += mass_key(m[i]) >= cand;
-    if (block_sum(c, buf) >= want && want > 0) T = cand;
+  // this CTA's positions, and of them the middle ones
+  const int S = ((L + C - 1) / C + 31) & ~31;
+  const int begin = (int)min((int64_t)rank * S, (int64_t)L), end = (int)min((int64_t)begin + S, (int64_t)L);
+  const int mlo = max(begin, p.first), mhi = min(end, L - p.recent), want = p.budget - p.first - p.recent;
+  const float *m = p.mass + (int64_t)row * p.stride;
+  auto key_at = [&](int i) { return STAGED ? keys[i - begin] : mass_key(m[i]); };
+
+  uint32_t T = 0xFFFFFFFFu;  // with want 0 nothing of the middle stays
+  int need = 0;
+  if (want > 0) {
+    uint32_t klo = 0xFFFFFFFFu, khi = 0;
+#pragma unroll 8
+    for (int i = mlo + tid; i < mhi; i += kSelThreads) {
+      const uint32_t k = mass_key(m[i]);
+      if (STAGED) keys[i - begin] = k;
+      klo = min(klo, k);
+      khi = max(khi, k);
+    }
+    klo = __reduce_min_sync(~0u, klo);
+    khi = __reduce_max_sync(~0u, khi);
+    if (lane == 0) {
+      sm.wlo[warp] = klo;
+      sm.whi[warp] = khi;
+    }
+    for (int b = tid; b < kBins; b += kSelThreads) sm.hist[0][b] = 0;
+    __syncthreads();
+    if (warp == 0) {
+      klo = __reduce_min_sync(~0u, sm.wlo[lane]);
+      khi = __reduce_max_sync(~0u, sm.whi[lane]);
+      if (lane == 0) {
+        sm.range[0] = klo;
+        sm.range[1] = khi;
+      }
+    }
+    pa::cluster_sync();
+    const uint2 kr = lane < C ? load_cluster(sm.range, lane) : make_uint2(0xFFFFFFFFu, 0u);
+    uint32_t base = __reduce_min_sync(~0u, kr.x);
+    uint32_t span = __reduce_max_sync(~0u, kr.y) - base;  // keys in [base, base + span] are still open
+    need = want;
+    for (int step = 0;; ++step) {
+      if (span == 0) {  // one key left: it is T, and `need` of its tokens stay
+        T = base;
+        break;
+      }
+      uint32_t *hist = sm.hist[step & 1];
+      const int shift = max(0, 21 - __clz(span));  // (span >> shift) < 2048
+      for (int i = mlo + tid; i < mhi; i += kSelThreads) {
+        const uint32_t d = key_at(i) - base;
+        if (d <= span) atomicAdd(hist + (d >> shift), 1u);
+      }
+      pa::cluster_sync();
+      // bins 2 tid and 2 tid + 1 over the cluster; prefix sums from the top
+      uint2 c = make_uint2(0u, 0u);
+      for (int q = 0; q < C; ++q) {
+        const uint2 x = load_cluster(hist + 2 * tid, q);
+        c.x += x.x;
+        c.y += x.y;
+      }
+      for (int b = tid; b < kBins; b += kSelThreads) sm.hist[(step + 1) & 1][b] = 0;  // read by all a step ago
+      const int mine = (int)(c.x + c.y), upto = warp_scan(mine, lane);
+      if (lane == 31) sm.scan[warp] = upto;
+      __syncthreads();
+      const int w = sm.scan[lane], wincl = warp_scan(w, lane);
+      const int all = __shfl_sync(~0u, wincl, 31), below = __shfl_sync(~0u, wincl - w, warp);
+      const int above1 = all - (below + upto);  // keys in bins above 2 tid + 1
+      const int above0 = above1 + (int)c.y;
+      if (above1 < need && need <= above0) {
+        sm.pick[0] = 2 * tid + 1;
+        sm.pick[1] = above1;
+        sm.pick[2] = (int)c.y;
+      } else if (above0 < need && need <= above0 + (int)c.x) {
+        sm.pick[0] = 2 * tid;
+        sm.pick[1] = above0;
+        sm.pick[2] = (int)c.x;
+      }
+      __syncthreads();
+      base += (uint32_t)sm.pick[0] << shift;
+      need -= sm.pick[1];
+      if (need == sm.pick[2]) {  // the whole bin stays: everything from its lowest key on
+        T = base;
+        need = INT_MAX;
+        break;
+      }
+      span = (1u << shift) - 1u;
+    }
   }
-  int above = 0;
-  for (int64_t i = (int64_t)lo + tid; i < hi; i += kSelThreads) above += mass_key(m[i]) > T;
-  int ties = want - block_sum(above, buf);  // equal keys that stay
-  int at = 0;
-  for (int64_t base = 0; base < L; base += kSelThreads) {
-    const int64_t i = base + tid;
-    const bool mid = i >= lo && i < hi && want > 0;
-    const uint32_t k = mid ? mass_key(m[i]) : 0u;
-    const bool eq = mid && k == T;
-    int total;
-    const int e = block_scan(eq, buf, &total);
-    const bool stays = (i < L && (i < lo || i >= hi)) || (mid && (k > T || (eq && e < ties)));
-    ties -= min(ties, total);
-    const int x = block_scan(stays, buf, &total);
-    if (stays) keep[at + x] = (int32_t)i;
-    at += total;
+  __syncthreads();
+
+  // ---- each warp's stretch: count, then write
+  const int wl = ((end - begin + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int wb = min(begin + warp * wl, end), we = min(wb + wl, end);
+  auto classify = [&](int i, bool &sure, bool &eq) {
+    sure = eq = false;
+    if (i >= we) return;
+    if (i < mlo || i >= mhi) {
+      sure = true;  // not in the middle: one of the first or of the recent
+    } else if (want > 0) {
+      const uint32_t k = key_at(i);
+      sure = k > T;
+      eq = k == T;
+    }
+  };
+  int nsure = 0, neq = 0;
+  for (int i = wb + lane; i - lane < we; i += 32) {
+    bool sure, eq;
+    classify(i, sure, eq);
+    nsure += sure;
+    neq += eq;
   }
+  nsure = __reduce_add_sync(~0u, nsure);
+  neq = __reduce_add_sync(~0u, neq);
+  if (lane == 0) {
+    sm.wsure[warp] = nsure;
+    sm.weq[warp] = neq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int e = __reduce_add_sync(~0u, sm.weq[lane]), u = __reduce_add_sync(~0u, sm.wsure[lane]);
+    if (lane == 0) {
+      sm.total[0] = e;
+      sm.total[1] = u;
+    }
+  }
+  pa::cluster_sync();
+  const uint2 ct = lane < C ? load_cluster(sm.total, lane) : make_uint2(0u, 0u);
+  pa::cluster_arrive();  // no CTA leaves before the others have read its totals
+  const int ceq = (int)ct.x, ceq_before = warp_scan(ceq, lane) - ceq;
+  const int ckept = (int)ct.y + ties_taken(need, ceq_before, ceq);
+  const int cstart = warp_scan(ckept, lane) - ckept;
+  int before = __shfl_sync(~0u, ceq_before, rank), at = __shfl_sync(~0u, cstart, rank);
+  {
+    const int e = sm.weq[lane], eb = before + warp_scan(e, lane) - e;
+    const int kept = sm.wsure[lane] + ties_taken(need, eb, e), start = at + warp_scan(kept, lane) - kept;
+    before = __shfl_sync(~0u, eb, warp);
+    at = __shfl_sync(~0u, start, warp);
+  }
+  const unsigned lt = (1u << lane) - 1u;
+  for (int i = wb + lane; i - lane < we; i += 32) {
+    bool sure, eq;
+    classify(i, sure, eq);
+    const unsigned eqs = __ballot_sync(~0u, eq);
+    const bool stays = sure || (eq && before + __popc(eqs & lt) < need);
+    const unsigned st = __ballot_sync(~0u, stays);
+    if (stays) keep[at + __popc(st & lt)] = i;
+    at += __popc(st);
+    before += __popc(eqs);
+  }
+  pa::cluster_wait();
 }
 
 // -------------------------------------------------------------------------- compaction
@@ -123,71 +258,157 @@ struct CompactParams {
   float *mass_out;
   uint32_t *status;
   int64_t num_pages;
-  int32_t Hkv, ps, ps_shift, row_chunks, keep_stride, bt_stride, dt_stride, m_stride, mo_stride;
-  int32_t in_place;
+  int32_t Hkv, ps, ps_shift, keep_stride, bt_stride, dt_stride, m_stride, mo_stride;
 };
 
-constexpr int kMoveThreads = 512;
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 4;    // tokens per thread and round: 8 16-byte loads in flight
+constexpr int kMaxMoveCluster = 16;  // more than 8 needs the kernel's opt-in
 
-// A CTA per (request, KV head), in rounds of kMoveThreads / row_chunks tokens: the round's rows are
-// read into registers, then written.  Kept positions ascend, so keep[i] >= i: a round's
-// destinations are sources of this round or an earlier one only, whose reads are done.
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactParams p) {
-  const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
-  const int32_t *keep = p.keep + ((int64_t)r * p.Hkv + h) * p.keep_stride;
-  int n = p.new_lens[r];
+// What a thread carries of kMoveUnroll tokens: 16 bytes of K and V each, and the K scale, the V scale
+// or the mass (threads 0, 1 and 2 of a token).
+struct Moved {
+  uint4 k[kMoveUnroll], v[kMoveUnroll];
+  float x[kMoveUnroll];
+  int64_t to[kMoveUnroll];  // destination row, or -1
+};
+
+// RC threads per token, one for each 16 bytes of its row.  The tokens [first, first + RT) of
+// (request r, KV head h): every index load, then every row load.
+template <int RC, bool IN_PLACE>
+__device__ __forceinline__ void load_tokens(const CompactParams &p, const int32_t *keep, int r, int h, int n,
+                                            int64_t first, Moved &m) {
+  constexpr int kStep = kMoveThreads / RC;
+  const int t = threadIdx.x / RC, c = threadIdx.x % RC;
+  int s[kMoveUnroll], prev[kMoveUnroll], sp[kMoveUnroll], dp[kMoveUnroll];
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    const int64_t i = first + t + u * kStep;
+    s[u] = i < n ? keep[i] : -1;
+    prev[u] = i < n && i > 0 ? keep[i - 1] : -1;
+    dp[u] = i < n ? p.dt[(int64_t)r * p.dt_stride + (i >> p.ps_shift)] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    const int64_t i = first + t + u * kStep;
+    sp[u] = -1;
+    if (i >= n || (IN_PLACE && s[u] == i && prev[u] < s[u])) {
+      s[u] = -1;  // nothing to move
+    } else if (s[u] <= prev[u] || s[u] < i || s[u] >> p.ps_shift >= p.bt_stride ||
+               (p.mass != nullptr && s[u] >= p.m_stride)) {
+      if (c == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_KEEP);
+      s[u] = -1;
+    } else {
+      sp[u] = p.bt[(int64_t)r * p.bt_stride + (s[u] >> p.ps_shift)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    const int64_t i = first + t + u * kStep;
+    m.to[u] = -1;
+    if (s[u] < 0) continue;
+    if (sp[u] < 0 || sp[u] >= p.num_pages || dp[u] < 0 || dp[u] >= p.num_pages) {
+      if (c == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_PAGE);
+      continue;
+    }
+    const int64_t from = (((int64_t)sp[u] * p.Hkv + h) << p.ps_shift) + (s[u] & (p.ps - 1));
+    m.to[u] = (((int64_t)dp[u] * p.Hkv + h) << p.ps_shift) + (i & (p.ps - 1));
+    m.k[u] = *reinterpret_cast<const uint4 *>(p.k + from * (16 * RC) + 16 * c);
+    m.v[u] = *reinterpret_cast<const uint4 *>(p.v + from * (16 * RC) + 16 * c);
+    if (c < 2 && p.ks != nullptr) m.x[u] = (c == 0 ? p.ks : p.vs)[from];
+    if (c == 2 && p.mass != nullptr) m.x[u] = p.mass[((int64_t)r * p.Hkv + h) * p.m_stride + s[u]];
+  }
+}
+
+template <int RC>
+__device__ __forceinline__ void store_tokens(const CompactParams &p, int r, int h, int64_t first, const Moved &m) {
+  constexpr int kStep = kMoveThreads / RC;
+  const int t = threadIdx.x / RC, c = threadIdx.x % RC;
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    if (m.to[u] < 0) continue;
+    *reinterpret_cast<uint4 *>(p.k + m.to[u] * (16 * RC) + 16 * c) = m.k[u];
+    *reinterpret_cast<uint4 *>(p.v + m.to[u] * (16 * RC) + 16 * c) = m.v[u];
+    if (c < 2 && p.ks != nullptr) (c == 0 ? p.ks : p.vs)[m.to[u]] = m.x[u];
+    if (c == 2 && p.mass != nullptr) p.mass_out[((int64_t)r * p.Hkv + h) * p.mo_stride + first + t + u * kStep] = m.x[u];
+  }
+}
+
+// The request's new length, or 0 where it cannot be (flagged once).
+__device__ __forceinline__ int new_length(const CompactParams &p, int r, bool flag) {
+  const int n = p.new_lens[r];
   if (n < 0 || n > p.keep_stride || ((int64_t)n + p.ps - 1) >> p.ps_shift > p.dt_stride ||
       (p.mass != nullptr && n > p.mo_stride)) {
-    if (h == 0 && tid == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_KEEP);
-    n = 0;
+    if (flag && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_KEEP);
+    return 0;
   }
-  const int per = kMoveThreads / p.row_chunks, c = tid % p.row_chunks, row_bytes = 16 * p.row_chunks;
-  for (int64_t base = 0; base < n; base += per) {
-    const int64_t i = base + tid / p.row_chunks;
-    uint4 kx, vx;
-    float ksx = 0.f, vsx = 0.f, mx = 0.f;
-    int64_t to = -1;
-    if (i < n) {
-      const int s = keep[i], prev = i > 0 ? keep[i - 1] : -1;
-      uint32_t fl = 0;
-      if (s <= prev || s < i || s >> p.ps_shift >= p.bt_stride || (p.mass != nullptr && s >= p.m_stride))
-        fl = PA_DEV_BAD_KEEP;
-      int sp = -1, dp = -1;
-      if (!fl) {
-        sp = p.bt[(int64_t)r * p.bt_stride + (s >> p.ps_shift)];
-        dp = p.dt[(int64_t)r * p.dt_stride + (i >> p.ps_shift)];
-        if (sp < 0 || sp >= p.num_pages || dp < 0 || dp >= p.num_pages) fl = PA_DEV_BAD_PAGE;
-      }
-      if (fl) {
-        if (c == 0 && p.status != nullptr) atomicOr(p.status, fl);
-      } else if (!p.in_place || s != i) {
-        const int64_t from = (((int64_t)sp * p.Hkv + h) << p.ps_shift) + (s & (p.ps - 1));
-        to = (((int64_t)dp * p.Hkv + h) << p.ps_shift) + (i & (p.ps - 1));
-        kx = *reinterpret_cast<const uint4 *>(p.k + from * row_bytes + 16 * c);
-        vx = *reinterpret_cast<const uint4 *>(p.v + from * row_bytes + 16 * c);
-        if (c == 0) {
-          if (p.ks != nullptr) {
-            ksx = p.ks[from];
-            vsx = p.vs[from];
-          }
-          if (p.mass != nullptr) mx = p.mass[((int64_t)r * p.Hkv + h) * p.m_stride + s];
-        }
-      }
-    }
-    __syncthreads();
-    if (to >= 0) {
-      *reinterpret_cast<uint4 *>(p.k + to * row_bytes + 16 * c) = kx;
-      *reinterpret_cast<uint4 *>(p.v + to * row_bytes + 16 * c) = vx;
-      if (c == 0) {
-        if (p.ks != nullptr) {
-          p.ks[to] = ksx;
-          p.vs[to] = vsx;
-        }
-        if (p.mass != nullptr) p.mass_out[((int64_t)r * p.Hkv + h) * p.mo_stride + i] = mx;
-      }
-    }
-    __syncthreads();
+  return n;
+}
+
+// Into other pages: every CTA moves its own tokens.
+template <int RC>
+__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactParams p) {
+  constexpr int kTokens = kMoveThreads / RC * kMoveUnroll;
+  const int h = blockIdx.y % p.Hkv, r = blockIdx.y / p.Hkv;
+  const int n = new_length(p, r, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+  const int64_t first = (int64_t)blockIdx.x * kTokens;
+  if (first >= n) return;
+  Moved m;
+  load_tokens<RC, false>(p, p.keep + (int64_t)blockIdx.y * p.keep_stride, r, h, n, first, m);
+  store_tokens<RC>(p, r, h, first, m);
+}
+
+// In place: a cluster per (request, KV head) moves its tokens in rounds.  Kept positions ascend, so
+// keep[i] >= i: the destinations of a round are sources of this round or an earlier one only.
+// A round is stored once every CTA has read it (one cluster barrier), and the next round is
+// read before that: its sources lie past the destinations of this one.
+template <int RC>
+__global__ void __launch_bounds__(kMoveThreads) kv_compact_in_place_kernel(const CompactParams p) {
+  constexpr int kTokens = kMoveThreads / RC * kMoveUnroll;
+  const int C = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
+  const int row = blockIdx.x / C, h = row % p.Hkv, r = row / p.Hkv;
+  const int n = new_length(p, r, rank == 0 && h == 0 && threadIdx.x == 0);
+  const int32_t *keep = p.keep + (int64_t)row * p.keep_stride;
+  const int64_t round = (int64_t)C * kTokens;
+  int64_t first = (int64_t)rank * kTokens;
+  const int rounds = (int)((n + round - 1) / round);
+  if (rounds == 0) return;  // the same for the whole cluster
+  Moved a, b;
+  load_tokens<RC, true>(p, keep, r, h, n, first, a);
+  for (int k = 0; k < rounds; k += 2) {
+    pa::cluster_arrive();
+    if (k + 1 < rounds) load_tokens<RC, true>(p, keep, r, h, n, first + round, b);
+    pa::cluster_wait();
+    store_tokens<RC>(p, r, h, first, a);
+    if (k + 1 >= rounds) break;
+    pa::cluster_arrive();
+    if (k + 2 < rounds) load_tokens<RC, true>(p, keep, r, h, n, first + 2 * round, a);
+    pa::cluster_wait();
+    store_tokens<RC>(p, r, h, first + round, b);
+    first += 2 * round;
   }
+}
+
+// The current device's SM count, and its kernels' shared-memory opt-in, once per device; 0 for a
+// device beyond those tracked, -1 when a call fails.
+int evict_device() {
+  static std::once_flag once[pa_host::kMaxDevices];
+  static int sms[pa_host::kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev < 0 || dev >= pa_host::kMaxDevices) return 0;
+  std::call_once(once[dev], [dev]() {
+    int n = 0;
+    const bool ok = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+                    cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kStageKeys * (int)sizeof(uint32_t)) == cudaSuccess &&
+                    cudaFuncSetAttribute(kv_compact_in_place_kernel<8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                        cudaSuccess &&
+                    cudaFuncSetAttribute(kv_compact_in_place_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                        cudaSuccess;
+    sms[dev] = ok ? n : -1;
+  });
+  return sms[dev];
 }
 
 }  // namespace
@@ -197,7 +418,9 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   if (a->num_seqs < 0 || a->num_kv_heads < 1 || a->mass_stride < 1 || a->budget < 1 || a->keep_first < 0 ||
       a->keep_recent < 0 || (int64_t)a->keep_first + a->keep_recent > a->budget || a->reserved != 0)
     return PA_ERR_INVALID_ARG;
-  if (a->num_kv_heads > pa_host::kMaxHeads || a->num_seqs > kMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (a->num_kv_heads > pa_host::kMaxHeads || (int64_t)a->num_seqs * a->num_kv_heads > kMaxRows ||
+      a->mass_stride > kMaxPositions)
+    return PA_ERR_UNSUPPORTED;
   if (a->mass == nullptr || a->context_lens == nullptr || a->keep == nullptr || a->new_lens == nullptr ||
       (const int32_t *)a->new_lens == a->context_lens)
     return PA_ERR_INVALID_ARG;
@@ -217,8 +440,31 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   p.first = a->keep_first;
   p.recent = a->keep_recent;
   (void)cudaGetLastError();  // drop an earlier, unrelated launch error
-  evict_select_kernel<<<dim3(a->num_kv_heads, a->num_seqs), kSelThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const int sms = evict_device();
+  if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+  // CTAs per row: more while each keeps 2048 positions and all run at once (one per SM), or
+  // while a row's keys do not fit their shared memory
+  const int64_t rows = (int64_t)a->num_seqs * a->num_kv_heads;
+  int C = 1;
+  while (C < kMaxCluster && a->mass_stride / (2 * C) >= 2048 &&
+         (rows * 2 * C <= sms || a->mass_stride > (int64_t)C * kStageKeys))
+    C *= 2;
+  const int64_t stretch = ((((int64_t)a->mass_stride + C - 1) / C) + 31) & ~(int64_t)31;
+  const bool staged = stretch <= kStageKeys;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = staged ? (size_t)stretch * sizeof(uint32_t) : 0;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = staged ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p)
+                               : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream) {
@@ -230,7 +476,7 @@ extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream
   const pa_status_t st = pa_host::check_cache(a->num_pages, a->num_kv_heads, a->head_dim, a->page_size,
                                               a->kv_dtype, a->scale_mode);
   if (st != PA_OK) return st;
-  if (a->num_seqs > kMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)a->num_seqs * a->num_kv_heads > kMaxRows) return PA_ERR_UNSUPPORTED;
   const bool per_token = a->scale_mode == PA_SCALE_PER_TOKEN;
   if (a->keep == nullptr || a->new_lens == nullptr || a->block_table == nullptr || a->k_cache == nullptr ||
       a->v_cache == nullptr || (per_token && (a->k_scale == nullptr || a->v_scale == nullptr)))
@@ -264,14 +510,40 @@ extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream
   p.Hkv = a->num_kv_heads;
   p.ps = a->page_size;
   p.ps_shift = pa_host::log2_page(a->page_size);
-  p.row_chunks = a->kv_dtype == PA_KV_BF16 ? 16 : 8;
   p.keep_stride = a->keep_stride;
   p.bt_stride = a->block_table_stride;
   p.dt_stride = in_place ? a->block_table_stride : a->dst_block_table_stride;
   p.m_stride = a->mass_stride;
   p.mo_stride = a->mass_out_stride;
-  p.in_place = in_place;
   (void)cudaGetLastError();  // drop an earlier, unrelated launch error
-  kv_compact_kernel<<<dim3(a->num_kv_heads, a->num_seqs), kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const bool wide = a->kv_dtype == PA_KV_BF16;
+  const int tokens = kMoveThreads / (wide ? 16 : 8) * kMoveUnroll;
+  const int rows = a->num_seqs * a->num_kv_heads;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!in_place) {
+    const dim3 grid((unsigned)(((int64_t)a->keep_stride + tokens - 1) / tokens), rows);
+    if (wide)
+      kv_compact_kernel<16><<<grid, kMoveThreads, 0, s>>>(p);
+    else
+      kv_compact_kernel<8><<<grid, kMoveThreads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  const int sms = evict_device();
+  if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+  // CTAs per row: more while all rows' CTAs run at once (two per SM) and there are tokens for them
+  int C = 1;
+  while (C < kMaxMoveCluster && (int64_t)rows * C <= sms && (int64_t)C * tokens < a->keep_stride) C *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * C);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, kv_compact_in_place_kernel<16>, p)
+                             : cudaLaunchKernelEx(&cfg, kv_compact_in_place_kernel<8>, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -65,6 +65,7 @@ SELECT = dict(num_seqs=0, num_kv_heads=1, mass_stride=1024, budget=128, keep_fir
 @pytest.mark.parametrize("over,want", [
     (dict(), OK), (dict(reserved=1), INVALID), (dict(num_seqs=-1), INVALID), (dict(num_seqs=65536), UNSUP),
     (dict(num_kv_heads=0), INVALID), (dict(num_kv_heads=65), UNSUP), (dict(mass_stride=0), INVALID),
+    (dict(mass_stride=2**30 + 1), UNSUP), (dict(num_seqs=1024, num_kv_heads=64), UNSUP),
     (dict(budget=0), INVALID), (dict(keep_first=-1), INVALID), (dict(keep_recent=-1), INVALID),
     (dict(keep_first=64, keep_recent=65), INVALID), (dict(keep_first=64, keep_recent=64), OK),
     (dict(keep_first=2**31 - 1, keep_recent=2**31 - 1), INVALID), (dict(mass=None), INVALID),
