@@ -3,13 +3,30 @@
 //
 //   w[p] = sum over rows t, heads g of exp(sm_scale q[t][g] . k[p] k_scale[p] - lse[t][g])
 //
-// A thread per cached token: it reads the token's K row once per query row and keeps the 16
-// heads' products in registers; the query rows sit in shared memory as fp32.  With the
-// log-sum-exp known beforehand the weights need no running maximum and no second pass.
+// The K cache is read once per four query rows.  With the log-sum-exp known beforehand there is no
+// running maximum, no second product and nothing to join: a 128-token tile of one (request, KV
+// head) is
+//   S[tok][n] = K[tok][:] . Q[n][:]   tcgen05.mma, M = 128 tokens, A = the tile as TMA left it
+//                                     (K-major, 128-byte swizzle): kind::f8f6f4 on the cache's e4m3
+//                                     bytes, kind::f16 on a bf16 cache
+//   mass[tok] += sum_n 2^(S c - lse)  TMEM lane = token: a thread sums its token's columns in
+//                                     registers, and the mass is read and written once, coalesced.
+// For e4m3 keys a query row of 128 bf16 values is an e4m3 pair hi + lo / 32 at its own power of
+// two, in two columns of N: exact for elements within 2^-14 of the row's largest, and within
+// 2^-22 of that for smaller ones.  So N = 32 columns per query row (16 heads), or 16 for bf16.
+//
+// Warp roles (320 threads, one CTA per SM, each with an equal share of the tiles): warps 0-3 and 4-7
+// are two epilogue groups that take even and odd tiles and convert the queries of the segment to come
+// ((request, KV head, up to four rows) of the CTA's share); warp 8 gathers pages by TMA into a ring of
+// stages; warp 9 issues the MMAs, up to two tiles ahead of each group.  Every wait is bounded.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "pa.h"
 #include "pa_host.cuh"
@@ -19,97 +36,519 @@ namespace {
 
 using pa_host::aligned;
 
-constexpr int kG = 16;          // query heads per KV head
+constexpr int kG = 16;            // query heads per KV head
 constexpr int kD = pa_host::kD;
-constexpr int kTile = 128;      // tokens per CTA
+constexpr int kTile = 128;        // tokens per tile
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxQ = 64;
+constexpr int kMaxPositions = 1 << 30;
+constexpr int kRows = 4;          // query rows per pass over the keys
+constexpr int kGroups = 2;        // epilogue groups of four warps
+constexpr int kEpiWarps = 4 * kGroups;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kMaxStages = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct MassParams {
+  CUtensorMap tm_k;
   const uint16_t *q;
-  const uint8_t *k;
   const float *ks;
   const int32_t *bt, *L, *cu;
   const float *lse, *mass;
   float *out;
   uint32_t *status;
   int64_t num_pages;
-  int32_t B, R, Hkv, ps, ps_shift, bt_stride, mass_stride, maxq, bf16;
+  int32_t B, R, Hkv, ps, ps_shift, ppt, bt_stride, mass_stride, maxq;
+  int32_t nstage, stage_bytes, qbuf_bytes, tmem_cols;
   float kfold, decay;  // kfold = sm_scale * log2 e (* k_scale_scalar)
 };
 
-__global__ void __launch_bounds__(kTile) attn_mass_kernel(const MassParams p) {
-  __shared__ float qs[kG][kD];
-  __shared__ float l2[kG];
-  const int h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
-  const int L = p.L[r], row0 = p.cu[r], ql = p.cu[r + 1] - row0;
+// Shared memory: stages | 2 query operands | factors | barriers | tile prefix
+constexpr int kFactorBytes = 2 * kRows * 2 * kG * 4;  // per buffer and row: kf[16], lse2[16]
+struct MassBars {
+  uint32_t full, empty, s_full, s_free, qready, qfree, tdone, mmadone;
+};
+constexpr int kNumBars = 2 * kMaxStages + 4 + 4 + 2 + 2 + 2;
+constexpr int kCtrlBytes = kFactorBytes + kNumBars * 8 + kMaxStages * 4 + 16 + (kThreads / 32) * 4 + 64;
+
+struct MassSmem {
+  uint8_t *base;
+  uint32_t stages, q, factors, bars;
+  uint32_t *valid;   // per stage: which of the tile's pages are loaded
+  uint32_t *misc;    // [0] TMEM address, [1] abort
+  int32_t *wsum;     // per-warp sums of the scan
+  int32_t *tstart;   // [B + 1] tiles of the requests before, for one KV head
+};
+
+__device__ __forceinline__ MassSmem carve(uint8_t *raw, const MassParams &p) {
+  MassSmem s;
+  s.base = raw;
+  uint8_t *c = raw + (size_t)p.nstage * p.stage_bytes + 2 * (size_t)p.qbuf_bytes;
+  s.stages = pa::smem_u32(raw);
+  s.q = s.stages + p.nstage * p.stage_bytes;
+  s.factors = pa::smem_u32(c);
+  s.bars = s.factors + kFactorBytes;
+  s.valid = reinterpret_cast<uint32_t *>(c + kFactorBytes + kNumBars * 8);
+  s.misc = s.valid + kMaxStages;
+  s.wsum = reinterpret_cast<int32_t *>(s.misc + 4);
+  s.tstart = reinterpret_cast<int32_t *>(c + kCtrlBytes);
+  return s;
+}
+
+__device__ __forceinline__ uint32_t bar_full(const MassSmem &s, int i) { return s.bars + 8 * i; }
+__device__ __forceinline__ uint32_t bar_empty(const MassSmem &s, int i) { return s.bars + 8 * (kMaxStages + i); }
+__device__ __forceinline__ uint32_t bar_sfull(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + i); }
+__device__ __forceinline__ uint32_t bar_sfree(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 4 + i); }
+__device__ __forceinline__ uint32_t bar_qready(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 8 + i); }
+__device__ __forceinline__ uint32_t bar_qfree(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 10 + i); }
+__device__ __forceinline__ uint32_t bar_tdone(const MassSmem &s) { return s.bars + 8 * (2 * kMaxStages + 12); }
+__device__ __forceinline__ uint32_t bar_mmadone(const MassSmem &s) { return s.bars + 8 * (2 * kMaxStages + 13); }
+
+// What one request contributes, and what is wrong with it.
+struct Request {
+  int L, row0, ql;
+};
+__device__ __forceinline__ uint32_t read_request(const MassParams &p, int r, Request &q) {
+  q.L = p.L[r];
+  q.row0 = p.cu[r];
+  q.ql = p.cu[r + 1] - q.row0;
   uint32_t fl = 0;
-  if (L < 0 || L > p.mass_stride || ((int64_t)L + p.ps - 1) >> p.ps_shift > p.bt_stride)
+  if (q.L < 0 || q.L > p.mass_stride || ((int64_t)q.L + p.ps - 1) >> p.ps_shift > p.bt_stride)
     fl |= PA_DEV_BAD_CONTEXT;
-  if (ql < 0 || ql > p.maxq || L < ql || row0 < 0 || row0 > p.R - ql) fl |= PA_DEV_BAD_QLEN;
-  if (fl) {
-    if (blockIdx.x == 0 && h == 0 && tid == 0 && p.status != nullptr) atomicOr(p.status, fl);
-    return;
-  }
-  const int64_t base = (int64_t)blockIdx.x * kTile;
-  if (ql == 0 || base >= L) return;
-  const int pos = (int)base + tid;
-  const bool live = pos < L;
-  int64_t krow = -1;
-  if (live) {
-    const int page = p.bt[(int64_t)r * p.bt_stride + (pos >> p.ps_shift)];
-    if (page < 0 || page >= p.num_pages) {
-      if (p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_PAGE);
-    } else {
-      krow = (((int64_t)page * p.Hkv + h) << p.ps_shift) + (pos & (p.ps - 1));
+  if (q.ql < 0 || q.ql > p.maxq || q.L < q.ql || q.row0 < 0 || q.row0 > p.R - q.ql) fl |= PA_DEV_BAD_QLEN;
+  return fl;
+}
+
+// tstart[r]: the tiles of requests 0 .. r - 1 (per KV head); flagged requests and those without rows
+// have none.  Returns the flags.
+__device__ uint32_t scan_requests(const MassParams &p, const MassSmem &s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t flags = 0;
+  int run = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int r = b0 + tid;
+    int n = 0;
+    if (r < p.B) {
+      Request q;
+      const uint32_t fl = read_request(p, r, q);
+      flags |= fl;
+      if (!fl && q.ql > 0) n = (q.L + kTile - 1) / kTile;
     }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s.wsum[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int v = s.wsum[w];
+      before += w < warp ? v : 0;
+      all += v;
+    }
+    if (r < p.B) s.tstart[r] = run + before + x - n;
+    run += all;
   }
-  const float c = krow < 0 ? 0.f : (p.ks != nullptr ? p.kfold * p.ks[krow] : p.kfold);
-  const int64_t Hq = (int64_t)p.Hkv * kG;
-  float w = 0.f;
-  for (int t = 0; t < ql; ++t) {
-    const int64_t qrow = (int64_t)(row0 + t) * Hq + h * kG;
-    __syncthreads();
-    for (int i = tid; i < kG * kD; i += kTile)
-      qs[i / kD][i % kD] = __uint_as_float((uint32_t)p.q[qrow * kD + i] << 16);
-    if (tid < kG) l2[tid] = p.lse[qrow + tid] * kLog2e;
-    __syncthreads();
-    if (krow < 0 || pos >= L - ql + t + 1) continue;
-    float acc[kG];
-#pragma unroll
-    for (int g = 0; g < kG; ++g) acc[g] = 0.f;
-    for (int d0 = 0; d0 < kD; d0 += 8) {
-      float x[8];
-      if (p.bf16) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p.k + krow * (2 * kD) + 2 * d0);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[2 * j] = pa::bf16lo(u[j]);
-          x[2 * j + 1] = pa::bf16hi(u[j]);
-        }
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p.k + krow * kD + d0);
-        pa::e4m3x2_to_f32x2(v.x & 0xFFFFu, x[0], x[1]);
-        pa::e4m3x2_to_f32x2(v.x >> 16, x[2], x[3]);
-        pa::e4m3x2_to_f32x2(v.y & 0xFFFFu, x[4], x[5]);
-        pa::e4m3x2_to_f32x2(v.y >> 16, x[6], x[7]);
+  if (tid == 0) s.tstart[p.B] = run;
+  __syncthreads();
+  return flags;
+}
+
+// A segment: tiles [t0, t1) of (request r, KV head h) against its query rows [tok0, tok0 + nr).
+// Every role walks the same segments of the CTA's tiles [a, b), in order; the rows of a
+// (request, head) beyond four come in further segments over the same tiles.
+struct Segment {
+  int r, h, t0, t1, tok0, nr;
+  Request q;
+};
+struct Walk {
+  int64_t at, end;
+  Segment s;
+  bool open;
+  __device__ Walk(int64_t a, int64_t b) : at(a), end(b), open(false) {}
+  __device__ bool next(const MassParams &p, const MassSmem &sm) {
+    if (open && s.tok0 + s.nr < s.q.ql) {
+      s.tok0 += s.nr;
+      s.nr = min(kRows, s.q.ql - s.tok0);
+      return true;
+    }
+    if (open) at += s.t1 - s.t0;
+    open = at < end;
+    if (!open) return false;
+    int lo = 0, hi = p.B - 1;  // the last request with tstart * Hkv <= at
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)sm.tstart[mid] * p.Hkv <= at)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int nt = sm.tstart[lo + 1] - sm.tstart[lo];
+    const int64_t rem = at - (int64_t)sm.tstart[lo] * p.Hkv;
+    s.r = lo;
+    s.h = (int)(rem / nt);
+    s.t0 = (int)(rem - (int64_t)s.h * nt);
+    s.t1 = (int)min((int64_t)nt, s.t0 + (end - at));
+    read_request(p, lo, s.q);
+    s.tok0 = 0;
+    s.nr = min(kRows, s.q.ql);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void raise(const MassParams &p, uint32_t flag) {
+  if (p.status != nullptr) atomicOr(p.status, flag);
+}
+
+// A bounded wait by a whole warp: false for all lanes if it gave up for one.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(~0u, pa::mbar_wait_bounded(bar, parity)) != 0;
+}
+
+// ---------------------------------------------------------------------------- producer
+
+template <bool BF16>
+__device__ void run_producer(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b) {
+  const int lane = threadIdx.x & 31;
+  const int nb = 32 / p.ppt, slot = lane / p.ppt, kpg = lane - slot * p.ppt;
+  const uint64_t pol = pa::l2_evict_first_policy();
+  const uint32_t page_tx = (uint32_t)p.ps * (BF16 ? 2 * kD : kD) + (p.ks != nullptr ? 4u * p.ps : 0u);
+  int i = 0;
+  bool ok = true;
+  Walk w(a, b);
+  while (ok && w.next(p, sm)) {
+    const Segment &s = w.s;
+    const int np = (s.q.L + p.ps - 1) >> p.ps_shift;
+    const int32_t *row = p.bt + (int64_t)s.r * p.bt_stride;
+    // nb tiles' pages at a time, one per lane
+    auto lookup = [&](int t) {
+      const int idx = (t + slot) * p.ppt + kpg;
+      return t + slot < s.t1 && idx < np ? row[idx] : -2;  // -2: past the context
+    };
+    int ahead = lookup(s.t0);
+    for (int t = s.t0; t < s.t1 && ok; t += nb) {
+      int phys = ahead;
+      if (t + nb < s.t1) ahead = lookup(t + nb);
+      if (phys != -2 && (phys < 0 || phys >= p.num_pages)) {
+        raise(p, PA_DEV_BAD_PAGE);
+        phys = -2;
       }
-#pragma unroll
-      for (int g = 0; g < kG; ++g)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[g] = fmaf(qs[g][d0 + j], x[j], acc[g]);
+      const uint32_t valid = __ballot_sync(~0u, phys >= 0);
+      for (int j = 0; j < nb && t + j < s.t1; ++j, ++i) {
+        const int st = i % p.nstage, src = j * p.ppt;
+        int go = 1;
+        if (lane == 0 && i >= p.nstage) go = pa::mbar_wait_bounded(bar_empty(sm, st), (i / p.nstage - 1) & 1);
+        ok = __shfl_sync(~0u, go, 0) != 0;
+        if (!ok) break;
+        const uint32_t bits = (valid >> src) & (p.ppt == 32 ? ~0u : (1u << p.ppt) - 1u);
+        if (lane == 0) {
+          sm.valid[st] = bits;
+          pa::mbar_arrive_expect_tx(bar_full(sm, st), __popc(bits) * page_tx);
+        }
+        __syncwarp();
+        if (lane >= src && lane < src + p.ppt && phys >= 0) {
+          const int32_t y = (phys * p.Hkv + s.h) * p.ps;
+          const uint32_t dst = sm.stages + st * p.stage_bytes, off = kpg * p.ps * 128, fb = bar_full(sm, st);
+          pa::tma_load_2d(dst + off, &p.tm_k, 0, y, fb, pol);
+          if (BF16) pa::tma_load_2d(dst + 16384 + off, &p.tm_k, 64, y, fb, pol);
+          if (p.ks != nullptr) pa::bulk_load_hint(dst + 16384 + kpg * p.ps * 4, p.ks + y, p.ps * 4, fb, pol);
+        }
+      }
     }
+  }
+  if (!ok) {
+    if (lane == 0) {
+      raise(p, PA_DEV_TIMEOUT);
+      for (int k = max(0, i - p.nstage); k < i; ++k)  // copies in flight land before the CTA can exit
+        pa::mbar_wait_bounded(bar_full(sm, k % p.nstage), (k / p.nstage) & 1);
+    }
+  }
+}
+
+// --------------------------------------------------------------------------------- MMA
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// TMEM columns of group g's buffer k.
+__device__ __forceinline__ uint32_t tmem_buf(const MassParams &p, int g, int k) {
+  return (uint32_t)((2 * g + k) * (p.tmem_cols >> 2));
+}
+
+template <bool BF16>
+__device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b, uint32_t tm) {
+  const int lane = threadIdx.x & 31;
+  int i = 0, seg = 0, cnt[kGroups] = {0, 0};
+  bool ok = true;
+  Walk w(a, b);
+  while (ok && w.next(p, sm)) {
+    const int qb = seg & 1;
+    ok = warp_wait(bar_qready(sm, qb), (seg >> 1) & 1);
+    const uint32_t q = sm.q + qb * p.qbuf_bytes;
+    const int N = w.s.nr * (BF16 ? kG : 2 * kG);
+    const uint32_t id = BF16 ? idesc_bf16(kTile, N) : pa::umma_idesc_e4m3(kTile, N, 0, 0);
+    for (int t = w.s.t0; t < w.s.t1 && ok; ++t, ++i) {
+      const int st = i % p.nstage, g = t & 1, k = cnt[g] & 1, u = cnt[g] >> 1;
+      ok = warp_wait(bar_full(sm, st), (i / p.nstage) & 1);
+      if (ok && u > 0) ok = warp_wait(bar_sfree(sm, 2 * g + k), (u - 1) & 1);
+      if (!ok) break;
+      ++cnt[g];
+      pa::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t ka = sm.stages + st * p.stage_bytes, d = tm + tmem_buf(p, g, k);
+        if (BF16) {
 #pragma unroll
-    for (int g = 0; g < kG; ++g)
-      if (l2[g] != -INFINITY) w += pa::fast_exp2(fmaf(acc[g], c, -l2[g]));
+          for (int x = 0; x < 8; ++x)  // 16 elements each; the second half of the row in its own 16 KB
+            pa::umma_f16(d, pa::umma_sdesc(ka + (x >> 2) * 16384 + 32 * (x & 3), 1024, 1024, 2),
+                         pa::umma_sdesc(q + (x >> 2) * (p.qbuf_bytes >> 1) + 32 * (x & 3), 1024, 1024, 2), id, x > 0);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            pa::umma_e4m3(d, pa::umma_sdesc(ka + 32 * x, 1024, 1024, 2), pa::umma_sdesc(q + 32 * x, 1024, 1024, 2), id,
+                          x > 0);
+        }
+        pa::umma_commit(bar_sfull(sm, 2 * g + k));
+        pa::umma_commit(bar_empty(sm, st));
+        if (t + 1 == w.s.t1) pa::umma_commit(bar_qfree(sm, qb));
+      }
+      __syncwarp();
+    }
+    ++seg;
   }
-  if (live) {
-    const int64_t o = ((int64_t)r * p.Hkv + h) * p.mass_stride + pos;
-    const float old = pos < L - ql && p.decay != 0.f ? p.decay * p.mass[o] : 0.f;
-    p.out[o] = old + w;
+  if (lane == 0) {
+    if (!ok) raise(p, PA_DEV_TIMEOUT);
+    pa::umma_commit(bar_mmadone(sm));
   }
+  __syncwarp();
+  if (!warp_wait(bar_mmadone(sm), 0) && lane == 0) raise(p, PA_DEV_TIMEOUT);
+  if (!warp_wait(bar_tdone(sm), 0) && lane == 0) raise(p, PA_DEV_TIMEOUT);
+  pa::tc_fence_after();
+  pa::tmem_dealloc(tm, p.tmem_cols);
+}
+
+// ---------------------------------------------------------------------------- epilogue
+
+// The segment's query rows as the MMA's B operand (K-major, 128-byte swizzle), and per (row, head) the
+// factor of its scores and its lse in base 2 (+inf where the row has no key: 2^(x - inf) = 0).
+template <bool BF16>
+__device__ void convert_queries(const MassParams &p, const MassSmem &sm, const Segment &s, int qb, int etid) {
+  const uint32_t dst = sm.q + qb * p.qbuf_bytes, fac = sm.factors + qb * (kFactorBytes / 2);
+  const int64_t Hq = (int64_t)p.Hkv * kG;
+  const int64_t qrow = (int64_t)(s.q.row0 + s.tok0) * Hq + s.h * kG;  // (row t, head g): + t Hq + g
+  for (int u = etid; u < s.nr * kG; u += 32 * kEpiWarps) {
+    const float l = p.lse[qrow + (u / kG) * Hq + u % kG];
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac + (u / kG) * (2 * kG * 4) + (kG + u % kG) * 4),
+                 "f"(l == -INFINITY ? INFINITY : l * kLog2e) : "memory");
+  }
+  if (BF16) {
+    for (int u = etid; u < s.nr * kG * 16; u += 32 * kEpiWarps) {  // 16 bytes: 8 elements
+      const int n = u >> 4, c = u & 15;
+      const uint4 v = *reinterpret_cast<const uint4 *>(p.q + (qrow + (n / kG) * Hq + n % kG) * kD + 8 * c);
+      pa::sts128(dst + (c >> 3) * (p.qbuf_bytes >> 1) + n * 128 + (((c & 7) ^ (n & 7)) << 4), v);
+      if (c == 0)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac + (n / kG) * (2 * kG * 4) + (n % kG) * 4), "f"(p.kfold) : "memory");
+    }
+  } else {
+    for (int u0 = 0; u0 < s.nr * kG * 8; u0 += 32 * kEpiWarps) {  // 16 elements; 8 lanes per (row, head)
+      const int u = u0 + etid, n = u >> 3, c = u & 7;
+      const bool live = u < s.nr * kG * 8;
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      if (live) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (qrow + (n / kG) * Hq + n % kG) * kD + 16 * c);
+        x = src[0];
+        y = src[1];
+      }
+      const uint32_t wd[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(pa::bf16lo(wd[j])), fabsf(pa::bf16hi(wd[j]))));
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+      if (!live) continue;
+      // 2^sig puts the largest magnitude in [128, 256)
+      int sig = 0;
+      if (amax > 0.f) sig = min(max(7 - ((int)(__float_as_uint(amax) >> 23) - 127), -126), 126);
+      const float up = __uint_as_float((uint32_t)(sig + 127) << 23);
+      uint32_t hw[4] = {0u, 0u, 0u, 0u}, lw[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // word j: d = 16 c + 2 j, + 1
+        const float y0 = pa::bf16lo(wd[j]) * up, y1 = pa::bf16hi(wd[j]) * up;
+        const uint32_t hc = pa::pack_e4m3x2(y0, y1);
+        float h0, h1;
+        pa::e4m3x2_to_f32x2(hc, h0, h1);
+        const uint32_t lc = pa::pack_e4m3x2((y0 - h0) * 32.f, (y1 - h1) * 32.f);
+        hw[j >> 1] |= hc << (16 * (j & 1));
+        lw[j >> 1] |= lc << (16 * (j & 1));
+      }
+      const int row = (n / kG) * 2 * kG + n % kG;  // hi; lo 16 rows on
+      const uint32_t off = row * 128 + ((c ^ (row & 7)) << 4);
+      pa::sts128(dst + off, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+      pa::sts128(dst + kG * 128 + off, make_uint4(lw[0], lw[1], lw[2], lw[3]));
+      if (c == 0)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac + (n / kG) * (2 * kG * 4) + (n % kG) * 4),
+                     "f"(p.kfold * __uint_as_float((uint32_t)(127 - sig) << 23)) : "memory");
+    }
+  }
+  pa::fence_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) pa::mbar_arrive(bar_qready(sm, qb));
+}
+
+template <bool BF16>
+__device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b, uint32_t tm) {
+  const int etid = threadIdx.x, lane = etid & 31, warp = etid >> 5, g = warp >> 2, quarter = warp & 3;
+  const int tok = 32 * quarter + lane;  // of a tile: the TMEM lane
+  const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+  int i = 0, seg = 0, cnt = 0;
+  bool ok = true;
+  Walk w(a, b), ahead(a, b);
+  if (ahead.next(p, sm)) convert_queries<BF16>(p, sm, ahead.s, 0, etid);
+  while (ok && w.next(p, sm)) {
+    const Segment s = w.s;
+    const int qb = seg & 1;
+    if (ahead.next(p, sm)) {
+      // segment seg - 1, which had the other buffers: its MMAs and both groups are done
+      if (seg >= 1) ok = warp_wait(bar_qfree(sm, qb ^ 1), ((seg - 1) >> 1) & 1);
+      if (!ok) break;
+      convert_queries<BF16>(p, sm, ahead.s, qb ^ 1, etid);
+    }
+    ok = warp_wait(bar_qready(sm, qb), (seg >> 1) & 1);
+    const uint32_t fac = sm.factors + qb * (kFactorBytes / 2);
+    const int64_t mrow = ((int64_t)s.r * p.Hkv + s.h) * p.mass_stride;
+    for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+      if ((t & 1) != g) continue;
+      const int st = i % p.nstage, k = cnt & 1, pos = t * kTile + tok;
+      const bool live = pos < s.q.L;
+      float old = 0.f;
+      if (live) {
+        if (s.tok0 > 0)
+          old = p.out[mrow + pos];  // this thread's own sum over the rows before
+        else if (pos < s.q.L - s.q.ql && p.decay != 0.f)
+          old = p.decay * p.mass[mrow + pos];
+      }
+      ok = warp_wait(bar_full(sm, st), (i / p.nstage) & 1) &&
+           warp_wait(bar_sfull(sm, 2 * g + k), (cnt >> 1) & 1);
+      if (!ok) break;
+      ++cnt;
+      float ks = 1.f;
+      const uint32_t base = sm.stages + st * p.stage_bytes;
+      if (!BF16 && p.ks != nullptr) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(base + 16384 + 4 * tok) : "memory");
+      const bool valid = (sm.valid[st] >> (tok >> p.ps_shift)) & 1u;
+      __syncwarp();
+      if (lane == 0) pa::mbar_arrive(bar_empty(sm, st));
+      pa::tc_fence_after();
+      float sum = 0.f;
+      for (int x = 0; x < s.nr; ++x) {
+        uint32_t hi[kG], lo[kG];
+        const uint32_t col = tl + tmem_buf(p, g, k) + x * (BF16 ? kG : 2 * kG);
+        pa::tmem_ld16_async(col, hi);
+        if (!BF16) pa::tmem_ld16_async(col + kG, lo);
+        pa::tmem_wait16(hi);
+        if (!BF16) pa::tmem_wait16(lo);
+        const uint32_t f = fac + x * (2 * kG * 4);
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kG; j += 4) {
+          const uint4 kv = pa::lds128(f + 4 * j), lv = pa::lds128(f + 4 * (kG + j));
+          const uint32_t kf[4] = {kv.x, kv.y, kv.z, kv.w}, l2[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float d = __uint_as_float(hi[j + e]);
+            if (!BF16) d = fmaf(__uint_as_float(lo[j + e]), 1.f / 32.f, d);
+            part[e] += pa::fast_exp2(fmaf(d, __uint_as_float(kf[e]) * ks, -__uint_as_float(l2[e])));
+          }
+        }
+        if (pos < s.q.L - s.q.ql + s.tok0 + x + 1) sum += (part[0] + part[1]) + (part[2] + part[3]);
+      }
+      pa::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) pa::mbar_arrive(bar_sfree(sm, 2 * g + k));
+      if (live) p.out[mrow + pos] = old + (valid ? sum : 0.f);
+    }
+    if (ok && lane == 0) pa::mbar_arrive(bar_qfree(sm, qb));  // the factors have been read
+    __syncwarp();
+    ++seg;
+  }
+  if (!ok && lane == 0) raise(p, PA_DEV_TIMEOUT);
+  pa::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) pa::mbar_arrive(bar_tdone(sm));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) attn_mass_kernel(const __grid_constant__ MassParams p) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t mis = pa::smem_u32(raw) & 1023u;
+  const MassSmem sm = carve(raw + ((1024u - mis) & 1023u), p);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < p.nstage; ++k) {
+      pa::mbar_init(bar_full(sm, k), 1);
+      pa::mbar_init(bar_empty(sm, k), 1 + 4);  // the MMAs' commit, the warps of the tile's group
+    }
+    for (int k = 0; k < 2 * kGroups; ++k) {
+      pa::mbar_init(bar_sfull(sm, k), 1);
+      pa::mbar_init(bar_sfree(sm, k), 4);
+    }
+    for (int k = 0; k < 2; ++k) {
+      pa::mbar_init(bar_qready(sm, k), kEpiWarps);
+      pa::mbar_init(bar_qfree(sm, k), 1 + kEpiWarps);  // the MMAs' commit, the epilogue's warps
+    }
+    pa::mbar_init(bar_tdone(sm), kEpiWarps);
+    pa::mbar_init(bar_mmadone(sm), 1);
+    pa::fence_barrier_init();
+  }
+  const uint32_t fl = scan_requests(p, sm);  // synchronises the CTA
+  if (blockIdx.x == 0 && fl) raise(p, fl);
+  const int64_t total = (int64_t)sm.tstart[p.B] * p.Hkv;
+  const int64_t a = total * blockIdx.x / gridDim.x, b = total * (blockIdx.x + 1) / gridDim.x;
+  if (a >= b) return;  // the whole CTA
+  if (warp == kEpiWarps + 1) pa::tmem_alloc(pa::smem_u32(sm.misc), p.tmem_cols);
+  pa::tc_fence_before();
+  __syncthreads();
+  pa::tc_fence_after();
+  const uint32_t tm = sm.misc[0];
+  if (warp < kEpiWarps)
+    run_epilogue<BF16>(p, sm, a, b, tm);
+  else if (warp == kEpiWarps)
+    run_producer<BF16>(p, sm, a, b);
+  else
+    run_mma<BF16>(p, sm, a, b, tm);
+}
+
+// ------------------------------------------------------------------------------- host
+
+struct MassDevice {
+  int sms = 0, smem = 0;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+};
+
+// The current device's SM count and shared memory, the kernels' opt-in, and the tensor-map
+// encoder, once per device; NULL when a call fails or the device is beyond those tracked.
+const MassDevice *mass_device() {
+  static std::once_flag once[pa_host::kMaxDevices];
+  static MassDevice devs[pa_host::kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= pa_host::kMaxDevices) return nullptr;
+  std::call_once(once[dev], [dev]() {
+    MassDevice d;
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_mass_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_mass_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem) != cudaSuccess ||
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess)
+      return;
+    d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    devs[dev] = d;
+  });
+  return devs[dev].encode != nullptr ? &devs[dev] : nullptr;
 }
 
 }  // namespace
@@ -123,7 +562,8 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
   const pa_status_t st = pa_host::check_cache(a->num_pages, a->num_kv_heads, a->head_dim, a->page_size,
                                               a->kv_dtype, a->scale_mode);
   if (st != PA_OK) return st;
-  if (a->group_size != kG || a->max_q_len > kMaxQ || a->num_seqs > kMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (a->group_size != kG || a->max_q_len > kMaxQ || a->num_seqs > kMaxSeqs || a->mass_stride > kMaxPositions)
+    return PA_ERR_UNSUPPORTED;
   if (a->scale_mode == PA_SCALE_SCALAR && (!std::isfinite(a->k_scale_scalar) || a->k_scale_scalar < 0.f))
     return PA_ERR_INVALID_ARG;
   const bool per_token = a->scale_mode == PA_SCALE_PER_TOKEN;
@@ -140,9 +580,11 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
     return PA_ERR_INVALID_ARG;
   if (a->num_seqs == 0 || a->num_rows == 0) return PA_OK;
 
+  const MassDevice *dev = mass_device();
+  if (dev == nullptr) return PA_ERR_CUDA;
+
   MassParams p;
   p.q = static_cast<const uint16_t *>(a->q);
-  p.k = static_cast<const uint8_t *>(a->k_cache);
   p.ks = per_token ? a->k_scale : nullptr;
   p.bt = a->block_table;
   p.L = a->context_lens;
@@ -160,12 +602,39 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
   p.bt_stride = a->block_table_stride;
   p.mass_stride = a->mass_stride;
   p.maxq = a->max_q_len;
-  p.bf16 = a->kv_dtype == PA_KV_BF16;
+  const bool bf16 = a->kv_dtype == PA_KV_BF16;
+  p.ppt = kTile / a->page_size;
   p.kfold = (float)((double)a->sm_scale * 1.4426950408889634 *
                     (a->scale_mode == PA_SCALE_SCALAR ? (double)a->k_scale_scalar : 1.0));
   p.decay = a->decay;
+  // Query operand and TMEM for the rows a segment can have; as many stages as fit.
+  const int nr = std::min(a->max_q_len, kRows);
+  p.qbuf_bytes = nr * 2 * kG * 128;  // e4m3: 32 rows of 128 bytes; bf16: two halves of 16 rows
+  p.tmem_cols = 4 * 32;
+  while (p.tmem_cols < 4 * 2 * kG * nr) p.tmem_cols *= 2;
+  p.stage_bytes = bf16 ? 32768 : 16384 + 1024;  // keys, then an e4m3 tile's scales
+  const int fixed = 1024 + 2 * p.qbuf_bytes + kCtrlBytes + (a->num_seqs + 1) * 4;
+  p.nstage = std::min(kMaxStages, (dev->smem - fixed) / p.stage_bytes);
+  if (p.nstage < 2) return PA_ERR_UNSUPPORTED;
+  const size_t smem = (size_t)fixed + (size_t)p.nstage * p.stage_bytes;
+
+  cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)(a->num_pages * a->num_kv_heads * a->page_size)};
+  cuuint64_t strides[1] = {(cuuint64_t)(bf16 ? 2 * kD : kD)};
+  cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : 128), (cuuint32_t)a->page_size};
+  cuuint32_t estr[2] = {1, 1};
+  if (dev->encode(&p.tm_k, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                  const_cast<void *>(a->k_cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return PA_ERR_CUDA;
+
+  // One CTA per SM, or fewer where the mass rows cannot hold that many tiles
+  const int64_t tiles = (int64_t)a->num_seqs * a->num_kv_heads * ((a->mass_stride + kTile - 1) / kTile);
+  const int grid = (int)std::min<int64_t>(dev->sms, tiles);
   (void)cudaGetLastError();  // drop an earlier, unrelated launch error
-  const dim3 grid((unsigned)(((int64_t)a->mass_stride + kTile - 1) / kTile), a->num_kv_heads, a->num_seqs);
-  attn_mass_kernel<<<grid, kTile, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  if (bf16)
+    attn_mass_kernel<true><<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+  else
+    attn_mass_kernel<false><<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
