@@ -109,12 +109,19 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
   int need = 0;
   if (want > 0) {
     uint32_t klo = 0xFFFFFFFFu, khi = 0;
-#pragma unroll 8
-    for (int i = mlo + tid; i < mhi; i += kSelThreads) {
-      const uint32_t k = mass_key(m[i]);
-      if (STAGED) keys[i - begin] = k;
-      klo = min(klo, k);
-      khi = max(khi, k);
+    for (int i0 = mlo + tid; i0 < mhi; i0 += 8 * kSelThreads) {  // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = i0 + u * kSelThreads < mhi ? m[i0 + u * kSelThreads] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kSelThreads;
+        if (i >= mhi) break;
+        const uint32_t k = mass_key(x[u]);
+        if (STAGED) keys[i - begin] = k;
+        klo = min(klo, k);
+        khi = max(khi, k);
+      }
     }
     klo = __reduce_min_sync(~0u, klo);
     khi = __reduce_max_sync(~0u, khi);
@@ -150,11 +157,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
       }
       pa::cluster_sync();
       // bins 2 tid and 2 tid + 1 over the cluster; prefix sums from the top
-      uint2 c = make_uint2(0u, 0u);
-      for (int q = 0; q < C; ++q) {
-        const uint2 x = load_cluster(hist + 2 * tid, q);
-        c.x += x.x;
-        c.y += x.y;
+      uint2 c = make_uint2(0u, 0u), x[kMaxCluster];
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) x[q] = q < C ? load_cluster(hist + 2 * tid, q) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        c.x += x[q].x;
+        c.y += x[q].y;
       }
       for (int b = tid; b < kBins; b += kSelThreads) sm.hist[(step + 1) & 1][b] = 0;  // read by all a step ago
       const int mine = (int)(c.x + c.y), upto = warp_scan(mine, lane);
@@ -265,19 +274,22 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;    // tokens per thread and round: 8 16-byte loads in flight
 constexpr int kMaxMoveCluster = 16;  // more than 8 needs the kernel's opt-in
 
-// What a thread carries of kMoveUnroll tokens: 16 bytes of K and V each, and the K scale, the V scale
-// or the mass (threads 0, 1 and 2 of a token).
+// Where a thread's tokens of a round come from and go to (rows of the cache, which fit 31 bits), and
+// their old positions; from -1: nothing to move.
+struct Route {
+  int32_t from[kMoveUnroll], to[kMoveUnroll], pos[kMoveUnroll];
+};
+// What it carries of them: 16 bytes of K and V each, and the K scale, the V scale or the mass
+// (threads 0, 1 and 2 of a token).
 struct Moved {
   uint4 k[kMoveUnroll], v[kMoveUnroll];
   float x[kMoveUnroll];
-  int64_t to[kMoveUnroll];  // destination row, or -1
 };
 
-// RC threads per token, one for each 16 bytes of its row.  The tokens [first, first + RT) of
-// (request r, KV head h): every index load, then every row load.
+// RC threads per token, one for each 16 bytes of its row: token first + t + u * (threads / RC).
 template <int RC, bool IN_PLACE>
-__device__ __forceinline__ void load_tokens(const CompactParams &p, const int32_t *keep, int r, int h, int n,
-                                            int64_t first, Moved &m) {
+__device__ __forceinline__ void find_tokens(const CompactParams &p, const int32_t *keep, int r, int h, int n,
+                                            int64_t first, Route &m) {
   constexpr int kStep = kMoveThreads / RC;
   const int t = threadIdx.x / RC, c = threadIdx.x % RC;
   int s[kMoveUnroll], prev[kMoveUnroll], sp[kMoveUnroll], dp[kMoveUnroll];
@@ -293,7 +305,7 @@ __device__ __forceinline__ void load_tokens(const CompactParams &p, const int32_
     const int64_t i = first + t + u * kStep;
     sp[u] = -1;
     if (i >= n || (IN_PLACE && s[u] == i && prev[u] < s[u])) {
-      s[u] = -1;  // nothing to move
+      s[u] = -1;
     } else if (s[u] <= prev[u] || s[u] < i || s[u] >> p.ps_shift >= p.bt_stride ||
                (p.mass != nullptr && s[u] >= p.m_stride)) {
       if (c == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_KEEP);
@@ -305,32 +317,45 @@ __device__ __forceinline__ void load_tokens(const CompactParams &p, const int32_
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {
     const int64_t i = first + t + u * kStep;
-    m.to[u] = -1;
+    m.from[u] = m.to[u] = -1;
+    m.pos[u] = s[u];
     if (s[u] < 0) continue;
     if (sp[u] < 0 || sp[u] >= p.num_pages || dp[u] < 0 || dp[u] >= p.num_pages) {
       if (c == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_PAGE);
       continue;
     }
-    const int64_t from = (((int64_t)sp[u] * p.Hkv + h) << p.ps_shift) + (s[u] & (p.ps - 1));
-    m.to[u] = (((int64_t)dp[u] * p.Hkv + h) << p.ps_shift) + (i & (p.ps - 1));
-    m.k[u] = *reinterpret_cast<const uint4 *>(p.k + from * (16 * RC) + 16 * c);
-    m.v[u] = *reinterpret_cast<const uint4 *>(p.v + from * (16 * RC) + 16 * c);
-    if (c < 2 && p.ks != nullptr) m.x[u] = (c == 0 ? p.ks : p.vs)[from];
-    if (c == 2 && p.mass != nullptr) m.x[u] = p.mass[((int64_t)r * p.Hkv + h) * p.m_stride + s[u]];
+    m.from[u] = ((sp[u] * p.Hkv + h) << p.ps_shift) + (s[u] & (p.ps - 1));
+    m.to[u] = ((dp[u] * p.Hkv + h) << p.ps_shift) + (int)(i & (p.ps - 1));
   }
 }
 
 template <int RC>
-__device__ __forceinline__ void store_tokens(const CompactParams &p, int r, int h, int64_t first, const Moved &m) {
+__device__ __forceinline__ void load_tokens(const CompactParams &p, int64_t row, const Route &f, Moved &m) {
+  const int c = threadIdx.x % RC;
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    if (f.from[u] < 0) continue;
+    const int64_t at = (int64_t)f.from[u] * (16 * RC) + 16 * c;
+    m.k[u] = *reinterpret_cast<const uint4 *>(p.k + at);
+    m.v[u] = *reinterpret_cast<const uint4 *>(p.v + at);
+    if (c < 2 && p.ks != nullptr) m.x[u] = (c == 0 ? p.ks : p.vs)[f.from[u]];
+    if (c == 2 && p.mass != nullptr) m.x[u] = p.mass[row * p.m_stride + f.pos[u]];
+  }
+}
+
+template <int RC>
+__device__ __forceinline__ void store_tokens(const CompactParams &p, int64_t row, int64_t first, const Route &f,
+                                             const Moved &m) {
   constexpr int kStep = kMoveThreads / RC;
   const int t = threadIdx.x / RC, c = threadIdx.x % RC;
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {
-    if (m.to[u] < 0) continue;
-    *reinterpret_cast<uint4 *>(p.k + m.to[u] * (16 * RC) + 16 * c) = m.k[u];
-    *reinterpret_cast<uint4 *>(p.v + m.to[u] * (16 * RC) + 16 * c) = m.v[u];
-    if (c < 2 && p.ks != nullptr) (c == 0 ? p.ks : p.vs)[m.to[u]] = m.x[u];
-    if (c == 2 && p.mass != nullptr) p.mass_out[((int64_t)r * p.Hkv + h) * p.mo_stride + first + t + u * kStep] = m.x[u];
+    if (f.from[u] < 0) continue;
+    const int64_t at = (int64_t)f.to[u] * (16 * RC) + 16 * c;
+    *reinterpret_cast<uint4 *>(p.k + at) = m.k[u];
+    *reinterpret_cast<uint4 *>(p.v + at) = m.v[u];
+    if (c < 2 && p.ks != nullptr) (c == 0 ? p.ks : p.vs)[f.to[u]] = m.x[u];
+    if (c == 2 && p.mass != nullptr) p.mass_out[row * p.mo_stride + first + t + u * kStep] = m.x[u];
   }
 }
 
@@ -345,17 +370,27 @@ __device__ __forceinline__ int new_length(const CompactParams &p, int r, bool fl
   return n;
 }
 
-// Into other pages: every CTA moves its own tokens.
+// Into other pages: the CTAs of a row (blockIdx.y) take its rounds in turn, and look the next round's
+// tokens up while this one's bytes are on their way.
 template <int RC>
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 3) kv_compact_kernel(const CompactParams p) {
   constexpr int kTokens = kMoveThreads / RC * kMoveUnroll;
+  const int64_t row = blockIdx.y;
   const int h = blockIdx.y % p.Hkv, r = blockIdx.y / p.Hkv;
   const int n = new_length(p, r, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-  const int64_t first = (int64_t)blockIdx.x * kTokens;
+  const int32_t *keep = p.keep + row * p.keep_stride;
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  int64_t first = (int64_t)blockIdx.x * kTokens;
   if (first >= n) return;
-  Moved m;
-  load_tokens<RC, false>(p, p.keep + (int64_t)blockIdx.y * p.keep_stride, r, h, n, first, m);
-  store_tokens<RC>(p, r, h, first, m);
+  Route f;
+  find_tokens<RC, false>(p, keep, r, h, n, first, f);
+  for (; first < n; first += step) {
+    Moved m;
+    load_tokens<RC>(p, row, f, m);
+    const Route g = f;
+    if (first + step < n) find_tokens<RC, false>(p, keep, r, h, n, first + step, f);
+    store_tokens<RC>(p, row, first, g, m);
+  }
 }
 
 // In place: a cluster per (request, KV head) moves its tokens in rounds.  Kept positions ascend, so
@@ -363,28 +398,37 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
 // A round is stored once every CTA has read it (one cluster barrier), and the next round is
 // read before that: its sources lie past the destinations of this one.
 template <int RC>
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_in_place_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 2) kv_compact_in_place_kernel(const CompactParams p) {
   constexpr int kTokens = kMoveThreads / RC * kMoveUnroll;
   const int C = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
-  const int row = blockIdx.x / C, h = row % p.Hkv, r = row / p.Hkv;
+  const int64_t row = blockIdx.x / C;
+  const int h = (int)(row % p.Hkv), r = (int)(row / p.Hkv);
   const int n = new_length(p, r, rank == 0 && h == 0 && threadIdx.x == 0);
-  const int32_t *keep = p.keep + (int64_t)row * p.keep_stride;
+  const int32_t *keep = p.keep + row * p.keep_stride;
   const int64_t round = (int64_t)C * kTokens;
   int64_t first = (int64_t)rank * kTokens;
   const int rounds = (int)((n + round - 1) / round);
   if (rounds == 0) return;  // the same for the whole cluster
+  Route f, g;
   Moved a, b;
-  load_tokens<RC, true>(p, keep, r, h, n, first, a);
+  find_tokens<RC, true>(p, keep, r, h, n, first, f);
+  load_tokens<RC>(p, row, f, a);
   for (int k = 0; k < rounds; k += 2) {
     pa::cluster_arrive();
-    if (k + 1 < rounds) load_tokens<RC, true>(p, keep, r, h, n, first + round, b);
+    if (k + 1 < rounds) {
+      find_tokens<RC, true>(p, keep, r, h, n, first + round, g);
+      load_tokens<RC>(p, row, g, b);
+    }
     pa::cluster_wait();
-    store_tokens<RC>(p, r, h, first, a);
+    store_tokens<RC>(p, row, first, f, a);
     if (k + 1 >= rounds) break;
     pa::cluster_arrive();
-    if (k + 2 < rounds) load_tokens<RC, true>(p, keep, r, h, n, first + 2 * round, a);
+    if (k + 2 < rounds) {
+      find_tokens<RC, true>(p, keep, r, h, n, first + 2 * round, f);
+      load_tokens<RC>(p, row, f, a);
+    }
     pa::cluster_wait();
-    store_tokens<RC>(p, r, h, first + round, b);
+    store_tokens<RC>(p, row, first + round, g, b);
     first += 2 * round;
   }
 }
@@ -520,16 +564,19 @@ extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream
   const int tokens = kMoveThreads / (wide ? 16 : 8) * kMoveUnroll;
   const int rows = a->num_seqs * a->num_kv_heads;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = evict_device();
+  if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   if (!in_place) {
-    const dim3 grid((unsigned)(((int64_t)a->keep_stride + tokens - 1) / tokens), rows);
+    // one wave (three CTAs per SM), or a round per CTA where that is fewer
+    const int64_t wave = (3 * (int64_t)sms + rows - 1) / rows;
+    const int64_t need = ((int64_t)a->keep_stride + tokens - 1) / tokens;
+    const dim3 grid((unsigned)(wave < need ? wave : need), rows);
     if (wide)
       kv_compact_kernel<16><<<grid, kMoveThreads, 0, s>>>(p);
     else
       kv_compact_kernel<8><<<grid, kMoveThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
-  const int sms = evict_device();
-  if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per row: more while all rows' CTAs run at once (two per SM) and there are tokens for them
   int C = 1;
   while (C < kMaxMoveCluster && (int64_t)rows * C <= sms && (int64_t)C * tokens < a->keep_stride) C *= 2;

@@ -15,10 +15,10 @@
 // two, in two columns of N: exact for elements within 2^-14 of the row's largest, and within
 // 2^-22 of that for smaller ones.  So N = 32 columns per query row (16 heads), or 16 for bf16.
 //
-// Warp roles (320 threads, one CTA per SM, each with an equal share of the tiles): warps 0-3 and 4-7
-// are two epilogue groups that take even and odd tiles and convert the queries of the segment to come
-// ((request, KV head, up to four rows) of the CTA's share); warp 8 gathers pages by TMA into a ring of
-// stages; warp 9 issues the MMAs, up to two tiles ahead of each group.  Every wait is bounded.
+// Warp roles (576 threads, one CTA per SM, each with an equal share of the tiles): warps 0-15 are four
+// epilogue groups that take every fourth tile and convert the queries of the segment to come
+// ((request, KV head, up to four rows) of the CTA's share); warp 16 gathers pages by TMA into a ring of
+// stages; warp 17 issues the MMAs, up to two tiles ahead of each group.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -43,7 +43,7 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kMaxQ = 64;
 constexpr int kMaxPositions = 1 << 30;
 constexpr int kRows = 4;          // query rows per pass over the keys
-constexpr int kGroups = 2;        // epilogue groups of four warps
+constexpr int kGroups = 4;        // epilogue groups of four warps
 constexpr int kEpiWarps = 4 * kGroups;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr int kMaxStages = 12;
@@ -59,16 +59,15 @@ struct MassParams {
   uint32_t *status;
   int64_t num_pages;
   int32_t B, R, Hkv, ps, ps_shift, ppt, bt_stride, mass_stride, maxq;
-  int32_t nstage, stage_bytes, qbuf_bytes, tmem_cols;
+  int32_t nstage, stage_bytes, qbuf_bytes;
+  int32_t nbuf, buf_cols, tmem_cols;  // TMEM: nbuf buffers of buf_cols columns for each group
   float kfold, decay;  // kfold = sm_scale * log2 e (* k_scale_scalar)
 };
 
-// Shared memory: stages | 2 query operands | factors | barriers | tile prefix
-constexpr int kFactorBytes = 2 * kRows * 2 * kG * 4;  // per buffer and row: kf[16], lse2[16]
-struct MassBars {
-  uint32_t full, empty, s_full, s_free, qready, qfree, tdone, mmadone;
-};
-constexpr int kNumBars = 2 * kMaxStages + 4 + 4 + 2 + 2 + 2;
+// Shared memory: stages | 2 query operands | factors | barriers | requests (tile prefix, L, row0, q_len)
+constexpr int kFactorBytes = 2 * kRows * 2 * kG * 4;  // per buffer and row: factor[16], -lse2[16]
+constexpr int kSBars = 2 * kGroups;  // two buffers per group at most
+constexpr int kNumBars = 2 * kMaxStages + 2 * kSBars + 2 + 2 + 2;
 constexpr int kCtrlBytes = kFactorBytes + kNumBars * 8 + kMaxStages * 4 + 16 + (kThreads / 32) * 4 + 64;
 
 struct MassSmem {
@@ -78,6 +77,7 @@ struct MassSmem {
   uint32_t *misc;    // [0] TMEM address, [1] abort
   int32_t *wsum;     // per-warp sums of the scan
   int32_t *tstart;   // [B + 1] tiles of the requests before, for one KV head
+  int32_t *info;     // [B][3]: context length, first row, rows
 };
 
 __device__ __forceinline__ MassSmem carve(uint8_t *raw, const MassParams &p) {
@@ -92,17 +92,18 @@ __device__ __forceinline__ MassSmem carve(uint8_t *raw, const MassParams &p) {
   s.misc = s.valid + kMaxStages;
   s.wsum = reinterpret_cast<int32_t *>(s.misc + 4);
   s.tstart = reinterpret_cast<int32_t *>(c + kCtrlBytes);
+  s.info = s.tstart + p.B + 1;
   return s;
 }
 
 __device__ __forceinline__ uint32_t bar_full(const MassSmem &s, int i) { return s.bars + 8 * i; }
 __device__ __forceinline__ uint32_t bar_empty(const MassSmem &s, int i) { return s.bars + 8 * (kMaxStages + i); }
 __device__ __forceinline__ uint32_t bar_sfull(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + i); }
-__device__ __forceinline__ uint32_t bar_sfree(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 4 + i); }
-__device__ __forceinline__ uint32_t bar_qready(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 8 + i); }
-__device__ __forceinline__ uint32_t bar_qfree(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 10 + i); }
-__device__ __forceinline__ uint32_t bar_tdone(const MassSmem &s) { return s.bars + 8 * (2 * kMaxStages + 12); }
-__device__ __forceinline__ uint32_t bar_mmadone(const MassSmem &s) { return s.bars + 8 * (2 * kMaxStages + 13); }
+__device__ __forceinline__ uint32_t bar_sfree(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + kSBars + i); }
+__device__ __forceinline__ uint32_t bar_qready(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 2 * kSBars + i); }
+__device__ __forceinline__ uint32_t bar_qfree(const MassSmem &s, int i) { return s.bars + 8 * (2 * kMaxStages + 2 * kSBars + 2 + i); }
+__device__ __forceinline__ uint32_t bar_tdone(const MassSmem &s) { return s.bars + 8 * (2 * kMaxStages + 2 * kSBars + 4); }
+__device__ __forceinline__ uint32_t bar_mmadone(const MassSmem &s) { return s.bars + 8 * (2 * kMaxStages + 2 * kSBars + 5); }
 
 // What one request contributes, and what is wrong with it.
 struct Request {
@@ -133,6 +134,9 @@ __device__ uint32_t scan_requests(const MassParams &p, const MassSmem &s) {
       const uint32_t fl = read_request(p, r, q);
       flags |= fl;
       if (!fl && q.ql > 0) n = (q.L + kTile - 1) / kTile;
+      s.info[3 * r] = q.L;
+      s.info[3 * r + 1] = q.row0;
+      s.info[3 * r + 2] = q.ql;
     }
     int x = n;
 #pragma unroll
@@ -192,7 +196,7 @@ struct Walk {
     s.h = (int)(rem / nt);
     s.t0 = (int)(rem - (int64_t)s.h * nt);
     s.t1 = (int)min((int64_t)nt, s.t0 + (end - at));
-    read_request(p, lo, s.q);
+    s.q = Request{sm.info[3 * lo], sm.info[3 * lo + 1], sm.info[3 * lo + 2]};
     s.tok0 = 0;
     s.nr = min(kRows, s.q.ql);
     return true;
@@ -276,13 +280,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
 
 // TMEM columns of group g's buffer k.
 __device__ __forceinline__ uint32_t tmem_buf(const MassParams &p, int g, int k) {
-  return (uint32_t)((2 * g + k) * (p.tmem_cols >> 2));
+  return (uint32_t)((g * p.nbuf + k) * p.buf_cols);
 }
 
 template <bool BF16>
 __device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b, uint32_t tm) {
   const int lane = threadIdx.x & 31;
-  int i = 0, seg = 0, cnt[kGroups] = {0, 0};
+  int i = 0, seg = 0;
+  int uses[kGroups] = {0, 0, 0, 0};  // each group's tiles so far
   bool ok = true;
   Walk w(a, b);
   while (ok && w.next(p, sm)) {
@@ -292,24 +297,25 @@ __device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int6
     const int N = w.s.nr * (BF16 ? kG : 2 * kG);
     const uint32_t id = BF16 ? idesc_bf16(kTile, N) : pa::umma_idesc_e4m3(kTile, N, 0, 0);
     for (int t = w.s.t0; t < w.s.t1 && ok; ++t, ++i) {
-      const int st = i % p.nstage, g = t & 1, k = cnt[g] & 1, u = cnt[g] >> 1;
+      const int st = i % p.nstage, g = t % kGroups;
+      int n = 0;
+#pragma unroll
+      for (int x = 0; x < kGroups; ++x) n = x == g ? uses[x]++ : n;
+      const int k = n & (p.nbuf - 1), u = n >> (p.nbuf - 1);  // one or two buffers
       ok = warp_wait(bar_full(sm, st), (i / p.nstage) & 1);
       if (ok && u > 0) ok = warp_wait(bar_sfree(sm, 2 * g + k), (u - 1) & 1);
       if (!ok) break;
-      ++cnt[g];
       pa::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t ka = sm.stages + st * p.stage_bytes, d = tm + tmem_buf(p, g, k);
-        if (BF16) {
+      const uint32_t ka = sm.stages + st * p.stage_bytes, d = tm + tmem_buf(p, g, k);
+      if (pa::elect_one()) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x)  // 16 elements each; the second half of the row in its own 16 KB
-            pa::umma_f16(d, pa::umma_sdesc(ka + (x >> 2) * 16384 + 32 * (x & 3), 1024, 1024, 2),
-                         pa::umma_sdesc(q + (x >> 2) * (p.qbuf_bytes >> 1) + 32 * (x & 3), 1024, 1024, 2), id, x > 0);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            pa::umma_e4m3(d, pa::umma_sdesc(ka + 32 * x, 1024, 1024, 2), pa::umma_sdesc(q + 32 * x, 1024, 1024, 2), id,
-                          x > 0);
+        for (int x = 0; x < (BF16 ? 8 : 4); ++x) {  // bf16: the second half of a row in its own 16 KB
+          const uint64_t da = pa::umma_sdesc(ka + (BF16 ? (x >> 2) * 16384 + 32 * (x & 3) : 32 * x), 1024, 1024, 2);
+          const uint64_t db = pa::umma_sdesc(q + (BF16 ? (x >> 2) * (p.qbuf_bytes >> 1) + 32 * (x & 3) : 32 * x), 1024, 1024, 2);
+          if (BF16)
+            pa::umma_f16(d, da, db, id, x > 0);
+          else
+            pa::umma_e4m3(d, da, db, id, x > 0);
         }
         pa::umma_commit(bar_sfull(sm, 2 * g + k));
         pa::umma_commit(bar_empty(sm, st));
@@ -319,10 +325,9 @@ __device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int6
     }
     ++seg;
   }
-  if (lane == 0) {
-    if (!ok) raise(p, PA_DEV_TIMEOUT);
-    pa::umma_commit(bar_mmadone(sm));
-  }
+  if (!ok && lane == 0) raise(p, PA_DEV_TIMEOUT);
+  __syncwarp();
+  if (pa::elect_one()) pa::umma_commit(bar_mmadone(sm));
   __syncwarp();
   if (!warp_wait(bar_mmadone(sm), 0) && lane == 0) raise(p, PA_DEV_TIMEOUT);
   if (!warp_wait(bar_tdone(sm), 0) && lane == 0) raise(p, PA_DEV_TIMEOUT);
@@ -333,7 +338,7 @@ __device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int6
 // ---------------------------------------------------------------------------- epilogue
 
 // The segment's query rows as the MMA's B operand (K-major, 128-byte swizzle), and per (row, head) the
-// factor of its scores and its lse in base 2 (+inf where the row has no key: 2^(x - inf) = 0).
+// factor of its scores and its -lse in base 2 (-inf where the row has no key: 2^(x - inf) = 0).
 template <bool BF16>
 __device__ void convert_queries(const MassParams &p, const MassSmem &sm, const Segment &s, int qb, int etid) {
   const uint32_t dst = sm.q + qb * p.qbuf_bytes, fac = sm.factors + qb * (kFactorBytes / 2);
@@ -342,7 +347,7 @@ __device__ void convert_queries(const MassParams &p, const MassSmem &sm, const S
   for (int u = etid; u < s.nr * kG; u += 32 * kEpiWarps) {
     const float l = p.lse[qrow + (u / kG) * Hq + u % kG];
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac + (u / kG) * (2 * kG * 4) + (kG + u % kG) * 4),
-                 "f"(l == -INFINITY ? INFINITY : l * kLog2e) : "memory");
+                 "f"(l == -INFINITY ? l : -l * kLog2e) : "memory");
   }
   if (BF16) {
     for (int u = etid; u < s.nr * kG * 16; u += 32 * kEpiWarps) {  // 16 bytes: 8 elements
@@ -419,19 +424,25 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
     ok = warp_wait(bar_qready(sm, qb), (seg >> 1) & 1);
     const uint32_t fac = sm.factors + qb * (kFactorBytes / 2);
     const int64_t mrow = ((int64_t)s.r * p.Hkv + s.h) * p.mass_stride;
-    for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
-      if ((t & 1) != g) continue;
-      const int st = i % p.nstage, k = cnt & 1, pos = t * kTile + tok;
+    // What the mass of this thread's position in tile t was, asked for two of the group's tiles ahead.
+    auto before = [&](int t) {
+      const int pos = t * kTile + tok;
+      if (t >= s.t1 || pos >= s.q.L) return 0.f;
+      if (s.tok0 > 0) return p.out[mrow + pos];  // this thread's own sum over the rows before
+      return pos < s.q.L - s.q.ql && p.decay != 0.f ? p.mass[mrow + pos] : 0.f;
+    };
+    const float keep = s.tok0 > 0 ? 1.f : p.decay;
+    int t = s.t0 + ((g - s.t0) & (kGroups - 1));  // the group's first tile
+    float old0 = before(t), old1 = before(t + kGroups);
+    i += t - s.t0;
+    for (; t < s.t1 && ok; t += kGroups, i += kGroups) {
+      const int st = i % p.nstage, k = cnt & (p.nbuf - 1), pos = t * kTile + tok;
       const bool live = pos < s.q.L;
-      float old = 0.f;
-      if (live) {
-        if (s.tok0 > 0)
-          old = p.out[mrow + pos];  // this thread's own sum over the rows before
-        else if (pos < s.q.L - s.q.ql && p.decay != 0.f)
-          old = p.decay * p.mass[mrow + pos];
-      }
+      const float old = keep * old0;
+      old0 = old1;
+      old1 = before(t + 2 * kGroups);
       ok = warp_wait(bar_full(sm, st), (i / p.nstage) & 1) &&
-           warp_wait(bar_sfull(sm, 2 * g + k), (cnt >> 1) & 1);
+           warp_wait(bar_sfull(sm, 2 * g + k), (cnt >> (p.nbuf - 1)) & 1);
       if (!ok) break;
       ++cnt;
       float ks = 1.f;
@@ -441,6 +452,7 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
       __syncwarp();
       if (lane == 0) pa::mbar_arrive(bar_empty(sm, st));
       pa::tc_fence_after();
+      const pa::f32x2 ks2 = pa::pack2(ks, ks), lo_unit = pa::pack2(1.f / 32.f, 1.f / 32.f);
       float sum = 0.f;
       for (int x = 0; x < s.nr; ++x) {
         uint32_t hi[kG], lo[kG];
@@ -450,25 +462,33 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
         pa::tmem_wait16(hi);
         if (!BF16) pa::tmem_wait16(lo);
         const uint32_t f = fac + x * (2 * kG * 4);
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        pa::f32x2 part[2] = {pa::pack2(0.f, 0.f), pa::pack2(0.f, 0.f)};
 #pragma unroll
         for (int j = 0; j < kG; j += 4) {
           const uint4 kv = pa::lds128(f + 4 * j), lv = pa::lds128(f + 4 * (kG + j));
           const uint32_t kf[4] = {kv.x, kv.y, kv.z, kv.w}, l2[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float d = __uint_as_float(hi[j + e]);
-            if (!BF16) d = fmaf(__uint_as_float(lo[j + e]), 1.f / 32.f, d);
-            part[e] += pa::fast_exp2(fmaf(d, __uint_as_float(kf[e]) * ks, -__uint_as_float(l2[e])));
+          for (int e = 0; e < 4; e += 2) {
+            pa::f32x2 d = pa::pack2(__uint_as_float(hi[j + e]), __uint_as_float(hi[j + e + 1]));
+            if (!BF16) d = pa::fma2(pa::pack2(__uint_as_float(lo[j + e]), __uint_as_float(lo[j + e + 1])), lo_unit, d);
+            const pa::f32x2 c = pa::mul2(pa::pack2(__uint_as_float(kf[e]), __uint_as_float(kf[e + 1])), ks2);
+            d = pa::fma2(d, c, pa::pack2(__uint_as_float(l2[e]), __uint_as_float(l2[e + 1])));
+            float d0, d1;
+            pa::unpack2(d, d0, d1);
+            part[e >> 1] = pa::add2(part[e >> 1], pa::pack2(pa::fast_exp2(d0), pa::fast_exp2(d1)));
           }
         }
-        if (pos < s.q.L - s.q.ql + s.tok0 + x + 1) sum += (part[0] + part[1]) + (part[2] + part[3]);
+        float p0, p1, p2, p3;
+        pa::unpack2(part[0], p0, p1);
+        pa::unpack2(part[1], p2, p3);
+        if (pos < s.q.L - s.q.ql + s.tok0 + x + 1) sum += (p0 + p1) + (p2 + p3);
       }
       pa::tc_fence_before();
       __syncwarp();
       if (lane == 0) pa::mbar_arrive(bar_sfree(sm, 2 * g + k));
       if (live) p.out[mrow + pos] = old + (valid ? sum : 0.f);
     }
+    i -= t - s.t1;  // the segment's tiles, of either group
     if (ok && lane == 0) pa::mbar_arrive(bar_qfree(sm, qb));  // the factors have been read
     __syncwarp();
     ++seg;
@@ -490,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mass_kernel(const __grid_con
       pa::mbar_init(bar_full(sm, k), 1);
       pa::mbar_init(bar_empty(sm, k), 1 + 4);  // the MMAs' commit, the warps of the tile's group
     }
-    for (int k = 0; k < 2 * kGroups; ++k) {
+    for (int k = 0; k < kSBars; ++k) {
       pa::mbar_init(bar_sfull(sm, k), 1);
       pa::mbar_init(bar_sfree(sm, k), 4);
     }
@@ -610,10 +630,12 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
   // Query operand and TMEM for the rows a segment can have; as many stages as fit.
   const int nr = std::min(a->max_q_len, kRows);
   p.qbuf_bytes = nr * 2 * kG * 128;  // e4m3: 32 rows of 128 bytes; bf16: two halves of 16 rows
-  p.tmem_cols = 4 * 32;
-  while (p.tmem_cols < 4 * 2 * kG * nr) p.tmem_cols *= 2;
+  p.buf_cols = nr * (bf16 ? kG : 2 * kG);
+  p.nbuf = 2 * kGroups * p.buf_cols <= 512 ? 2 : 1;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < kGroups * p.nbuf * p.buf_cols) p.tmem_cols *= 2;
   p.stage_bytes = bf16 ? 32768 : 16384 + 1024;  // keys, then an e4m3 tile's scales
-  const int fixed = 1024 + 2 * p.qbuf_bytes + kCtrlBytes + (a->num_seqs + 1) * 4;
+  const int fixed = 1024 + 2 * p.qbuf_bytes + kCtrlBytes + (4 * a->num_seqs + 1) * 4;
   p.nstage = std::min(kMaxStages, (dev->smem - fixed) / p.stage_bytes);
   if (p.nstage < 2) return PA_ERR_UNSUPPORTED;
   const size_t smem = (size_t)fixed + (size_t)p.nstage * p.stage_bytes;
