@@ -271,92 +271,25 @@ struct CompactParams {
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;    // tokens per thread and round: 8 16-byte loads in flight
+constexpr int kMoveBytes = 65536;    // K and V rows of a CTA's round in shared memory: three CTAs per SM
 constexpr int kMaxMoveCluster = 16;  // more than 8 needs the kernel's opt-in
 
-// Where a thread's tokens of a round come from and go to (rows of the cache, which fit 31 bits), and
-// their old positions; from -1: nothing to move.
-struct Route {
-  int32_t from[kMoveUnroll], to[kMoveUnroll], pos[kMoveUnroll];
-};
-// What it carries of them: 16 bytes of K and V each, and the K scale, the V scale or the mass
-// (threads 0, 1 and 2 of a token).
-struct Moved {
-  uint4 k[kMoveUnroll], v[kMoveUnroll];
-  float x[kMoveUnroll];
+// Tokens of a round: 256 with 128-byte rows, 128 with 256-byte ones.
+template <int RC>
+__host__ __device__ constexpr int move_tokens() { return kMoveBytes / (32 * RC); }
+
+struct MoveShared {
+  int32_t from[256];  // cache row of each token of the round, or -1: not to be written
+  unsigned odd;       // destination pages (of the round) with a token that is not to be written
+  unsigned moved;     // and those with one that is, and comes from elsewhere
 };
 
-// RC threads per token, one for each 16 bytes of its row: token first + t + u * (threads / RC).
-template <int RC, bool IN_PLACE>
-__device__ __forceinline__ void find_tokens(const CompactParams &p, const int32_t *keep, int r, int h, int n,
-                                            int64_t first, Route &m) {
-  constexpr int kStep = kMoveThreads / RC;
-  const int t = threadIdx.x / RC, c = threadIdx.x % RC;
-  int s[kMoveUnroll], prev[kMoveUnroll], sp[kMoveUnroll], dp[kMoveUnroll];
-#pragma unroll
-  for (int u = 0; u < kMoveUnroll; ++u) {
-    const int64_t i = first + t + u * kStep;
-    s[u] = i < n ? keep[i] : -1;
-    prev[u] = i < n && i > 0 ? keep[i - 1] : -1;
-    dp[u] = i < n ? p.dt[(int64_t)r * p.dt_stride + (i >> p.ps_shift)] : -1;
-  }
-#pragma unroll
-  for (int u = 0; u < kMoveUnroll; ++u) {
-    const int64_t i = first + t + u * kStep;
-    sp[u] = -1;
-    if (i >= n || (IN_PLACE && s[u] == i && prev[u] < s[u])) {
-      s[u] = -1;
-    } else if (s[u] <= prev[u] || s[u] < i || s[u] >> p.ps_shift >= p.bt_stride ||
-               (p.mass != nullptr && s[u] >= p.m_stride)) {
-      if (c == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_KEEP);
-      s[u] = -1;
-    } else {
-      sp[u] = p.bt[(int64_t)r * p.bt_stride + (s[u] >> p.ps_shift)];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kMoveUnroll; ++u) {
-    const int64_t i = first + t + u * kStep;
-    m.from[u] = m.to[u] = -1;
-    m.pos[u] = s[u];
-    if (s[u] < 0) continue;
-    if (sp[u] < 0 || sp[u] >= p.num_pages || dp[u] < 0 || dp[u] >= p.num_pages) {
-      if (c == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_PAGE);
-      continue;
-    }
-    m.from[u] = ((sp[u] * p.Hkv + h) << p.ps_shift) + (s[u] & (p.ps - 1));
-    m.to[u] = ((dp[u] * p.Hkv + h) << p.ps_shift) + (int)(i & (p.ps - 1));
-  }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-
-template <int RC>
-__device__ __forceinline__ void load_tokens(const CompactParams &p, int64_t row, const Route &f, Moved &m) {
-  const int c = threadIdx.x % RC;
-#pragma unroll
-  for (int u = 0; u < kMoveUnroll; ++u) {
-    if (f.from[u] < 0) continue;
-    const int64_t at = (int64_t)f.from[u] * (16 * RC) + 16 * c;
-    m.k[u] = *reinterpret_cast<const uint4 *>(p.k + at);
-    m.v[u] = *reinterpret_cast<const uint4 *>(p.v + at);
-    if (c < 2 && p.ks != nullptr) m.x[u] = (c == 0 ? p.ks : p.vs)[f.from[u]];
-    if (c == 2 && p.mass != nullptr) m.x[u] = p.mass[row * p.m_stride + f.pos[u]];
-  }
-}
-
-template <int RC>
-__device__ __forceinline__ void store_tokens(const CompactParams &p, int64_t row, int64_t first, const Route &f,
-                                             const Moved &m) {
-  constexpr int kStep = kMoveThreads / RC;
-  const int t = threadIdx.x / RC, c = threadIdx.x % RC;
-#pragma unroll
-  for (int u = 0; u < kMoveUnroll; ++u) {
-    if (f.from[u] < 0) continue;
-    const int64_t at = (int64_t)f.to[u] * (16 * RC) + 16 * c;
-    *reinterpret_cast<uint4 *>(p.k + at) = m.k[u];
-    *reinterpret_cast<uint4 *>(p.v + at) = m.v[u];
-    if (c < 2 && p.ks != nullptr) (c == 0 ? p.ks : p.vs)[f.to[u]] = m.x[u];
-    if (c == 2 && p.mass != nullptr) p.mass_out[row * p.mo_stride + first + t + u * kStep] = m.x[u];
-  }
+// Contiguous bulk copy shared -> global (16-byte aligned addresses and size).
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
 // The request's new length, or 0 where it cannot be (flagged once).
@@ -370,70 +303,119 @@ __device__ __forceinline__ int new_length(const CompactParams &p, int r, bool fl
   return n;
 }
 
-// Into other pages: the CTAs of a row (blockIdx.y) take its rounds in turn, and look the next round's
-// tokens up while this one's bytes are on their way.
-template <int RC>
+// A round of a (request, KV head): T tokens, whose rows are gathered into shared memory with 16-byte
+// asynchronous copies (all of a round's 64 KB in flight at once) and leave it as one bulk store of K and
+// one of V per destination page, since the destinations are consecutive slots.  A thread per
+// token looks its row up and carries its scales and mass.
+//
+// Into other pages each CTA moves one round.  In place the CTAs of a cluster share the rounds of a
+// row: kept positions ascend, so keep[i] >= i, and the destinations of a round are sources of
+// this round or an earlier one only.  So a round is written once every CTA has read its part of it
+// (one cluster barrier), and the next may be read meanwhile: its sources lie further on.
+template <int RC, bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads, 3) kv_compact_kernel(const CompactParams p) {
-  constexpr int kTokens = kMoveThreads / RC * kMoveUnroll;
-  const int64_t row = blockIdx.y;
-  const int h = blockIdx.y % p.Hkv, r = blockIdx.y / p.Hkv;
-  const int n = new_length(p, r, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-  const int32_t *keep = p.keep + row * p.keep_stride;
-  const int64_t step = (int64_t)gridDim.x * kTokens;
-  int64_t first = (int64_t)blockIdx.x * kTokens;
-  if (first >= n) return;
-  Route f;
-  find_tokens<RC, false>(p, keep, r, h, n, first, f);
-  for (; first < n; first += step) {
-    Moved m;
-    load_tokens<RC>(p, row, f, m);
-    const Route g = f;
-    if (first + step < n) find_tokens<RC, false>(p, keep, r, h, n, first + step, f);
-    store_tokens<RC>(p, row, first, g, m);
-  }
-}
-
-// In place: a cluster per (request, KV head) moves its tokens in rounds.  Kept positions ascend, so
-// keep[i] >= i: the destinations of a round are sources of this round or an earlier one only.
-// A round is stored once every CTA has read it (one cluster barrier), and the next round is
-// read before that: its sources lie past the destinations of this one.
-template <int RC>
-__global__ void __launch_bounds__(kMoveThreads, 2) kv_compact_in_place_kernel(const CompactParams p) {
-  constexpr int kTokens = kMoveThreads / RC * kMoveUnroll;
-  const int C = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
-  const int64_t row = blockIdx.x / C;
+  constexpr int T = move_tokens<RC>(), kRow = 16 * RC;
+  extern __shared__ __align__(128) uint8_t tile[];  // K rows, then V rows
+  __shared__ MoveShared sm;
+  const int tid = threadIdx.x;
+  const int C = IN_PLACE ? (int)pa::cluster_ctas() : (int)gridDim.x, rank = IN_PLACE ? (int)pa::cluster_rank() : (int)blockIdx.x;
+  const int64_t row = IN_PLACE ? blockIdx.x / C : blockIdx.y;
   const int h = (int)(row % p.Hkv), r = (int)(row / p.Hkv);
-  const int n = new_length(p, r, rank == 0 && h == 0 && threadIdx.x == 0);
+  const int n = new_length(p, r, rank == 0 && h == 0 && tid == 0);
   const int32_t *keep = p.keep + row * p.keep_stride;
-  const int64_t round = (int64_t)C * kTokens;
-  int64_t first = (int64_t)rank * kTokens;
-  const int rounds = (int)((n + round - 1) / round);
-  if (rounds == 0) return;  // the same for the whole cluster
-  Route f, g;
-  Moved a, b;
-  find_tokens<RC, true>(p, keep, r, h, n, first, f);
-  load_tokens<RC>(p, row, f, a);
-  for (int k = 0; k < rounds; k += 2) {
-    pa::cluster_arrive();
-    if (k + 1 < rounds) {
-      find_tokens<RC, true>(p, keep, r, h, n, first + round, g);
-      load_tokens<RC>(p, row, g, b);
+  const uint32_t ks_at = pa::smem_u32(tile), vs_at = ks_at + T * kRow;
+  const int64_t round = (int64_t)C * T;
+  // every CTA of a cluster takes part in every round's barrier
+  for (int64_t start = 0; start < n; start += round) {
+    const int64_t first = start + (int64_t)rank * T, i = first + tid;
+    if (!IN_PLACE && first >= n) return;
+    if (tid == 0) sm.odd = sm.moved = 0;
+    __syncthreads();
+    float kx = 0.f, vx = 0.f, mx = 0.f;
+    int from = -1, to = -1;
+    bool moves = false;
+    if (tid < T && i < n) {
+      const int s = keep[i], prev = i > 0 ? keep[i - 1] : -1;
+      const int dp = p.dt[(int64_t)r * p.dt_stride + (i >> p.ps_shift)];
+      if (s <= prev || s < i || s >> p.ps_shift >= p.bt_stride || (p.mass != nullptr && s >= p.m_stride)) {
+        if (p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_KEEP);
+      } else {
+        const int sp = p.bt[(int64_t)r * p.bt_stride + (s >> p.ps_shift)];
+        if (sp < 0 || sp >= p.num_pages || dp < 0 || dp >= p.num_pages) {
+          if (p.status != nullptr) atomicOr(p.status, PA_DEV_BAD_PAGE);
+        } else {
+          from = ((sp * p.Hkv + h) << p.ps_shift) + (s & (p.ps - 1));
+          to = ((dp * p.Hkv + h) << p.ps_shift) + (int)(i & (p.ps - 1));
+          moves = !IN_PLACE || s != i;
+          if (moves) {
+            if (p.ks != nullptr) {
+              kx = p.ks[from];
+              vx = p.vs[from];
+            }
+            if (p.mass != nullptr) mx = p.mass[row * p.m_stride + s];
+          }
+        }
+      }
+      const unsigned seg = 1u << (tid >> p.ps_shift);
+      if (from < 0) atomicOr(&sm.odd, seg);
+      if (moves) atomicOr(&sm.moved, seg);
     }
-    pa::cluster_wait();
-    store_tokens<RC>(p, row, first, f, a);
-    if (k + 1 >= rounds) break;
-    pa::cluster_arrive();
-    if (k + 2 < rounds) {
-      find_tokens<RC, true>(p, keep, r, h, n, first + 2 * round, f);
-      load_tokens<RC>(p, row, f, a);
+    if (tid < T) sm.from[tid] = from;
+    __syncthreads();
+    const unsigned moved = sm.moved, odd = sm.odd;
+#pragma unroll 4
+    for (int u = tid; u < T * RC; u += kMoveThreads) {
+      const int t = u / RC, c = u % RC, f = sm.from[t];
+      if (f >= 0 && (moved >> (t >> p.ps_shift)) & 1u) {
+        cp_async16(ks_at + 16 * u, p.k + (int64_t)f * kRow + 16 * c);
+        cp_async16(vs_at + 16 * u, p.v + (int64_t)f * kRow + 16 * c);
+      }
     }
-    pa::cluster_wait();
-    store_tokens<RC>(p, row, first + round, g, b);
-    first += 2 * round;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // what was read and copied through the generic proxy comes before the bulk stores
+    asm volatile("fence.proxy.async;" ::: "memory");
+    if (IN_PLACE)
+      pa::cluster_sync();
+    else
+      __syncthreads();
+    if (moves) {
+      if (p.ks != nullptr) {
+        p.ks[to] = kx;
+        p.vs[to] = vx;
+      }
+      if (p.mass != nullptr) p.mass_out[row * p.mo_stride + i] = mx;
+    }
+    // page tid of the round: its rows go out together, or one by one where some must not be written
+    if (tid < T >> p.ps_shift && (moved >> tid) & 1u) {
+      const int64_t slot = first + ((int64_t)tid << p.ps_shift);
+      const int cnt = (int)min((int64_t)p.ps, n - slot);
+      const int dp = p.dt[(int64_t)r * p.dt_stride + (slot >> p.ps_shift)];
+      const int at = tid << p.ps_shift;
+      if (!((odd >> tid) & 1u)) {
+        const int64_t dst = ((int64_t)(dp * p.Hkv + h) << p.ps_shift) * kRow;
+        bulk_store(p.k + dst, ks_at + at * kRow, cnt * kRow);
+        bulk_store(p.v + dst, vs_at + at * kRow, cnt * kRow);
+      } else {
+        for (int t = at; t < at + cnt; ++t) {
+          if (sm.from[t] < 0) continue;
+          const int64_t dst = (((int64_t)(dp * p.Hkv + h) << p.ps_shift) + t - at) * kRow;
+          bulk_store(p.k + dst, ks_at + t * kRow, kRow);
+          bulk_store(p.v + dst, vs_at + t * kRow, kRow);
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    if (!IN_PLACE) return;
+    __syncthreads();  // the tile is free again
   }
 }
 
-// The current device's SM count, and its kernels' shared-memory opt-in, once per device; 0 for a
+bool move_opt_in(void (*kernel)(CompactParams)) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) == cudaSuccess &&
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+}
+
+// The current device's SM count, and its kernels' opt-ins, once per device; 0 for a
 // device beyond those tracked, -1 when a call fails.
 int evict_device() {
   static std::once_flag once[pa_host::kMaxDevices];
@@ -446,10 +428,8 @@ int evict_device() {
     const bool ok = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
                     cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kStageKeys * (int)sizeof(uint32_t)) == cudaSuccess &&
-                    cudaFuncSetAttribute(kv_compact_in_place_kernel<8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                        cudaSuccess &&
-                    cudaFuncSetAttribute(kv_compact_in_place_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                        cudaSuccess;
+                    move_opt_in(kv_compact_kernel<8, true>) && move_opt_in(kv_compact_kernel<16, true>) &&
+                    move_opt_in(kv_compact_kernel<8, false>) && move_opt_in(kv_compact_kernel<16, false>);
     sms[dev] = ok ? n : -1;
   });
   return sms[dev];
@@ -561,36 +541,33 @@ extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream
   p.mo_stride = a->mass_out_stride;
   (void)cudaGetLastError();  // drop an earlier, unrelated launch error
   const bool wide = a->kv_dtype == PA_KV_BF16;
-  const int tokens = kMoveThreads / (wide ? 16 : 8) * kMoveUnroll;
-  const int rows = a->num_seqs * a->num_kv_heads;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int tokens = wide ? move_tokens<16>() : move_tokens<8>();
+  const int64_t rows = (int64_t)a->num_seqs * a->num_kv_heads;
   const int sms = evict_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
-  if (!in_place) {
-    // one wave (three CTAs per SM), or a round per CTA where that is fewer
-    const int64_t wave = (3 * (int64_t)sms + rows - 1) / rows;
-    const int64_t need = ((int64_t)a->keep_stride + tokens - 1) / tokens;
-    const dim3 grid((unsigned)(wave < need ? wave : need), rows);
-    if (wide)
-      kv_compact_kernel<16><<<grid, kMoveThreads, 0, s>>>(p);
-    else
-      kv_compact_kernel<8><<<grid, kMoveThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-  }
-  // CTAs per row: more while all rows' CTAs run at once (two per SM) and there are tokens for them
-  int C = 1;
-  while (C < kMaxMoveCluster && (int64_t)rows * C <= sms && (int64_t)C * tokens < a->keep_stride) C *= 2;
+  const int64_t rounds = ((int64_t)a->keep_stride + tokens - 1) / tokens;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * C);
   cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = s;
+  cfg.dynamicSmemBytes = kMoveBytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
+  if (!in_place) {
+    cfg.gridDim = dim3((unsigned)rounds, (unsigned)rows);
+    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, kv_compact_kernel<16, false>, p)
+                               : cudaLaunchKernelEx(&cfg, kv_compact_kernel<8, false>, p);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  // CTAs per row: more while all rows' CTAs run at once (three per SM, with room for the clusters'
+  // placement: two) and there are rounds for them
+  int C = 1;
+  while (C < kMaxMoveCluster && rows * C <= sms && C < rounds) C *= 2;
+  cfg.gridDim = dim3((unsigned)(rows * C));
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, kv_compact_in_place_kernel<16>, p)
-                             : cudaLaunchKernelEx(&cfg, kv_compact_in_place_kernel<8>, p);
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, kv_compact_kernel<16, true>, p)
+                             : cudaLaunchKernelEx(&cfg, kv_compact_kernel<8, true>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
