@@ -27,37 +27,48 @@ struct SelectParams {
   int32_t Hkv, stride, budget, first, recent;
 };
 
-// Unsigned keys in the order of the masses: NaN lowest, -0 = +0.
+// Unsigned keys in the order of the masses, from 1 (NaN) to that of +inf; -0 = +0.  0 stands for a
+// position that is not a middle one.
 __device__ __forceinline__ uint32_t mass_key(float m) {
-  if (m != m) return 0u;
   const uint32_t u = __float_as_uint(m + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return m != m ? 1u : k;
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
-constexpr int kStageKeys = 49152;  // keys a CTA can hold in shared memory (192 KB)
+constexpr int kMaxCluster = 8;   // 16 measured slower: its barriers cost more than the halved stretches save
+constexpr int kMaxKeys = 32;     // keys a thread can hold
 
-// A cluster of C CTAs per (request, KV head), each with one stretch of the positions.  The masses
-// are read once, as keys into shared memory (rows beyond C * kStageKeys are read again instead).
-// The key T of the last middle token taken is found by counting keys in 2048 bins of the
-// range that still holds it: at first the range of the middle's keys (so the bins are as fine as the
-// data allow, and shared-memory counters rarely collide), then one bin of the step before; three
-// steps narrow 2^32 to a single key.  The CTAs' counts meet through distributed shared memory,
-// one cluster barrier per step.  Then the kept positions are written in order: those above T and
-// the first `need` equal to it, at offsets from the counts of the warps and CTAs before.
+// A cluster of C CTAs per (request, KV head), each with one stretch of the positions, a warp with
+// one stretch of those.  The masses are read once, as keys into registers, KPT per thread; rows
+// beyond C * 512 * 32 positions (KPT 0) are read again instead.  The key T of the last middle token
+// taken is found by counting keys in 2048 bins of the range that still holds it: the top 11 bits,
+// then the 11 bits below them of the keys in one bin, then the last 10.  The CTAs' counts meet
+// through distributed shared memory: each CTA sums its share of the bins, then all read the
+// shares' totals and the one share that matters (8 KB of traffic per CTA and step in place of
+// 64 KB).  A bin that is taken whole ends the search early.  Then the kept positions are written in order: those above T and the
+// first `need` equal to it, at offsets from the counts of the warps and CTAs before.
 struct SelectShared {
   uint32_t hist[2][kBins];
-  uint32_t range[2];             // this CTA's smallest and largest middle key
+  uint32_t part[kBins];          // this CTA's share of the bins, from each CTA of the cluster
+  uint32_t share[kBins];         // and summed: the first kBins / C of these
+  int share_total[2];
   int total[2];                  // this CTA's keys equal to T, and certain ones
-  uint32_t wlo[kSelWarps], whi[kSelWarps];
   int weq[kSelWarps], wsure[kSelWarps], scan[kSelWarps];
   int pick[3];                   // the chosen bin, keys above it, keys in it
 };
 
-// 8 bytes at this shared-memory address in CTA `rank` of the cluster.
+// 16 or 8 bytes at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint4 load_cluster4(const void *p, uint32_t rank) {
+  uint32_t a;
+  uint4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint2 load_cluster(const void *p, uint32_t rank) {
   uint32_t a;
   uint2 v;
@@ -79,9 +90,8 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
 // The number of `eq` equal keys that stay when `before` of them come earlier.
 __device__ __forceinline__ int ties_taken(int need, int before, int eq) { return min(max(need - before, 0), eq); }
 
-template <bool STAGED>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t keys[];
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
   __shared__ __align__(16) SelectShared sm;
   const int C = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
   const int row = blockIdx.x / C, r = row / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -98,123 +108,141 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     for (int64_t i = gid; i < p.budget; i += gsz) keep[i] = i < n ? (int)i : -1;
     return;
   }
-  // this CTA's positions, and of them the middle ones
-  const int S = ((L + C - 1) / C + 31) & ~31;
-  const int begin = (int)min((int64_t)rank * S, (int64_t)L), end = (int)min((int64_t)begin + S, (int64_t)L);
-  const int mlo = max(begin, p.first), mhi = min(end, L - p.recent), want = p.budget - p.first - p.recent;
+  // this warp's positions [wb, we), and of the row the middle ones [mlo, mhi)
+  const int stretch = ((L + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31;
+  const int wb = (int)min((int64_t)(rank * kSelWarps + warp) * stretch, (int64_t)L);
+  const int we = (int)min((int64_t)wb + stretch, (int64_t)L);
+  const int mlo = p.first, mhi = L - p.recent, want = p.budget - p.first - p.recent;
   const float *m = p.mass + (int64_t)row * p.stride;
-  auto key_at = [&](int i) { return STAGED ? keys[i - begin] : mass_key(m[i]); };
+
+  // Position u of a lane is wb + 32 u + lane; the warp's middle ones are [lo, hi).
+  const int lo = max(wb, mlo), hi = min(we, mhi);
+  auto key_of = [&](int i) { return (unsigned)(i - lo) < (unsigned)max(hi - lo, 0) ? mass_key(m[i]) : 0u; };
+  uint32_t key[KPT > 0 ? KPT : 1];
+  if (KPT > 0) {
+    const unsigned count = (unsigned)max(hi - lo, 0);
+    float x[KPT > 0 ? KPT : 1];
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      const int i = wb + 32 * u + lane;
+      x[u] = (unsigned)(i - lo) < count ? m[i] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) key[u] = (unsigned)(wb + 32 * u + lane - lo) < count ? mass_key(x[u]) : 0u;
+  }
+  for (int b = tid; b < kBins; b += kSelThreads) sm.hist[0][b] = 0;
+  __syncthreads();
 
   uint32_t T = 0xFFFFFFFFu;  // with want 0 nothing of the middle stays
   int need = 0;
   if (want > 0) {
-    uint32_t klo = 0xFFFFFFFFu, khi = 0;
-    for (int i0 = mlo + tid; i0 < mhi; i0 += 8 * kSelThreads) {  // eight loads in flight
-      float x[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = i0 + u * kSelThreads < mhi ? m[i0 + u * kSelThreads] : 0.f;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kSelThreads;
-        if (i >= mhi) break;
-        const uint32_t k = mass_key(x[u]);
-        if (STAGED) keys[i - begin] = k;
-        klo = min(klo, k);
-        khi = max(khi, k);
-      }
-    }
-    klo = __reduce_min_sync(~0u, klo);
-    khi = __reduce_max_sync(~0u, khi);
-    if (lane == 0) {
-      sm.wlo[warp] = klo;
-      sm.whi[warp] = khi;
-    }
-    for (int b = tid; b < kBins; b += kSelThreads) sm.hist[0][b] = 0;
-    __syncthreads();
-    if (warp == 0) {
-      klo = __reduce_min_sync(~0u, sm.wlo[lane]);
-      khi = __reduce_max_sync(~0u, sm.whi[lane]);
-      if (lane == 0) {
-        sm.range[0] = klo;
-        sm.range[1] = khi;
-      }
-    }
-    pa::cluster_sync();
-    const uint2 kr = lane < C ? load_cluster(sm.range, lane) : make_uint2(0xFFFFFFFFu, 0u);
-    uint32_t base = __reduce_min_sync(~0u, kr.x);
-    uint32_t span = __reduce_max_sync(~0u, kr.y) - base;  // keys in [base, base + span] are still open
+    // keys in [base, base + span] are still open; 0 never is (the largest key is that of +inf)
+    uint32_t base = 1, span = 0xFFFFFFFEu;
     need = want;
     for (int step = 0;; ++step) {
-      if (span == 0) {  // one key left: it is T, and `need` of its tokens stay
-        T = base;
-        break;
-      }
       uint32_t *hist = sm.hist[step & 1];
-      const int shift = max(0, 21 - __clz(span));  // (span >> shift) < 2048
-      for (int i = mlo + tid; i < mhi; i += kSelThreads) {
-        const uint32_t d = key_at(i) - base;
-        if (d <= span) atomicAdd(hist + (d >> shift), 1u);
+      const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
+      if (KPT > 0) {
+#pragma unroll
+        for (int u = 0; u < KPT; ++u) {
+          const uint32_t d = key[u] - base;
+          if (d <= span) atomicAdd(hist + (d >> shift), 1u);
+        }
+      } else {
+        for (int i = lo + lane; i < hi; i += 32) {
+          const uint32_t d = mass_key(m[i]) - base;
+          if (d <= span) atomicAdd(hist + (d >> shift), 1u);
+        }
       }
       pa::cluster_sync();
-      // bins 2 tid and 2 tid + 1 over the cluster; prefix sums from the top
-      uint2 c = make_uint2(0u, 0u), x[kMaxCluster];
-#pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) x[q] = q < C ? load_cluster(hist + 2 * tid, q) : make_uint2(0u, 0u);
-#pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {
-        c.x += x[q].x;
-        c.y += x[q].y;
-      }
+      // sum this CTA's share: every thread fetches four bins of it from one CTA
+      const int quads = kBins / 4 / C, q = tid / quads, e4 = tid - q * quads;
+      *reinterpret_cast<uint4 *>(sm.part + 4 * tid) = load_cluster4(hist + 4 * (rank * quads + e4), q);
       for (int b = tid; b < kBins; b += kSelThreads) sm.hist[(step + 1) & 1][b] = 0;  // read by all a step ago
-      const int mine = (int)(c.x + c.y), upto = warp_scan(mine, lane);
-      if (lane == 31) sm.scan[warp] = upto;
       __syncthreads();
-      const int w = sm.scan[lane], wincl = warp_scan(w, lane);
-      const int all = __shfl_sync(~0u, wincl, 31), below = __shfl_sync(~0u, wincl - w, warp);
-      const int above1 = all - (below + upto);  // keys in bins above 2 tid + 1
-      const int above0 = above1 + (int)c.y;
-      if (above1 < need && need <= above0) {
-        sm.pick[0] = 2 * tid + 1;
-        sm.pick[1] = above1;
-        sm.pick[2] = (int)c.y;
-      } else if (above0 < need && need <= above0 + (int)c.x) {
-        sm.pick[0] = 2 * tid;
-        sm.pick[1] = above0;
-        sm.pick[2] = (int)c.x;
+      if (tid < quads) {
+        uint4 c = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < C; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(sm.part + 4 * (k * quads + tid));
+          c.x += x.x;
+          c.y += x.y;
+          c.z += x.z;
+          c.w += x.w;
+        }
+        *reinterpret_cast<uint4 *>(sm.share + 4 * tid) = c;
+      }
+      int mine = 0;
+      if (tid < quads) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(sm.share + 4 * tid);
+        mine = (int)(c.x + c.y + c.z + c.w);
+      }
+      mine = __reduce_add_sync(~0u, mine);
+      if (lane == 0) sm.scan[warp] = mine;
+      __syncthreads();
+      if (warp == 0) {
+        const int t = __reduce_add_sync(~0u, lane < kSelWarps ? sm.scan[lane] : 0);
+        if (lane == 0) sm.share_total[0] = t;
+      }
+      pa::cluster_sync();
+      // the share that holds the want-th key from the top, then its bins
+      const int tot = lane < C ? (int)load_cluster(sm.share_total, lane).x : 0, upto = warp_scan(tot, lane);
+      const int over = __shfl_sync(~0u, upto, C - 1) - upto;  // keys in the shares after the lane's
+      // (one lane finds it; none only if the masses change under the call)
+      const int src = max(__ffs(__ballot_sync(~0u, lane < C && over < need && need <= over + tot)) - 1, 0);
+      int above = __shfl_sync(~0u, over, src);
+      uint4 c = make_uint4(0u, 0u, 0u, 0u);
+      if (tid < quads) c = load_cluster4(sm.share + 4 * tid, src);
+      const int four = (int)(c.x + c.y + c.z + c.w), incl = warp_scan(four, lane);
+      __syncthreads();  // sm.scan has been read
+      if (lane == 31) sm.scan[warp] = incl;
+      __syncthreads();
+      const int w = lane < kSelWarps ? sm.scan[lane] : 0, wincl = warp_scan(w, lane);
+      above += __shfl_sync(~0u, wincl, 31) - (__shfl_sync(~0u, wincl - w, warp) + incl);
+      const uint32_t bins[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int e = 3; e >= 0; --e) {
+        if (above < need && need <= above + (int)bins[e]) {
+          sm.pick[0] = 4 * (src * quads + tid) + e;
+          sm.pick[1] = above;
+          sm.pick[2] = (int)bins[e];
+        }
+        above += (int)bins[e];
       }
       __syncthreads();
       base += (uint32_t)sm.pick[0] << shift;
       need -= sm.pick[1];
+      T = base;
+      if (shift == 0) break;  // T is the key, and `need` of its tokens stay
       if (need == sm.pick[2]) {  // the whole bin stays: everything from its lowest key on
-        T = base;
         need = INT_MAX;
         break;
       }
       span = (1u << shift) - 1u;
     }
   }
-  __syncthreads();
 
-  // ---- each warp's stretch: count, then write
-  const int wl = ((end - begin + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int wb = min(begin + warp * wl, end), we = min(wb + wl, end);
-  auto classify = [&](int i, bool &sure, bool &eq) {
-    sure = eq = false;
-    if (i >= we) return;
-    if (i < mlo || i >= mhi) {
-      sure = true;  // not in the middle: one of the first or of the recent
-    } else if (want > 0) {
-      const uint32_t k = key_at(i);
-      sure = k > T;
-      eq = k == T;
-    }
-  };
+  // ---- count, then write.  Bit u of `sure` and `eq`: position u stays; it has key T
+  uint32_t sure = 0, eq = 0;
   int nsure = 0, neq = 0;
-  for (int i = wb + lane; i - lane < we; i += 32) {
-    bool sure, eq;
-    classify(i, sure, eq);
-    nsure += sure;
-    neq += eq;
+  const bool ends = wb < mlo || we > mhi;  // the warp has some of the first or the recent positions
+  auto always = [&](int i) { return i < we && (i < mlo || i >= mhi); };
+  if (KPT > 0) {
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      sure |= (uint32_t)(key[u] > T) << u;
+      eq |= (uint32_t)(key[u] == T) << u;
+    }
+    if (ends)
+#pragma unroll
+      for (int u = 0; u < KPT; ++u) sure |= (uint32_t)always(wb + 32 * u + lane) << u;
+    nsure = __popc(sure);
+    neq = __popc(eq);
+  } else {
+    for (int i = wb + lane; i < we; i += 32) {
+      const uint32_t k = key_of(i);
+      nsure += k > T || always(i);
+      neq += k == T;
+    }
   }
   nsure = __reduce_add_sync(~0u, nsure);
   neq = __reduce_add_sync(~0u, neq);
@@ -224,10 +252,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
   }
   __syncthreads();
   if (warp == 0) {
-    const int e = __reduce_add_sync(~0u, sm.weq[lane]), u = __reduce_add_sync(~0u, sm.wsure[lane]);
+    const int e = __reduce_add_sync(~0u, lane < kSelWarps ? sm.weq[lane] : 0);
+    const int y = __reduce_add_sync(~0u, lane < kSelWarps ? sm.wsure[lane] : 0);
     if (lane == 0) {
       sm.total[0] = e;
-      sm.total[1] = u;
+      sm.total[1] = y;
     }
   }
   pa::cluster_sync();
@@ -238,21 +267,39 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
   const int cstart = warp_scan(ckept, lane) - ckept;
   int before = __shfl_sync(~0u, ceq_before, rank), at = __shfl_sync(~0u, cstart, rank);
   {
-    const int e = sm.weq[lane], eb = before + warp_scan(e, lane) - e;
-    const int kept = sm.wsure[lane] + ties_taken(need, eb, e), start = at + warp_scan(kept, lane) - kept;
+    const int e = lane < kSelWarps ? sm.weq[lane] : 0, eb = before + warp_scan(e, lane) - e;
+    const int kept = (lane < kSelWarps ? sm.wsure[lane] : 0) + ties_taken(need, eb, e);
+    const int start = at + warp_scan(kept, lane) - kept;
     before = __shfl_sync(~0u, eb, warp);
     at = __shfl_sync(~0u, start, warp);
   }
   const unsigned lt = (1u << lane) - 1u;
-  for (int i = wb + lane; i - lane < we; i += 32) {
-    bool sure, eq;
-    classify(i, sure, eq);
-    const unsigned eqs = __ballot_sync(~0u, eq);
-    const bool stays = sure || (eq && before + __popc(eqs & lt) < need);
+  auto emit = [&](int i, bool is_sure, bool is_eq) {
+    const unsigned eqs = __ballot_sync(~0u, is_eq);
+    const bool stays = is_sure || (is_eq && before + __popc(eqs & lt) < need);
     const unsigned st = __ballot_sync(~0u, stays);
-    if (stays) keep[at + __popc(st & lt)] = i;
+    if (stays && at + __popc(st & lt) < p.budget) keep[at + __popc(st & lt)] = i;
     at += __popc(st);
     before += __popc(eqs);
+  };
+  if (KPT > 0) {
+    if (before >= need || neq <= need - before) {  // none or all of the warp's equal keys stay: no ranks to count
+      const uint32_t stays = before >= need ? sure : sure | eq;
+#pragma unroll
+      for (int u = 0; u < KPT; ++u) {
+        const unsigned st = __ballot_sync(~0u, (stays >> u) & 1u);
+        if ((stays >> u) & 1u) keep[at + __popc(st & lt)] = wb + 32 * u + lane;
+        at += __popc(st);
+      }
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < KPT; ++u) emit(wb + 32 * u + lane, (sure >> u) & 1u, (eq >> u) & 1u);
+    }
+  } else {
+    for (int i0 = wb; i0 < we; i0 += 32) {
+      const uint32_t k = key_of(i0 + lane);
+      emit(i0 + lane, k > T || always(i0 + lane), k == T);
+    }
   }
   pa::cluster_wait();
 }
@@ -426,8 +473,6 @@ int evict_device() {
   std::call_once(once[dev], [dev]() {
     int n = 0;
     const bool ok = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-                    cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kStageKeys * (int)sizeof(uint32_t)) == cudaSuccess &&
                     move_opt_in(kv_compact_kernel<8, true>) && move_opt_in(kv_compact_kernel<16, true>) &&
                     move_opt_in(kv_compact_kernel<8, false>) && move_opt_in(kv_compact_kernel<16, false>);
     sms[dev] = ok ? n : -1;
@@ -466,19 +511,19 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   (void)cudaGetLastError();  // drop an earlier, unrelated launch error
   const int sms = evict_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
-  // CTAs per row: more while each keeps 2048 positions and all run at once (one per SM), or
-  // while a row's keys do not fit their shared memory
+  // CTAs per row: more while each keeps 2048 positions and all run at once (two per SM), or
+  // while a row's keys do not fit their registers
   const int64_t rows = (int64_t)a->num_seqs * a->num_kv_heads;
   int C = 1;
   while (C < kMaxCluster && a->mass_stride / (2 * C) >= 2048 &&
-         (rows * 2 * C <= sms || a->mass_stride > (int64_t)C * kStageKeys))
+         (rows * 2 * C <= 2 * sms || a->mass_stride > (int64_t)C * kSelThreads * kMaxKeys))
     C *= 2;
-  const int64_t stretch = ((((int64_t)a->mass_stride + C - 1) / C) + 31) & ~(int64_t)31;
-  const bool staged = stretch <= kStageKeys;
+  // the keys a warp's stretch of the longest row gives each lane
+  const int64_t warps = (int64_t)C * kSelWarps;
+  const int64_t keys = (((int64_t)a->mass_stride + warps - 1) / warps + 31) / 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = staged ? (size_t)stretch * sizeof(uint32_t) : 0;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -486,8 +531,10 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = staged ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p)
-                               : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+  const cudaError_t e = keys <= 4          ? cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, p)
+                        : keys <= 16       ? cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, p)
+                        : keys <= kMaxKeys ? cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys>, p)
+                                           : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
