@@ -102,12 +102,25 @@ struct Vec<uint16_t> {
     const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
     return (e & 1) ? pa::bf16hi(w) : pa::bf16lo(w);
   }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // the largest element (NaN only if all are)
+  static __device__ __forceinline__ float max(const uint4 &v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(pa::bf16lo(m), pa::bf16hi(m));
+  }
 };
 template <>
 struct Vec<float> {
   static constexpr int E = 4;
   static __device__ __forceinline__ float get(const uint4 &v, int e) {
     return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ float max(const uint4 &v) {
+    return fmaxf(fmaxf(get(v, 0), get(v, 1)), fmaxf(get(v, 2), get(v, 3)));
   }
 };
 
@@ -190,40 +203,55 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   const int lo = (int)((int64_t)r.nv * part / p.parts), hi = (int)((int64_t)r.nv * (part + 1) / p.parts);
 
   // ---- one pass: maximum, sum of 2^((x - m) log2 e), and the vector of the maximum
-  float m = -INFINITY, s = 0.f;
+  float m = -INFINITY;
   int best = lo + tid;
   uint4 bv = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-  bool nan = false;
-  for (int j0 = lo + tid; j0 < hi; j0 += kUnroll * kBeamThreads) {
+  pa::f32x2 sum = pa::pack2(0.f, 0.f), minus_m = sum;
+  const pa::f32x2 log2e = pa::pack2(kLog2e, kLog2e);
+  auto take = [&](const uint4 &v, int j) {
+    const float mx = Vec<T>::max(v);
+    if (mx > m) {
+      const float f = pa::fast_exp2((m - mx) * kLog2e);
+      sum = pa::mul2(sum, pa::pack2(f, f));
+      minus_m = pa::pack2(-mx, -mx);
+      m = mx;
+      bv = v;
+      best = j;
+    }
+    // the difference first: exact near the maximum, and in range at the types' lowest values
+    // (while m is still -inf, -inf - 0 gives 0)
+    pa::f32x2 t[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      float a, b;
+      pa::unpack2(pa::mul2(pa::add2(pa::pack2(Vec<T>::get(v, 2 * e), Vec<T>::get(v, 2 * e + 1)), minus_m), log2e), a, b);
+      t[e] = pa::pack2(pa::fast_exp2(a), pa::fast_exp2(b));
+    }
+#pragma unroll
+    for (int n = E / 4; n >= 1; n >>= 1)
+#pragma unroll
+      for (int e = 0; e < n; ++e) t[e] = pa::add2(t[e], t[e + n]);
+    sum = pa::add2(sum, t[0]);
+  };
+  int j = lo + tid;
+  if (j == 0 && r.e0 > 0 && j < hi) {  // a ragged beginning
+    take(r.load(0), 0);
+    j += kBeamThreads;
+  }
+  const int whole = min(hi, (r.e0 + p.V) / E);  // the vectors before it end within the row
+  for (; j + (kUnroll - 1) * kBeamThreads < whole; j += kUnroll * kBeamThreads) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(r.x + r.first(j));
     uint4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (j0 + u * kBeamThreads < hi) v[u] = r.load(j0 + u * kBeamThreads);
+    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(src + u * kBeamThreads);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (j0 + u * kBeamThreads >= hi) break;
-      float mx = Vec<T>::get(v[u], 0);
-#pragma unroll
-      for (int e = 1; e < E; ++e) mx = fmaxf(mx, Vec<T>::get(v[u], e));
-      if (mx > m) {
-        s *= pa::fast_exp2((m - mx) * kLog2e);
-        m = mx;
-        bv = v[u];
-        best = j0 + u * kBeamThreads;
-      }
-      // the difference first: exact near the maximum, and in range at the types' lowest values
-      const float ref = m == -INFINITY ? 0.f : m;
-      float t[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = pa::fast_exp2((Vec<T>::get(v[u], e) - ref) * kLog2e);
-#pragma unroll
-      for (int n = E / 2; n >= 1; n >>= 1)
-#pragma unroll
-        for (int e = 0; e < n; ++e) t[e] += t[e + n];
-      s += t[0];
-    }
+    for (int u = 0; u < kUnroll; ++u) take(v[u], j + u * kBeamThreads);
   }
-  nan = s != s;  // a NaN or +inf among the elements
+  for (; j < hi; j += kBeamThreads) take(r.load(j), j);
+  float s, s1;
+  pa::unpack2(sum, s, s1);
+  s += s1;
+  const bool nan = s != s;  // a NaN or +inf among the elements
   u64 key = 0;
   if (lo + tid < hi) {
     int at = max(r.first(lo + tid), 0);  // nothing above -inf: the first element

@@ -155,43 +155,47 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
         }
       }
       pa::cluster_sync();
-      // sum this CTA's share: every thread fetches four bins of it from one CTA
-      const int quads = kBins / 4 / C, q = tid / quads, e4 = tid - q * quads;
-      *reinterpret_cast<uint4 *>(sm.part + 4 * tid) = load_cluster4(hist + 4 * (rank * quads + e4), q);
+      const int quads = kBins / 4 / C;
       for (int b = tid; b < kBins; b += kSelThreads) sm.hist[(step + 1) & 1][b] = 0;  // read by all a step ago
-      __syncthreads();
-      if (tid < quads) {
-        uint4 c = make_uint4(0u, 0u, 0u, 0u);
-        for (int k = 0; k < C; ++k) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(sm.part + 4 * (k * quads + tid));
-          c.x += x.x;
-          c.y += x.y;
-          c.z += x.z;
-          c.w += x.w;
+      int src = 0, above = 0;
+      if (C > 1) {
+        // sum this CTA's share: every thread fetches four bins of it from one CTA
+        const int q = tid / quads, e4 = tid - q * quads;
+        *reinterpret_cast<uint4 *>(sm.part + 4 * tid) = load_cluster4(hist + 4 * (rank * quads + e4), q);
+        __syncthreads();
+        if (tid < quads) {
+          uint4 c = make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < C; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(sm.part + 4 * (k * quads + tid));
+            c.x += x.x;
+            c.y += x.y;
+            c.z += x.z;
+            c.w += x.w;
+          }
+          *reinterpret_cast<uint4 *>(sm.share + 4 * tid) = c;
         }
-        *reinterpret_cast<uint4 *>(sm.share + 4 * tid) = c;
+        int mine = 0;
+        if (tid < quads) {
+          const uint4 c = *reinterpret_cast<const uint4 *>(sm.share + 4 * tid);
+          mine = (int)(c.x + c.y + c.z + c.w);
+        }
+        mine = __reduce_add_sync(~0u, mine);
+        if (lane == 0) sm.scan[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+          const int t = __reduce_add_sync(~0u, lane < kSelWarps ? sm.scan[lane] : 0);
+          if (lane == 0) sm.share_total[0] = t;
+        }
+        pa::cluster_sync();
+        // the share that holds the want-th key from the top, then its bins
+        const int tot = lane < C ? (int)load_cluster(sm.share_total, lane).x : 0, upto = warp_scan(tot, lane);
+        const int over = __shfl_sync(~0u, upto, C - 1) - upto;  // keys in the shares after the lane's
+        // (one lane finds it; none only if the masses change under the call)
+        src = max(__ffs(__ballot_sync(~0u, lane < C && over < need && need <= over + tot)) - 1, 0);
+        above = __shfl_sync(~0u, over, src);
       }
-      int mine = 0;
-      if (tid < quads) {
-        const uint4 c = *reinterpret_cast<const uint4 *>(sm.share + 4 * tid);
-        mine = (int)(c.x + c.y + c.z + c.w);
-      }
-      mine = __reduce_add_sync(~0u, mine);
-      if (lane == 0) sm.scan[warp] = mine;
-      __syncthreads();
-      if (warp == 0) {
-        const int t = __reduce_add_sync(~0u, lane < kSelWarps ? sm.scan[lane] : 0);
-        if (lane == 0) sm.share_total[0] = t;
-      }
-      pa::cluster_sync();
-      // the share that holds the want-th key from the top, then its bins
-      const int tot = lane < C ? (int)load_cluster(sm.share_total, lane).x : 0, upto = warp_scan(tot, lane);
-      const int over = __shfl_sync(~0u, upto, C - 1) - upto;  // keys in the shares after the lane's
-      // (one lane finds it; none only if the masses change under the call)
-      const int src = max(__ffs(__ballot_sync(~0u, lane < C && over < need && need <= over + tot)) - 1, 0);
-      int above = __shfl_sync(~0u, over, src);
       uint4 c = make_uint4(0u, 0u, 0u, 0u);
-      if (tid < quads) c = load_cluster4(sm.share + 4 * tid, src);
+      if (tid < quads) c = C > 1 ? load_cluster4(sm.share + 4 * tid, src) : *reinterpret_cast<const uint4 *>(hist + 4 * tid);
       const int four = (int)(c.x + c.y + c.z + c.w), incl = warp_scan(four, lane);
       __syncthreads();  // sm.scan has been read
       if (lane == 31) sm.scan[warp] = incl;
