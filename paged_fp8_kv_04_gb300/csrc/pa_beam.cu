@@ -160,13 +160,57 @@ constexpr int kMaxLists = kMaxBeams;  // rows * parts <= 32
 
 struct BeamShared {
   u64 buf[kBeamWarps][32];
-  u64 list[kMaxLists][kMaxBeams];  // the first CTA's: each (row, part)'s best, descending
-  long long sum[kMaxLists];        // sum of exp(x - m) in units of 2^-36, or -1: NaN
-  float max[kMaxLists];
   long long wsum[kBeamWarps];
-  double lse[kMaxBeams];
-  double norm[kMaxBeams];          // max(new length, 1) ^ length_penalty
+  // the first CTA's
+  u64 list[kMaxLists][kMaxBeams];   // each (row, part)'s best, descending; then each row's
+  long long sum[kMaxLists];         // sum of exp(x - m) in units of 2^-36, or -1: NaN
+  float max[kMaxLists];
+  double part[kMaxLists];           // that sum relative to the row's maximum
+  double lse[kMaxBeams], norm[kMaxBeams];  // norm: max(new length, 1) ^ length_penalty
+  u64 rank[kMaxBeams][kMaxBeams];   // of each beam's candidates, descending; 0: none
+  float total[kMaxBeams][kMaxBeams];
+  int token[kMaxBeams][kMaxBeams];
 };
+
+// The few logarithms and powers of a step in fp64, which this GPU computes slowly: short
+// evaluations in place of the general functions (whose pow alone took 7 us here).
+// e^x by its Taylor polynomial of degree 12, for |x| <= 0.36: within 3e-16 of e^x, relative.
+__device__ __forceinline__ double exp_small(double x) {
+  double r = 1.0 / 479001600.0;
+  r = fma(r, x, 1.0 / 39916800.0);
+  r = fma(r, x, 1.0 / 3628800.0);
+  r = fma(r, x, 1.0 / 362880.0);
+  r = fma(r, x, 1.0 / 40320.0);
+  r = fma(r, x, 1.0 / 5040.0);
+  r = fma(r, x, 1.0 / 720.0);
+  r = fma(r, x, 1.0 / 120.0);
+  r = fma(r, x, 1.0 / 24.0);
+  r = fma(r, x, 1.0 / 6.0);
+  r = fma(r, x, 0.5);
+  r = fma(r, x, 1.0);
+  return fma(r, x, 1.0);
+}
+constexpr double kLn2 = 0.69314718055994530942;
+// e^x: x = k ln 2 + t, |t| <= ln 2 / 2; 0 below -700 and +inf above 700.
+__device__ __forceinline__ double exp64(double x) {
+  if (!(x > -700.0)) return 0.0;
+  if (x > 700.0) return INFINITY;
+  const int k = __float2int_rn((float)x * kLog2e);
+  return exp_small(fma(-(double)k, kLn2, x)) * __longlong_as_double((long long)(k + 1023) << 52);
+}
+// ln s for a normal s > 0: with s = 2^e f, f in [1/sqrt 2, sqrt 2], one Newton step from the fp32
+// logarithm l of f: ln f = l + ln(f e^-l), and f e^-l is within 1e-6 of 1.
+__device__ __forceinline__ double ln64(double s) {
+  const long long b = __double_as_longlong(s);
+  int e = (int)((b >> 52) & 2047) - 1023;
+  double f = __longlong_as_double((b & 0xFFFFFFFFFFFFFll) | (1023ll << 52));
+  if (f > 1.4142135623730951) {
+    f *= 0.5;
+    ++e;
+  }
+  const double l = (double)logf((float)f), r = fma(f, exp_small(-l), -1.0);
+  return fma((double)e, kLn2, l + r * fma(-0.5, r, 1.0));
+}
 
 // This shared-memory address in the cluster's first CTA.
 __device__ __forceinline__ uint32_t in_first_cta(const void *p) {
@@ -347,15 +391,6 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
   const int n = blockIdx.x / C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t base = (int64_t)n * p.W, me = base + lane;
   const bool mine = lane < p.W;
-  bool done = false;
-  int len = 0;
-  if (rank == 0 && warp == 0) {
-    // lane b: beam b's length and its power, while the others' loads are on their way
-    done = mine && p.finished != nullptr && p.finished[me] != 0;
-    len = mine && p.lengths != nullptr ? p.lengths[me] : 0;
-    if (!done && len < INT_MAX) ++len;
-    sm.norm[lane] = p.penalty == 0.f ? 1.0 : pow((double)max(len, 1), (double)p.penalty);
-  }
   const int units = p.W * p.parts;
   bool waited = false;
   for (int u = rank; u < units; u += C) {
@@ -367,72 +402,94 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
   if (rank != 0) return;
   pa::cluster_wait();
 
-  // ---- the first CTA: a warp joins the parts of a row
-  for (int b = warp; b < p.W; b += kBeamWarps) {
-    const int s0 = b * p.parts;
-    u64 k = sm.list[s0][lane];
-    for (int q = 1; q < p.parts; ++q) k = merge32(k, sm.list[s0 + q][31 - lane], lane);
-    const float m = lane < p.parts ? sm.max[s0 + lane] : -INFINITY;
-    const long long t = lane < p.parts ? sm.sum[s0 + lane] : 0;
-    float M = m;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    double sum = (double)t * (1.0 / 68719476736.0);
-    if (p.parts > 1) {
-      sum = m == -INFINITY ? 0.0 : sum * exp((double)m - (double)M);
-#pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  // ---- the first CTA.  Lane u < units of warp 0: its part's sum relative to the row's maximum; then
+  // lane b: beam b's lse and the power of its length.  The other warps join the rows' lists meanwhile.
+  const float cum = mine ? p.scores[me] : -INFINITY;
+  const bool done = mine && p.finished != nullptr && p.finished[me] != 0;
+  int len = mine && p.lengths != nullptr ? p.lengths[me] : 0;
+  if (!done && len < INT_MAX) ++len;
+  if (warp == 0) {
+    if (lane < units) {
+      const int s0 = lane / p.parts * p.parts;
+      float M = sm.max[s0];
+      for (int q = 1; q < p.parts; ++q) M = fmaxf(M, sm.max[s0 + q]);
+      const long long t = sm.sum[lane];
+      const double x = (double)t * (1.0 / 68719476736.0);
+      sm.part[lane] = t < 0 ? (double)NAN : sm.max[lane] == M ? x : x * exp64((double)sm.max[lane] - (double)M);
     }
-    const bool bad = __any_sync(~0u, t < 0);
     __syncwarp();
-    if (lane == 0) sm.lse[b] = bad ? (double)NAN : (double)M + log(sum);
-    sm.list[s0][lane] = k;
+    if (mine) {
+      double sum = 0.0;
+      float M = -INFINITY;
+      for (int q = 0; q < p.parts; ++q) {
+        sum += sm.part[lane * p.parts + q];
+        M = fmaxf(M, sm.max[lane * p.parts + q]);
+      }
+      // a sum that is NaN or 0 (nothing above -inf) has no logarithm
+      sm.lse[lane] = sum > 0.0 ? (double)M + ln64(sum) : (double)NAN;
+      sm.norm[lane] = p.penalty == 0.f ? 1.0 : exp64((double)p.penalty * ln64((double)max(len, 1)));
+    }
+  } else if (p.parts > 1) {
+    for (int b = warp - 1; b < p.W; b += kBeamWarps - 1) {
+      u64 k = sm.list[b * p.parts][lane];
+      for (int q = 1; q < p.parts; ++q) k = merge32(k, sm.list[b * p.parts + q][31 - lane], lane);
+      sm.list[b * p.parts][lane] = k;
+    }
+  }
+  __syncthreads();
+  // every (beam, place) candidate's token, total and rank: a warp per beam, a lane per place
+  for (int b = warp; b < p.W; b += kBeamWarps) {
+    const float c = __shfl_sync(~0u, cum, b);
+    const bool ended = __shfl_sync(~0u, (int)done, b) != 0;
+    const double lse = sm.lse[b];
+    // no continuation at a number: every candidate counts as -inf
+    const bool dead = c != c || c == -INFINITY || (!ended && !(fabs(lse) < INFINITY));
+    int tok = lane;
+    double total = -INFINITY;
+    if (!dead && ended) {
+      tok = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
+      if (lane == 0) total = (double)c;
+    } else if (!dead) {
+      const u64 k = sm.list[b * p.parts][lane];
+      tok = key_index(k);
+      total = (double)c + ((double)key_value(k) - lse);
+      if (total != total) total = -INFINITY;
+    }
+    if (p.penalty != 0.f && total > -INFINITY) total /= sm.norm[b];
+    sm.rank[b][lane] = lane < p.W && lane < p.V ? rank_key(total) : 0ull;
+    if (p.penalty != 0.f && total > -INFINITY)  // the total itself again
+      total = ended ? (double)c : (double)c + ((double)key_value(sm.list[b * p.parts][lane]) - lse);
+    sm.total[b][lane] = (float)total;
+    sm.token[b][lane] = tok;
   }
   __syncthreads();
   if (warp != 0) return;
-  // Lane b walks beam b's candidates in order: `at` counts those taken.
-  const float cum = mine ? p.scores[me] : -INFINITY;
-  const double lse = mine ? sm.lse[lane] : 0.0, norm = sm.norm[lane];
-  const u64 *list = sm.list[mine ? lane * p.parts : 0];
-  // no continuation at a number: every candidate counts as -inf
-  const bool dead = mine && (cum != cum || cum == -INFINITY || (!done && !(fabs(lse) < INFINITY)));
-  int at = 0, tok = -1;
-  double total = -INFINITY;
-  u64 key = 0;
-  auto next = [&]() {
-    key = 0;
-    total = -INFINITY;
-    if (!mine || at >= p.V) return;
-    if (dead) {
-      tok = at;
-    } else if (done) {
-      tok = at == 0 ? p.eos : (at <= p.eos ? at - 1 : at);
-      if (at == 0) total = (double)cum;
-    } else {
-      tok = key_index(list[at]);
-      total = (double)cum + ((double)key_value(list[at]) - lse);
-      if (total != total) total = -INFINITY;
-    }
-    key = rank_key(p.penalty == 0.f ? total : total / norm);
-  };
-  next();
+  // lane b walks beam b's candidates; lane j keeps the j-th best of all
+  u64 key = mine ? sm.rank[lane][0] : 0ull;
+  int at = 0, from = 0, place = 0;
   for (int j = 0; j < p.W; ++j) {
-    u64 top = key;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const u64 y = __shfl_xor_sync(~0u, top, o);
-      top = top > y ? top : y;
+    const uint32_t hi = (uint32_t)(key >> 32), top = __reduce_max_sync(~0u, hi);
+    const uint32_t lo = hi == top ? (uint32_t)key : 0u, low = __reduce_max_sync(~0u, lo);
+    const int win = __ffs(__ballot_sync(~0u, hi == top && lo == low && key != 0)) - 1;  // equal ranks: the lower beam
+    const int p_win = __shfl_sync(~0u, at, max(win, 0));
+    if (lane == j) {
+      from = max(win, 0);
+      place = p_win;
     }
-    const int win = __ffs(__ballot_sync(~0u, key == top)) - 1;  // equal ranks: the lower beam
     if (lane == win) {
-      p.tokens[base + j] = tok;
-      p.parents[base + j] = lane;
-      p.scores_out[base + j] = (float)total;
-      if (p.finished_out != nullptr) p.finished_out[base + j] = done || (p.eos >= 0 && tok == p.eos);
-      if (p.lengths_out != nullptr) p.lengths_out[base + j] = len;
       ++at;
-      if (at < p.W) next();
+      key = at < p.W ? sm.rank[lane][at] : 0ull;
     }
+  }
+  const bool from_done = __shfl_sync(~0u, (int)done, from) != 0;
+  const int from_len = __shfl_sync(~0u, len, from);
+  if (mine) {
+    const int tok = sm.token[from][place];
+    p.tokens[me] = tok;
+    p.parents[me] = from;
+    p.scores_out[me] = sm.total[from][place];
+    if (p.finished_out != nullptr) p.finished_out[me] = from_done || (p.eos >= 0 && tok == p.eos);
+    if (p.lengths_out != nullptr) p.lengths_out[me] = from_len;
   }
 }
 
