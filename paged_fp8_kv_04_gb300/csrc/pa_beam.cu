@@ -28,8 +28,8 @@ constexpr int kMaxReqs = 65535;
 // running maximum and sum of exponentials of its elements, and the vector its maximum came from.
 //   lse = m + log sum exp(x - m),  total = score + (x - lse).
 // Within a row the order of the totals is the order of the logits, so the W best of a part are
-// found without its lse: of the threads' best elements the W-th, tau, bounds them from below, and
-// elements at or above tau lie with the at most W threads whose best does.  Only those threads'
+// found without its lse: of the half warps' best elements the W-th, tau, bounds them from below, and
+// elements at or above tau lie with the few threads whose best does.  Only those threads'
 // elements are looked at again (from L2), whatever the values: keys are (value, index) pairs,
 // all different.  Every CTA leaves its list, maximum and sum in the shared memory of the
 // cluster's first CTA, one cluster barrier follows, and a warp there joins parts and beams.
@@ -160,35 +160,31 @@ constexpr int kMaxLists = kMaxBeams;  // rows * parts <= 32
 
 struct BeamShared {
   u64 buf[kBeamWarps][32];
+  u64 half[32];                     // the best element of each half warp
+  u64 cand[32];                     // the part's elements at or above tau, in any order
+  int owners, cands;
   long long wsum[kBeamWarps];
   // the first CTA's
   u64 list[kMaxLists][kMaxBeams];   // each (row, part)'s best, descending; then each row's
   long long sum[kMaxLists];         // sum of exp(x - m) in units of 2^-36, or -1: NaN
   float max[kMaxLists];
   double part[kMaxLists];           // that sum relative to the row's maximum
-  double lse[kMaxBeams], norm[kMaxBeams];  // norm: max(new length, 1) ^ length_penalty
+  double lse[kMaxBeams], inv[kMaxBeams];  // inv: max(new length, 1) ^ -length_penalty
   u64 rank[kMaxBeams][kMaxBeams];   // of each beam's candidates, descending; 0: none
   float total[kMaxBeams][kMaxBeams];
   int token[kMaxBeams][kMaxBeams];
 };
 
-// The few logarithms and powers of a step in fp64, which this GPU computes slowly: short
-// evaluations in place of the general functions (whose pow alone took 7 us here).
-// e^x by its Taylor polynomial of degree 12, for |x| <= 0.36: within 3e-16 of e^x, relative.
+// The few logarithms and powers of a step in fp64, which this GPU computes slowly (some 70 cycles for
+// each dependent operation): short evaluations in place of the general functions, whose pow
+// alone took 7 us here.  They are far more exact than the sums of exponentials they are taken of.
+// e^x by its Taylor polynomial of degree 9, in pairs (Estrin), for |x| <= 0.36: the next term is
+// 0.36^10 / 10! = 1e-11.
 __device__ __forceinline__ double exp_small(double x) {
-  double r = 1.0 / 479001600.0;
-  r = fma(r, x, 1.0 / 39916800.0);
-  r = fma(r, x, 1.0 / 3628800.0);
-  r = fma(r, x, 1.0 / 362880.0);
-  r = fma(r, x, 1.0 / 40320.0);
-  r = fma(r, x, 1.0 / 5040.0);
-  r = fma(r, x, 1.0 / 720.0);
-  r = fma(r, x, 1.0 / 120.0);
-  r = fma(r, x, 1.0 / 24.0);
-  r = fma(r, x, 1.0 / 6.0);
-  r = fma(r, x, 0.5);
-  r = fma(r, x, 1.0);
-  return fma(r, x, 1.0);
+  const double x2 = x * x, x4 = x2 * x2;
+  const double a = 1.0 + x, b = fma(x, 1.0 / 6.0, 0.5), c = fma(x, 1.0 / 120.0, 1.0 / 24.0);
+  const double d = fma(x, 1.0 / 5040.0, 1.0 / 720.0), e = fma(x, 1.0 / 362880.0, 1.0 / 40320.0);
+  return fma(x4, fma(x4, e, fma(x2, d, c)), fma(x2, b, a));
 }
 constexpr double kLn2 = 0.69314718055994530942;
 // e^x: x = k ln 2 + t, |t| <= ln 2 / 2; 0 below -700 and +inf above 700.
@@ -312,13 +308,25 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
     key = pair_key(m, at);
   }
 
-  // ---- the W-th of the threads' best elements
-  __syncthreads();  // the buffers' readers of an earlier part are done
-  u64 k = join_warps(sort32(key, lane), sm, warp, lane, kBeamWarps);
+  // ---- tau: the W-th best of the half warps' best elements, so at least W elements reach it
+  u64 k = key;
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) {
+    const u64 y = __shfl_xor_sync(~0u, k, o);
+    k = k > y ? k : y;
+  }
+  __syncthreads();  // an earlier part's readers are done
+  if ((lane & 15) == 0) sm.half[tid >> 4] = k;
+  if (tid == 0) sm.owners = sm.cands = 0;
+  __syncthreads();
+  k = sort32(sm.half[lane], lane);
+  const u64 tau = __shfl_sync(~0u, k, p.W - 1);
+  const float top = key_value(__shfl_sync(~0u, k, 0));
+  // the threads whose best reaches it
+  u64 *owners = &sm.buf[0][0];
+  if (key >= tau && key != 0) owners[atomicAdd(&sm.owners, 1)] = key;
   // the part's sum: every thread's relative to the part's maximum, in fixed point (2^-36), so that
   // joining 512 of them loses nothing
-  __syncthreads();
-  const float top = key_value(sm.buf[0][0]);
   const float scaled = m == -INFINITY ? 0.f : s * pa::fast_exp2((m - top) * kLog2e);
   long long fixed = nan ? 0 : __float2ll_rn(scaled * 68719476736.f);
 #pragma unroll
@@ -326,50 +334,70 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   const bool wnan = __any_sync(~0u, nan);
   if (lane == 0) sm.wsum[warp] = wnan ? -1 : fixed;
 
-  // ---- the elements at or above tau, from the threads whose best is one of the W: a warp for each
-  const u64 tau = sm.buf[0][p.W - 1];
-  u64 mine = 0;
-  for (int i = warp; i < p.W; i += kBeamWarps) {
-    const u64 owner = sm.buf[0][i];
-    if (owner == 0) break;
-    const int oj = (key_index(owner) + r.e0) / E;
-    for (int j0 = lo + (oj - lo) % kBeamThreads; j0 < hi; j0 += 32 * kBeamThreads) {
-      const int64_t j = (int64_t)j0 + (int64_t)lane * kBeamThreads;
-      uint4 v;
-      if (j < hi) v = r.load((int)j);
-      unsigned left = 0;  // this lane's elements at or above tau
+  __syncthreads();
+
+  // ---- the elements at or above tau, all of them with those threads: a warp looks through the vectors
+  // of one, a lane per vector
+  const int nowners = sm.owners;
+  auto search = [&](auto &&found) {
+    for (int i = warp; i < nowners; i += kBeamWarps) {
+      const int oj = (key_index(owners[i]) + r.e0) / E;
+      for (int j0 = lo + (oj - lo) % kBeamThreads; j0 < hi; j0 += 32 * kBeamThreads) {
+        const int64_t jl = (int64_t)j0 + (int64_t)lane * kBeamThreads;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        unsigned left = 0;  // this lane's elements at or above tau
+        if (jl < hi) {
+          v = r.load((int)jl);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int at = r.first((int)j) + e;
-        if (j < hi && at >= 0 && at < p.V && pair_key(Vec<T>::get(v, e), at) >= tau) left |= 1u << e;
+          for (int e = 0; e < E; ++e) {
+            const int at = r.first((int)jl) + e;
+            if (at >= 0 && at < p.V && pair_key(Vec<T>::get(v, e), at) >= tau) left |= 1u << e;
+          }
+        }
+        found(v, (int)jl, left);
       }
+    }
+  };
+  auto element = [&](const uint4 &v, int jl, unsigned left) {  // the key of the first of `left`
+    const int e = __ffs(left) - 1;
+    float x = 0.f;
+#pragma unroll
+    for (int q = 0; q < E; ++q)
+      if (q == e) x = Vec<T>::get(v, q);
+    return pair_key(x, r.first(jl) + e);
+  };
+  search([&](const uint4 &v, int jl, unsigned left) {
+    for (; left != 0; left &= left - 1) {
+      const int at = atomicAdd(&sm.cands, 1);
+      if (at < 32) sm.cand[at] = element(v, jl, left);
+    }
+  });
+  if (wait) pa::cluster_wait();  // the first CTA runs: its shared memory can be written
+  __syncthreads();
+  if (sm.cands <= 32) {  // as a rule: not many more than W
+    if (warp == 0) k = sort32(lane < sm.cands ? sm.cand[lane] : 0ull, lane);
+  } else {
+    // many (long runs of equal or rising values): each warp keeps its best 32 in order, then they are joined
+    u64 mine = 0;
+    search([&](const uint4 &v, int jl, unsigned left) {
       while (__any_sync(~0u, left != 0)) {
-        const unsigned who = __ballot_sync(~0u, left != 0);
-        const int src = __ffs(who) - 1;
+        const int src = __ffs(__ballot_sync(~0u, left != 0)) - 1;
         u64 c = 0;
         if (lane == src) {
-          const int e = __ffs(left) - 1;
+          c = element(v, jl, left);
           left &= left - 1;
-          float x = 0.f;
-#pragma unroll
-          for (int q = 0; q < E; ++q)
-            if (q == e) x = Vec<T>::get(v, q);
-          c = pair_key(x, r.first((int)j) + e);
         }
         c = __shfl_sync(~0u, c, src);
-        // insert: lanes above it keep theirs, the others shift down by one
+        // lanes above it keep theirs, the others shift down by one
         const int pos = __popc(__ballot_sync(~0u, mine > c));
         const u64 up = __shfl_up_sync(~0u, mine, 1);
         if (lane == pos) mine = c;
         if (lane > pos) mine = up;
       }
-    }
+    });
+    __syncthreads();  // the owners have been read
+    k = join_warps(mine, sm, warp, lane, kBeamWarps);
   }
-  if (wait) pa::cluster_wait();  // the first CTA runs: its shared memory can be written
-  __syncthreads();
-  int lists = 1;
-  while (lists < kBeamWarps && lists < p.W) lists <<= 1;
-  k = join_warps(mine, sm, warp, lane, lists);
   if (warp == 0) {
     long long t = lane < kBeamWarps ? sm.wsum[lane] : 0;
     const bool bad = __any_sync(~0u, t < 0);
@@ -391,6 +419,11 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
   const int n = blockIdx.x / C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t base = (int64_t)n * p.W, me = base + lane;
   const bool mine = lane < p.W;
+  // lane b: what beam b brings (read by all, used by the first CTA; the loads run ahead of the rows')
+  const float cum = mine ? p.scores[me] : -INFINITY;
+  const bool done = mine && p.finished != nullptr && p.finished[me] != 0;
+  int len = mine && p.lengths != nullptr ? p.lengths[me] : 0;
+  if (!done && len < INT_MAX) ++len;
   const int units = p.W * p.parts;
   bool waited = false;
   for (int u = rank; u < units; u += C) {
@@ -404,10 +437,6 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
 
   // ---- the first CTA.  Lane u < units of warp 0: its part's sum relative to the row's maximum; then
   // lane b: beam b's lse and the power of its length.  The other warps join the rows' lists meanwhile.
-  const float cum = mine ? p.scores[me] : -INFINITY;
-  const bool done = mine && p.finished != nullptr && p.finished[me] != 0;
-  int len = mine && p.lengths != nullptr ? p.lengths[me] : 0;
-  if (!done && len < INT_MAX) ++len;
   if (warp == 0) {
     if (lane < units) {
       const int s0 = lane / p.parts * p.parts;
@@ -427,7 +456,7 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
       }
       // a sum that is NaN or 0 (nothing above -inf) has no logarithm
       sm.lse[lane] = sum > 0.0 ? (double)M + ln64(sum) : (double)NAN;
-      sm.norm[lane] = p.penalty == 0.f ? 1.0 : exp64((double)p.penalty * ln64((double)max(len, 1)));
+      sm.inv[lane] = p.penalty == 0.f ? 1.0 : exp64(-(double)p.penalty * ln64((double)max(len, 1)));
     }
   } else if (p.parts > 1) {
     for (int b = warp - 1; b < p.W; b += kBeamWarps - 1) {
@@ -455,10 +484,8 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
       total = (double)c + ((double)key_value(k) - lse);
       if (total != total) total = -INFINITY;
     }
-    if (p.penalty != 0.f && total > -INFINITY) total /= sm.norm[b];
-    sm.rank[b][lane] = lane < p.W && lane < p.V ? rank_key(total) : 0ull;
-    if (p.penalty != 0.f && total > -INFINITY)  // the total itself again
-      total = ended ? (double)c : (double)c + ((double)key_value(sm.list[b * p.parts][lane]) - lse);
+    const double rank = p.penalty != 0.f && total > -INFINITY ? total * sm.inv[b] : total;
+    sm.rank[b][lane] = lane < p.W && lane < p.V ? rank_key(rank) : 0ull;
     sm.total[b][lane] = (float)total;
     sm.token[b][lane] = tok;
   }
