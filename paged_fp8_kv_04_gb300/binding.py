@@ -6,6 +6,7 @@ raises on a non-OK status.  It fails loudly when the shared library is missing.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -544,13 +545,11 @@ def _enqueue(name, entry, args, dev, stream):
         raise PaError(st, name)
 
 
-def _empty(shape, dtype, dev, stream):
-    """An output allocated for use on the launching stream."""
+def _allocating_on(stream):
+    """Context in which outputs belong to the launching stream (torch's allocator reuses a block in
+    the order of the stream it was allocated on)."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+    return torch.cuda.stream(stream)
 
 
 def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *, max_q_len,
@@ -596,10 +595,11 @@ def evict_select(mass, context_lens, *, budget, first=0, recent=0, keep=None, ne
     i32, dev = torch.int32, _device_of(mass)
     B, heads, width = shape = _rank("mass", mass, 3)
     kept = (B, heads, budget if budget > 0 else 1)  # the library refuses a budget below 1
-    if keep is None:
-        keep = _empty(kept, i32, dev, stream)
-    if new_lens is None:
-        new_lens = _empty((B,), i32, dev, stream)
+    with _allocating_on(stream) if stream is not None else contextlib.nullcontext():
+        if keep is None:
+            keep = torch.empty(kept, dtype=i32, device=dev)
+        if new_lens is None:
+            new_lens = torch.empty_like(context_lens)
     a = EvictSelectArgs(
         _need("mass", mass, torch.float32, shape, dev), _need("context_lens", context_lens, i32, (B,), dev),
         _need("keep", keep, i32, kept, dev), _need("new_lens", new_lens, i32, (B,), dev),
@@ -665,25 +665,21 @@ def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_p
             stride, even = st[0] if N * W > 1 else V, True
         if (V > 1 and st[-1] != 1) or stride < V or not even:
             raise ValueError("logits: rows must be dense and evenly spaced")
-    if tokens is None:
-        tokens = _empty(shape, i32, dev, stream)
-    if parents is None:
-        parents = _empty(shape, i32, dev, stream)
-    if scores_out is None:
-        scores_out = _empty(shape, f32, dev, stream)
-    fp = fop = lp = lop = None
-    if finished is not None:
-        fp = _need("finished", finished, u8, shape, dev)
-        if finished_out is None:
-            finished_out = _empty(shape, u8, dev, stream)
-    if finished_out is not None:
-        fop = _need("finished_out", finished_out, u8, shape, dev)
-    if lengths is not None:
-        lp = _need("lengths", lengths, i32, shape, dev)
-        if lengths_out is None:
-            lengths_out = _empty(shape, i32, dev, stream)
-    if lengths_out is not None:
-        lop = _need("lengths_out", lengths_out, i32, shape, dev)
+    with _allocating_on(stream) if stream is not None else contextlib.nullcontext():
+        if scores_out is None:
+            scores_out = torch.empty_like(scores)
+        if tokens is None:
+            tokens = torch.empty_like(scores, dtype=i32)
+        if parents is None:
+            parents = torch.empty_like(scores, dtype=i32)
+        if finished is not None and finished_out is None:
+            finished_out = torch.empty_like(finished)
+        if lengths is not None and lengths_out is None:
+            lengths_out = torch.empty_like(lengths)
+    fp = None if finished is None else _need("finished", finished, u8, shape, dev)
+    lp = None if lengths is None else _need("lengths", lengths, i32, shape, dev)
+    fop = None if finished_out is None else _need("finished_out", finished_out, u8, shape, dev)
+    lop = None if lengths_out is None else _need("lengths_out", lengths_out, i32, shape, dev)
     a = BeamSelectArgs(
         logits.data_ptr(), _need("scores", scores, f32, shape, dev), fp, lp, _need("tokens", tokens, i32, shape, dev),
         _need("parents", parents, i32, shape, dev), _need("scores_out", scores_out, f32, shape, dev), fop, lop,
