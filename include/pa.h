@@ -409,6 +409,11 @@ pa_status_t pa_attn_mass(const pa_attn_mass_args_t *args, void *stream);
 
 /* ---- eviction: which tokens a bounded cache keeps, and their move to the front ---- */
 
+/* A pa_decode on a plan without PA_PLAN_NO_PDL reads its index inputs before the kernel enqueued
+ * just before it has completed (see the flag).  pa_evict_select writes new_lens and
+ * pa_beam_reorder writes block_table_out, which are such inputs: another kernel has to lie between
+ * them and that decode (the write of the step's new tokens does), or the plan has to have the flag. */
+
 #define PA_DEV_BAD_KEEP 0x400u /* pa_kv_compact: new_lens outside [0, keep_stride] or past the tables, or a keep row
                                   that is not ascending positions of the request's cache */
 
@@ -474,8 +479,8 @@ typedef struct pa_kv_compact_args {
  * slot i of r's destination pages takes the K and V rows, the scales and the mass of position
  * keep[r][h][i], bit for bit; afterwards new_lens is the request's context_lens.  Positions
  * keep their order, so causal cutoffs, recency and the indexer's last page stay meaningful.
- * In place nothing but the request's own first pages is written, and tokens that do not move are
- * not touched; slots past new_lens are left as they are.  Pages that another request reads
+ * In place nothing but the request's own first pages is written, and pages all of whose tokens
+ * stay are not; slots past new_lens are left as they are.  Pages that another request reads
  * as well (a common prefix, beams) must not be compacted in place: give dst_block_table, whose pages
  * are then written and must be nobody else's (not the source's either).  An entry that is not above the one before it
  * or lies past the tables, and a bad page, are flagged and that token is not moved.  One kernel launch
