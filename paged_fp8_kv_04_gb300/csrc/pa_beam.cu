@@ -16,7 +16,6 @@ namespace {
 
 using pa_host::aligned;
 
-constexpr int kD = pa_host::kD;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kMaxReqs = 65535;

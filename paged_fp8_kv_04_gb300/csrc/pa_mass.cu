@@ -522,15 +522,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mass_kernel(const __grid_con
     pa::mbar_init(bar_mmadone(sm), 1);
     pa::fence_barrier_init();
   }
+  if (warp == kEpiWarps + 1) pa::tmem_alloc(pa::smem_u32(sm.misc), p.tmem_cols);
+  pa::tc_fence_before();
+  // Up to here the CTA may run beside the kernel before it (programmatic dependent launch): it has
+  // read nothing.  The next kernel may start as soon as this one's inputs are complete.
+  pa::pdl_wait();
+  pa::pdl_launch_dependents();
   const uint32_t fl = scan_requests(p, sm);  // synchronises the CTA
+  pa::tc_fence_after();
   if (blockIdx.x == 0 && fl) raise(p, fl);
   const int64_t total = (int64_t)sm.tstart[p.B] * p.Hkv;
   const int64_t a = total * blockIdx.x / gridDim.x, b = total * (blockIdx.x + 1) / gridDim.x;
-  if (a >= b) return;  // the whole CTA
-  if (warp == kEpiWarps + 1) pa::tmem_alloc(pa::smem_u32(sm.misc), p.tmem_cols);
-  pa::tc_fence_before();
-  __syncthreads();
-  pa::tc_fence_after();
+  if (a >= b) {  // the whole CTA
+    if (warp == kEpiWarps + 1) pa::tmem_dealloc(sm.misc[0], p.tmem_cols);
+    return;
+  }
   const uint32_t tm = sm.misc[0];
   if (warp < kEpiWarps)
     run_epilogue<BF16>(p, sm, a, b, tm);
@@ -653,10 +659,17 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
   // One CTA per SM, or fewer where the mass rows cannot hold that many tiles
   const int64_t tiles = (int64_t)a->num_seqs * a->num_kv_heads * ((a->mass_stride + kTile - 1) / kTile);
   const int grid = (int)std::min<int64_t>(dev->sms, tiles);
-  (void)cudaGetLastError();  // drop an earlier, unrelated launch error
-  if (bf16)
-    attn_mass_kernel<true><<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-  else
-    attn_mass_kernel<false><<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, attn_mass_kernel<true>, p)
+                             : cudaLaunchKernelEx(&cfg, attn_mass_kernel<false>, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
