@@ -207,6 +207,22 @@ __device__ __forceinline__ void raise(const MassParams &p, uint32_t flag) {
   if (p.status != nullptr) atomicOr(p.status, flag);
 }
 
+// A tile's place in the ring of stages, and the parity of its use of it.
+struct Place {
+  int st = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int n, int nstage) {
+    st += n;
+    if (st >= 2 * nstage) {  // (a whole segment at once)
+      parity ^= (uint32_t)(st / nstage) & 1u;
+      st %= nstage;
+    } else if (st >= nstage) {
+      st -= nstage;
+      parity ^= 1u;
+    }
+  }
+};
+
 // A bounded wait by a whole warp: false for all lanes if it gave up for one.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(~0u, pa::mbar_wait_bounded(bar, parity)) != 0;
@@ -221,6 +237,7 @@ __device__ void run_producer(const MassParams &p, const MassSmem &sm, int64_t a,
   const uint64_t pol = pa::l2_evict_first_policy();
   const uint32_t page_tx = (uint32_t)p.ps * (BF16 ? 2 * kD : kD) + (p.ks != nullptr ? 4u * p.ps : 0u);
   int i = 0;
+  Place at;
   bool ok = true;
   Walk w(a, b);
   while (ok && w.next(p, sm)) {
@@ -241,25 +258,26 @@ __device__ void run_producer(const MassParams &p, const MassSmem &sm, int64_t a,
         phys = -2;
       }
       const uint32_t valid = __ballot_sync(~0u, phys >= 0);
+      const int32_t y = (phys * p.Hkv + s.h) * p.ps;  // the page's first row (unused where phys is -2)
       for (int j = 0; j < nb && t + j < s.t1; ++j, ++i) {
-        const int st = i % p.nstage, src = j * p.ppt;
-        int go = 1;
-        if (lane == 0 && i >= p.nstage) go = pa::mbar_wait_bounded(bar_empty(sm, st), (i / p.nstage - 1) & 1);
-        ok = __shfl_sync(~0u, go, 0) != 0;
+        const int src = j * p.ppt;
+        // the stage's earlier tile has been released: the parity of that use, one before this one
+        if (i >= p.nstage) ok = warp_wait(bar_empty(sm, at.st), at.parity ^ 1u);
         if (!ok) break;
-        const uint32_t bits = (valid >> src) & (p.ppt == 32 ? ~0u : (1u << p.ppt) - 1u);
-        if (lane == 0) {
-          sm.valid[st] = bits;
-          pa::mbar_arrive_expect_tx(bar_full(sm, st), __popc(bits) * page_tx);
+        const uint32_t bits = (valid >> src) & ((1u << p.ppt) - 1u);
+        const uint32_t dst = sm.stages + at.st * p.stage_bytes, fb = bar_full(sm, at.st);
+        if (lane == src) {  // a page's first lane announces the tile's bytes, then each lane fetches its page
+          sm.valid[at.st] = bits;
+          pa::mbar_arrive_expect_tx(fb, __popc(bits) * page_tx);
         }
         __syncwarp();
         if (lane >= src && lane < src + p.ppt && phys >= 0) {
-          const int32_t y = (phys * p.Hkv + s.h) * p.ps;
-          const uint32_t dst = sm.stages + st * p.stage_bytes, off = kpg * p.ps * 128, fb = bar_full(sm, st);
+          const uint32_t off = kpg * p.ps * 128;
           pa::tma_load_2d(dst + off, &p.tm_k, 0, y, fb, pol);
           if (BF16) pa::tma_load_2d(dst + 16384 + off, &p.tm_k, 64, y, fb, pol);
           if (p.ks != nullptr) pa::bulk_load_hint(dst + 16384 + kpg * p.ps * 4, p.ks + y, p.ps * 4, fb, pol);
         }
+        at.advance(1, p.nstage);
       }
     }
   }
@@ -286,7 +304,8 @@ __device__ __forceinline__ uint32_t tmem_buf(const MassParams &p, int g, int k) 
 template <bool BF16>
 __device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b, uint32_t tm) {
   const int lane = threadIdx.x & 31;
-  int i = 0, seg = 0;
+  int seg = 0;
+  Place at;
   int uses[kGroups] = {0, 0, 0, 0};  // each group's tiles so far
   bool ok = true;
   Walk w(a, b);
@@ -296,13 +315,13 @@ __device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int6
     const uint32_t q = sm.q + qb * p.qbuf_bytes;
     const int N = w.s.nr * (BF16 ? kG : 2 * kG);
     const uint32_t id = BF16 ? idesc_bf16(kTile, N) : pa::umma_idesc_e4m3(kTile, N, 0, 0);
-    for (int t = w.s.t0; t < w.s.t1 && ok; ++t, ++i) {
-      const int st = i % p.nstage, g = t % kGroups;
+    for (int t = w.s.t0; t < w.s.t1 && ok; ++t, at.advance(1, p.nstage)) {
+      const int st = at.st, g = t % kGroups;
       int n = 0;
 #pragma unroll
       for (int x = 0; x < kGroups; ++x) n = x == g ? uses[x]++ : n;
       const int k = n & (p.nbuf - 1), u = n >> (p.nbuf - 1);  // one or two buffers
-      ok = warp_wait(bar_full(sm, st), (i / p.nstage) & 1);
+      ok = warp_wait(bar_full(sm, st), at.parity);
       if (ok && u > 0) ok = warp_wait(bar_sfree(sm, 2 * g + k), (u - 1) & 1);
       if (!ok) break;
       pa::tc_fence_after();
@@ -408,7 +427,8 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
   const int etid = threadIdx.x, lane = etid & 31, warp = etid >> 5, g = warp >> 2, quarter = warp & 3;
   const int tok = 32 * quarter + lane;  // of a tile: the TMEM lane
   const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
-  int i = 0, seg = 0, cnt = 0;
+  int seg = 0, cnt = 0;
+  Place begin;  // of the segment
   bool ok = true;
   Walk w(a, b), ahead(a, b);
   if (ahead.next(p, sm)) convert_queries<BF16>(p, sm, ahead.s, 0, etid);
@@ -434,14 +454,16 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
     const float keep = s.tok0 > 0 ? 1.f : p.decay;
     int t = s.t0 + ((g - s.t0) & (kGroups - 1));  // the group's first tile
     float old0 = before(t), old1 = before(t + kGroups);
-    i += t - s.t0;
-    for (; t < s.t1 && ok; t += kGroups, i += kGroups) {
-      const int st = i % p.nstage, k = cnt & (p.nbuf - 1), pos = t * kTile + tok;
+    Place at = begin;
+    at.advance(t - s.t0, p.nstage);
+    begin.advance(s.t1 - s.t0, p.nstage);
+    for (; t < s.t1 && ok; t += kGroups, at.advance(kGroups, p.nstage)) {
+      const int st = at.st, k = cnt & (p.nbuf - 1), pos = t * kTile + tok;
       const bool live = pos < s.q.L;
       const float old = keep * old0;
       old0 = old1;
       old1 = before(t + 2 * kGroups);
-      ok = warp_wait(bar_full(sm, st), (i / p.nstage) & 1) &&
+      ok = warp_wait(bar_full(sm, st), at.parity) &&
            warp_wait(bar_sfull(sm, 2 * g + k), (cnt >> (p.nbuf - 1)) & 1);
       if (!ok) break;
       ++cnt;
@@ -488,7 +510,6 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
       if (lane == 0) pa::mbar_arrive(bar_sfree(sm, 2 * g + k));
       if (live) p.out[mrow + pos] = old + (valid ? sum : 0.f);
     }
-    i -= t - s.t1;  // the segment's tiles, of either group
     if (ok && lane == 0) pa::mbar_arrive(bar_qfree(sm, qb));  // the factors have been read
     __syncwarp();
     ++seg;
