@@ -420,6 +420,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
 template <typename T>
 __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const BeamParams p) {
   __shared__ BeamShared sm;
+  pa::pdl_wait();
   pa::cluster_arrive();
   const uint32_t C = pa::cluster_ctas(), rank = pa::cluster_rank();
   const int n = blockIdx.x / C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -554,6 +555,7 @@ __device__ void copy_row(const uint8_t *src, uint8_t *dst, int64_t n, int64_t i,
 // so that nothing has to be exchanged.  Copies only, bound by latency at the sizes of a step: 32 x 8 beams
 // with 32 KB of mass each (20 MB, 2.9 us at a copy's rate) take 6.6 us, a request of four beams 3.0 us.
 __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const ReorderParams p) {
+  pa::pdl_wait();
   const int n = blockIdx.y / p.W, j = blockIdx.y % p.W, tid = threadIdx.x, lane = tid & 31;
   const int64_t base = (int64_t)n * p.W, row = base + j;
   const unsigned beams = p.W == 32 ? ~0u : (1u << p.W) - 1u;
@@ -688,18 +690,9 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   int C = 1;
   while (C < kMaxCluster && (int64_t)a->num_reqs * C <= sms && bytes / (2 * C) >= 16384) C *= 2;
   p.parts = C > a->num_beams ? C / a->num_beams : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a->num_reqs * C);
-  cfg.blockDim = dim3(kBeamThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, beam_select_kernel<float>, p)
-                            : cudaLaunchKernelEx(&cfg, beam_select_kernel<uint16_t>, p);
+  const pa_host::Launch run(dim3((unsigned)a->num_reqs * C), dim3(kBeamThreads), 0, stream, C);
+  const cudaError_t e = f32 ? cudaLaunchKernelEx(run.cfg(), beam_select_kernel<float>, p)
+                            : cudaLaunchKernelEx(run.cfg(), beam_select_kernel<uint16_t>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -770,8 +763,6 @@ extern "C" pa_status_t pa_beam_reorder(const pa_beam_reorder_args_t *a, void *st
   const int64_t page_bytes = (int64_t)a->num_kv_heads * a->page_size * 16 * p.row_chunks;
   int64_t gx = ((page_bytes > widest ? page_bytes : widest) + 16383) / 16384;
   gx = gx < 1 ? 1 : (gx > 64 ? 64 : gx);
-  (void)cudaGetLastError();  // drop an earlier, unrelated launch error
-  beam_reorder_kernel<<<dim3((unsigned)gx, a->num_reqs * a->num_beams), kReorderThreads, 0,
-                        static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const pa_host::Launch run(dim3((unsigned)gx, a->num_reqs * a->num_beams), dim3(kReorderThreads), 0, stream);
+  return cudaLaunchKernelEx(run.cfg(), beam_reorder_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -101,6 +101,7 @@ __device__ __forceinline__ int ties_taken(int need, int before, int eq) { return
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
   __shared__ __align__(16) SelectShared sm;
+  pa::pdl_wait();
   const int C = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
   const int row = blockIdx.x / C, r = row / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = p.L[r];
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) kv_compact_kernel(const Compa
   constexpr int T = move_tokens<RC>(), kRow = 16 * RC;
   extern __shared__ __align__(128) uint8_t tile[];  // K rows, then V rows
   __shared__ MoveShared sm;
+  pa::pdl_wait();
   const int tid = threadIdx.x;
   const int C = IN_PLACE ? (int)pa::cluster_ctas() : (int)gridDim.x, rank = IN_PLACE ? (int)pa::cluster_rank() : (int)blockIdx.x;
   const int64_t row = IN_PLACE ? blockIdx.x / C : blockIdx.y;
@@ -522,7 +524,6 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   p.budget = a->budget;
   p.first = a->keep_first;
   p.recent = a->keep_recent;
-  (void)cudaGetLastError();  // drop an earlier, unrelated launch error
   const int sms = evict_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per row: more while each keeps 2048 positions and all run at once (two per SM), or
@@ -538,20 +539,11 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   // 32), and keeping them beats reading them again (131072: 19.0 us with 32, 34.3 re-read).
   const int64_t warps = (int64_t)C * kSelWarps;
   const int64_t keys = (((int64_t)a->mass_stride + warps - 1) / warps + 31) / 32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = keys <= 4          ? cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, p)
-                        : keys <= 16       ? cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, p)
-                        : keys <= kMaxKeys ? cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys>, p)
-                                           : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, p);
+  const pa_host::Launch run(dim3((unsigned)(rows * C)), dim3(kSelThreads), 0, stream, C);
+  const cudaError_t e = keys <= 4          ? cudaLaunchKernelEx(run.cfg(), evict_select_kernel<4>, p)
+                        : keys <= 16       ? cudaLaunchKernelEx(run.cfg(), evict_select_kernel<16>, p)
+                        : keys <= kMaxKeys ? cudaLaunchKernelEx(run.cfg(), evict_select_kernel<kMaxKeys>, p)
+                                           : cudaLaunchKernelEx(run.cfg(), evict_select_kernel<0>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -603,35 +595,24 @@ extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream
   p.dt_stride = in_place ? a->block_table_stride : a->dst_block_table_stride;
   p.m_stride = a->mass_stride;
   p.mo_stride = a->mass_out_stride;
-  (void)cudaGetLastError();  // drop an earlier, unrelated launch error
   const bool wide = a->kv_dtype == PA_KV_BF16;
   const int tokens = wide ? move_tokens<16>() : move_tokens<8>();
   const int64_t rows = (int64_t)a->num_seqs * a->num_kv_heads;
   const int sms = evict_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   const int64_t rounds = ((int64_t)a->keep_stride + tokens - 1) / tokens;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = kMoveBytes;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
   if (!in_place) {
-    cfg.gridDim = dim3((unsigned)rounds, (unsigned)rows);
-    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, kv_compact_kernel<16, false>, p)
-                               : cudaLaunchKernelEx(&cfg, kv_compact_kernel<8, false>, p);
+    const pa_host::Launch run(dim3((unsigned)rounds, (unsigned)rows), dim3(kMoveThreads), kMoveBytes, stream);
+    const cudaError_t e = wide ? cudaLaunchKernelEx(run.cfg(), kv_compact_kernel<16, false>, p)
+                               : cudaLaunchKernelEx(run.cfg(), kv_compact_kernel<8, false>, p);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
   // CTAs per row: more while all rows' CTAs run at once (three per SM, with room for the clusters'
   // placement: two) and there are rounds for them (8 rows x 4095: 6.5 us with 16, 8.4 with 8, 14.9 with 4)
   int C = 1;
   while (C < kMaxMoveCluster && rows * C <= sms && C < rounds) C *= 2;
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, kv_compact_kernel<16, true>, p)
-                             : cudaLaunchKernelEx(&cfg, kv_compact_kernel<8, true>, p);
+  const pa_host::Launch run(dim3((unsigned)(rows * C)), dim3(kMoveThreads), kMoveBytes, stream, C);
+  const cudaError_t e = wide ? cudaLaunchKernelEx(run.cfg(), kv_compact_kernel<16, true>, p)
+                             : cudaLaunchKernelEx(run.cfg(), kv_compact_kernel<8, true>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

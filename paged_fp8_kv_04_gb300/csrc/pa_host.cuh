@@ -2,6 +2,8 @@
 // pa_evict.cu, pa_beam.cu).
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <climits>
 #include <cstdint>
 
@@ -37,6 +39,31 @@ inline pa_status_t check_cache(int64_t num_pages, int num_kv_heads, int head_dim
   if (num_pages > INT32_MAX / ((int64_t)num_kv_heads * page_size)) return PA_ERR_CAPACITY;
   return PA_OK;
 }
+
+// A launch configuration: with programmatic dependent launch (each of these kernels begins with
+// griddepcontrol.wait, so that only its launch overlaps the end of the kernel before it), and with
+// clusters of `cluster` CTAs where that is more than 0.
+class Launch {
+ public:
+  Launch(dim3 grid, dim3 block, size_t smem, void *stream, int cluster = 0) {
+    cfg_.gridDim = grid;
+    cfg_.blockDim = block;
+    cfg_.dynamicSmemBytes = smem;
+    cfg_.stream = static_cast<cudaStream_t>(stream);
+    attr_[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr_[0].val.programmaticStreamSerializationAllowed = 1;
+    attr_[1].id = cudaLaunchAttributeClusterDimension;
+    attr_[1].val.clusterDim.x = cluster;
+    attr_[1].val.clusterDim.y = attr_[1].val.clusterDim.z = 1;
+    cfg_.attrs = attr_;
+    cfg_.numAttrs = cluster > 0 ? 2 : 1;
+  }
+  const cudaLaunchConfig_t *cfg() const { return &cfg_; }
+
+ private:
+  cudaLaunchConfig_t cfg_ = {};
+  cudaLaunchAttribute attr_[2] = {};
+};
 
 // Whether [a, a + na) and [b, b + nb) share a byte.
 inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {

@@ -447,7 +447,7 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a,
     const Segment s = w.s;
     const int qb = seg & 1;
     if (ahead.next(p, sm)) {
-      // segment seg - 1, which had the other buffers: its MMAs and both groups are done
+      // segment seg - 1, which had the other buffers: its MMAs and every group are done
       if (seg >= 1) ok = warp_wait(bar_qfree(sm, qb ^ 1), ((seg - 1) >> 1) & 1);
       if (!ok) break;
       convert_queries<BF16>(p, sm, ahead.s, qb ^ 1, etid);
@@ -692,17 +692,8 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
   // One CTA per SM, or fewer where the mass rows cannot hold that many tiles
   const int64_t tiles = (int64_t)a->num_seqs * a->num_kv_heads * ((a->mass_stride + kTile - 1) / kTile);
   const int grid = (int)std::min<int64_t>(dev->sms, tiles);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, attn_mass_kernel<true>, p)
-                             : cudaLaunchKernelEx(&cfg, attn_mass_kernel<false>, p);
+  pa_host::Launch run(dim3((unsigned)grid), dim3(kThreads), smem, stream);
+  const cudaError_t e = bf16 ? cudaLaunchKernelEx(run.cfg(), attn_mass_kernel<true>, p)
+                             : cudaLaunchKernelEx(run.cfg(), attn_mass_kernel<false>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
