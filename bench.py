@@ -72,13 +72,13 @@ def parse():
 # (sha256 over the code, comments stripped, of the C header and the decode kernels'
 # translation unit); any other code gives traffic null.
 MEASURED_TRAFFIC = {
-    "long128k": {"bytes": 279795712, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
-    "long128k_scalar": {"bytes": 271356672, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
-    "dense8k": {"bytes": 69845504, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
-    "bf16ctl": {"bytes": 137146112, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
-    "ragged": {"bytes": 143980288, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
-    "sparse": {"bytes": 70723072, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
-    "prefill": {"bytes": 11238912, "csrc_sha256": "4e6a9e7f65c13427e0a29642480a21a0bac6d1e3447b6ab972697edbde97000e"},
+    "long128k": {"bytes": 279870976, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
+    "long128k_scalar": {"bytes": 271453440, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
+    "dense8k": {"bytes": 69881856, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
+    "bf16ctl": {"bytes": 136912128, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
+    "ragged": {"bytes": 144009728, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
+    "sparse": {"bytes": 70716672, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
+    "prefill": {"bytes": 11238400, "csrc_sha256": "f4da2999452d327622423c1087d51a776dc0a44675b57a16e000e16613a13438"},
 }
 
 
@@ -109,8 +109,8 @@ def csrc_sha256():
 
 # The same for the quantise-and-write kernel (sha256 over the C header and pa_kv_write.cu).
 # The indexer's two launches of one call (score + select), from the same kind of capture.
-MEASURED_TRAFFIC_INDEXER = {"bytes": 557434624, "src_sha256": "a918cb0e5c67066640d7d2684ba2a3b67dcbca4bb89e22515f76e3b672048126"}
-MEASURED_TRAFFIC_KV_WRITE = {"bytes": 171521280, "src_sha256": "49a3afa5fd2f1b5d646e1a730f4d43126864abe7033fb499ac2c430b677719ee"}
+MEASURED_TRAFFIC_INDEXER = {"bytes": 557066496, "src_sha256": "e43c835aab743bf9b2028a35aee6fb760934dbea886c2bfbf66f29bf234743af"}
+MEASURED_TRAFFIC_KV_WRITE = {"bytes": 171430144, "src_sha256": "15f09cf1b01e5aeec14716226a2a040b4e213762b700073086ae1cbe49d9a9a3"}
 
 
 def index_sha256():
