@@ -3,10 +3,11 @@
 Every step of the attention runs in the library's CUDA kernels; this module checks
 tensor dtypes and devices, passes data pointers and the current torch stream, and
 raises on a non-OK status.  It fails loudly when the shared library is missing.
+The cache operators between two decode steps are marshalled by a compiled module
+(csrc/pa_torch.cpp), since their kernels are shorter than the same checks in Python.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -465,91 +466,35 @@ def lse_merge(part_out, part_lse, out, lse=None, stream=None, args: Optional[Lse
 #
 # These calls take tensors, check types, shapes and layout (the library sees only
 # pointers), allocate the outputs that are not given on the launching stream, and run on
-# the device of their tensors whatever the current device is.
+# the device of their tensors whatever the current device is.  Wrong tensors raise TypeError
+# or ValueError, a refusal by the library PaError.
 
-def _need(name, t, dtype, shape, dev):
-    """Pointer of a dense tensor of this dtype and shape on CUDA device number dev."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    raise ValueError(f"{name}: on {t.device}, expected cuda:{dev} like the rest of the call")
+_module = None
 
 
-def _rank(name, t, dims):
-    if t.dim() != dims:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dims}")
-    return t.shape
+def torch_module():
+    """pa_torch.so (built in-tree by __graft_entry__.build()), bound to the library; raises if missing."""
+    global _module
+    if _module is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are loaded first)
+        path = _build.torch_module_path()
+        if not os.path.exists(path):
+            raise ImportError(f"pa_torch.so is not built ({path}); run __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("pa_torch", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_torch", loader))
+        loader.exec_module(m)
+        L = lib()
+        m.bind(PaError, *(ctypes.cast(f, P).value for f in (
+            L.pa_attn_mass, L.pa_evict_select, L.pa_kv_compact, L.pa_beam_select, L.pa_beam_reorder)))
+        _module = m
+    return _module
 
 
-def _device_of(t) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"tensors on {t.device}, expected a CUDA device")
-    return dev
-
-
-def _status_ptr(status, dev):
-    if status is None:
-        return None
-    if status.element_size() != 4 or status.numel() < 1 or status.get_device() != dev:
-        raise ValueError("status: a 4-byte word on the call's device")
-    return status.data_ptr()
-
-
-def _kv_mode(k_cache, k_scale):
-    """(KV_*, SCALE_*) of a cache tensor."""
-    import torch
-    dt = k_cache.dtype
-    if dt is torch.uint8 or dt is torch.float8_e4m3fn:
-        return KV_FP8_E4M3, SCALE_SCALAR if k_scale is None else SCALE_PER_TOKEN
-    if dt is not torch.bfloat16:
-        raise TypeError(f"k_cache: {dt}, expected uint8, float8_e4m3fn or bfloat16")
-    if k_scale is not None:
-        raise ValueError("k_scale: a bf16 cache has no scales")
-    return KV_BF16, SCALE_NONE
-
-
-def _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev):
-    """Pointers, mode and shape of a K and V cache pair with optional per-token scales."""
-    import torch
-    kv, sm = _kv_mode(k_cache, k_scale)
-    shape = _rank("k_cache", k_cache, 4)
-    kp = _need("k_cache", k_cache, k_cache.dtype, shape, dev)
-    vp = _need("v_cache", v_cache, k_cache.dtype, shape, dev)
-    if k_scale is None:
-        if v_scale is not None:
-            raise ValueError("k_scale and v_scale: both or neither")
-        return kp, vp, None, None, kv, sm, shape
-    if v_scale is None:
-        raise ValueError("k_scale and v_scale: both or neither")
-    return (kp, vp, _need("k_scale", k_scale, torch.float32, shape[:3], dev),
-            _need("v_scale", v_scale, torch.float32, shape[:3], dev), kv, sm, shape)
-
-
-def _enqueue(name, entry, args, dev, stream):
-    """Calls a C entry on device number dev and `stream` (default: torch's current stream there)."""
-    import torch
-    # the raw handle of torch's current stream: its Stream object costs as much as the launch
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        st = entry(ctypes.byref(args), s)
-    else:
-        with torch.cuda.device(dev):
-            st = entry(ctypes.byref(args), s)
-    if st != 0:
-        raise PaError(st, name)
-
-
-def _allocating_on(stream):
-    """Context in which outputs belong to the launching stream (torch's allocator reuses a block in
-    the order of the stream it was allocated on)."""
-    import torch
-    return torch.cuda.stream(stream)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *, max_q_len,
@@ -561,28 +506,9 @@ def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *,
     mass fp32 [B, Hkv, stride]; updated in place, or into `out` when given (positions past a
     request's context are not written).  max_q_len bounds every request's rows.  Returns
     the updated tensor."""
-    import torch
-    i32, f32, dev = torch.int32, torch.float32, _device_of(k_cache)
-    kv, sm = _kv_mode(k_cache, k_scale)
-    cache = _rank("k_cache", k_cache, 4)
-    pages, heads, ps, d = cache
-    rows, Hq, _ = _rank("q", q, 3)
-    B, _, width = shape = _rank("mass", mass, 3)
-    table = _rank("block_table", block_table, 2)
-    if Hq % heads or shape[1] != heads or table[0] != B:
-        raise ValueError(f"q {tuple(q.shape)}, mass {tuple(shape)} and block_table {tuple(table)} for {heads} KV heads")
-    if out is None:
-        out = mass
-    a = AttnMassArgs(
-        _need("q", q, torch.bfloat16, (rows, Hq, d), dev), _need("k_cache", k_cache, k_cache.dtype, cache, dev),
-        None if k_scale is None else _need("k_scale", k_scale, f32, cache[:3], dev),
-        _need("block_table", block_table, i32, table, dev), _need("context_lens", context_lens, i32, (B,), dev),
-        _need("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev), _need("lse", lse, f32, (rows, Hq), dev),
-        _need("mass", mass, f32, shape, dev), _need("out", out, f32, shape, dev), _status_ptr(status, dev),
-        pages, B, rows, heads, Hq // heads, d, ps, kv, sm, table[1], width, max_q_len, k_scale_scalar,
-        sm_scale if sm_scale is not None else d ** -0.5, decay, 0)
-    _enqueue("pa_attn_mass", lib().pa_attn_mass, a, dev, stream)
-    return out
+    return (_module or torch_module()).attn_mass(
+        q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, out, k_scale, status, _handle(stream),
+        max_q_len, sm_scale, decay, k_scale_scalar)
 
 
 def evict_select(mass, context_lens, *, budget, first=0, recent=0, keep=None, new_lens=None,
@@ -591,21 +517,8 @@ def evict_select(mass, context_lens, *, budget, first=0, recent=0, keep=None, ne
     the first `first`, the last `recent` and the largest mass between.  mass fp32
     [B, Hkv, stride], context_lens int32 [B].  Returns (keep int32 [B, Hkv, budget], ascending,
     -1 after; new_lens int32 [B])."""
-    import torch
-    i32, dev = torch.int32, _device_of(mass)
-    B, heads, width = shape = _rank("mass", mass, 3)
-    kept = (B, heads, budget if budget > 0 else 1)  # the library refuses a budget below 1
-    with _allocating_on(stream) if stream is not None else contextlib.nullcontext():
-        if keep is None:
-            keep = torch.empty(kept, dtype=i32, device=dev)
-        if new_lens is None:
-            new_lens = torch.empty_like(context_lens)
-    a = EvictSelectArgs(
-        _need("mass", mass, torch.float32, shape, dev), _need("context_lens", context_lens, i32, (B,), dev),
-        _need("keep", keep, i32, kept, dev), _need("new_lens", new_lens, i32, (B,), dev),
-        _status_ptr(status, dev), B, heads, width, budget, first, recent, 0)
-    _enqueue("pa_evict_select", lib().pa_evict_select, a, dev, stream)
-    return keep, new_lens
+    return (_module or torch_module()).evict_select(
+        mass, context_lens, keep, new_lens, status, _handle(stream), budget, first, recent)
 
 
 def kv_compact(keep, new_lens, block_table, k_cache, v_cache, *, dst_block_table=None, k_scale=None,
@@ -614,29 +527,9 @@ def kv_compact(keep, new_lens, block_table, k_cache, v_cache, *, dst_block_table
     (pa_kv_compact).  keep int32 [B, Hkv, n] and new_lens int32 [B] as evict_select gives
     them; mass fp32 [B, Hkv, stride] moves along, in place or, with dst_block_table, into
     mass_out.  Afterwards new_lens are the context lengths."""
-    import torch
-    i32, f32, dev = torch.int32, torch.float32, _device_of(k_cache)
-    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev)
-    B, _, n = _rank("keep", keep, 3)
-    width = _rank("block_table", block_table, 2)[1]
-    dp = mp = mop = None
-    dst_width = mass_width = out_width = 0
-    if dst_block_table is not None:
-        dst_width = _rank("dst_block_table", dst_block_table, 2)[1]
-        dp = _need("dst_block_table", dst_block_table, i32, (B, dst_width), dev)
-    elif mass_out is None:
-        mass_out = mass
-    if (mass is None) != (mass_out is None):
-        raise ValueError("mass and mass_out: both or neither (in place mass alone)")
-    if mass is not None:
-        mass_width, out_width = _rank("mass", mass, 3)[2], _rank("mass_out", mass_out, 3)[2]
-        mp = _need("mass", mass, f32, (B, heads, mass_width), dev)
-        mop = _need("mass_out", mass_out, f32, (B, heads, out_width), dev)
-    a = KvCompactArgs(
-        _need("keep", keep, i32, (B, heads, n), dev), _need("new_lens", new_lens, i32, (B,), dev),
-        _need("block_table", block_table, i32, (B, width), dev), dp, kp, vp, ksp, vsp, mp, mop,
-        _status_ptr(status, dev), pages, B, heads, d, ps, kv, sm, n, width, dst_width, mass_width, out_width, 0)
-    _enqueue("pa_kv_compact", lib().pa_kv_compact, a, dev, stream)
+    (_module or torch_module()).kv_compact(
+        keep, new_lens, block_table, dst_block_table, k_cache, v_cache, k_scale, v_scale, mass, mass_out, status,
+        _handle(stream))
 
 
 def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_penalty=0.0, tokens=None,
@@ -646,46 +539,9 @@ def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_p
     vocabulary), scores fp32 [N, W] (-inf: no such beam yet), finished uint8 and lengths int32
     [N, W], both optional.  Returns (tokens, parents, scores, finished, lengths), each [N, W];
     the last two are None where their input is and no output is given."""
-    import torch
-    i32, u8, f32, dev = torch.int32, torch.uint8, torch.float32, _device_of(logits)
-    N, W = shape = _rank("scores", scores, 2)
-    if logits.dtype is not torch.bfloat16 and logits.dtype is not f32:
-        raise TypeError(f"logits: {logits.dtype}, expected bfloat16 or float32")
-    full = logits.shape
-    V = full[-1]
-    if full != (N, W, V) and full != (N * W, V):
-        raise ValueError(f"logits: shape {tuple(full)} for {N} x {W} beams")
-    stride = V
-    if not logits.is_contiguous():
-        st = logits.stride()
-        if len(full) == 3:  # the stride of a dimension of size 1 means nothing
-            stride = st[1] if W > 1 else st[0] if N > 1 else V
-            even = N == 1 or st[0] == W * stride
-        else:
-            stride, even = st[0] if N * W > 1 else V, True
-        if (V > 1 and st[-1] != 1) or stride < V or not even:
-            raise ValueError("logits: rows must be dense and evenly spaced")
-    with _allocating_on(stream) if stream is not None else contextlib.nullcontext():
-        if scores_out is None:
-            scores_out = torch.empty_like(scores)
-        if tokens is None:
-            tokens = torch.empty_like(scores, dtype=i32)
-        if parents is None:
-            parents = torch.empty_like(scores, dtype=i32)
-        if finished is not None and finished_out is None:
-            finished_out = torch.empty_like(finished)
-        if lengths is not None and lengths_out is None:
-            lengths_out = torch.empty_like(lengths)
-    fp = None if finished is None else _need("finished", finished, u8, shape, dev)
-    lp = None if lengths is None else _need("lengths", lengths, i32, shape, dev)
-    fop = None if finished_out is None else _need("finished_out", finished_out, u8, shape, dev)
-    lop = None if lengths_out is None else _need("lengths_out", lengths_out, i32, shape, dev)
-    a = BeamSelectArgs(
-        logits.data_ptr(), _need("scores", scores, f32, shape, dev), fp, lp, _need("tokens", tokens, i32, shape, dev),
-        _need("parents", parents, i32, shape, dev), _need("scores_out", scores_out, f32, shape, dev), fop, lop,
-        stride, N, W, V, LOGITS_F32 if logits.dtype is f32 else LOGITS_BF16, eos, length_penalty, 0)
-    _enqueue("pa_beam_select", lib().pa_beam_select, a, dev, stream)
-    return tokens, parents, scores_out, finished_out, lengths_out
+    return (_module or torch_module()).beam_select(
+        logits, scores, finished, lengths, tokens, parents, scores_out, finished_out, lengths_out, _handle(stream),
+        eos, length_penalty)
 
 
 def beam_reorder(parents, context_lens, block_table, block_table_out, k_cache, v_cache, *, k_scale=None,
@@ -693,24 +549,6 @@ def beam_reorder(parents, context_lens, block_table, block_table_out, k_cache, v
     """Lets the beams' histories follow their parents (pa_beam_reorder).  parents int32 [N, W],
     context_lens int32 [N * W], block tables int32 [N * W, stride]; states: up to four
     (in, out) pairs of tensors with N * W rows, gathered by parent."""
-    import torch
-    i32, dev = torch.int32, _device_of(k_cache)
-    kp, vp, ksp, vsp, kv, sm, (pages, heads, ps, d) = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev)
-    N, W = shape = _rank("parents", parents, 2)
-    R = N * W
-    table = (R, _rank("block_table", block_table, 2)[1])
-    if len(states) > MAX_BEAM_STATES:
-        raise ValueError(f"states: at most {MAX_BEAM_STATES}")
-    sin, sout, size = [], [], []
-    for x, y in states:
-        if x.dim() < 1 or x.shape[0] != R:
-            raise ValueError(f"states: shape {tuple(x.shape)}, expected {R} rows")
-        sin.append(_need("states' input", x, x.dtype, x.shape, dev))
-        sout.append(_need("states' output", y, x.dtype, x.shape, dev))
-        size.append(x.numel() // max(R, 1) * x.element_size())
-    a = BeamReorderArgs(
-        _need("parents", parents, i32, shape, dev), _need("context_lens", context_lens, i32, (R,), dev),
-        _need("block_table", block_table, i32, table, dev), _need("block_table_out", block_table_out, i32, table, dev),
-        kp, vp, ksp, vsp, _status_ptr(status, dev), tuple(sin), tuple(sout), tuple(size), pages, len(states), N, W, heads,
-        d, ps, kv, sm, table[1], 0)
-    _enqueue("pa_beam_reorder", lib().pa_beam_reorder, a, dev, stream)
+    (_module or torch_module()).beam_reorder(
+        parents, context_lens, block_table, block_table_out, k_cache, v_cache, k_scale, v_scale, states, status,
+        _handle(stream))

@@ -1,4 +1,5 @@
-"""Builds libpagedfp8.so for sm_103a with nvcc, in-tree (paged_fp8_kv_04_gb300/_build/)."""
+"""Builds libpagedfp8.so for sm_103a with nvcc, and pa_torch.so (the torch side of the cache
+operators' calls) with the host compiler, in-tree (paged_fp8_kv_04_gb300/_build/)."""
 from __future__ import annotations
 
 import glob
@@ -14,6 +15,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libpagedfp8.so")
 # The same library with the decode kernel's launch trace compiled in (pa_debug_trace).
 TRACE_LIB_PATH = os.path.join(BUILD_DIR, "libpagedfp8_trace.so")
+TORCH_SOURCE = os.path.join(CSRC, "pa_torch.cpp")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -38,6 +40,49 @@ def up_to_date(path: str = LIB_PATH) -> bool:
         return False
     t = os.path.getmtime(path)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def torch_module_path() -> str:
+    """pa_torch.so is built against one torch: its version is in the name."""
+    import torch
+    return os.path.join(BUILD_DIR, f"pa_torch.{torch.__version__}.so")
+
+
+def _start_torch_module(force: bool):
+    """Starts the compilation of pa_torch.cpp if it is due: (process, temporary file) or None."""
+    import sysconfig
+
+    import torch
+    out = torch_module_path()
+    due = force or not os.path.exists(out) or any(
+        os.path.getmtime(f) > os.path.getmtime(out) for f in (TORCH_SOURCE, os.path.join(INCLUDE, "pa.h")))
+    if not due:
+        return None
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = out + f".tmp{os.getpid()}"
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE]
+    for i in includes:
+        cmd += ["-isystem", i]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", tmp, TORCH_SOURCE,
+            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp, out
+
+
+def build_all(force: bool = False) -> str:
+    """libpagedfp8.so and pa_torch.so, side by side."""
+    started = _start_torch_module(force)
+    lib = build(force)
+    if started is not None:
+        proc, tmp, out = started
+        text, _ = proc.communicate()
+        if proc.returncode != 0:
+            raise RuntimeError("pa_torch.cpp failed to compile:\n" + text)
+        os.replace(tmp, out)
+    return lib
 
 
 def build(force: bool = False, verbose: bool = False, trace: bool = False) -> str:

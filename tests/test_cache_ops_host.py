@@ -201,3 +201,43 @@ def test_oracle_beam_reorder_by_hand():
     assert t.tolist() == [[0, 2, 11, 90], [0, 2, 12, 91], [0, 1, 10, 92], [0, 2, 13, 93]]
     assert y[12, 0].tolist() == [11, 11, 12, 12] and y[13, 0].tolist() == [11, 11, 13, 13]
     assert np.array_equal(np.delete(y, [12, 13], 0), np.delete(x, [12, 13], 0))
+
+
+# ------------------------------------------------- the torch side, which refuses on the CPU
+
+@pytest.fixture(scope="module")
+def built():
+    libbuild.build_all()
+    return B.torch_module()
+
+
+def test_the_torch_module_refuses_wrong_arguments(built):
+    import torch
+    mass, lens = torch.zeros(2, 1, 8), torch.zeros(2, dtype=torch.int32)
+    k = torch.zeros(4, 1, 16, 128, dtype=torch.uint8)
+    table = torch.zeros(2, 2, dtype=torch.int32)
+    keep = torch.zeros(2, 1, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="expected a CUDA device"):
+        B.evict_select(mass, lens, budget=4)
+    with pytest.raises(ValueError, match="expected a CUDA device"):
+        B.kv_compact(keep, lens, table, k, k.clone())
+    with pytest.raises(ValueError, match="expected a CUDA device"):
+        B.beam_select(torch.zeros(1, 2, 9), torch.zeros(1, 2))
+    with pytest.raises(ValueError, match="expected a CUDA device"):
+        B.beam_reorder(torch.zeros(1, 2, dtype=torch.int32), lens, table, table.clone(), k, k.clone())
+    with pytest.raises(ValueError, match="expected a CUDA device"):
+        B.attn_mass(torch.zeros(2, 16, 128).bfloat16(), k, table, lens, torch.zeros(3, dtype=torch.int32), torch.zeros(2, 16), mass,
+                    max_q_len=1)
+    with pytest.raises(TypeError, match="expected a tensor"):
+        B.evict_select(np.zeros((2, 1, 8), np.float32), lens, budget=4)
+    with pytest.raises(TypeError):
+        built.evict_select(mass, lens)
+
+
+def test_torch_module_missing_fails_loudly(built, monkeypatch, tmp_path):
+    """Without the compiled module the calls raise; there is no other path."""
+    import torch
+    monkeypatch.setattr(B, "_module", None)
+    monkeypatch.setattr(libbuild, "torch_module_path", lambda: str(tmp_path / "pa_torch.so"))
+    with pytest.raises(ImportError):
+        B.evict_select(torch.zeros(2, 1, 8), torch.zeros(2, dtype=torch.int32), budget=4)
