@@ -179,37 +179,43 @@ struct BeamShared {
   int token[kMaxBeams][kMaxBeams];
 };
 
-// The few logarithms and powers of a step in fp64, which this GPU computes slowly (some 70 cycles for
-// each dependent operation): short evaluations in place of the general functions, whose pow
-// alone took 7 us here.  They are far more exact than the sums of exponentials they are taken of.
-// e^x by its Taylor polynomial of degree 9, in pairs (Estrin), for |x| <= 0.36: the next term is
-// 0.36^10 / 10! = 1e-11.
-__device__ __forceinline__ double exp_small(double x) {
-  const double x2 = x * x, x4 = x2 * x2;
-  const double a = 1.0 + x, b = fma(x, 1.0 / 6.0, 0.5), c = fma(x, 1.0 / 120.0, 1.0 / 24.0);
-  const double d = fma(x, 1.0 / 5040.0, 1.0 / 720.0), e = fma(x, 1.0 / 362880.0, 1.0 / 40320.0);
-  return fma(x4, fma(x4, e, fma(x2, d, c)), fma(x2, b, a));
-}
+// The few logarithms and powers of a step.  This GPU computes in fp64 slowly (some 70 cycles for each
+// dependent operation; the general pow took 7 us here, and Taylor polynomials in fp64 2 to 3), so
+// they are taken by tables with the small terms in fp32, after P. T. P. Tang's table-driven logarithm
+// and exponential: within 1e-10, a hundredth of what the sums of exponentials carry.
 constexpr double kLn2 = 0.69314718055994530942;
-// e^x: x = k ln 2 + t, |t| <= ln 2 / 2; 0 below -700 and +inf above 700.
+__constant__ float kInverse[16] = {  // 1 / (1 + (k + 1/2) / 16), to fp32
+    0.969696999f, 0.914285719f, 0.864864886f, 0.820512831f, 0.780487776f, 0.744186044f, 0.711111128f, 0.680851042f,
+    0.653061211f, 0.627451003f, 0.603773594f, 0.581818163f, 0.561403513f, 0.542372882f, 0.524590135f, 0.507936537f};
+__constant__ double kMinusLnInverse[16] = {  // of those very numbers
+    0.030771628864431744, 0.089612153101751704, 0.14518198563011125, 0.19782573029140393,
+    0.24783620115748495,  0.2954642166191262,   0.34092656275620659, 0.38441173057530009,
+    0.4260844157999969,   0.46608969453434201,  0.50455599585123423, 0.54159731409771239,
+    0.57731535758424302,  0.61180153924334779,  0.64513801725294073, 0.67739876584980818};
+__constant__ double kExp2Sixteenths[16] = {  // 2^(j / 16)
+    1.0,                1.0442737824274138, 1.0905077326652577, 1.1387886347566916, 1.189207115002721,  1.241857812073484,
+    1.2968395546510096, 1.3542555469368927, 1.4142135623730951, 1.4768261459394993, 1.5422108254079407, 1.6104903319492543,
+    1.681792830507429,  1.7562521603732995, 1.8340080864093424, 1.9152065613971474};
+// e^x: x = k ln 2 / 16 + t, |t| <= ln 2 / 32, e^t - 1 - t by Taylor; 0 below -700 and +inf above 700.
 __device__ __forceinline__ double exp64(double x) {
   if (!(x > -700.0)) return 0.0;
   if (x > 700.0) return INFINITY;
-  const int k = __float2int_rn((float)x * kLog2e);
-  return exp_small(fma(-(double)k, kLn2, x)) * __longlong_as_double((long long)(k + 1023) << 52);
+  const int k = __float2int_rn((float)x * (16.f * kLog2e));
+  const double t = fma(-(double)k, kLn2 / 16, x);
+  const float u = (float)t;
+  const float q = u * u * fmaf(fmaf(fmaf(1.f / 120, u, 1.f / 24), u, 1.f / 6), u, 0.5f);
+  return (1.0 + (t + (double)q)) * (kExp2Sixteenths[k & 15] * __longlong_as_double((long long)((k >> 4) + 1023) << 52));
 }
-// ln s for a normal s > 0: with s = 2^e f, f in [1/sqrt 2, sqrt 2], one Newton step from the fp32
-// logarithm l of f: ln f = l + ln(f e^-l), and f e^-l is within 1e-6 of 1.
+// ln s for a normal s > 0: s = 2^e m, 1 <= m < 2, i = the inverse of the middle of m's sixteenth, and
+// ln m = -ln i + ln(1 + r), r = i m - 1 exactly in two fp32 numbers, |r| <= 1/31.
 __device__ __forceinline__ double ln64(double s) {
   const long long b = __double_as_longlong(s);
-  int e = (int)((b >> 52) & 2047) - 1023;
-  double f = __longlong_as_double((b & 0xFFFFFFFFFFFFFll) | (1023ll << 52));
-  if (f > 1.4142135623730951) {
-    f *= 0.5;
-    ++e;
-  }
-  const double l = (double)logf((float)f), r = fma(f, exp_small(-l), -1.0);
-  return fma((double)e, kLn2, l + r * fma(-0.5, r, 1.0));
+  const int e = (int)((b >> 52) & 2047) - 1023, k = (int)((b >> 48) & 15);
+  const double m = __longlong_as_double((b & 0xFFFFFFFFFFFFFll) | (1023ll << 52));
+  const float hi = (float)m, lo = (float)(m - (double)hi), i = kInverse[k];
+  const float p = hi * i, r1 = p - 1.f, r2 = fmaf(lo, i, fmaf(hi, i, -p)), r = r1 + r2;
+  const float q = r * r * fmaf(fmaf(fmaf(fmaf(fmaf(1.f / 7, r, -1.f / 6), r, 1.f / 5), r, -1.f / 4), r, 1.f / 3), r, -0.5f);
+  return fma((double)e, kLn2, kMinusLnInverse[k] + ((double)r1 + (double)(r2 + q)));
 }
 
 // This shared-memory address in the cluster's first CTA.
@@ -323,9 +329,14 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   if ((lane & 15) == 0) sm.half[tid >> 4] = k;
   if (tid == 0) sm.owners = sm.cands = 0;
   __syncthreads();
-  k = sort32(sm.half[lane], lane);
-  const u64 tau = __shfl_sync(~0u, k, p.W - 1);
-  const float top = key_value(__shfl_sync(~0u, k, 0));
+  // (the keys differ but for 0, of which any will do: a key's place is the number of larger ones)
+  k = sm.half[lane];
+  int place = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) place += sm.half[i] > k;
+  const unsigned at_w = __ballot_sync(~0u, place == p.W - 1);
+  const u64 tau = at_w != 0 ? __shfl_sync(~0u, k, __ffs(at_w) - 1) : 0ull;
+  const float top = key_value(__shfl_sync(~0u, k, __ffs(__ballot_sync(~0u, place == 0)) - 1));
   // the threads whose best reaches it
   u64 *owners = &sm.buf[0][0];
   if (key >= tau && key != 0) owners[atomicAdd(&sm.owners, 1)] = key;
@@ -378,10 +389,19 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   });
   if (wait) pa::cluster_wait();  // the first CTA runs: its shared memory can be written
   __syncthreads();
-  // As a rule there are not many more than W, and one warp sorts them (joining the warps' lists in every
-  // case cost 2 us more: 25.6 against 23.5).
+  // As a rule there are not many more than W, and one warp puts them in order (joining the warps' lists in
+  // every case cost 2 us more: 25.6 against 23.5).
+  int slot_at = lane;  // the place of this lane's candidate in the list
   if (sm.cands <= 32) {
-    if (warp == 0) k = sort32(lane < sm.cands ? sm.cand[lane] : 0ull, lane);
+    if (warp == 0) {
+      const int cands = sm.cands;
+      k = lane < cands ? sm.cand[lane] : 0ull;
+      slot_at = lane;  // those without a candidate fill the end
+      if (lane < cands) {
+        slot_at = 0;
+        for (int i = 0; i < cands; ++i) slot_at += sm.cand[i] > k;
+      }
+    }
   } else {
     // many (long runs of equal or rising values): each warp keeps its best 32 in order, then they are joined
     u64 mine = 0;
@@ -409,7 +429,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
     const bool bad = __any_sync(~0u, t < 0);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-    store_cluster(in_first_cta(&sm.list[slot][lane]), k);
+    store_cluster(in_first_cta(&sm.list[slot][slot_at]), k);
     if (lane == 0) {
       store_cluster(in_first_cta(&sm.max[slot]), top);
       store_cluster(in_first_cta(&sm.sum[slot]), (u64)(bad ? -1 : t));
@@ -440,10 +460,12 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
   if (!waited) pa::cluster_wait();
   pa::cluster_arrive();
   if (rank != 0) return;
+  // lane b of the last warp, while the others' lists arrive: the power of beam b's length
+  if (warp == kBeamWarps - 1) sm.inv[lane] = p.penalty == 0.f ? 1.0 : exp64(-(double)p.penalty * ln64((double)max(len, 1)));
   pa::cluster_wait();
 
   // ---- the first CTA.  Lane u < units of warp 0: its part's sum relative to the row's maximum; then
-  // lane b: beam b's lse and the power of its length.  The other warps join the rows' lists meanwhile.
+  // lane b: beam b's lse.  The other warps join the rows' lists meanwhile.
   if (warp == 0) {
     if (lane < units) {
       const int s0 = lane / p.parts * p.parts;
@@ -463,7 +485,6 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
       }
       // a sum that is NaN or 0 (nothing above -inf) has no logarithm
       sm.lse[lane] = sum > 0.0 ? (double)M + ln64(sum) : (double)NAN;
-      sm.inv[lane] = p.penalty == 0.f ? 1.0 : exp64(-(double)p.penalty * ln64((double)max(len, 1)));
     }
   } else if (p.parts > 1) {
     for (int b = warp - 1; b < p.W; b += kBeamWarps - 1) {
