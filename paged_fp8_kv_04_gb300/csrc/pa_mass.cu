@@ -180,10 +180,10 @@ struct Segment {
   Request q;
 };
 struct Walk {
-  int64_t at, end;
+  int at, end;  // tiles of the call, over all heads (their mass takes 512 bytes each: fewer than 2^31)
   Segment s;
   bool open;
-  __device__ Walk(int64_t a, int64_t b) : at(a), end(b), open(false) {}
+  __device__ Walk(int a, int b) : at(a), end(b), open(false) {}
   __device__ bool next(const MassParams &p, const MassSmem &sm) {
     if (open && s.tok0 + s.nr < s.q.ql) {
       s.tok0 += s.nr;
@@ -196,17 +196,16 @@ struct Walk {
     int lo = 0, hi = p.B - 1;  // the last request with tstart * Hkv <= at
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)sm.tstart[mid] * p.Hkv <= at)
+      if (sm.tstart[mid] * p.Hkv <= at)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const int nt = sm.tstart[lo + 1] - sm.tstart[lo];
-    const int64_t rem = at - (int64_t)sm.tstart[lo] * p.Hkv;
+    const int begin = sm.tstart[lo], nt = sm.tstart[lo + 1] - begin, rem = at - begin * p.Hkv;
     s.r = lo;
-    s.h = (int)(rem / nt);
-    s.t0 = (int)(rem - (int64_t)s.h * nt);
-    s.t1 = (int)min((int64_t)nt, s.t0 + (end - at));
+    s.h = p.Hkv == 1 ? 0 : rem / nt;
+    s.t0 = rem - s.h * nt;
+    s.t1 = min(nt, s.t0 + (end - at));
     s.q = Request{sm.info[3 * lo], sm.info[3 * lo + 1], sm.info[3 * lo + 2]};
     s.tok0 = 0;
     s.nr = min(kRows, s.q.ql);
@@ -242,7 +241,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 // ---------------------------------------------------------------------------- producer
 
 template <bool BF16>
-__device__ void run_producer(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b) {
+__device__ void run_producer(const MassParams &p, const MassSmem &sm, int a, int b) {
   const int lane = threadIdx.x & 31;
   const int nb = 32 / p.ppt, slot = lane / p.ppt, kpg = lane - slot * p.ppt;
   const uint64_t pol = pa::l2_evict_first_policy();
@@ -313,7 +312,7 @@ __device__ __forceinline__ uint32_t tmem_buf(const MassParams &p, int g, int k) 
 }
 
 template <bool BF16>
-__device__ void run_mma(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b, uint32_t tm) {
+__device__ void run_mma(const MassParams &p, const MassSmem &sm, int a, int b, uint32_t tm) {
   const int lane = threadIdx.x & 31;
   int seg = 0;
   Place at;
@@ -434,7 +433,7 @@ __device__ void convert_queries(const MassParams &p, const MassSmem &sm, const S
 }
 
 template <bool BF16>
-__device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int64_t a, int64_t b, uint32_t tm) {
+__device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int a, int b, uint32_t tm) {
   const int etid = threadIdx.x, lane = etid & 31, warp = etid >> 5, g = warp >> 2, quarter = warp & 3;
   const int tok = 32 * quarter + lane;  // of a tile: the TMEM lane
   const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
@@ -563,8 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mass_kernel(const __grid_con
   const uint32_t fl = scan_requests(p, sm);  // synchronises the CTA
   pa::tc_fence_after();
   if (blockIdx.x == 0 && fl) raise(p, fl);
-  const int64_t total = (int64_t)sm.tstart[p.B] * p.Hkv;
-  const int64_t a = total * blockIdx.x / gridDim.x, b = total * (blockIdx.x + 1) / gridDim.x;
+  // this CTA's tiles: an equal share, the first `more` CTAs with one more
+  const int total = sm.tstart[p.B] * p.Hkv, grid = (int)gridDim.x, cta = (int)blockIdx.x;
+  const int each = total / grid, more = total - each * grid;
+  const int a = cta * each + min(cta, more), b = a + each + (cta < more ? 1 : 0);
   if (a >= b) {  // the whole CTA
     if (warp == kEpiWarps + 1) pa::tmem_dealloc(sm.misc[0], p.tmem_cols);
     return;
