@@ -242,3 +242,44 @@ def test_reorder_flags_bad_pages():
     assert int(st[0]) == 0x1
     good, page = table[1, 1], table[0, 1]
     assert np.array_equal(new[0][good, :, :4], arrays[0][page, :, :4]) and np.array_equal(new[0][good, :, 4:], arrays[0][good, :, 4:])
+
+
+# ------------------------------------------------- how exactly totals and ranks are computed
+
+def test_length_penalties_are_exact_to_1e9():
+    """Ended beams whose ranks lie within an fp32 step of each other: the order is fp64's wherever they differ by
+    more than 1e-9 (relative), for lengths up to 2^31 - 1 and many penalties."""
+    rng = np.random.default_rng(12)
+    N = 4000
+    n = np.stack([rng.integers(1, 600, size=N), rng.integers(1, 600, size=N)], 1)
+    n[:50] = rng.integers(1, 2 ** 31 - 1, size=(50, 2))
+    for p in (0.6, 1.0, 0.25, 2.0, 1.7):
+        p32 = float(np.float32(p))
+        t1 = (-1 - 40 * rng.random(N)).astype(np.float32)
+        with np.errstate(over="ignore"):
+            t2 = (t1 * (n[:, 1] / n[:, 0]) ** p32).astype(np.float32)
+        rank = np.stack([t1 / n[:, 0].astype(np.float64) ** p32, t2 / n[:, 1].astype(np.float64) ** p32], 1)
+        gap = (rank[:, 0] - rank[:, 1]) / np.abs(rank[:, 0])
+        clear = np.abs(gap) > 1e-9
+        assert clear.sum() > N // 2 and np.abs(gap).max() < 1e-6
+        got = B.beam_select(torch.zeros(N, 2, 3, device="cuda"), dev(np.stack([t1, t2], 1)), eos=1,
+                            finished=torch.ones(N, 2, dtype=torch.uint8, device="cuda"), lengths=dev(n.astype(np.int32)), length_penalty=p)
+        assert np.array_equal((host(got[1])[:, 0] == 0)[clear], (gap > 0)[clear])
+
+
+@pytest.mark.parametrize("shift", [0.0, 11.5, -7.25])
+def test_logarithms_are_exact_to_1e9(shift):
+    """A live beam over V equal logits has total score - ln V; against an ended beam at the nearest fp32
+    number, the order is fp64's wherever they differ by more than 2e-9."""
+    rng = np.random.default_rng(13)
+    for V in list(range(1, 70)) + [100, 511, 512, 4099, 32771, 131072]:
+        N = 64
+        s1 = (-0.5 - 4 * rng.random(N)).astype(np.float32)
+        total = s1.astype(np.float64) - np.log(V)
+        s2 = total.astype(np.float32)
+        gap = total - s2.astype(np.float64)
+        clear = np.abs(gap) > 2e-9
+        fin = np.zeros((N, 2), np.uint8)
+        fin[:, 1] = 1
+        got = B.beam_select(torch.full((N, 2, V), shift, device="cuda"), dev(np.stack([s1, s2], 1)), eos=0, finished=dev(fin))
+        assert np.array_equal((host(got[1])[:, 0] == 0)[clear], (gap > 0)[clear]), V

@@ -322,3 +322,45 @@ def test_bindings_refuse_wrong_tensors():
         with pytest.raises((TypeError, ValueError, B.PaError)):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_calls_on_two_streams_at_once():
+    """The operators keep nothing between calls and share no workspace: two streams running them side by
+    side give what one gives."""
+    def work(seed):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        p = synth.make_problem(60 + seed, num_seqs=3, context_lens=[900, 2000, 4000], q_lens=[1, 2, 1], page_size=32)
+        d = dv.to_device(p)
+        lse = dev(O.decode(p)[1].astype(np.float32))
+        logits = torch.randn(3, 4, 40000, generator=g, device="cuda")
+        scores = torch.randn(3, 4, generator=g, device="cuda")
+        parents = torch.randint(0, 3, (1, 3), generator=g, device="cuda", dtype=torch.int32)
+        lens = torch.full((3,), 500, dtype=torch.int32, device="cuda")
+
+        def run():
+            c = [d[k].clone() for k in ("k_cache", "v_cache", "k_scale", "v_scale")]
+            m = B.attn_mass(d["q"], c[0], d["block_table"], d["context_lens"], d["cu_seqlens_q"], lse,
+                            torch.zeros(3, 1, 4000, device="cuda"), max_q_len=2, sm_scale=p.sm_scale, decay=0.0, k_scale=c[2])
+            keep, new = B.evict_select(m, d["context_lens"], budget=700, first=4, recent=64)
+            B.kv_compact(keep, new, d["block_table"], c[0], c[1], k_scale=c[2], v_scale=c[3], mass=m)
+            table = torch.empty_like(d["block_table"])
+            B.beam_reorder(parents, lens, d["block_table"], table, c[0], c[1], k_scale=c[2], v_scale=c[3])
+            t = B.beam_select(logits, scores)
+            return [m[:, :, :700].clone(), keep, new, table, *c, *t[:3]]
+        return run
+
+    runs = [work(1), work(2)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(runs[i]())
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        for g in many:
+            for a, b in zip(w, g):
+                assert torch.equal(a, b)
