@@ -21,13 +21,13 @@
 // stages; warp 17 issues the MMAs, up to two tiles ahead of each group.  Every wait is bounded.
 //
 // Bound by HBM: 132 B of keys and 8 B of mass per token against 4096 flop per query row.  Measured
-// (GB300): 8 requests x 131072 tokens, 143 MB, 27.1 us (5.3 TB/s); from twice that size the steady
+// (GB300): 8 requests x 131072 tokens, 143 MB, 27.4 us (5.2 TB/s); from twice that size the steady
 // rate is 6.66 TB/s, 0.98 of the 6.78 a copy measures, and some 6.6 us are launch, schedule, the
 // first tile's way through the roles and the last one's.  What it took: one thread per token on
 // fp32 arithmetic 173 us; this kernel with two epilogue groups and the MMAs issued by "lane 0"
 // 37 us; issued by an elected lane 30 us (without that the issue alone took 270 cycles per MMA);
 // launched ahead of the kernel before it 29 us; ring positions kept by counters, not by
-// divisions, 27 us.
+// divisions, 27 us.  Keys marked to leave L2 first: without that 29.2 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -562,10 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mass_kernel(const __grid_con
   const uint32_t fl = scan_requests(p, sm);  // synchronises the CTA
   pa::tc_fence_after();
   if (blockIdx.x == 0 && fl) raise(p, fl);
-  // this CTA's tiles: an equal share, the first `more` CTAs with one more
+  // this CTA's tiles: an equal share, the odd ones spread over the CTAs (all to the first ones: 27.7 us
+  // against 27.4 for 8 x 131072)
   const int total = sm.tstart[p.B] * p.Hkv, grid = (int)gridDim.x, cta = (int)blockIdx.x;
   const int each = total / grid, more = total - each * grid;
-  const int a = cta * each + min(cta, more), b = a + each + (cta < more ? 1 : 0);
+  const int a = cta * each + cta * more / grid, b = (cta + 1) * each + (cta + 1) * more / grid;
   if (a >= b) {  // the whole CTA
     if (warp == kEpiWarps + 1) pa::tmem_dealloc(sm.misc[0], p.tmem_cols);
     return;
