@@ -27,7 +27,7 @@ constexpr int kMaxReqs = 65535;
 // running maximum and sum of exponentials of its elements, and the vector its maximum came from.
 //   lse = m + log sum exp(x - m),  total = score + (x - lse).
 // Within a row the order of the totals is the order of the logits, so the W best of a part are
-// found without its lse: of the half warps' best elements the W-th, tau, bounds them from below, and
+// found without its lse: of the best elements of every 16 (or 8) threads the W-th, tau, bounds them from below, and
 // elements at or above tau lie with the few threads whose best does.  Only those threads'
 // elements are looked at again (from L2), whatever the values: keys are (value, index) pairs,
 // all different.  Every CTA leaves its list, maximum and sum in the shared memory of the
@@ -162,10 +162,12 @@ struct RowView {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxLists = kMaxBeams;  // rows * parts <= 32
 
+constexpr int kMaxCands = 256;        // elements at or above tau that are put in order at once
+
 struct BeamShared {
   u64 buf[kBeamWarps][32];
-  u64 half[32];                     // the best element of each half warp
-  u64 cand[32];                     // the part's elements at or above tau, in any order
+  u64 best[kBeamThreads / 8];       // the best element of every 16 or 8 threads
+  u64 cand[kMaxCands];              // the part's elements at or above tau, in any order
   int owners, cands;
   long long wsum[kBeamWarps];
   // the first CTA's
@@ -244,6 +246,43 @@ __device__ __forceinline__ u64 join_warps(u64 k, BeamShared &sm, int warp, int l
   return k;
 }
 
+// The W-th best of the best keys of every G threads (0: there are not as many), and the best one's value.
+template <int G>
+__device__ u64 lower_bound(u64 k, BeamShared &sm, int W, int tid, float &top) {
+  constexpr int kGroups = kBeamThreads / G, Q = kGroups / 32;
+  const int lane = tid & 31;
+#pragma unroll
+  for (int o = G / 2; o >= 1; o >>= 1) {
+    const u64 y = __shfl_xor_sync(~0u, k, o);
+    k = k > y ? k : y;
+  }
+  __syncthreads();  // an earlier part's readers are done
+  if (tid % G == 0) sm.best[tid / G] = k;
+  if (tid == 0) sm.owners = sm.cands = 0;
+  __syncthreads();
+  // (the keys differ but for 0, of which any will do: a key's place is the number of larger ones)
+  u64 mine[Q], tau = 0;
+  int place[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    mine[q] = sm.best[32 * q + lane];
+    place[q] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const u64 y = sm.best[i];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) place[q] += y > mine[q];
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const unsigned at_w = __ballot_sync(~0u, place[q] == W - 1), first = __ballot_sync(~0u, place[q] == 0);
+    if (at_w != 0) tau = __shfl_sync(~0u, mine[q], __ffs(at_w) - 1);
+    if (first != 0) top = key_value(__shfl_sync(~0u, mine[q], __ffs(first) - 1));
+  }
+  return tau;
+}
+
 // One part of one row: its list, maximum and sum go to slot `slot` of the first CTA.
 template <typename T>
 __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int part, int slot, bool wait) {
@@ -318,25 +357,11 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
     key = pair_key(m, at);
   }
 
-  // ---- tau: the W-th best of the half warps' best elements, so at least W elements reach it
-  u64 k = key;
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) {
-    const u64 y = __shfl_xor_sync(~0u, k, o);
-    k = k > y ? k : y;
-  }
-  __syncthreads();  // an earlier part's readers are done
-  if ((lane & 15) == 0) sm.half[tid >> 4] = k;
-  if (tid == 0) sm.owners = sm.cands = 0;
-  __syncthreads();
-  // (the keys differ but for 0, of which any will do: a key's place is the number of larger ones)
-  k = sm.half[lane];
-  int place = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) place += sm.half[i] > k;
-  const unsigned at_w = __ballot_sync(~0u, place == p.W - 1);
-  const u64 tau = at_w != 0 ? __shfl_sync(~0u, k, __ffs(at_w) - 1) : 0ull;
-  const float top = key_value(__shfl_sync(~0u, k, __ffs(__ballot_sync(~0u, place == 0)) - 1));
+  // ---- tau: the W-th of the best elements of every 16 threads, so at least W elements reach it.  With more
+  // beams of every 8: the fewer groups there are to spare, the lower tau lies and the more elements reach it
+  // (1 x 32 x 131072: 32.6 us with 8 against 61.6 with 16; 1 x 4 x 32001: 9.6 against 8.6)
+  float top;
+  const u64 tau = p.W <= 16 ? lower_bound<16>(key, sm, p.W, tid, top) : lower_bound<8>(key, sm, p.W, tid, top);
   // the threads whose best reaches it
   u64 *owners = &sm.buf[0][0];
   if (key >= tau && key != 0) owners[atomicAdd(&sm.owners, 1)] = key;
@@ -384,24 +409,22 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   search([&](const uint4 &v, int jl, unsigned left) {
     for (; left != 0; left &= left - 1) {
       const int at = atomicAdd(&sm.cands, 1);
-      if (at < 32) sm.cand[at] = element(v, jl, left);
+      if (at < kMaxCands) sm.cand[at] = element(v, jl, left);
     }
   });
   if (wait) pa::cluster_wait();  // the first CTA runs: its shared memory can be written
   __syncthreads();
-  // As a rule there are not many more than W, and one warp puts them in order (joining the warps' lists in
-  // every case cost 2 us more: 25.6 against 23.5).
-  int slot_at = lane;  // the place of this lane's candidate in the list
-  if (sm.cands <= 32) {
-    if (warp == 0) {
-      const int cands = sm.cands;
-      k = lane < cands ? sm.cand[lane] : 0ull;
-      slot_at = lane;  // those without a candidate fill the end
-      if (lane < cands) {
-        slot_at = 0;
-        for (int i = 0; i < cands; ++i) slot_at += sm.cand[i] > k;
-      }
+  // As a rule there are not many more than W: each is put in its place by counting the larger ones (joining
+  // the warps' lists in every case cost 2 us more: 25.6 against 23.5).
+  const int cands = sm.cands;
+  if (cands <= kMaxCands) {
+    if (tid < cands) {
+      const u64 c = sm.cand[tid];
+      int to = 0;
+      for (int i = 0; i < cands; ++i) to += sm.cand[i] > c;
+      if (to < kMaxBeams) store_cluster(in_first_cta(&sm.list[slot][to]), c);
     }
+    if (tid >= cands && tid < kMaxBeams) store_cluster(in_first_cta(&sm.list[slot][tid]), (u64)0);
   } else {
     // many (long runs of equal or rising values): each warp keeps its best 32 in order, then they are joined
     u64 mine = 0;
@@ -422,14 +445,14 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
       }
     });
     __syncthreads();  // the owners have been read
-    k = join_warps(mine, sm, warp, lane, kBeamWarps);
+    const u64 k = join_warps(mine, sm, warp, lane, kBeamWarps);
+    if (warp == 0) store_cluster(in_first_cta(&sm.list[slot][lane]), k);
   }
   if (warp == 0) {
     long long t = lane < kBeamWarps ? sm.wsum[lane] : 0;
     const bool bad = __any_sync(~0u, t < 0);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-    store_cluster(in_first_cta(&sm.list[slot][slot_at]), k);
     if (lane == 0) {
       store_cluster(in_first_cta(&sm.max[slot]), top);
       store_cluster(in_first_cta(&sm.sum[slot]), (u64)(bad ? -1 : t));
