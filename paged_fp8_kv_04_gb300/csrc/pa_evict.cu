@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;   // 16 measured slower: its barriers cost more than the halved stretches save
+constexpr int kMaxCluster = 8;   // and 16 where a row's keys then fit and do not with 8
 constexpr int kMaxKeys = 32;     // keys a thread can hold
 constexpr int kBatch = 16;       // masses a thread has on their way where it holds no keys (1 x 262144: 43.5 us, one at a time 55.7)
 
@@ -502,7 +502,8 @@ int evict_device() {
     int n = 0;
     const bool ok = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
                     move_opt_in(kv_compact_kernel<8, true>) && move_opt_in(kv_compact_kernel<16, true>) &&
-                    move_opt_in(kv_compact_kernel<8, false>) && move_opt_in(kv_compact_kernel<16, false>);
+                    move_opt_in(kv_compact_kernel<8, false>) && move_opt_in(kv_compact_kernel<16, false>) &&
+                    cudaFuncSetAttribute(evict_select_kernel<kMaxKeys>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
     sms[dev] = ok ? n : -1;
   });
   return sms[dev];
@@ -545,6 +546,10 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   int C = 1;
   while (C < kMaxCluster && a->mass_stride / (2 * C) >= 2048 &&
          (rows * 2 * C <= 2 * sms || a->mass_stride > (int64_t)C * kSelThreads * kMaxKeys))
+    C *= 2;
+  // 16 CTAs where the keys then fit after all: 1 row x 262144 18.8 us against 43.5 with 8, 16 rows 36.2
+  // against 43.6, 32 rows (which no longer run at once) 62.7 against 60.4.
+  if (a->mass_stride > (int64_t)C * kSelThreads * kMaxKeys && a->mass_stride <= (int64_t)2 * C * kSelThreads * kMaxKeys)
     C *= 2;
   // The keys a warp's stretch of the longest row gives each lane.  The loops are unrolled over the keys a
   // lane can have, so fewer is faster for short rows (1000 positions: 5.0 us with 4, 6.9 with 16, 9.4 with

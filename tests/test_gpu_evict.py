@@ -82,6 +82,15 @@ def test_select_very_long_rows():
     _select(_values("tail", rng, (1, 1, 900001)), [900001], 100000, 4, 1000)
 
 
+@pytest.mark.parametrize("kind", ["tail", "ties", "odd"])
+@pytest.mark.parametrize("n", [131073, 200000, 262144, 262145])
+def test_select_rows_of_the_widest_clusters_and_beyond(kind, n):
+    rng = np.random.default_rng(n)
+    mass = _values(kind, rng, (2, 2, n))
+    for budget in (1000, n // 2 + 1, n - 1):
+        _select(mass, [n, n - 77777], budget, 4, 64)
+
+
 def test_select_many_rows():
     rng = np.random.default_rng(4)
     mass = _values("tail", rng, (200, 3, 257))
