@@ -184,6 +184,9 @@ struct Walk {
   Segment s;
   bool open;
   __device__ Walk(int a, int b) : at(a), end(b), open(false) {}
+  // The epilogue group of tile t: in turn over the CTA's tiles, so that short segments spread over the groups
+  // too, and the same for all rows of a (request, head).
+  __device__ __forceinline__ int group(int t) const { return (at + t - s.t0) & (kGroups - 1); }
   __device__ bool next(const MassParams &p, const MassSmem &sm) {
     if (open && s.tok0 + s.nr < s.q.ql) {
       s.tok0 += s.nr;
@@ -326,7 +329,7 @@ __device__ void run_mma(const MassParams &p, const MassSmem &sm, int a, int b, u
     const int N = w.s.nr * (BF16 ? kG : 2 * kG);
     const uint32_t id = BF16 ? idesc_bf16(kTile, N) : pa::umma_idesc_e4m3(kTile, N, 0, 0);
     for (int t = w.s.t0; t < w.s.t1 && ok; ++t, at.advance(1, p.nstage)) {
-      const int st = at.st, g = t % kGroups;
+      const int st = at.st, g = w.group(t);
       int n = 0;
 #pragma unroll
       for (int x = 0; x < kGroups; ++x) n = x == g ? uses[x]++ : n;
@@ -462,7 +465,7 @@ __device__ void run_epilogue(const MassParams &p, const MassSmem &sm, int a, int
       return pos < s.q.L - s.q.ql && p.decay != 0.f ? p.mass[mrow + pos] : 0.f;
     };
     const float keep = s.tok0 > 0 ? 1.f : p.decay;
-    int t = s.t0 + ((g - s.t0) & (kGroups - 1));  // the group's first tile
+    int t = s.t0 + ((g - w.group(s.t0)) & (kGroups - 1));  // the group's first tile
     float old0 = before(t), old1 = before(t + kGroups);
     Place at = begin;
     at.advance(t - s.t0, p.nstage);
