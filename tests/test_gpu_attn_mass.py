@@ -71,6 +71,18 @@ def test_many_requests_and_heads():
     _check(p, 0.9)
 
 
+@pytest.mark.parametrize("kv,scale", [("fp8", "per_token"), ("bf16", "none")])
+@pytest.mark.parametrize("most", [1, 2, 9])
+def test_more_short_requests_than_sms(kv, scale, most):
+    """Many requests of a tile or two for every CTA, some of them without rows."""
+    rng = np.random.default_rng(most)
+    L = rng.integers(0, 200, size=900)
+    ql = np.where(rng.random(900) < 0.2, 0, rng.integers(1, most + 1, size=900)).clip(max=L)
+    p = synth.make_problem(24, num_seqs=900, context_lens=L, q_lens=ql, page_size=16, num_kv_heads=2, kv_dtype=kv,
+                           scale_mode=scale)
+    _check(p, 0.5)
+
+
 def test_wide_magnitudes():
     """Key rows over 2^-3 .. 2^3 and query elements over 2^-2 .. 2^2."""
     p = synth.make_problem(15, num_seqs=3, context_lens=[90, 300, 513], q_lens=[1, 2, 1], page_size=64,
