@@ -728,11 +728,14 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   const bool f32 = a->logits_dtype == PA_LOGITS_F32;
   const int sms = beam_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
-  // CTAs per request: as many as keep one wave (two CTAs per SM) and 16 KB of logits each.  32 x 8 x 131072:
-  // 23.5 us with 8, 31.8 with 4, 101 with 1; 1 x 4 x 32001 fp32: 9.3 us with 16 or 8, 9.5 with 4, 24.3 with 1.
+  // CTAs per request: as many as keep one wave (two CTAs per SM) and have a beam or 16 KB of logits each.
+  // 32 x 8 x 131072: 23.5 us with 8, 31.8 with 4, 101 with 1; 1 x 4 x 32001 fp32: 9.3 us with 16 or 8, 9.5
+  // with 4, 24.3 with 1; 1 x 8 x 1000: 9.0 us with 8, 33.6 with 1; 64 x 4 x 32000: 10.6 with 4, 18.2 with 8.
   const int64_t bytes = (int64_t)a->num_beams * a->vocab * (f32 ? 4 : 2);
   int C = 1;
-  while (C < kMaxCluster && (int64_t)a->num_reqs * C <= sms && bytes / (2 * C) >= 16384) C *= 2;
+  while (C < kMaxCluster && (int64_t)a->num_reqs * C <= sms &&
+         (C < a->num_beams || bytes / (2 * C) >= 16384))
+    C *= 2;
   p.parts = C > a->num_beams ? C / a->num_beams : 1;
   const pa_host::Launch run(dim3((unsigned)a->num_reqs * C), dim3(kBeamThreads), 0, stream, C);
   const cudaError_t e = f32 ? cudaLaunchKernelEx(run.cfg(), beam_select_kernel<float>, p)
