@@ -313,13 +313,26 @@ PyObject *evict_select(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.budget = int_arg(x[6], "budget");
     a.keep_first = int_arg(x[7], "first");
     a.keep_recent = int_arg(x[8], "recent");
-    // (the library refuses a budget below 1)
-    Output keep(x[2], "keep", ScalarType::Int, {s[0], s[1], a.budget > 0 ? a.budget : 1}, dev, stream, x[5] != Py_None);
-    Output lens(x[3], "new_lens", ScalarType::Int, s[0], dev, stream, x[5] != Py_None);
-    a.keep = keep.as<int32_t>();
-    a.new_lens = lens.as<int32_t>();
+    const int64_t width = a.budget > 0 ? a.budget : 1;  // (the library refuses a budget below 1)
+    const int64_t rows = s[0] * s[1];
+    const bool own_stream = x[5] != Py_None;
+    std::optional<Output> keep, lens;
+    // both in one allocation, unless holding on to the lengths would hold on to much
+    if (x[2] == Py_None && x[3] == Py_None && rows <= 16384 && rows * width <= 16384) {
+      const int64_t cells = rows * width;
+      std::optional<c10::cuda::CUDAStreamGuard> on;
+      if (own_stream) on.emplace(stream);
+      const Tensor block = at::empty({cells + s[0]}, at::TensorOptions().dtype(ScalarType::Int).device(at::kCUDA, (c10::DeviceIndex)dev));
+      keep.emplace(carve(block, 0, ScalarType::Int, {s[0], s[1], width}));
+      lens.emplace(carve(block, 4 * cells, ScalarType::Int, s[0]));
+    } else {
+      keep.emplace(x[2], "keep", ScalarType::Int, IntArrayRef({s[0], s[1], width}), dev, stream, own_stream);
+      lens.emplace(x[3], "new_lens", ScalarType::Int, s[0], dev, stream, own_stream);
+    }
+    a.keep = keep->as<int32_t>();
+    a.new_lens = lens->as<int32_t>();
     enqueue("pa_evict_select", g_lib.evict_select, a, dev, stream);
-    return Py_BuildValue("(NN)", keep.release(), lens.release());
+    return Py_BuildValue("(NN)", keep->release(), lens->release());
   });
 }
 
