@@ -55,35 +55,31 @@ constexpr int kBatch = 16;       // masses a thread has on their way where it ho
 // beyond C * 512 * 32 positions (KPT 0) are read again instead.  The key T of the last middle token
 // taken is found by counting keys in 2048 bins of the range that still holds it: the top 11 bits,
 // then the 11 bits below them of the keys in one bin, then the last 10.  The CTAs' counts meet
-// through distributed shared memory: each CTA sums its share of the bins, then all read the
-// shares' totals and the one share that matters (8 KB of traffic per CTA and step in place of
-// 64 KB).  A bin that is taken whole ends the search early.  Then the kept positions are written in order: those above T and the
-// first `need` equal to it, at offsets from the counts of the warps and CTAs before.
+// through distributed shared memory: each CTA sums its share of the bins and sends the sums to all, 16
+// bytes per thread and direction in place of 64 KB per CTA.  They are stores: loads of what the others
+// have left measured a round trip more each.  A bin that is taken whole ends the search early.  Then the
+// kept positions are written in order: those above T and the first `need` equal to it, at offsets from
+// the counts of the warps and CTAs before.
 struct SelectShared {
-  uint32_t hist[2][kBins];
-  uint32_t part[kBins];          // this CTA's share of the bins, from each CTA of the cluster
-  uint32_t share[kBins];         // and summed: the first kBins / C of these
-  int share_total[2];
-  int total[2];                  // this CTA's keys equal to T, and certain ones
+  uint32_t hist[kBins];          // this CTA's keys
+  uint32_t part[kBins];          // its share of the bins, from each CTA of the cluster
+  uint32_t own[kBins / 2];       // and summed
+  uint32_t all[kBins];           // the cluster's keys
+  uint2 totals[2 * kMaxCluster];  // of each CTA: keys equal to T, and certain ones
   int weq[kSelWarps], wsure[kSelWarps], scan[kSelWarps];
   int pick[3];                   // the chosen bin, keys above it, keys in it
 };
 
-// 16 or 8 bytes at this shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ uint4 load_cluster4(const void *p, uint32_t rank) {
+// Stores to this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ void push_cluster(void *p, uint32_t rank, const uint4 &v) {
   uint32_t a;
-  uint4 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ uint2 load_cluster(const void *p, uint32_t rank) {
+__device__ __forceinline__ void push_cluster(void *p, uint32_t rank, const uint2 &v) {
   uint32_t a;
-  uint2 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Inclusive prefix sum over the warp.
@@ -118,6 +114,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     for (int64_t i = gid; i < p.budget; i += gsz) keep[i] = i < n ? (int)i : -1;
     return;
   }
+  pa::cluster_arrive();
   // this warp's positions [wb, we), and of the row the middle ones [mlo, mhi)
   const int stretch = ((L + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31;
   const int wb = (int)min((int64_t)(rank * kSelWarps + warp) * stretch, (int64_t)L);
@@ -155,8 +152,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 #pragma unroll
     for (int u = 0; u < KPT; ++u) key[u] = (unsigned)(wb + 32 * u + lane - lo) < count ? mass_key(x[u]) : 0u;
   }
-  for (int b = tid; b < kBins; b += kSelThreads) sm.hist[0][b] = 0;
+  static_assert(kBins == 4 * kSelThreads, "four bins per thread");
+  uint4 *hist4 = reinterpret_cast<uint4 *>(sm.hist) + tid;
+  *hist4 = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
+  pa::cluster_wait();  // every CTA of the cluster runs: its shared memory can be written
 
   uint32_t T = 0xFFFFFFFFu;  // with want 0 nothing of the middle stays
   int need = 0;
@@ -165,31 +165,29 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     uint32_t base = 1, span = 0xFFFFFFFEu;
     need = want;
     for (int step = 0;; ++step) {
-      uint32_t *hist = sm.hist[step & 1];
       const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
       if (KPT > 0) {
 #pragma unroll
         for (int u = 0; u < KPT; ++u) {
           const uint32_t d = key[u] - base;
-          if (d <= span) atomicAdd(hist + (d >> shift), 1u);
+          if (d <= span) atomicAdd(sm.hist + (d >> shift), 1u);
         }
       } else {
         batches(lo, hi, [&](int, uint32_t k) {
           const uint32_t d = k - base;
-          if (d <= span) atomicAdd(hist + (d >> shift), 1u);
+          if (d <= span) atomicAdd(sm.hist + (d >> shift), 1u);
         });
       }
-      pa::cluster_sync();
-      const int quads = kBins / 4 / C;
-      for (int b = tid; b < kBins; b += kSelThreads) sm.hist[(step + 1) & 1][b] = 0;  // read by all a step ago
-      int src = 0, above = 0;
+      __syncthreads();
+      uint4 c = *hist4;
+      *hist4 = make_uint4(0u, 0u, 0u, 0u);
       if (C > 1) {
-        // sum this CTA's share: every thread fetches four bins of it from one CTA
-        const int q = tid / quads, e4 = tid - q * quads;
-        *reinterpret_cast<uint4 *>(sm.part + 4 * tid) = load_cluster4(hist + 4 * (rank * quads + e4), q);
-        __syncthreads();
+        // four bins per thread, to the CTA that sums them, and the sums to all
+        const int quads = kBins / 4 / C, q = tid / quads, e4 = tid - q * quads;
+        push_cluster(sm.part + 4 * (rank * quads + e4), q, c);
+        pa::cluster_sync();
         if (tid < quads) {
-          uint4 c = make_uint4(0u, 0u, 0u, 0u);
+          c = make_uint4(0u, 0u, 0u, 0u);
           for (int k = 0; k < C; ++k) {
             const uint4 x = *reinterpret_cast<const uint4 *>(sm.part + 4 * (k * quads + tid));
             c.x += x.x;
@@ -197,32 +195,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
             c.z += x.z;
             c.w += x.w;
           }
-          *reinterpret_cast<uint4 *>(sm.share + 4 * tid) = c;
+          *reinterpret_cast<uint4 *>(sm.own + 4 * tid) = c;
         }
-        int mine = 0;
-        if (tid < quads) {
-          const uint4 c = *reinterpret_cast<const uint4 *>(sm.share + 4 * tid);
-          mine = (int)(c.x + c.y + c.z + c.w);
-        }
-        mine = __reduce_add_sync(~0u, mine);
-        if (lane == 0) sm.scan[warp] = mine;
         __syncthreads();
-        if (warp == 0) {
-          const int t = __reduce_add_sync(~0u, lane < kSelWarps ? sm.scan[lane] : 0);
-          if (lane == 0) sm.share_total[0] = t;
-        }
+        push_cluster(sm.all + 4 * (rank * quads + e4), q, *reinterpret_cast<const uint4 *>(sm.own + 4 * e4));
         pa::cluster_sync();
-        // the share that holds the want-th key from the top, then its bins
-        const int tot = lane < C ? (int)load_cluster(sm.share_total, lane).x : 0, upto = warp_scan(tot, lane);
-        const int over = __shfl_sync(~0u, upto, C - 1) - upto;  // keys in the shares after the lane's
-        // (one lane finds it; none only if the masses change under the call)
-        src = max(__ffs(__ballot_sync(~0u, lane < C && over < need && need <= over + tot)) - 1, 0);
-        above = __shfl_sync(~0u, over, src);
+        c = *reinterpret_cast<const uint4 *>(sm.all + 4 * tid);
       }
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);
-      if (tid < quads) c = C > 1 ? load_cluster4(sm.share + 4 * tid, src) : *reinterpret_cast<const uint4 *>(hist + 4 * tid);
+      // the bin that holds the want-th key from the top (one thread finds it; none only if the masses change
+      // under the call)
+      int above = 0;
       const int four = (int)(c.x + c.y + c.z + c.w), incl = warp_scan(four, lane);
-      __syncthreads();  // sm.scan has been read
       if (lane == 31) sm.scan[warp] = incl;
       __syncthreads();
       const int w = lane < kSelWarps ? sm.scan[lane] : 0, wincl = warp_scan(w, lane);
@@ -231,7 +214,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 #pragma unroll
       for (int e = 3; e >= 0; --e) {
         if (above < need && need <= above + (int)bins[e]) {
-          sm.pick[0] = 4 * (src * quads + tid) + e;
+          sm.pick[0] = 4 * tid + e;
           sm.pick[1] = above;
           sm.pick[2] = (int)bins[e];
         }
@@ -282,14 +265,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   if (warp == 0) {
     const int e = __reduce_add_sync(~0u, lane < kSelWarps ? sm.weq[lane] : 0);
     const int y = __reduce_add_sync(~0u, lane < kSelWarps ? sm.wsure[lane] : 0);
-    if (lane == 0) {
-      sm.total[0] = e;
-      sm.total[1] = y;
-    }
+    if (lane < C) push_cluster(&sm.totals[rank], lane, make_uint2((uint32_t)e, (uint32_t)y));
   }
-  pa::cluster_sync();
-  const uint2 ct = lane < C ? load_cluster(sm.total, lane) : make_uint2(0u, 0u);
-  pa::cluster_arrive();  // no CTA leaves before the others have read its totals
+  pa::cluster_sync();  // the last access to another CTA's memory is behind it
+  const uint2 ct = lane < C ? sm.totals[lane] : make_uint2(0u, 0u);
   const int ceq = (int)ct.x, ceq_before = warp_scan(ceq, lane) - ceq;
   const int ckept = (int)ct.y + ties_taken(need, ceq_before, ceq);
   const int cstart = warp_scan(ckept, lane) - ckept;
@@ -326,7 +305,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   } else {
     batches(wb, we, [&](int i, uint32_t k) { emit(i, k > T || always(i), k == T); });
   }
-  pa::cluster_wait();
 }
 
 // -------------------------------------------------------------------------- compaction
