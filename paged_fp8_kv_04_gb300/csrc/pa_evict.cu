@@ -56,8 +56,8 @@ constexpr int kBatch = 16;       // masses a thread has on their way where it ho
 // taken is found by counting keys in 2048 bins of the range that still holds it: the top 11 bits,
 // then the 11 bits below them of the keys in one bin, then the last 10.  The CTAs' counts meet
 // through distributed shared memory: each CTA sums its share of the bins and sends the sums to all, 16
-// bytes per thread and direction in place of 64 KB per CTA.  They are stores: loads of what the others
-// have left measured a round trip more each.  A bin that is taken whole ends the search early.  Then the
+// bytes per thread and direction in place of 64 KB per CTA.  They are asynchronous stores that the
+// receiver counts: loads of what the others have left, or cluster barriers, measured a round trip more.  A bin that is taken whole ends the search early.  Then the
 // kept positions are written in order: those above T and the first `need` equal to it, at offsets from
 // the counts of the warps and CTAs before.
 struct SelectShared {
@@ -66,20 +66,45 @@ struct SelectShared {
   uint32_t own[kBins / 2];       // and summed
   uint32_t all[kBins];           // the cluster's keys
   uint2 totals[2 * kMaxCluster];  // of each CTA: keys equal to T, and certain ones
+  uint64_t bars[3];              // part, all, totals: what the cluster sends has arrived
   int weq[kSelWarps], wsure[kSelWarps], scan[kSelWarps];
   int pick[3];                   // the chosen bin, keys above it, keys in it
 };
 
-// Stores to this shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ void push_cluster(void *p, uint32_t rank, const uint4 &v) {
+// Asynchronous stores to this shared-memory address in CTA `rank` of the cluster, which count towards
+// the barrier `bar` there.
+__device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  return a;
 }
-__device__ __forceinline__ void push_cluster(void *p, uint32_t rank, const uint2 &v) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pa::smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+__device__ __forceinline__ void push_cluster(void *p, uint64_t *bar, uint32_t rank, const uint4 &v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(in_cta(p, rank)),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(in_cta(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void push_cluster(void *p, uint64_t *bar, uint32_t rank, const uint2 &v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(in_cta(p, rank)),
+               "r"(v.x), "r"(v.y), "r"(in_cta(bar, rank))
+               : "memory");
+}
+
+// A bounded wait for a phase of what the cluster sends; false if it gave up.
+__device__ __forceinline__ bool wait_cluster(const uint64_t *bar, uint32_t parity) {
+  const uint32_t a = pa::smem_u32(bar);
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > pa::kWaitCycles) return false;
+  }
 }
 
 // Inclusive prefix sum over the warp.
@@ -125,7 +150,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     for (int64_t i = gid; i < p.budget; i += gsz) keep[i] = i < n ? (int)i : -1;
     return;
   }
+  if (C > 1 && tid == 0) {
+    for (int b = 0; b < 3; ++b) pa::mbar_init(pa::smem_u32(&sm.bars[b]), 1);
+    pa::fence_barrier_init();
+    pa::mbar_arrive_expect_tx(pa::smem_u32(&sm.bars[2]), C * sizeof(uint2));
+  }
   pa::cluster_arrive();
+  // A wait for what the cluster sends.  Where one runs out (bounded: it does not) the request is flagged, and
+  // no CTA leaves while another may still send to it.
+  auto arrived = [&](int b, uint32_t parity) { return wait_cluster(&sm.bars[b], parity); };
+  auto give_up = [&]() {
+    if (tid == 0 && p.status != nullptr) atomicOr(p.status, PA_DEV_TIMEOUT);
+    pa::cluster_sync();
+  };
   // of the row the middle positions [mlo, mhi)
   const int we = (int)max((int64_t)wb, min((int64_t)wb + stretch, (int64_t)L));
   const int mlo = p.first, mhi = L - p.recent, want = p.budget - p.first - p.recent;
@@ -186,8 +223,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       if (C > 1) {
         // four bins per thread, to the CTA that sums them, and the sums to all
         const int quads = kBins / 4 / C, q = tid / quads, e4 = tid - q * quads;
-        push_cluster(sm.part + 4 * (rank * quads + e4), q, c);
-        pa::cluster_sync();
+        if (tid == 0) {
+          pa::mbar_arrive_expect_tx(pa::smem_u32(&sm.bars[0]), sizeof(sm.part));
+          pa::mbar_arrive_expect_tx(pa::smem_u32(&sm.bars[1]), sizeof(sm.all));
+        }
+        push_cluster(sm.part + 4 * (rank * quads + e4), &sm.bars[0], q, c);
+        bool ok = arrived(0, step & 1);
         if (tid < quads) {
           c = make_uint4(0u, 0u, 0u, 0u);
           for (int k = 0; k < C; ++k) {
@@ -199,9 +240,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
           }
           *reinterpret_cast<uint4 *>(sm.own + 4 * tid) = c;
         }
-        __syncthreads();
-        push_cluster(sm.all + 4 * (rank * quads + e4), q, *reinterpret_cast<const uint4 *>(sm.own + 4 * e4));
-        pa::cluster_sync();
+        if (__syncthreads_or(!ok)) return give_up();
+        push_cluster(sm.all + 4 * (rank * quads + e4), &sm.bars[1], q, *reinterpret_cast<const uint4 *>(sm.own + 4 * e4));
+        ok = arrived(1, step & 1);
+        if (__syncthreads_or(!ok)) return give_up();
         c = *reinterpret_cast<const uint4 *>(sm.all + 4 * tid);
       }
       // the bin that holds the want-th key from the top (one thread finds it; none only if the masses change
@@ -267,9 +309,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   if (warp == 0) {
     const int e = __reduce_add_sync(~0u, lane < kSelWarps ? sm.weq[lane] : 0);
     const int y = __reduce_add_sync(~0u, lane < kSelWarps ? sm.wsure[lane] : 0);
-    if (lane < C) push_cluster(&sm.totals[rank], lane, make_uint2((uint32_t)e, (uint32_t)y));
+    if (C == 1)
+      sm.totals[0] = make_uint2((uint32_t)e, (uint32_t)y);
+    else if (lane < C)
+      push_cluster(&sm.totals[rank], &sm.bars[2], lane, make_uint2((uint32_t)e, (uint32_t)y));
   }
-  pa::cluster_sync();  // the last access to another CTA's memory is behind it
+  if (__syncthreads_or(C > 1 && !arrived(2, 0))) return give_up();
   const uint2 ct = lane < C ? sm.totals[lane] : make_uint2(0u, 0u);
   const int ceq = (int)ct.x, ceq_before = warp_scan(ceq, lane) - ceq;
   const int ckept = (int)ct.y + ties_taken(need, ceq_before, ceq);
