@@ -2,9 +2,9 @@
 // pa_kv_compact moves them to the front of their pages.  See include/pa.h for the contract.
 //
 // The selection has little to read (4 B per position) and is bound by its dependent steps:
-// measured on 16 rows x 131072 (8.4 MB, 1.3 us at HBM rate) 19.0 us, of which the masses take 5, a
-// counting step 3 to 4 (two cluster barriers and the exchange between them, two or three steps as a rule),
-// counting and writing 3.  One CTA per row, bit by bit, took 475 us.
+// measured on 16 rows x 131072 (8.4 MB, 1.3 us at HBM rate) 17.4 us, of which the masses take 2.5, a
+// counting step 3 (counting, two exchanges of 0.5 to 0.7 each, the pick; two or three steps as a rule), counting
+// and writing 3; some SMs have CTAs of two rows (8 rows: 13.8 us).  One CTA per row, bit by bit, took 475 us.
 // The compaction is bound by HBM: 528 B and more per kept token.  32 x 8192 tokens into other pages, 142 MB,
 // take 27.2 us (5.2 TB/s, 0.77 of a copy's rate); 8 x 4095 in place 6.5 us.  One CTA per row
 // took 203 and 70 us; rows carried in registers 33 and 10 us.
@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;   // and 16 where a row's keys then fit and do not with 8
+constexpr int kMaxCluster = 8;   // and twice that where it pays
 constexpr int kMaxKeys = 32;     // keys a thread can hold
 constexpr int kBatch = 16;       // masses a thread has on their way where it holds no keys (1 x 262144: 43.5 us, one at a time 55.7)
 
@@ -510,9 +510,13 @@ __global__ void __launch_bounds__(kMoveThreads, 3) kv_compact_kernel(const Compa
   }
 }
 
+// Clusters of more than 8 CTAs.
+template <typename Params>
+bool wide_opt_in(void (*kernel)(Params)) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+}
 bool move_opt_in(void (*kernel)(CompactParams)) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) == cudaSuccess &&
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) == cudaSuccess && wide_opt_in(kernel);
 }
 
 // The current device's SM count, and its kernels' opt-ins, once per device; 0 for a
@@ -528,7 +532,8 @@ int evict_device() {
     const bool ok = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
                     move_opt_in(kv_compact_kernel<8, true>) && move_opt_in(kv_compact_kernel<16, true>) &&
                     move_opt_in(kv_compact_kernel<8, false>) && move_opt_in(kv_compact_kernel<16, false>) &&
-                    cudaFuncSetAttribute(evict_select_kernel<kMaxKeys>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+                    wide_opt_in(evict_select_kernel<4>) && wide_opt_in(evict_select_kernel<16>) &&
+                    wide_opt_in(evict_select_kernel<kMaxKeys>) && wide_opt_in(evict_select_kernel<0>);
     sms[dev] = ok ? n : -1;
   });
   return sms[dev];
@@ -565,20 +570,18 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   const int sms = evict_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per row: more while each keeps 2048 positions and all run at once (two per SM), or
-  // while a row's keys do not fit their registers.  16 rows x 131072: 19.0 us with 8 CTAs per row, 54.9 with 4
-  // (whose keys no longer fit), 29.8 with 16; 4 rows x 1000: 5.0 us with one CTA, 7.4 with two or more.
+  // while a row's keys do not fit their registers.  16 rows x 131072: 17.4 us with 8 CTAs per row; 4 rows x
+  // 1000: 4.0 us with one CTA; 1 x 4096 6.5 with two, 1 x 2048 4.4 with one and 6.3 with two.
   const int64_t rows = (int64_t)a->num_seqs * a->num_kv_heads;
+  auto fits = [&](int ctas) { return a->mass_stride <= (int64_t)ctas * kSelThreads * kMaxKeys; };
   int C = 1;
-  while (C < kMaxCluster && a->mass_stride / (2 * C) >= 2048 &&
-         (rows * 2 * C <= 2 * sms || a->mass_stride > (int64_t)C * kSelThreads * kMaxKeys))
-    C *= 2;
-  // 16 CTAs where the keys then fit after all: 1 row x 262144 18.8 us against 43.5 with 8, 16 rows 36.2
-  // against 43.6, 32 rows (which no longer run at once) 62.7 against 60.4.
-  if (a->mass_stride > (int64_t)C * kSelThreads * kMaxKeys && a->mass_stride <= (int64_t)2 * C * kSelThreads * kMaxKeys)
-    C *= 2;
+  while (C < kMaxCluster && a->mass_stride / (2 * C) >= 2048 && (rows * 2 * C <= 2 * sms || !fits(C))) C *= 2;
+  // 16 CTAs where each has an SM for itself (4 rows x 131072: 11.4 us against 14.4), or where the keys then
+  // fit after all (1 row x 262144: 12.6 us against 43.5 with 8, 16 rows 29.5 against 43.6).
+  if (C == kMaxCluster && a->mass_stride / (2 * C) >= 2048 && (rows * 2 * C <= sms || (!fits(C) && fits(2 * C)))) C *= 2;
   // The keys a warp's stretch of the longest row gives each lane.  The loops are unrolled over the keys a
-  // lane can have, so fewer is faster for short rows (1000 positions: 5.0 us with 4, 6.9 with 16, 9.4 with
-  // 32), and keeping them beats reading them again (131072: 19.0 us with 32, 34.3 re-read).
+  // lane can have, so fewer is faster for short rows (4 x 1000: +1.9 us with 16, +4.4 with 32), and keeping
+  // them beats reading them again (16 x 131072: 17.4 us with 32, twice that re-read).
   const int64_t warps = (int64_t)C * kSelWarps;
   const int64_t keys = (((int64_t)a->mass_stride + warps - 1) / warps + 31) / 32;
   const pa_host::Launch run(dim3((unsigned)(rows * C)), dim3(kSelThreads), 0, stream, C);
