@@ -21,7 +21,7 @@
 // stages; warp 17 issues the MMAs, up to two tiles ahead of each group.  Every wait is bounded.
 //
 // Bound by HBM: 132 B of keys and 8 B of mass per token against 4096 flop per query row.  Measured
-// (GB300): 8 requests x 131072 tokens, 143 MB, 27.4 us (5.2 TB/s); from twice that size the steady
+// (GB300): 8 requests x 131072 tokens, 143 MB, 27.2 us (5.2 TB/s); from twice that size the steady
 // rate is 6.66 TB/s, 0.98 of the 6.78 a copy measures, and some 6.6 us are launch, schedule, the
 // first tile's way through the roles and the last one's.  What it took: one thread per token on
 // fp32 arithmetic 173 us; this kernel with two epilogue groups and the MMAs issued by "lane 0"
@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mass_kernel(const __grid_con
   const uint32_t fl = scan_requests(p, sm);  // synchronises the CTA
   pa::tc_fence_after();
   if (blockIdx.x == 0 && fl) raise(p, fl);
-  // this CTA's tiles: an equal share, the odd ones spread over the CTAs (all to the first ones: 27.7 us
-  // against 27.4 for 8 x 131072)
+  // this CTA's tiles: an equal share, the odd ones spread over the CTAs (all to the first ones: 0.3 us
+  // more for 8 x 131072)
   const int total = sm.tstart[p.B] * p.Hkv, grid = (int)gridDim.x, cta = (int)blockIdx.x;
   const int each = total / grid, more = total - each * grid;
   const int a = cta * each + cta * more / grid, b = (cta + 1) * each + (cta + 1) * more / grid;
