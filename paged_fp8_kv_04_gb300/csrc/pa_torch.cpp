@@ -210,9 +210,11 @@ Tensor carve(const Tensor &block, int64_t at, ScalarType type, IntArrayRef shape
 }
 
 // Calls an entry point on the device and stream; a status other than PA_OK becomes the error class.
+// An empty batch enqueues nothing (torch's empty tensors have no pointer that the library could check).
 template <typename Args>
-void enqueue(const char *name, pa_status_t (*entry)(const Args *, void *), const Args &a, int dev,
+void enqueue(const char *name, pa_status_t (*entry)(const Args *, void *), const Args &a, bool empty, int dev,
              const c10::cuda::CUDAStream &stream) {
+  if (empty) return;
   if (entry == nullptr) throw Refusal(PyExc_RuntimeError, "the library is not bound");
   pa_status_t st;
   if (c10::cuda::current_device() == dev) {
@@ -290,7 +292,7 @@ PyObject *attn_mass(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.sm_scale = x[12] == Py_None ? (float)(1.0 / std::sqrt((double)c[3])) : float_arg(x[12]);
     a.decay = float_arg(x[13]);
     a.k_scale_scalar = float_arg(x[14]);
-    enqueue("pa_attn_mass", g_lib.attn_mass, a, dev, stream_arg(x[10], dev));
+    enqueue("pa_attn_mass", g_lib.attn_mass, a, B == 0 || qs[0] == 0, dev, stream_arg(x[10], dev));
     Py_INCREF(out);
     return out;
   });
@@ -331,7 +333,7 @@ PyObject *evict_select(PyObject *, PyObject *const *x, Py_ssize_t n) {
     }
     a.keep = keep->as<int32_t>();
     a.new_lens = lens->as<int32_t>();
-    enqueue("pa_evict_select", g_lib.evict_select, a, dev, stream);
+    enqueue("pa_evict_select", g_lib.evict_select, a, s[0] == 0, dev, stream);
     return Py_BuildValue("(NN)", keep->release(), lens->release());
   });
 }
@@ -366,7 +368,7 @@ PyObject *kv_compact(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.num_seqs = int_of(B, "keep");
     a.keep_stride = int_of(ks[2], "keep");
     a.block_table_stride = int_of(ts[1], "block_table");
-    enqueue("pa_kv_compact", g_lib.kv_compact, a, dev, stream_arg(x[11], dev));
+    enqueue("pa_kv_compact", g_lib.kv_compact, a, B == 0, dev, stream_arg(x[11], dev));
     Py_RETURN_NONE;
   });
 }
@@ -413,7 +415,7 @@ PyObject *beam_select(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.length_penalty = float_arg(x[11]);
     // the outputs that are not given share one allocation, each 16-byte aligned in it
     const int64_t words = (4 * N * W + 15) / 16 * 16, bytes = (N * W + 15) / 16 * 16;
-    const bool ends = a.finished != nullptr || x[7] != Py_None, lasts = a.lengths != nullptr || x[8] != Py_None;
+    const bool ends = x[2] != Py_None || x[7] != Py_None, lasts = x[3] != Py_None || x[8] != Py_None;
     Tensor block;
     int64_t at = 0;
     auto output = [&](std::optional<Output> &o, int i, const char *name, ScalarType type, int64_t size) {
@@ -444,7 +446,7 @@ PyObject *beam_select(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.tokens = tokens->as<int32_t>();
     a.parents = parents->as<int32_t>();
     a.scores_out = totals->as<float>();
-    enqueue("pa_beam_select", g_lib.beam_select, a, dev, stream);
+    enqueue("pa_beam_select", g_lib.beam_select, a, N == 0, dev, stream);
     Output none;
     return Py_BuildValue("(NNNNN)", tokens->release(), parents->release(), totals->release(),
                          ended ? ended->release() : none.release(), lens ? lens->release() : none.release());
@@ -488,7 +490,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.num_reqs = int_of(s[0], "parents");
     a.num_beams = int_of(s[1], "parents");
     a.block_table_stride = int_of(ts[1], "block_table");
-    enqueue("pa_beam_reorder", g_lib.beam_reorder, a, dev, stream_arg(x[10], dev));
+    enqueue("pa_beam_reorder", g_lib.beam_reorder, a, s[0] == 0, dev, stream_arg(x[10], dev));
     Py_RETURN_NONE;
   });
 }

@@ -364,3 +364,34 @@ def test_calls_on_two_streams_at_once():
         for g in many:
             for a, b in zip(w, g):
                 assert torch.equal(a, b)
+
+
+def test_empty_batches_enqueue_nothing():
+    """No requests, or none with rows in this step: the outputs exist, and nothing is touched."""
+    k = torch.full((4, 1, 16, 128), 7, dtype=torch.uint8, device="cuda")
+    v = k.clone()
+    scale = torch.ones(4, 1, 16, device="cuda")
+
+    def ints(*shape):
+        return torch.zeros(shape, dtype=torch.int32, device="cuda")
+
+    def floats(*shape):
+        return torch.zeros(shape, device="cuda")
+
+    q = torch.zeros(0, 16, 128, dtype=torch.bfloat16, device="cuda")
+    none = floats(0, 1, 64)
+    assert B.attn_mass(q, k, ints(0, 4), ints(0), ints(1), floats(0, 16), none, max_q_len=1, k_scale=scale).shape == (0, 1, 64)
+    idle = torch.full((2, 1, 64), 3.0, device="cuda")
+    B.attn_mass(q, k, ints(2, 4), ints(2), ints(3), floats(0, 16), idle, max_q_len=1, k_scale=scale, decay=0.5)
+    assert torch.all(idle == 3.0)
+    keep, new = B.evict_select(none, ints(0), budget=8)
+    assert keep.shape == (0, 1, 8) and new.shape == (0,)
+    B.kv_compact(keep, new, ints(0, 4), k, v, k_scale=scale, v_scale=scale)
+    B.kv_compact(keep, new, ints(0, 4), k, v, dst_block_table=ints(0, 2), mass=none, mass_out=floats(0, 1, 8))
+    out = B.beam_select(floats(0, 4, 1000), floats(0, 4), eos=2, finished=torch.zeros(0, 4, dtype=torch.uint8, device="cuda"),
+                        lengths=ints(0, 4), length_penalty=0.6)
+    assert [tuple(x.shape) for x in out] == [(0, 4)] * 5
+    B.beam_reorder(ints(0, 4), ints(0), ints(0, 4), ints(0, 4), k, v, k_scale=scale, v_scale=scale,
+                   states=[(floats(0, 32), floats(0, 32))])
+    torch.cuda.synchronize()
+    assert torch.all(k == 7) and torch.all(v == 7)
