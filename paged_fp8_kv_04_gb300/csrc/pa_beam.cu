@@ -27,16 +27,17 @@ constexpr int kMaxReqs = 65535;
 // running maximum and sum of exponentials of its elements, and the vector its maximum came from.
 //   lse = m + log sum exp(x - m),  total = score + (x - lse).
 // Within a row the order of the totals is the order of the logits, so the W best of a part are
-// found without its lse: of the best elements of every 16 (or 8) threads the W-th, tau, bounds them from below, and
-// elements at or above tau lie with the few threads whose best does.  Only those threads'
+// found without its lse: of the best elements of every 16 (or 8) threads the W-th, tau, bounds them
+// from below, and elements at or above tau lie with the few threads whose best does.  Only those threads'
 // elements are looked at again (from L2), whatever the values: keys are (value, index) pairs,
 // all different.  Every CTA leaves its list, maximum and sum in the shared memory of the
 // cluster's first CTA, one cluster barrier follows, and a warp there joins parts and beams.
 //
 // Bound by HBM while the logits stream, then by the chain of joins.  Measured: 32 requests x 8 beams x
-// 131072 bf16, 67 MB (9.9 us at a copy's rate), 23.5 us: 11 to 13 us of streaming (5.3 TB/s), 2 to tau, 2 to
-// the part's list, 2 for the barrier, 4 in the first CTA, 2 of launch; 1 x 4 x 32001 fp32 9.3 us.  One CTA per
-// request and one pass per candidate took 1644 and 152 us.
+// 131072 bf16, 67 MB (9.9 us at a copy's rate), 21.4 us: 11 to 13 us of streaming (5.5 TB/s), 2 to tau, 2 to
+// the part's list, 2 for the barrier, 2 in the first CTA, 2 of launch; 1 x 4 x 32001 fp32 8.6 us.  One CTA per
+// request and one pass per candidate took 1644 and 152 us.  Lists sent as asynchronous stores that an mbarrier
+// counts, in place of stores and a cluster barrier, cost 0.5 us more: some hundred 8-byte transactions.
 struct BeamParams {
   const void *logits;
   const float *scores;
@@ -729,8 +730,8 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   const int sms = beam_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per request: as many as keep one wave (two CTAs per SM) and have a beam or 16 KB of logits each.
-  // 32 x 8 x 131072: 23.5 us with 8, 31.8 with 4, 101 with 1; 1 x 4 x 32001 fp32: 9.3 us with 16 or 8, 9.5
-  // with 4, 24.3 with 1; 1 x 8 x 1000: 9.0 us with 8, 33.6 with 1; 64 x 4 x 32000: 10.6 with 4, 18.2 with 8.
+  // 32 x 8 x 131072: 21.4 us with 8, 34.2 with 16, and +8 with 4; 1 x 4 x 32001 fp32: 8.6 us with 16, +15 with
+  // 1; 1 x 8 x 1000: 9.0 us with 8, 33.6 with 1; 64 x 4 x 32000: 10.6 with 4, 18.2 with 8.
   const int64_t bytes = (int64_t)a->num_beams * a->vocab * (f32 ? 4 : 2);
   int C = 1;
   while (C < kMaxCluster && (int64_t)a->num_reqs * C <= sms &&
