@@ -423,7 +423,7 @@ typedef struct pa_evict_select_args {
   const int32_t *context_lens;   /* [num_seqs] */
   int32_t *keep;                 /* out: [num_seqs, num_kv_heads, budget] kept positions, ascending, -1 after */
   int32_t *new_lens;             /* out: [num_seqs] min(context_len, budget); must not be context_lens */
-  uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT is OR-ed in */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT, PA_DEV_TIMEOUT are OR-ed in */
   int32_t num_seqs;              /* >= 0, num_seqs * num_kv_heads <= 65535; 0 enqueues nothing */
   int32_t num_kv_heads;          /* 1 .. 64 */
   int32_t mass_stride;           /* 1 .. 2^30 */

@@ -48,7 +48,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;   // and twice that where it pays
 constexpr int kMaxKeys = 32;     // keys a thread can hold
-constexpr int kBatch = 16;       // masses a thread has on their way where it holds no keys (1 x 262144: 43.5 us, one at a time 55.7)
+// Masses a thread has on their way where it holds no keys (one at a time: 55.7 us against 43.5 for 1 x 262144).
+constexpr int kBatch = 16;
 
 // A cluster of C CTAs per (request, KV head), each with one stretch of the positions, a warp with
 // one stretch of those.  The masses are read once, as keys into registers, KPT per thread; rows
@@ -57,7 +58,9 @@ constexpr int kBatch = 16;       // masses a thread has on their way where it ho
 // then the 11 bits below them of the keys in one bin, then the last 10.  The CTAs' counts meet
 // through distributed shared memory: each CTA sums its share of the bins and sends the sums to all, 16
 // bytes per thread and direction in place of 64 KB per CTA.  They are asynchronous stores that the
-// receiver counts: loads of what the others have left, or cluster barriers, measured a round trip more.  A bin that is taken whole ends the search early.  Then the
+// receiver counts: loads of what the others have left, or cluster barriers, measured a round trip more
+// (8 rows x 131072: 16.1 us against 14.4).  A part or a sum is overwritten in the next step only by CTAs that
+// have what its reader sent after reading it.  A bin that is taken whole ends the search early.  Then the
 // kept positions are written in order: those above T and the first `need` equal to it, at offsets from
 // the counts of the warps and CTAs before.
 struct SelectShared {
