@@ -34,7 +34,7 @@ constexpr int kMaxReqs = 65535;
 // cluster's first CTA, one cluster barrier follows, and a warp there joins parts and beams.
 //
 // Bound by HBM while the logits stream, then by the chain of joins.  Measured: 32 requests x 8 beams x
-// 131072 bf16, 67 MB (9.9 us at a copy's rate), 21.4 us: 11 to 13 us of streaming (5.5 TB/s), 2 to tau, 2 to
+// 131072 bf16, 67 MB (9.9 us at a copy's rate), 22.0 us: 11 to 13 us of streaming (5.5 TB/s), 2 to tau, 2 to
 // the part's list, 2 for the barrier, 2 in the first CTA, 2 of launch; 1 x 4 x 32001 fp32 8.6 us.  One CTA per
 // request and one pass per candidate took 1644 and 152 us.  Lists sent as asynchronous stores that an mbarrier
 // counts, in place of stores and a cluster barrier, cost 0.5 us more: some hundred 8-byte transactions.
@@ -96,6 +96,9 @@ __device__ __forceinline__ u64 merge32(u64 k, u64 other_reversed, int lane) {
 
 constexpr int kBeamThreads = 512;
 constexpr int kBeamWarps = kBeamThreads / 32;
+// Vectors cut from two: 1 x 4 x 32001 8.6 us with 3 at a time, 8.9 with 4; 32 x 8 x 131071 fp32 33.3 with 3, 32.3
+// with 4, 36.5 with 2 (30.9 where rows of other alignment were other vectors).
+constexpr int kCutUnroll = 3;
 constexpr int kUnroll = 4;  // 16-byte loads in flight per thread: 32 KB per CTA, two CTAs per SM
 
 template <typename T>
@@ -129,30 +132,56 @@ struct Vec<float> {
   }
 };
 
-// A row seen as 16-byte vectors on 16-byte boundaries: vector j holds the elements
-// E j - e0 .. E j - e0 + E - 1, of which the first and last vector may have fewer.
+// A row seen as vectors of 16 bytes: vector j holds the elements E j .. E j + E - 1, of which the last may
+// have fewer.  Also where the row does not begin on a 16-byte boundary: rows of the same values give the
+// same sums in the same order, wherever they lie, so that equal totals are equal.  Such a vector
+// is cut from the two it lies in (the second is in L1, it is the next thread's first).
 template <typename T>
 struct RowView {
   static constexpr int E = Vec<T>::E;
   const T *x;
-  int V, e0, nv;
+  int V, nv;
+  int mis;          // bytes that the row begins behind a boundary
+  int begin, whole;  // vectors [begin, whole) lie, with what is fetched around them, within the row
   __device__ RowView(const T *row, int vocab) : x(row), V(vocab) {
-    e0 = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    nv = (e0 + V + E - 1) / E;
+    mis = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
+    nv = (V + E - 1) / E;
+    begin = mis != 0;
+    whole = mis == 0 ? V / E : (V * (int)sizeof(T) + mis) / 16 - 1;
   }
-  __device__ __forceinline__ int first(int j) const { return E * j - e0; }  // may be negative
+  __device__ __forceinline__ int first(int j) const { return E * j; }
+  __device__ __forceinline__ const uint4 *aligned() const {
+    return reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(x) - mis);
+  }
+  // The 16 bytes from byte `mis` of a and b on.
+  __device__ __forceinline__ uint4 cut(const uint4 &a, const uint4 &b) const {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (mis & 8)
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    if (mis & 4)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    if (sizeof(T) == 2 && (mis & 2))
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
   __device__ __forceinline__ uint4 load(int j) const {
+    if (j >= begin && j < whole) {
+      const uint4 *at = aligned() + j;
+      return mis == 0 ? __ldg(at) : cut(__ldg(at), __ldg(at + 1));
+    }
     const int f = first(j);
-    if (f >= 0 && f + E <= V) return __ldg(reinterpret_cast<const uint4 *>(x + f));
     uint32_t w[4];  // a ragged end: what is missing is -inf
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (sizeof(T) == 4) {
-        w[i] = f + i >= 0 && f + i < V ? ((const uint32_t *)x)[f + i] : 0xFF800000u;
+        w[i] = f + i < V ? ((const uint32_t *)x)[f + i] : 0xFF800000u;
       } else {
         const int a = f + 2 * i;
-        const uint32_t lo = a >= 0 && a < V ? ((const uint16_t *)x)[a] : 0xFF80u;
-        const uint32_t hi = a + 1 >= 0 && a + 1 < V ? ((const uint16_t *)x)[a + 1] : 0xFF80u;
+        const uint32_t lo = a < V ? ((const uint16_t *)x)[a] : 0xFF80u;
+        const uint32_t hi = a + 1 < V ? ((const uint16_t *)x)[a + 1] : 0xFF80u;
         w[i] = lo | (hi << 16);
       }
     }
@@ -324,18 +353,32 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
     sum = pa::add2(sum, t[0]);
   };
   int j = lo + tid;
-  if (j == 0 && r.e0 > 0 && j < hi) {  // a ragged beginning
-    take(r.load(0), 0);
+  if (j < r.begin && j < hi) {  // what is fetched for the first vector begins before the row
+    take(r.load(j), j);
     j += kBeamThreads;
   }
-  const int whole = min(hi, (r.e0 + p.V) / E);  // the vectors before it end within the row
-  for (; j + (kUnroll - 1) * kBeamThreads < whole; j += kUnroll * kBeamThreads) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(r.x + r.first(j));
-    uint4 v[kUnroll];
+  const int whole = min(hi, r.whole);
+  if (r.mis == 0) {
+    for (; j + (kUnroll - 1) * kBeamThreads < whole; j += kUnroll * kBeamThreads) {
+      const uint4 *src = r.aligned() + j;
+      uint4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(src + u * kBeamThreads);
+      for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(src + u * kBeamThreads);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) take(v[u], j + u * kBeamThreads);
+      for (int u = 0; u < kUnroll; ++u) take(v[u], j + u * kBeamThreads);
+    }
+  } else {
+    for (; j + (kCutUnroll - 1) * kBeamThreads < whole; j += kCutUnroll * kBeamThreads) {
+      const uint4 *src = r.aligned() + j;
+      uint4 v[kCutUnroll], w[kCutUnroll];
+#pragma unroll
+      for (int u = 0; u < kCutUnroll; ++u) {
+        v[u] = __ldg(src + u * kBeamThreads);
+        w[u] = __ldg(src + u * kBeamThreads + 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kCutUnroll; ++u) take(r.cut(v[u], w[u]), j + u * kBeamThreads);
+    }
   }
   for (; j < hi; j += kBeamThreads) take(r.load(j), j);
   float s, s1;
@@ -344,7 +387,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   const bool nan = s != s;  // a NaN or +inf among the elements
   u64 key = 0;
   if (lo + tid < hi) {
-    int at = max(r.first(lo + tid), 0);  // nothing above -inf: the first element
+    int at = r.first(lo + tid);  // nothing above -inf: the first element
     if (m > -INFINITY) {
       at = r.first(best);
       bool found = false;
@@ -382,7 +425,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   const int nowners = sm.owners;
   auto search = [&](auto &&found) {
     for (int i = warp; i < nowners; i += kBeamWarps) {
-      const int oj = (key_index(owners[i]) + r.e0) / E;
+      const int oj = key_index(owners[i]) / E;
       for (int j0 = lo + (oj - lo) % kBeamThreads; j0 < hi; j0 += 32 * kBeamThreads) {
         const int64_t jl = (int64_t)j0 + (int64_t)lane * kBeamThreads;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -392,7 +435,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int at = r.first((int)jl) + e;
-            if (at >= 0 && at < p.V && pair_key(Vec<T>::get(v, e), at) >= tau) left |= 1u << e;
+            if (at < p.V && pair_key(Vec<T>::get(v, e), at) >= tau) left |= 1u << e;
           }
         }
         found(v, (int)jl, left);
@@ -730,7 +773,7 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   const int sms = beam_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per request: as many as keep one wave (two CTAs per SM) and have a beam or 16 KB of logits each.
-  // 32 x 8 x 131072: 21.4 us with 8, 34.2 with 16, and +8 with 4; 1 x 4 x 32001 fp32: 8.6 us with 16, +15 with
+  // 32 x 8 x 131072: 22.0 us with 8, 34.7 with 16, and +8 with 4; 1 x 4 x 32001 fp32: 8.6 us with 16, +15 with
   // 1; 1 x 8 x 1000: 9.0 us with 8, 33.6 with 1; 64 x 4 x 32000: 10.6 with 4, 18.2 with 8.
   const int64_t bytes = (int64_t)a->num_beams * a->vocab * (f32 ? 4 : 2);
   int C = 1;

@@ -104,6 +104,19 @@ def test_ties_go_to_the_lowest_beam_and_token(dt, V):
         _check(x, x.double().numpy(), np.array([[-2, -2, -2, -2, -2], [-64, -1, -1, -64, -1]], np.float32))
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("W", [12, 17, 32])
+@pytest.mark.parametrize("V", [300, 6000, 40000])
+def test_wide_beams_over_runs_of_equal_and_rising_logits(dt, W, V):
+    """More elements reach the bound than are put in order at once."""
+    scores = np.full((2, W), -2.0, np.float32)
+    scores[1] = np.where(np.arange(W) % 3 == 1, -1.0, -64.0)
+    for row in (torch.zeros(V), torch.linspace(-4, 4, V).bfloat16().float(), torch.linspace(4, -4, V).bfloat16().float(),
+                (torch.arange(V) // 8 % 40).float() / 8):
+        x = row.expand(2, W, V).to(dt).contiguous()
+        _check(x, x.double().numpy(), scores)
+
+
 def test_masked_infinite_and_nan_rows():
     rng = np.random.default_rng(9)
     x, _ = _logits(rng, 7, 3, 500, torch.float32)
