@@ -773,7 +773,7 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   const int sms = beam_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per request: as many as keep one wave (two CTAs per SM) and have a beam or 16 KB of logits each.
-  // 32 x 8 x 131072: 22.0 us with 8, 34.7 with 16, and +8 with 4; 1 x 4 x 32001 fp32: 8.6 us with 16, +15 with
+  // 32 x 8 x 131072: 22.0 us with 8, +12.7 with 16, +8 with 4; 1 x 4 x 32001 fp32: 8.6 us with 16, +15 with
   // 1; 1 x 8 x 1000: 9.0 us with 8, 33.6 with 1; 64 x 4 x 32000: 10.6 with 4, 18.2 with 8.
   const int64_t bytes = (int64_t)a->num_beams * a->vocab * (f32 ? 4 : 2);
   int C = 1;
