@@ -67,11 +67,14 @@ __device__ __forceinline__ float key_value(u64 k) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 __device__ __forceinline__ int key_index(u64 k) { return (int)(0xFFFFFFFFu - (uint32_t)(k & 0xFFFFFFFFull)); }
-// Ordered bits of a double that is not NaN; greater than 0 for every such double.
+// Ordered bits of a double that is not NaN, -0 = +0; greater than 0 for every such double.  (These tests go by the bits: a
+// comparison in fp64 takes as long as any of its operations.)
 __device__ __forceinline__ u64 rank_key(double x) {
-  const u64 u = (u64)__double_as_longlong(x + 0.0);
-  return (u >> 63) ? ~u : (u | (1ull << 63));
+  const u64 u = (u64)__double_as_longlong(x);
+  return u > (1ull << 63) ? ~u : (u | (1ull << 63));
 }
+__device__ __forceinline__ bool is_finite(double x) { return (__double2hiint(x) & 0x7FF00000) != 0x7FF00000; }
+__device__ __forceinline__ bool is_nan(double x) { return (__double2hiint(x) & 0x7FF80000) == 0x7FF80000; }  // a quiet one, as results are
 
 // 32 keys, one per lane, in descending order over the lanes: bitonic networks on shuffles.
 __device__ __forceinline__ u64 exchange(u64 k, int lane, int j, bool up) {
@@ -205,10 +208,11 @@ struct BeamShared {
   long long sum[kMaxLists];         // sum of exp(x - m) in units of 2^-36, or -1: NaN
   float max[kMaxLists];
   double part[kMaxLists];           // that sum relative to the row's maximum
-  double lse[kMaxBeams], inv[kMaxBeams];  // inv: max(new length, 1) ^ -length_penalty
+  double lse[kMaxBeams], inv[kMaxBeams];  // inv: max(new length, 1) ^ -length_penalty; then that power itself
   u64 rank[kMaxBeams][kMaxBeams];   // of each beam's candidates, descending; 0: none
   float total[kMaxBeams][kMaxBeams];
   int token[kMaxBeams][kMaxBeams];
+  bool unsure;                      // candidates of two lengths too close for the tables
 };
 
 // The few logarithms and powers of a step.  This GPU computes in fp64 slowly (some 70 cycles for each
@@ -239,7 +243,8 @@ __device__ __forceinline__ double exp64(double x) {
   return (1.0 + (t + (double)q)) * (kExp2Sixteenths[k & 15] * __longlong_as_double((long long)((k >> 4) + 1023) << 52));
 }
 // ln s for a normal s > 0: s = 2^e m, 1 <= m < 2, i = the inverse of the middle of m's sixteenth, and
-// ln m = -ln i + ln(1 + r), r = i m - 1 exactly in two fp32 numbers, |r| <= 1/31.
+// ln m = -ln i + ln(1 + r), r = i m - 1 exactly in two fp32 numbers, |r| <= 1/31.  A row with one
+// token to choose has a sum of 1, and its total is the score itself.
 __device__ __forceinline__ double ln64(double s) {
   const long long b = __double_as_longlong(s);
   const int e = (int)((b >> 52) & 2047) - 1023, k = (int)((b >> 48) & 15);
@@ -247,8 +252,19 @@ __device__ __forceinline__ double ln64(double s) {
   const float hi = (float)m, lo = (float)(m - (double)hi), i = kInverse[k];
   const float p = hi * i, r1 = p - 1.f, r2 = fmaf(lo, i, fmaf(hi, i, -p)), r = r1 + r2;
   const float q = r * r * fmaf(fmaf(fmaf(fmaf(fmaf(1.f / 7, r, -1.f / 6), r, 1.f / 5), r, -1.f / 4), r, 1.f / 3), r, -0.5f);
-  return fma((double)e, kLn2, kMinusLnInverse[k] + ((double)r1 + (double)(r2 + q)));
+  const double rest = (b & 0xFFFFFFFFFFFFFll) == 0 ? 0.0 : kMinusLnInverse[k] + ((double)r1 + (double)(r2 + q));
+  return fma((double)e, kLn2, rest);
 }
+
+// len^penalty for ranks that the tables cannot tell apart: a length itself is exact (so that total / length is
+// the nearest double), any other power CUDA's.
+__device__ __noinline__ double length_power(int len, float penalty) {
+  return penalty == 1.f ? (double)len : pow((double)len, (double)penalty);
+}
+// Ranks of different lengths this many steps of a double apart (2^-28 of their size or more) are
+// in the right order however the tables' 1e-10 fell.
+constexpr u64 kClearSteps = 1ull << 24;
+constexpr double kSmallInverse = 1e-200;  // below this products may underflow
 
 // This shared-memory address in the cluster's first CTA.
 __device__ __forceinline__ uint32_t in_first_cta(const void *p) {
@@ -561,57 +577,86 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
     }
   }
   __syncthreads();
-  // every (beam, place) candidate's token, total and rank: a warp per beam, a lane per place
-  for (int b = warp; b < p.W; b += kBeamWarps) {
-    const float c = __shfl_sync(~0u, cum, b);
-    const bool ended = __shfl_sync(~0u, (int)done, b) != 0;
-    const double lse = sm.lse[b];
-    // no continuation at a number: every candidate counts as -inf
-    const bool dead = c != c || c == -INFINITY || (!ended && !(fabs(lse) < INFINITY));
-    int tok = lane;
-    double total = -INFINITY;
-    if (!dead && ended) {
-      tok = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
-      if (lane == 0) total = (double)c;
-    } else if (!dead) {
-      const u64 k = sm.list[b * p.parts][lane];
-      tok = key_index(k);
-      total = (double)c + ((double)key_value(k) - lse);
-      if (total != total) total = -INFINITY;
+  // The candidates are ranked by total * length^-penalty from the tables.  Where that leaves the order of two of
+  // the chosen open -- beams of different lengths with ranks closer than the tables' error, so that
+  // equal ranks might not go to the lower beam -- it is done again with total / length^penalty.
+  const u64 lowest = rank_key(-INFINITY);
+  for (bool careful = false;; careful = true) {
+    // every (beam, place) candidate's token, total and rank: a warp per beam, a lane per place
+    for (int b = warp; b < p.W; b += kBeamWarps) {
+      const float c = __shfl_sync(~0u, cum, b);
+      const bool ended = __shfl_sync(~0u, (int)done, b) != 0;
+      const double lse = sm.lse[b];
+      // no continuation at a number: every candidate counts as -inf
+      const bool dead = c != c || c == -INFINITY || (!ended && !is_finite(lse));
+      int tok = lane;
+      double total = -INFINITY;
+      if (!dead && ended) {
+        tok = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
+        if (lane == 0) total = (double)c;
+      } else if (!dead) {
+        const u64 k = sm.list[b * p.parts][lane];
+        tok = key_index(k);
+        total = (double)c + ((double)key_value(k) - lse);
+        if (is_nan(total)) total = -INFINITY;
+      }
+      double rank = total;
+      if (p.penalty != 0.f && is_finite(total)) rank = careful ? total / sm.inv[b] : total * sm.inv[b];
+      sm.rank[b][lane] = lane < p.W && lane < p.V ? rank_key(rank) : 0ull;
+      sm.total[b][lane] = (float)total;
+      sm.token[b][lane] = tok;
     }
-    const double rank = p.penalty != 0.f && total > -INFINITY ? total * sm.inv[b] : total;
-    sm.rank[b][lane] = lane < p.W && lane < p.V ? rank_key(rank) : 0ull;
-    sm.total[b][lane] = (float)total;
-    sm.token[b][lane] = tok;
-  }
-  __syncthreads();
-  if (warp != 0) return;
-  // lane b walks beam b's candidates; lane j keeps the j-th best of all
-  u64 key = mine ? sm.rank[lane][0] : 0ull;
-  int at = 0, from = 0, place = 0;
-  for (int j = 0; j < p.W; ++j) {
-    const uint32_t hi = (uint32_t)(key >> 32), top = __reduce_max_sync(~0u, hi);
-    const uint32_t lo = hi == top ? (uint32_t)key : 0u, low = __reduce_max_sync(~0u, lo);
-    const int win = __ffs(__ballot_sync(~0u, hi == top && lo == low && key != 0)) - 1;  // equal ranks: the lower beam
-    const int p_win = __shfl_sync(~0u, at, max(win, 0));
-    if (lane == j) {
-      from = max(win, 0);
-      place = p_win;
+    __syncthreads();
+    if (warp == 0) {
+      // lane b walks beam b's candidates; lane j keeps the j-th best of all
+      u64 key = mine ? sm.rank[lane][0] : 0ull, chosen = 0;
+      int at = 0, from = 0, place = 0;
+      for (int j = 0; j < p.W; ++j) {
+        const uint32_t hi = (uint32_t)(key >> 32), top = __reduce_max_sync(~0u, hi);
+        const uint32_t lo = hi == top ? (uint32_t)key : 0u, low = __reduce_max_sync(~0u, lo);
+        const int win = __ffs(__ballot_sync(~0u, hi == top && lo == low && key != 0)) - 1;  // equal ranks: the lower beam
+        const int p_win = __shfl_sync(~0u, at, max(win, 0));
+        if (lane == j) {
+          from = max(win, 0);
+          place = p_win;
+          chosen = ((u64)top << 32) | low;
+        }
+        if (lane == win) {
+          ++at;
+          key = at < p.W ? sm.rank[lane][at] : 0ull;
+        }
+      }
+      const bool from_done = __shfl_sync(~0u, (int)done, from) != 0;
+      const int from_len = __shfl_sync(~0u, len, from);
+      if (mine) {
+        const int tok = sm.token[from][place];
+        p.tokens[me] = tok;
+        p.parents[me] = from;
+        p.scores_out[me] = sm.total[from][place];
+        if (p.finished_out != nullptr) p.finished_out[me] = from_done || (p.eos >= 0 && tok == p.eos);
+        if (p.lengths_out != nullptr) p.lengths_out[me] = from_len;
+      }
+      if (!careful) {
+        // The chosen are in the order of their computed ranks, so two of different lengths have neighbours of different
+        // lengths between them; what is left of a beam comes after its next candidate, which each lane compares with
+        // the last of the chosen.
+        bool unsure = false;
+        if (p.penalty != 0.f) {
+          const int next_len = __shfl_down_sync(~0u, from_len, 1), last_len = __shfl_sync(~0u, from_len, p.W - 1);
+          const u64 next = __shfl_down_sync(~0u, chosen, 1), last = __shfl_sync(~0u, chosen, p.W - 1);
+          unsure = mine && (sm.inv[lane] < kSmallInverse ||
+                            (lane + 1 < p.W && next_len != from_len && chosen > lowest && chosen - next < kClearSteps) ||
+                            (key != 0 && len != last_len && last > lowest && last - key < kClearSteps));
+        }
+        unsure = __any_sync(~0u, unsure);
+        if (lane == 0) sm.unsure = unsure;
+      }
     }
-    if (lane == win) {
-      ++at;
-      key = at < p.W ? sm.rank[lane][at] : 0ull;
-    }
-  }
-  const bool from_done = __shfl_sync(~0u, (int)done, from) != 0;
-  const int from_len = __shfl_sync(~0u, len, from);
-  if (mine) {
-    const int tok = sm.token[from][place];
-    p.tokens[me] = tok;
-    p.parents[me] = from;
-    p.scores_out[me] = sm.total[from][place];
-    if (p.finished_out != nullptr) p.finished_out[me] = from_done || (p.eos >= 0 && tok == p.eos);
-    if (p.lengths_out != nullptr) p.lengths_out[me] = from_len;
+    if (careful || p.penalty == 0.f) return;
+    __syncthreads();
+    if (!sm.unsure) return;
+    if (warp == kBeamWarps - 1) sm.inv[lane] = length_power(max(len, 1), p.penalty);
+    __syncthreads();
   }
 }
 
