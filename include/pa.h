@@ -530,7 +530,8 @@ typedef struct pa_beam_select_args {
  * where nothing better is left; its scores_out is -inf.  finished_out is set where the parent
  * had ended or the token is eos_token.  Totals and ranks are fp64 (the sum of exponentials is
  * accumulated in fp32 over short runs and joined in fp64; the power of a length is CUDA's pow, within two units
- * of its last place, and with a length_penalty of 1 the length itself); scores_out is rounded once.  One kernel launch on `stream`;
+ * of its last place, and with a length_penalty of 1 the length itself), and ranks that round to the same number are
+ * equal, also those of different logits; scores_out is rounded once.  One kernel launch on `stream`;
  * no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer or a value out
  * of range, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for more than 32 beams,
  * 65535 requests or 2^24 tokens, PA_ERR_CUDA when the launch fails. */

@@ -112,7 +112,7 @@ def kv_compact(keep, new_lens, src_table, dst_table, arrays, page_size, mass=Non
 
 def beam_select(logits, scores, eos=-1, finished=None, lengths=None, penalty=0.0):
     """(tokens, parents, totals fp64, finished, lengths) of one step; logits [N, W, V] doubles.
-    Every candidate is ranked: rank, then beam, then (within a beam) logit, then token."""
+    Every candidate is ranked: rank, then beam, then token."""
     N, W, V = logits.shape
     res = [np.zeros((N, W), d) for d in (np.int32, np.int32, np.float64, np.uint8, np.int32)]
     for n in range(N):
@@ -131,11 +131,13 @@ def beam_select(logits, scores, eos=-1, finished=None, lengths=None, penalty=0.0
                     tot[eos] = cum
                 elif np.isfinite(lse):
                     tot = cum + (x - lse)
-            norm = float(max(ln, 1)) ** penalty
-            order = np.lexsort((np.arange(V), np.where(np.isneginf(tot), 0.0, -x), -tot))[:W]
-            cand += [(-(tot[v] / norm), b, k, int(v), tot[v], ln, done) for k, v in enumerate(order)]
+            with np.errstate(over="ignore"):
+                norm = np.float64(max(ln, 1)) ** penalty
+            rank = np.where(np.isinf(tot), tot, tot / norm) + 0.0
+            order = np.lexsort((np.arange(V), -rank))[:W]
+            cand += [(-rank[v], b, int(v), tot[v], ln, done) for v in order]
         cand.sort(key=lambda c: c[:3])
-        for j, (_, b, _, v, total, ln, done) in enumerate(cand[:W]):
+        for j, (_, b, v, total, ln, done) in enumerate(cand[:W]):
             for a, val in zip(res, (v, b, total, done or (eos >= 0 and v == eos), ln)):
                 a[n, j] = val
     return res

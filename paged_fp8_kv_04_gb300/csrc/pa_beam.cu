@@ -212,6 +212,8 @@ struct BeamShared {
   u64 rank[kMaxBeams][kMaxBeams];   // of each beam's candidates, descending; 0: none
   float total[kMaxBeams][kMaxBeams];
   int token[kMaxBeams][kMaxBeams];
+  int used[kMaxBeams];              // of each beam: how many of its candidates are chosen,
+  int open[kMaxBeams];              // and the first place from which their order may not be that of the logits
   bool unsure;                      // candidates of two lengths too close for the tables
 };
 
@@ -520,8 +522,216 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
   }
 }
 
+// A total's rank: by the tables' inverse power, or with that power itself.
+__device__ __forceinline__ double rank_of(const BeamParams &p, double total, double inv, bool careful) {
+  if (p.penalty == 0.f || !is_finite(total)) return total;
+  return careful ? total / inv : total * inv;
+}
+__device__ __forceinline__ double total_of(float c, float x, double lse) {
+  const double t = (double)c + ((double)x - lse);
+  return is_nan(t) ? -INFINITY : t;
+}
+
+// No continuation at a number: every candidate of beam b counts as -inf.
+__device__ __forceinline__ bool is_dead(const BeamShared &sm, int b, float c, bool ended) {
+  return c != c || c == -INFINITY || (!ended && !is_finite(sm.lse[b]));
+}
+
+// Every (beam, place) candidate's token, total and rank: a warp per beam, a lane per place.  Lane b has what beam
+// b brings.
+template <bool CAREFUL>
+__device__ __forceinline__ void candidates(const BeamParams &p, BeamShared &sm, float cum, bool done) {
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x >> 5; b < p.W; b += kBeamWarps) {
+    const float c = __shfl_sync(~0u, cum, b);
+    const bool ended = __shfl_sync(~0u, (int)done, b) != 0, dead = is_dead(sm, b, c, ended);
+    int tok = lane, to = lane;
+    double total = -INFINITY;
+    if (!dead && ended) {
+      tok = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
+      if (lane == 0) total = (double)c;
+    } else if (!dead) {
+      const u64 k = sm.list[b * p.parts][lane];
+      tok = key_index(k);
+      total = total_of(c, key_value(k), sm.lse[b]);
+    }
+    const u64 key = lane < p.W && lane < p.V ? rank_key(rank_of(p, total, sm.inv[b], CAREFUL)) : 0ull;
+    if (CAREFUL) {
+      to = 0;
+      for (int j = 0; j < 32; ++j) {
+        const u64 y = __shfl_sync(~0u, key, j);
+        const int t = __shfl_sync(~0u, tok, j);
+        to += y > key || (y == key && (t < tok || (t == tok && j < lane)));
+      }
+    }
+    sm.rank[b][to] = key;
+    sm.total[b][to] = (float)total;
+    sm.token[b][to] = tok;
+  }
+}
+
+// The num_beams best of all beams' candidates, by one warp: lane j has the j-th best's beam, place and rank, and
+// lane b the rank of the first candidate of beam b that is left (0: none).
+struct Choice {
+  int from, place;
+  u64 rank, left;
+};
+__device__ __forceinline__ Choice choose(const BeamParams &p, BeamShared &sm) {
+  const int lane = threadIdx.x & 31;
+  Choice x = {0, 0, 0ull, lane < p.W ? sm.rank[lane][0] : 0ull};
+  int at = 0;
+  for (int j = 0; j < p.W; ++j) {
+    const uint32_t hi = (uint32_t)(x.left >> 32), top = __reduce_max_sync(~0u, hi);
+    const uint32_t lo = hi == top ? (uint32_t)x.left : 0u, low = __reduce_max_sync(~0u, lo);
+    const int win = __ffs(__ballot_sync(~0u, hi == top && lo == low && x.left != 0)) - 1;  // equal ranks: the lower beam
+    const int p_win = __shfl_sync(~0u, at, max(win, 0));
+    if (lane == j) {
+      x.from = max(win, 0);
+      x.place = p_win;
+      x.rank = ((u64)top << 32) | low;
+    }
+    if (lane == win) {
+      ++at;
+      x.left = at < p.W ? sm.rank[lane][at] : 0ull;
+    }
+  }
+  sm.used[lane] = at;
+  return x;
+}
+// And what the caller gets of it; returns the length that lane j's has.
+__device__ __forceinline__ int write_choice(const BeamParams &p, const BeamShared &sm, const Choice &x, int64_t me, bool done, int len) {
+  const bool from_done = __shfl_sync(~0u, (int)done, x.from) != 0;
+  const int from_len = __shfl_sync(~0u, len, x.from);
+  if ((threadIdx.x & 31) < p.W) {
+    const int tok = sm.token[x.from][x.place];
+    p.tokens[me] = tok;
+    p.parents[me] = x.from;
+    p.scores_out[me] = sm.total[x.from][x.place];
+    if (p.finished_out != nullptr) p.finished_out[me] = from_done || (p.eos >= 0 && tok == p.eos);
+    if (p.lengths_out != nullptr) p.lengths_out[me] = from_len;
+  }
+  return from_len;
+}
+
+// The order of totals is that of the logits unless their rounding makes one of several logits, as with scores
+// of -1e9 for beams that hardly exist: then the lower token comes first, which may not even be in the list.
+// The first place of beam b's list from which that can be so (32: nowhere), for a warp.  Ranks within
+// kSameSteps steps of a double may be equal once divided by the power itself.
+constexpr u64 kSameSteps = 8;
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const BeamParams p) {
+__device__ int open_from(const BeamParams &p, const BeamShared &sm, int b, float c) {
+  const int lane = threadIdx.x & 31, n = min(p.W, p.V), i = min(lane + 1, 31);
+  const u64 k = sm.list[b * p.parts][lane], next = sm.list[b * p.parts][i];
+  bool near = lane + 1 < n && sm.rank[b][lane] - sm.rank[b][i] <= kSameSteps, differ = near && k >> 32 != next >> 32;
+  if (lane == n - 1 && n < p.V) {
+    // beyond the list: is the step from its last logit x to the next lower value (2^-24 or 2^-8 of x or more) within
+    // 16 steps of a total (2^-50 of the largest of its terms or less)?
+    auto exponent = [](float y) { return max((int)(__float_as_uint(y) >> 23 & 255u), 1); };
+    const float x = key_value(k);
+    const int largest = max(exponent(c), max(exponent((float)sm.lse[b]), exponent(x)));
+    near = differ = x > -INFINITY && (c == INFINITY || exponent(x) + (sizeof(T) == 2 ? 16 : 0) + 22 <= largest);
+  }
+  const unsigned same = __ballot_sync(~0u, near), other = __ballot_sync(~0u, differ);
+  if (other == 0) return 32;
+  const unsigned apart = ~same & ((1u << (__ffs(other) - 1)) - 1u);  // equal ranks may begin before logits differ
+  return 32 - __clz(apart);
+}
+
+// The candidates chosen from beam b's list at its lowest rank: of all the row's tokens with that rank they have to
+// be the lowest.  The tokens' logits are an interval, whose lower end is found by bisection; each warp looks for the first
+// in a stretch of the row, and their tokens and totals take the place of those in the list.  For the whole CTA.
+template <typename T>
+__device__ __noinline__ void lowest_tokens(const BeamParams &p, BeamShared &sm, int64_t row, int b, float c) {
+  constexpr int E = Vec<T>::E;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const u64 rank = sm.rank[b][p.W - 1];
+  const int higher = __popc(__ballot_sync(~0u, sm.rank[b][lane] > rank)), need = sm.used[b] - higher;
+  if (need <= 0 || rank == rank_key(-INFINITY)) return;
+  const double lse = sm.lse[b], inv = sm.inv[b];
+  const uint32_t last = (uint32_t)(sm.list[b * p.parts][p.W - 1] >> 32), top = (uint32_t)(sm.list[b * p.parts][higher] >> 32);
+  uint32_t lo = (uint32_t)(pair_key(-INFINITY, 0) >> 32), hi = last;  // the lowest logit of this rank is one of [lo, hi]
+  while (lo < hi) {
+    const uint32_t step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi);
+    const double r = rank_of(p, total_of(c, key_value((u64)at << 32), lse), inv, true);
+    const unsigned has = __ballot_sync(~0u, rank_key(r) == rank);
+    if (has & 1u) {
+      hi = lo;
+    } else if (has != 0) {
+      const uint32_t from = lo;
+      lo = from + (__ffs(has) - 2) * step + 1;
+      hi = min(from + (__ffs(has) - 1) * step, hi);
+    } else {
+      lo += 31 * step + 1;
+    }
+  }
+  if (lo == last) return;  // one logit only, whose lowest tokens the list has
+  const T *x = static_cast<const T *>(p.logits) + row * p.stride;
+  const RowView<T> r(x, p.V);
+  const int begin = (int)((int64_t)r.nv * warp / kBeamWarps), end = (int)((int64_t)r.nv * (warp + 1) / kBeamWarps);
+  int got = 0;
+  for (int j0 = begin; j0 < end && got < need; j0 += 32 * kUnroll) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + 32 * u + lane;
+      v[u] = j < end ? r.load(j) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + 32 * u + lane;
+      unsigned left = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t o = (uint32_t)(pair_key(Vec<T>::get(v[u], e), 0) >> 32);
+        if (j < end && r.first(j) + e < p.V && o >= lo && o <= top) left |= 1u << e;
+      }
+      unsigned have;
+      while (got < need && (have = __ballot_sync(~0u, left != 0)) != 0) {
+        if (lane == __ffs(have) - 1) {
+          sm.buf[warp][got] = (u64)(r.first(j) + __ffs(left) - 1);
+          left &= left - 1;
+        }
+        ++got;
+      }
+    }
+  }
+  if (lane == 0) sm.wsum[warp] = got;
+  __syncthreads();
+  if (warp == 0 && lane < need) {
+    int from = 0, k = lane;
+    while (from < kBeamWarps && k >= (int)sm.wsum[from]) k -= (int)sm.wsum[from++];
+    if (from < kBeamWarps) {
+      const int token = (int)sm.buf[from][k];
+      const float y = sizeof(T) == 4 ? __uint_as_float((uint32_t)x[token]) : __uint_as_float((uint32_t)x[token] << 16);
+      sm.token[b][higher + lane] = token;
+      sm.total[b][higher + lane] = (float)total_of(c, y, lse);
+    }
+  }
+  __syncthreads();
+}
+
+// The choice where the first one is not certain to be right.  For the whole CTA.
+template <typename T>
+__device__ __noinline__ void choose_again(const BeamParams &p, BeamShared &sm, int64_t base, float cum, bool done, int len) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();  // what led here has been read
+  if (warp == 0 && p.penalty != 0.f) sm.inv[lane] = length_power(max(len, 1), p.penalty);
+  __syncthreads();
+  candidates<true>(p, sm, cum, done);
+  __syncthreads();
+  Choice x = {};
+  if (warp == 0) x = choose(p, sm);
+  __syncthreads();
+  for (int b = 0; b < p.W && p.V > p.W; ++b) {
+    const float c = __shfl_sync(~0u, cum, b);
+    const bool ended = __shfl_sync(~0u, (int)done, b) != 0;
+    if (!ended && !is_dead(sm, b, c, ended)) lowest_tokens<T>(p, sm, base + b, b, c);
+  }
+  if (warp == 0) write_choice(p, sm, x, base + lane, done, len);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __grid_constant__ BeamParams p) {
   __shared__ BeamShared sm;
   pa::pdl_wait();
   pa::cluster_arrive();
@@ -577,87 +787,39 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
     }
   }
   __syncthreads();
-  // The candidates are ranked by total * length^-penalty from the tables.  Where that leaves the order of two of
-  // the chosen open -- beams of different lengths with ranks closer than the tables' error, so that
-  // equal ranks might not go to the lower beam -- it is done again with total / length^penalty.
-  const u64 lowest = rank_key(-INFINITY);
-  for (bool careful = false;; careful = true) {
-    // every (beam, place) candidate's token, total and rank: a warp per beam, a lane per place
-    for (int b = warp; b < p.W; b += kBeamWarps) {
+  // The candidates are taken in the order of the logits, and ranked by total * length^-penalty from the tables.  Where
+  // that leaves the order of the chosen open -- different logits of a beam with all but the same total, beams of different
+  // lengths with ranks closer than the tables' error, so that of equal ranks not the lower token or beam might come
+  // first -- it is done again, with total / length^penalty and the tokens of equal ranks in order.
+  candidates<false>(p, sm, cum, done);
+  __syncthreads();
+  if (warp == 0) {
+    const Choice x = choose(p, sm);
+    const int from_len = write_choice(p, sm, x, me, done, len);
+    // The chosen are in the order of their computed ranks, so two of different lengths have neighbours of different
+    // lengths between them; what is left of a beam comes after its next candidate, which each lane compares with
+    // the last of the chosen.
+    bool unsure = false;
+    if (p.penalty != 0.f) {
+      const u64 lowest = rank_key(-INFINITY);
+      const int next_len = __shfl_down_sync(~0u, from_len, 1), last_len = __shfl_sync(~0u, from_len, p.W - 1);
+      const u64 next = __shfl_down_sync(~0u, x.rank, 1), last = __shfl_sync(~0u, x.rank, p.W - 1);
+      unsure = mine && (sm.inv[lane] < kSmallInverse ||
+                        (lane + 1 < p.W && next_len != from_len && x.rank > lowest && x.rank - next < kClearSteps) ||
+                        (x.left != 0 && len != last_len && last > lowest && last - x.left < kClearSteps));
+    }
+    unsure = __any_sync(~0u, unsure);
+    if (lane == 0) sm.unsure = unsure;
+  } else {
+    for (int b = warp - 1; b < p.W; b += kBeamWarps - 1) {
       const float c = __shfl_sync(~0u, cum, b);
       const bool ended = __shfl_sync(~0u, (int)done, b) != 0;
-      const double lse = sm.lse[b];
-      // no continuation at a number: every candidate counts as -inf
-      const bool dead = c != c || c == -INFINITY || (!ended && !is_finite(lse));
-      int tok = lane;
-      double total = -INFINITY;
-      if (!dead && ended) {
-        tok = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
-        if (lane == 0) total = (double)c;
-      } else if (!dead) {
-        const u64 k = sm.list[b * p.parts][lane];
-        tok = key_index(k);
-        total = (double)c + ((double)key_value(k) - lse);
-        if (is_nan(total)) total = -INFINITY;
-      }
-      double rank = total;
-      if (p.penalty != 0.f && is_finite(total)) rank = careful ? total / sm.inv[b] : total * sm.inv[b];
-      sm.rank[b][lane] = lane < p.W && lane < p.V ? rank_key(rank) : 0ull;
-      sm.total[b][lane] = (float)total;
-      sm.token[b][lane] = tok;
+      const int open = ended || is_dead(sm, b, c, ended) ? 32 : open_from<T>(p, sm, b, c);
+      if (lane == 0) sm.open[b] = open;
     }
-    __syncthreads();
-    if (warp == 0) {
-      // lane b walks beam b's candidates; lane j keeps the j-th best of all
-      u64 key = mine ? sm.rank[lane][0] : 0ull, chosen = 0;
-      int at = 0, from = 0, place = 0;
-      for (int j = 0; j < p.W; ++j) {
-        const uint32_t hi = (uint32_t)(key >> 32), top = __reduce_max_sync(~0u, hi);
-        const uint32_t lo = hi == top ? (uint32_t)key : 0u, low = __reduce_max_sync(~0u, lo);
-        const int win = __ffs(__ballot_sync(~0u, hi == top && lo == low && key != 0)) - 1;  // equal ranks: the lower beam
-        const int p_win = __shfl_sync(~0u, at, max(win, 0));
-        if (lane == j) {
-          from = max(win, 0);
-          place = p_win;
-          chosen = ((u64)top << 32) | low;
-        }
-        if (lane == win) {
-          ++at;
-          key = at < p.W ? sm.rank[lane][at] : 0ull;
-        }
-      }
-      const bool from_done = __shfl_sync(~0u, (int)done, from) != 0;
-      const int from_len = __shfl_sync(~0u, len, from);
-      if (mine) {
-        const int tok = sm.token[from][place];
-        p.tokens[me] = tok;
-        p.parents[me] = from;
-        p.scores_out[me] = sm.total[from][place];
-        if (p.finished_out != nullptr) p.finished_out[me] = from_done || (p.eos >= 0 && tok == p.eos);
-        if (p.lengths_out != nullptr) p.lengths_out[me] = from_len;
-      }
-      if (!careful) {
-        // The chosen are in the order of their computed ranks, so two of different lengths have neighbours of different
-        // lengths between them; what is left of a beam comes after its next candidate, which each lane compares with
-        // the last of the chosen.
-        bool unsure = false;
-        if (p.penalty != 0.f) {
-          const int next_len = __shfl_down_sync(~0u, from_len, 1), last_len = __shfl_sync(~0u, from_len, p.W - 1);
-          const u64 next = __shfl_down_sync(~0u, chosen, 1), last = __shfl_sync(~0u, chosen, p.W - 1);
-          unsure = mine && (sm.inv[lane] < kSmallInverse ||
-                            (lane + 1 < p.W && next_len != from_len && chosen > lowest && chosen - next < kClearSteps) ||
-                            (key != 0 && len != last_len && last > lowest && last - key < kClearSteps));
-        }
-        unsure = __any_sync(~0u, unsure);
-        if (lane == 0) sm.unsure = unsure;
-      }
-    }
-    if (careful || p.penalty == 0.f) return;
-    __syncthreads();
-    if (!sm.unsure) return;
-    if (warp == kBeamWarps - 1) sm.inv[lane] = length_power(max(len, 1), p.penalty);
-    __syncthreads();
   }
+  __syncthreads();
+  if (sm.unsure || __any_sync(~0u, mine && sm.used[lane] > sm.open[lane])) choose_again<T>(p, sm, base, cum, done, len);
 }
 
 // -------------------------------------------------------------------------- reordering

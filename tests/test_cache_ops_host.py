@@ -193,6 +193,18 @@ def test_oracle_beam_select_closed_forms():
     assert t.tolist() == [[0, 1, 0, 1]] and p.tolist() == [[0, 0, 1, 1]]
 
 
+def test_oracle_beam_select_orders_equal_ranks_by_beam_and_token():
+    lowest = np.finfo(np.float32).min
+    x = np.tile(np.array([0.0, 1.0, 2.0]), (1, 3, 1))
+    t, p, _, _, _ = C.beam_select(x, np.full((1, 3), lowest))
+    assert t.tolist() == [[0, 1, 2]] and p.tolist() == [[0, 0, 0]]
+    t, p, _, _, _ = C.beam_select(x[..., :2], np.array([[lowest, lowest, -1.0]]))
+    assert t.tolist() == [[1, 0, 0]] and p.tolist() == [[2, 2, 0]]
+    t, p, _, _, _ = C.beam_select(x, np.array([[-5.0, -1.0, -2.0]]), eos=1, finished=np.ones((1, 3)), lengths=np.array([[5, 1, 1]]),
+                                  penalty=1.0)
+    assert t.tolist() == [[1, 1, 1]] and p.tolist() == [[0, 1, 2]]
+
+
 def test_oracle_beam_reorder_by_hand():
     """Parents 1 1 0 1 of four beams with 10 tokens on pages of 4: beams 2 and 3 have no child."""
     table = np.array([[0, 1, 10, 90], [0, 2, 11, 91], [0, 3, 12, 92], [0, 4, 13, 93]], np.int32)

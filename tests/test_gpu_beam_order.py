@@ -1,10 +1,11 @@
-"""pa_beam_select where ranks are equal or all but equal (needs a GPU): the lower beam comes first,
-whatever the lengths the equal ranks come from."""
+"""pa_beam_select where ranks are equal or all but equal (needs a GPU): the lower beam comes first, then the
+lower token, whatever the lengths and logits the equal ranks come from."""
 import numpy as np
 import pytest
 import torch
 
 from cache_util import dev, host
+from oracle import cache_ops as C
 from paged_fp8_kv_04_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +87,61 @@ def test_powers_near_and_beyond_the_largest_double(penalty):
         rank = s.astype(np.float64) / n.astype(np.float64) ** float(np.float32(penalty)) + 0.0
     parents, _ = _ended(s, n, penalty)
     assert np.array_equal(parents, np.argsort(-rank, axis=1, kind="stable"))
+
+
+# ------------------------------------------------------------ equal totals within a beam
+
+def _same_as_definition(x, scores, lengths=None, penalty=0.0):
+    got = B.beam_select(x, dev(scores), lengths=None if lengths is None else dev(lengths), length_penalty=penalty)
+    want = C.beam_select(x.double().cpu().numpy(), scores, -1, None, lengths, penalty)
+    assert np.array_equal(host(got[0]), want[0]) and np.array_equal(host(got[1]), want[1])
+    # one rounding to fp32, and a log-sum-exp of some hundred thousand exponentials off by 2^-22 each
+    assert np.allclose(host(got[2]).astype(np.float64), want[2], rtol=2.0 ** -23, atol=2.0 ** -18)
+    if lengths is not None:
+        assert np.array_equal(host(got[4]), want[4])
+
+
+def test_a_score_that_swallows_the_logits():
+    lowest = torch.finfo(torch.float32).min
+    x = torch.tensor([[[0.0, 1.0, 2.0]] * 3], device="cuda")
+    tokens, parents, _, _, _ = B.beam_select(x, torch.full((1, 3), lowest, device="cuda"))
+    assert host(tokens).tolist() == [[0, 1, 2]] and host(parents).tolist() == [[0, 0, 0]]
+    tokens, parents, _, _, _ = B.beam_select(x, torch.tensor([[lowest, lowest, -1.0]], device="cuda"))
+    assert host(tokens).tolist() == [[2, 1, 0]] and host(parents).tolist() == [[2, 2, 2]]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("W", [1, 3, 8, 32])
+@pytest.mark.parametrize("V", [2, 7, 31, 300, 70001])
+def test_beams_that_hardly_exist(dt, W, V):
+    """The type's lowest value as the score of a beam that does not exist yet: all its tokens are equal."""
+    rng = np.random.default_rng(V + W)
+    lowest = np.finfo(np.float32).min
+    scores = np.full((3, W), lowest, np.float32)
+    scores[1, 0] = scores[2, W - 1] = -1.5                   # a first step
+    big = torch.from_numpy(3 * rng.standard_normal((3, W, V + 3)).astype(np.float32)).to(dt).cuda()
+    big[0, :, :] = big[0].sort(-1).values                    # the lowest tokens have the lowest logits
+    for lo in (0, 1, 3):                                     # rows that begin at any alignment
+        _same_as_definition(big[..., lo:lo + V], scores)
+
+
+@pytest.mark.parametrize("dt,score,unit,base", [(torch.float32, -1e12, 2.0 ** -16, 200.0), (torch.bfloat16, -2.0 ** 60, 8.0, 1280.0)])
+@pytest.mark.parametrize("W", [1, 4, 17, 32])
+@pytest.mark.parametrize("V,cells", [(50, 2), (3000, 100), (40000, 3), (40000, 1000), (140001, 64)])
+def test_totals_that_round_together(dt, score, unit, base, W, V, cells):
+    """Logits within a rounding cell of the total: fp64 numbers of the score's size lie 8 (fp32) or 32 (bf16) units
+    apart, the logits at most 3 or 12 units from a multiple of that, so that the last bits of the
+    log-sum-exp decide nothing.  One token has logit 0 and all others e^-200 of its weight or less: its log is 0."""
+    rng = np.random.default_rng(V + W)
+    cell = 8 if dt == torch.float32 else 32
+    cells = cells if dt == torch.float32 else min(cells, 3)
+    at = cell * rng.integers(0, cells, size=(2, W, V)) + rng.integers(-(3 * cell // 8), 3 * cell // 8 + 1, size=(2, W, V))
+    x = torch.from_numpy(-(base + unit * at)).to(dt)
+    assert np.array_equal(x.double().numpy(), -(base + unit * at))
+    x.scatter_(2, torch.from_numpy(rng.integers(0, V, size=(2, W, 1))), 0.0)
+    scores = np.full((2, W), score, np.float32)
+    scores[1, ::2] = 2 * score                               # whose cells are twice as wide
+    scores[1, 0] = score
+    x = x.cuda()
+    _same_as_definition(x, scores)
+    _same_as_definition(x, scores, np.full((2, W), 2, np.int32), 1.0)  # quotients by 3 round together what totals do not
