@@ -422,7 +422,7 @@ typedef struct pa_evict_select_args {
   const float *mass;             /* fp32 [num_seqs, num_kv_heads, mass_stride] */
   const int32_t *context_lens;   /* [num_seqs] */
   int32_t *keep;                 /* out: [num_seqs, num_kv_heads, budget] kept positions, ascending, -1 after */
-  int32_t *new_lens;             /* out: [num_seqs] min(context_len, budget); must not be context_lens */
+  int32_t *new_lens;             /* out: [num_seqs] min(context_len, budget) */
   uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT, PA_DEV_TIMEOUT are OR-ed in */
   int32_t num_seqs;              /* >= 0, num_seqs * num_kv_heads <= 65535; 0 enqueues nothing */
   int32_t num_kv_heads;          /* 1 .. 64 */
@@ -439,9 +439,10 @@ typedef struct pa_evict_select_args {
  * last keep_recent, and of those between the ones with the largest mass until there are budget
  * of them; equal masses (0 and -0 are equal) stay lowest position first, and a NaN counts as less
  * than any number.  The result is exact, whatever the values.  A request whose context is negative
- * or beyond mass_stride is flagged: its keep rows are all -1 and its new_lens 0.  One kernel
+ * or beyond mass_stride is flagged: its keep rows are all -1 and its new_lens 0.  keep and new_lens
+ * share no byte with each other, mass or context_lens.  One kernel
  * launch on `stream`; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing
- * pointer or a value out of range, PA_ERR_ALIGN for a pointer not aligned to 4 bytes,
+ * pointer, a value out of range or such an overlap, PA_ERR_ALIGN for a pointer not aligned to 4 bytes,
  * PA_ERR_UNSUPPORTED for a shape beyond the limits above, PA_ERR_CUDA when the launch fails. */
 pa_status_t pa_evict_select(const pa_evict_select_args_t *args, void *stream);
 

@@ -558,6 +558,10 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   if (!aligned(a->mass, 4) || !aligned(a->context_lens, 4) || !aligned(a->keep, 4) ||
       !aligned(a->new_lens, 4) || !aligned(a->status, 4))
     return PA_ERR_ALIGN;
+  const uint64_t lens = (uint64_t)a->num_seqs * 4, cells = lens * a->num_kv_heads;
+  const pa_host::Span mass = {a->mass, cells * a->mass_stride}, old = {a->context_lens, lens};
+  const pa_host::Span keep = {a->keep, cells * a->budget}, made = {a->new_lens, lens};
+  if (pa_host::overlaps(made, {old, mass, keep}) || pa_host::overlaps(keep, {old, mass})) return PA_ERR_INVALID_ARG;
   if (a->num_seqs == 0) return PA_OK;
   SelectParams p;
   p.mass = a->mass;

@@ -6,6 +6,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <initializer_list>
 
 #include "pa.h"
 
@@ -69,6 +70,19 @@ class Launch {
 inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+// The memory of one tensor of a call; absent ones have no bytes.
+struct Span {
+  const void *p;
+  uint64_t n;
+};
+// Whether an output shares a byte with one of the call's other tensors: several CTAs read what others write, in no order.
+inline bool overlaps(const Span &out, std::initializer_list<Span> others) {
+  if (out.p == nullptr || out.n == 0) return false;
+  for (const Span &o : others)
+    if (o.p != nullptr && o.n != 0 && overlap(out.p, out.n, o.p, o.n)) return true;
+  return false;
 }
 
 }  // namespace pa_host

@@ -158,6 +158,20 @@ def test_beam_reorder_state_overlaps(lib):
     assert call(1, (x, x + 4096, 64), (x + 4096, x + 8192, 64)) == INVALID    # one's output is another's input
 
 
+# Outputs that share bytes with what other CTAs of the call read or write: refused before any device is touched.
+
+X = 0x900000000
+
+
+@pytest.mark.parametrize("over", [
+    dict(context_lens=X, new_lens=X), dict(context_lens=X, new_lens=X + 4), dict(context_lens=X + 28, new_lens=X),
+    dict(mass=X, keep=X), dict(mass=X, keep=X + 8 * 4096 - 4), dict(mass=X + 8 * 512 - 4, keep=X), dict(mass=X, new_lens=X + 64),
+    dict(context_lens=X, keep=X + 16), dict(keep=X, new_lens=X + 8 * 512 - 4),
+])
+def test_evict_select_refuses_overlaps(lib, over):
+    assert lib.pa_evict_select(ctypes.byref(_fill(B.EvictSelectArgs, dict(SELECT, num_seqs=8), over)), None) == INVALID
+
+
 # ------------------------------------------------------------------------ the oracle
 
 def test_oracle_mass_sums_to_the_rows():
