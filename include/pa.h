@@ -533,8 +533,9 @@ typedef struct pa_beam_select_args {
  * accumulated in fp32 over short runs and joined in fp64; the power of a length is CUDA's pow, within two units
  * of its last place, and with a length_penalty of 1 the length itself), and ranks that round to the same number are
  * equal, also those of different logits; scores_out is rounded once.  One kernel launch on `stream`;
- * no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer or a value out
- * of range, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for more than 32 beams,
+ * no host synchronisation, no allocation.  Outputs share no byte with each other or an input, but for an output
+ * that begins where its own input does.  PA_ERR_INVALID_ARG for a missing pointer, a value out
+ * of range or another overlap, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for more than 32 beams,
  * 65535 requests or 2^24 tokens, PA_ERR_CUDA when the launch fails. */
 pa_status_t pa_beam_select(const pa_beam_select_args_t *args, void *stream);
 
@@ -545,14 +546,14 @@ typedef struct pa_beam_reorder_args {
   const int32_t *parents;        /* [num_reqs, num_beams]: pa_beam_select's */
   const int32_t *context_lens;   /* [num_reqs * num_beams]: tokens in each beam's cache, equal within a request */
   const int32_t *block_table;    /* [num_reqs * num_beams, block_table_stride] */
-  int32_t *block_table_out;      /* same shape; must not overlap block_table */
+  int32_t *block_table_out;      /* same shape; must not overlap block_table, parents, context_lens or a state */
   void *k_cache;                 /* [num_pages, num_kv_heads, page_size, head_dim], e4m3 or bf16; 16-B aligned */
   void *v_cache;
   float *k_scale;                /* fp32 [num_pages, num_kv_heads, page_size]; PER_TOKEN only, 4-B aligned */
   float *v_scale;
   uint32_t *status;              /* nullable: PA_DEV_BAD_BEAM, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_PAGE are OR-ed in */
   const void *state_in[PA_MAX_BEAM_STATES];  /* num_states device arrays of num_reqs * num_beams rows of */
-  void *state_out[PA_MAX_BEAM_STATES];       /*   state_bytes bytes each; in and out must not overlap */
+  void *state_out[PA_MAX_BEAM_STATES];       /*   state_bytes bytes each; outs overlap nothing else */
   int64_t state_bytes[PA_MAX_BEAM_STATES];   /* > 0 */
   int64_t num_pages;
   int32_t num_states;            /* 0 .. 4 */

@@ -3,6 +3,7 @@
 // the contract.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -960,6 +961,23 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
       !aligned(a->lengths, 4) || !aligned(a->tokens, 4) || !aligned(a->parents, 4) || !aligned(a->scores_out, 4) ||
       !aligned(a->lengths_out, 4))
     return PA_ERR_ALIGN;
+  {
+    using pa_host::Span;
+    const bool f32 = a->logits_dtype == PA_LOGITS_F32;
+    const uint64_t beams = (uint64_t)a->num_reqs * a->num_beams, stride = std::min<int64_t>(a->logits_stride, 1ll << 36);
+    const Span logits = {a->logits, beams == 0 ? 0 : ((beams - 1) * stride + a->vocab) * (f32 ? 4 : 2)};
+    const Span scores = {a->scores, 4 * beams}, finished = {a->finished, beams}, lengths = {a->lengths, 4 * beams};
+    const Span tokens = {a->tokens, 4 * beams}, parents = {a->parents, 4 * beams}, scores_out = {a->scores_out, 4 * beams};
+    const Span finished_out = {a->finished_out, beams}, lengths_out = {a->lengths_out, 4 * beams};
+    // an output in place of its input is that input; a part of it is another request's
+    auto unless = [](const Span &in, const Span &out) { return Span{in.p == out.p ? nullptr : in.p, in.n}; };
+    if (pa_host::overlaps(tokens, {logits, scores, finished, lengths, parents, scores_out, finished_out, lengths_out}) ||
+        pa_host::overlaps(parents, {logits, scores, finished, lengths, scores_out, finished_out, lengths_out}) ||
+        pa_host::overlaps(scores_out, {logits, unless(scores, scores_out), finished, lengths, finished_out, lengths_out}) ||
+        pa_host::overlaps(finished_out, {logits, scores, unless(finished, finished_out), lengths, lengths_out}) ||
+        pa_host::overlaps(lengths_out, {logits, scores, finished, unless(lengths, lengths_out)}))
+      return PA_ERR_INVALID_ARG;
+  }
   if (a->num_reqs == 0) return PA_OK;
   BeamParams p;
   p.logits = a->logits;
@@ -1010,13 +1028,17 @@ extern "C" pa_status_t pa_beam_reorder(const pa_beam_reorder_args_t *a, void *st
     return PA_ERR_INVALID_ARG;
   const uint64_t rows = (uint64_t)a->num_reqs * a->num_beams;
   const uint64_t tbytes = rows * a->block_table_stride * sizeof(int32_t);
-  if (pa_host::overlap(a->block_table, tbytes, a->block_table_out, tbytes)) return PA_ERR_INVALID_ARG;
+  const pa_host::Span parents = {a->parents, 4 * rows}, lens = {a->context_lens, 4 * rows}, table_out = {a->block_table_out, tbytes};
+  if (pa_host::overlaps(table_out, {{a->block_table, tbytes}, parents, lens})) return PA_ERR_INVALID_ARG;
   int64_t widest = 0;
   for (int k = 0; k < a->num_states; ++k) {
     if (a->state_in[k] == nullptr || a->state_out[k] == nullptr || a->state_bytes[k] < 1 ||
         a->state_bytes[k] > (INT64_MAX >> 17))
       return PA_ERR_INVALID_ARG;
     const uint64_t n = rows * (uint64_t)a->state_bytes[k];
+    if (pa_host::overlaps({a->state_out[k], n}, {{a->block_table, tbytes}, table_out, parents, lens}) ||
+        pa_host::overlaps(table_out, {{a->state_in[k], n}}))
+      return PA_ERR_INVALID_ARG;
     for (int i = 0; i <= k; ++i) {
       const uint64_t ni = rows * (uint64_t)a->state_bytes[i];
       if (pa_host::overlap(a->state_in[i], ni, a->state_out[k], n) ||

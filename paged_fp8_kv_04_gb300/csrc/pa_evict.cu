@@ -619,6 +619,11 @@ extern "C" pa_status_t pa_kv_compact(const pa_kv_compact_args_t *a, void *stream
     if (in_place ? (a->mass_out != a->mass || a->mass_out_stride != a->mass_stride)
                  : pa_host::overlap(a->mass, rows * a->mass_stride, a->mass_out, rows * a->mass_out_stride))
       return PA_ERR_INVALID_ARG;
+    const uint64_t lens = (uint64_t)a->num_seqs * 4;
+    if (pa_host::overlaps({a->mass_out, rows * a->mass_out_stride},
+                          {{a->keep, rows * a->keep_stride}, {a->new_lens, lens}, {a->block_table, lens * a->block_table_stride},
+                           {a->dst_block_table, in_place ? 0 : lens * a->dst_block_table_stride}}))
+      return PA_ERR_INVALID_ARG;
   }
   if (!aligned(a->keep, 4) || !aligned(a->new_lens, 4) || !aligned(a->block_table, 4) ||
       !aligned(a->dst_block_table, 4) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) ||

@@ -172,6 +172,42 @@ def test_evict_select_refuses_overlaps(lib, over):
     assert lib.pa_evict_select(ctypes.byref(_fill(B.EvictSelectArgs, dict(SELECT, num_seqs=8), over)), None) == INVALID
 
 
+@pytest.mark.parametrize("over", [
+    dict(mass_out=X, keep=X + 8), dict(mass_out=X, new_lens=X + 2048 - 4), dict(mass_out=X, block_table=X),
+    dict(mass_out=X + 12, dst_block_table=X),
+    dict(dst_block_table=None, mass=X, mass_out=X, mass_out_stride=1024, keep=X + 8188),
+])
+def test_kv_compact_refuses_overlaps(lib, over):
+    assert lib.pa_kv_compact(ctypes.byref(_fill(B.KvCompactArgs, dict(COMPACT, num_seqs=2), over)), None) == INVALID
+
+
+@pytest.mark.parametrize("over", [
+    dict(scores=X, scores_out=X + 4), dict(scores=X + 16, scores_out=X), dict(finished=X, finished_out=X + 1),
+    dict(lengths=X, lengths_out=X + 16), dict(tokens=X, parents=X), dict(tokens=X, scores=X + 44), dict(parents=X, lengths=X),
+    dict(scores_out=X, finished=X + 8), dict(tokens=X, finished_out=X), dict(lengths_out=X, scores=X), dict(scores_out=X, lengths_out=X),
+    dict(logits=X, tokens=X + 11 * 2000 + 1996), dict(logits=X, scores_out=X), dict(logits=X, finished_out=X + 5000),
+    dict(logits=X, lengths_out=X + 8, logits_stride=1 << 62),
+])
+def test_beam_select_refuses_overlaps(lib, over):
+    assert lib.pa_beam_select(ctypes.byref(_fill(B.BeamSelectArgs, dict(BEAM, num_reqs=3), over)), None) == INVALID
+
+
+@pytest.mark.parametrize("over", [
+    dict(parents=X, block_table_out=X), dict(context_lens=X + 96, block_table_out=X), dict(block_table=X, block_table_out=X + 4),
+])
+def test_beam_reorder_refuses_overlaps(lib, over):
+    assert lib.pa_beam_reorder(ctypes.byref(_fill(B.BeamReorderArgs, dict(REORDER, num_reqs=1), over)), None) == INVALID
+
+
+@pytest.mark.parametrize("name", ["parents", "context_lens", "block_table", "block_table_out"])
+def test_beam_reorder_refuses_states_over_its_tables(lib, name):
+    call = lambda s: lib.pa_beam_reorder(ctypes.byref(_states(_fill(  # noqa: E731
+        B.BeamReorderArgs, dict(REORDER, num_reqs=1), {name: X}), s)), None)
+    assert call((X + (1 << 20), X + 8, 64)) == INVALID
+    if name == "block_table_out":
+        assert call((X + 124, X + (1 << 20), 64)) == INVALID
+
+
 # ------------------------------------------------------------------------ the oracle
 
 def test_oracle_mass_sums_to_the_rows():
