@@ -368,7 +368,8 @@ typedef struct pa_attn_mass_args {
   const float *lse;              /* fp32 [num_rows, num_kv_heads * group_size]: pa_decode's lse of the same step
                                     (natural log; a row of -inf gives no weight) */
   const float *mass;             /* fp32 [num_seqs, num_kv_heads, mass_stride]; may be NULL when decay is 0 */
-  float *mass_out;               /* same shape; may be `mass` itself (any other overlap is refused) */
+  float *mass_out;               /* same shape; may be `mass` itself (any other overlap, also with q, lse or the index
+                                    inputs, is refused) */
   uint32_t *status;              /* nullable: PA_DEV_BAD_PAGE, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_QLEN,
                                     PA_DEV_TIMEOUT are OR-ed in */
   int64_t num_pages;
@@ -459,7 +460,8 @@ typedef struct pa_kv_compact_args {
   float *v_scale;
   const float *mass;             /* nullable: fp32 [num_seqs, num_kv_heads, mass_stride] */
   float *mass_out;               /* where the kept tokens' mass goes: [num_seqs, num_kv_heads, mass_out_stride]; in place
-                                    `mass` itself with the same stride, with dst_block_table not overlapping it */
+                                    `mass` itself with the same stride, with dst_block_table not overlapping it; and
+                                    not overlapping keep, new_lens or the tables */
   uint32_t *status;              /* nullable: PA_DEV_BAD_KEEP, PA_DEV_BAD_PAGE are OR-ed in */
   int64_t num_pages;
   int32_t num_seqs;              /* >= 0, num_seqs * num_kv_heads <= 65535; 0 enqueues nothing */

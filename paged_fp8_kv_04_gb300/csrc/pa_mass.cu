@@ -654,6 +654,10 @@ extern "C" pa_status_t pa_attn_mass(const pa_attn_mass_args_t *a, void *stream) 
   const uint64_t bytes = (uint64_t)a->num_seqs * a->num_kv_heads * a->mass_stride * sizeof(float);
   if (a->mass != nullptr && a->mass != a->mass_out && pa_host::overlap(a->mass, bytes, a->mass_out, bytes))
     return PA_ERR_INVALID_ARG;
+  const uint64_t lens = (uint64_t)a->num_seqs * 4, heads = (uint64_t)a->num_rows * a->num_kv_heads * kG;
+  if (pa_host::overlaps({a->mass_out, bytes}, {{a->q, heads * kD * 2}, {a->lse, heads * 4}, {a->context_lens, lens},
+                                               {a->cu_seqlens_q, lens + 4}, {a->block_table, lens * a->block_table_stride}}))
+    return PA_ERR_INVALID_ARG;
   if (a->num_seqs == 0 || a->num_rows == 0) return PA_OK;
 
   const MassDevice *dev = mass_device();

@@ -164,6 +164,14 @@ X = 0x900000000
 
 
 @pytest.mark.parametrize("over", [
+    dict(lse=X, mass_out=X + 8), dict(q=X, mass_out=X + 2 * 16 * 256 - 4), dict(context_lens=X + 4096, mass_out=X),
+    dict(cu_seqlens_q=X, mass_out=X + 8), dict(block_table=X, mass_out=X + 60),
+])
+def test_attn_mass_refuses_overlaps(lib, over):
+    assert lib.pa_attn_mass(ctypes.byref(_fill(B.AttnMassArgs, dict(MASS, num_seqs=2, num_rows=2), over)), None) == INVALID
+
+
+@pytest.mark.parametrize("over", [
     dict(context_lens=X, new_lens=X), dict(context_lens=X, new_lens=X + 4), dict(context_lens=X + 28, new_lens=X),
     dict(mass=X, keep=X), dict(mass=X, keep=X + 8 * 4096 - 4), dict(mass=X + 8 * 512 - 4, keep=X), dict(mass=X, new_lens=X + 64),
     dict(context_lens=X, keep=X + 16), dict(keep=X, new_lens=X + 8 * 512 - 4),
