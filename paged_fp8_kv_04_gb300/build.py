@@ -32,20 +32,27 @@ def sources():
 
 def _inputs():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        [os.path.join(INCLUDE, "pa.h")]
+        [os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
 
 
-def up_to_date(path: str = LIB_PATH) -> bool:
+def up_to_date(path: str = LIB_PATH, inputs: list[str] | None = None) -> bool:
+    """Whether `path` is newer than its inputs (default: the library's), this file's flags among them."""
     if not os.path.exists(path):
         return False
     t = os.path.getmtime(path)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return all(os.path.getmtime(f) <= t for f in (inputs or _inputs()))
 
 
 def torch_module_path() -> str:
-    """pa_torch.so is built against one torch: its version is in the name."""
+    """The torch module is built against one torch and one interpreter: both are in the name."""
+    import sysconfig
+
     import torch
-    return os.path.join(BUILD_DIR, f"pa_torch.{torch.__version__}.so")
+    return os.path.join(BUILD_DIR, f"pa_torch.{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _torch_module_inputs() -> list[str]:
+    return [TORCH_SOURCE, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
 
 
 def _start_torch_module(force: bool):
@@ -54,9 +61,7 @@ def _start_torch_module(force: bool):
 
     import torch
     out = torch_module_path()
-    due = force or not os.path.exists(out) or any(
-        os.path.getmtime(f) > os.path.getmtime(out) for f in (TORCH_SOURCE, os.path.join(INCLUDE, "pa.h")))
-    if not due:
+    if not force and up_to_date(out, _torch_module_inputs()):
         return None
     os.makedirs(BUILD_DIR, exist_ok=True)
     root = os.path.dirname(os.path.abspath(torch.__file__))

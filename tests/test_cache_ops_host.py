@@ -311,3 +311,20 @@ def test_torch_module_missing_fails_loudly(built, monkeypatch, tmp_path):
     monkeypatch.setattr(libbuild, "torch_module_path", lambda: str(tmp_path / "pa_torch.so"))
     with pytest.raises(ImportError):
         B.evict_select(torch.zeros(2, 1, 8), torch.zeros(2, dtype=torch.int32), budget=4)
+
+
+def test_the_torch_module_belongs_to_one_interpreter_and_one_set_of_flags(built, monkeypatch, tmp_path):
+    """Another Python finds no module of its own rather than this one's, and changed flags rebuild both libraries."""
+    import os
+    import sysconfig
+    mine = libbuild.torch_module_path()
+    assert os.path.exists(mine) and libbuild.up_to_date(mine, libbuild._torch_module_inputs())
+    assert os.path.abspath(libbuild.__file__) in libbuild._torch_module_inputs()
+    assert os.path.abspath(libbuild.__file__) in libbuild._inputs()
+    old = tmp_path / "old.so"
+    old.write_bytes(b"")
+    os.utime(old, (0, 0))
+    assert not libbuild.up_to_date(str(old)) and not libbuild.up_to_date(str(old), [libbuild.__file__])
+    real = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda k: ".cpython-399-other.so" if k == "EXT_SUFFIX" else real(k))
+    assert libbuild.torch_module_path() != mine and not os.path.exists(libbuild.torch_module_path())
