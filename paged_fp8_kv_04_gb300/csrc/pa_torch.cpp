@@ -9,7 +9,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -156,8 +157,21 @@ c10::cuda::CUDAStream stream_arg(PyObject *o, int dev) {
   return c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(h), (c10::DeviceIndex)dev);
 }
 
-// A given output, or one allocated on the launching stream (torch's allocator reuses a block in
-// the order of the stream it was allocated on).  Owns a reference to the Python object.
+// A new tensor from torch's allocator, on the launching stream (the allocator reuses a block in the order of the stream
+// it was allocated on).  Each output has storage of its own: tensors cut from one allocation would cost less, but a
+// caller's resize_ of one runs into its neighbour.  Without the dispatcher, which takes as long as the allocation.
+Tensor make(ScalarType type, IntArrayRef shape, int dev, const c10::cuda::CUDAStream &stream, bool own_stream) {
+  std::optional<c10::cuda::CUDAStreamGuard> on;
+  std::optional<c10::cuda::CUDAGuard> at_dev;
+  if (own_stream)
+    on.emplace(stream);
+  else if (c10::cuda::current_device() != dev)
+    at_dev.emplace((c10::DeviceIndex)dev);
+  return Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                          type, std::nullopt));
+}
+
+// A given output, or a new one.  Owns a reference to the Python object.
 class Output {
  public:
   Output() = default;
@@ -169,17 +183,12 @@ class Output {
       obj_ = given;
       return;
     }
-    std::optional<c10::cuda::CUDAStreamGuard> on;
-    if (own_stream) on.emplace(stream);
-    Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev));
+    Tensor t = make(type, shape, dev, stream, own_stream);
     ptr_ = t.data_ptr();
     obj_ = THPVariable_Wrap(std::move(t));
     if (obj_ == nullptr) throw Refusal(nullptr, "");
   }
   ~Output() { Py_XDECREF(obj_); }
-  explicit Output(Tensor t) : ptr_(t.data_ptr()), obj_(THPVariable_Wrap(std::move(t))) {
-    if (obj_ == nullptr) throw Refusal(nullptr, "");
-  }
   Output(const Output &) = delete;
   Output &operator=(const Output &) = delete;
   template <typename T>
@@ -197,17 +206,6 @@ class Output {
   void *ptr_ = nullptr;
   PyObject *obj_ = nullptr;
 };
-
-// Several small outputs of one call in one allocation: a tensor of `type` and `shape` over the bytes
-// [at, ...) of `block`.  (torch's allocation costs over a microsecond each, a tensor over given
-// storage a fifth of that.)
-Tensor carve(const Tensor &block, int64_t at, ScalarType type, IntArrayRef shape) {
-  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
-                                                      c10::scalarTypeToTypeMeta(type));
-  t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(type));
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  return t;
-}
 
 // Calls an entry point on the device and stream; a status other than PA_OK becomes the error class.
 // An empty batch enqueues nothing (torch's empty tensors have no pointer that the library could check).
@@ -316,25 +314,13 @@ PyObject *evict_select(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.keep_first = int_arg(x[7], "first");
     a.keep_recent = int_arg(x[8], "recent");
     const int64_t width = a.budget > 0 ? a.budget : 1;  // (the library refuses a budget below 1)
-    const int64_t rows = s[0] * s[1];
     const bool own_stream = x[5] != Py_None;
-    std::optional<Output> keep, lens;
-    // both in one allocation, unless holding on to the lengths would hold on to much
-    if (x[2] == Py_None && x[3] == Py_None && rows <= 16384 && rows * width <= 16384) {
-      const int64_t cells = rows * width;
-      std::optional<c10::cuda::CUDAStreamGuard> on;
-      if (own_stream) on.emplace(stream);
-      const Tensor block = at::empty({cells + s[0]}, at::TensorOptions().dtype(ScalarType::Int).device(at::kCUDA, (c10::DeviceIndex)dev));
-      keep.emplace(carve(block, 0, ScalarType::Int, {s[0], s[1], width}));
-      lens.emplace(carve(block, 4 * cells, ScalarType::Int, s[0]));
-    } else {
-      keep.emplace(x[2], "keep", ScalarType::Int, IntArrayRef({s[0], s[1], width}), dev, stream, own_stream);
-      lens.emplace(x[3], "new_lens", ScalarType::Int, s[0], dev, stream, own_stream);
-    }
-    a.keep = keep->as<int32_t>();
-    a.new_lens = lens->as<int32_t>();
+    Output keep(x[2], "keep", ScalarType::Int, {s[0], s[1], width}, dev, stream, own_stream);
+    Output lens(x[3], "new_lens", ScalarType::Int, s[0], dev, stream, own_stream);
+    a.keep = keep.as<int32_t>();
+    a.new_lens = lens.as<int32_t>();
     enqueue("pa_evict_select", g_lib.evict_select, a, s[0] == 0, dev, stream);
-    return Py_BuildValue("(NN)", keep->release(), lens->release());
+    return Py_BuildValue("(NN)", keep.release(), lens.release());
   });
 }
 
@@ -413,42 +399,20 @@ PyObject *beam_select(PyObject *, PyObject *const *x, Py_ssize_t n) {
     a.logits_dtype = t == ScalarType::Float ? PA_LOGITS_F32 : PA_LOGITS_BF16;
     a.eos_token = int_arg(x[10], "eos");
     a.length_penalty = float_arg(x[11]);
-    // the outputs that are not given share one allocation, each 16-byte aligned in it
-    const int64_t words = (4 * N * W + 15) / 16 * 16, bytes = (N * W + 15) / 16 * 16;
     const bool ends = x[2] != Py_None || x[7] != Py_None, lasts = x[3] != Py_None || x[8] != Py_None;
-    Tensor block;
-    int64_t at = 0;
-    auto output = [&](std::optional<Output> &o, int i, const char *name, ScalarType type, int64_t size) {
-      if (x[i] != Py_None) {
-        o.emplace(x[i], name, type, s, dev, stream, own);
-        return;
-      }
-      if (!block.defined()) {
-        std::optional<c10::cuda::CUDAStreamGuard> on;
-        if (own) on.emplace(stream);
-        block = at::empty({4 * words + bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
-      }
-      o.emplace(carve(block, at, type, s));
-      at += size;
-    };
-    std::optional<Output> tokens, parents, totals, ended, lens;
-    output(tokens, 4, "tokens", ScalarType::Int, words);
-    output(parents, 5, "parents", ScalarType::Int, words);
-    output(totals, 6, "scores_out", ScalarType::Float, words);
-    if (lasts) {
-      output(lens, 8, "lengths_out", ScalarType::Int, words);
-      a.lengths_out = lens->as<int32_t>();
-    }
-    if (ends) {
-      output(ended, 7, "finished_out", ScalarType::Byte, bytes);
-      a.finished_out = ended->as<uint8_t>();
-    }
-    a.tokens = tokens->as<int32_t>();
-    a.parents = parents->as<int32_t>();
-    a.scores_out = totals->as<float>();
+    Output tokens(x[4], "tokens", ScalarType::Int, s, dev, stream, own), parents(x[5], "parents", ScalarType::Int, s, dev, stream, own);
+    Output totals(x[6], "scores_out", ScalarType::Float, s, dev, stream, own);
+    std::optional<Output> ended, lens;
+    if (ends) ended.emplace(x[7], "finished_out", ScalarType::Byte, s, dev, stream, own);
+    if (lasts) lens.emplace(x[8], "lengths_out", ScalarType::Int, s, dev, stream, own);
+    a.tokens = tokens.as<int32_t>();
+    a.parents = parents.as<int32_t>();
+    a.scores_out = totals.as<float>();
+    if (ends) a.finished_out = ended->as<uint8_t>();
+    if (lasts) a.lengths_out = lens->as<int32_t>();
     enqueue("pa_beam_select", g_lib.beam_select, a, N == 0, dev, stream);
     Output none;
-    return Py_BuildValue("(NNNNN)", tokens->release(), parents->release(), totals->release(),
+    return Py_BuildValue("(NNNNN)", tokens.release(), parents.release(), totals.release(),
                          ended ? ended->release() : none.release(), lens ? lens->release() : none.release());
   });
 }
