@@ -145,3 +145,32 @@ def test_totals_that_round_together(dt, score, unit, base, W, V, cells):
     x = x.cuda()
     _same_as_definition(x, scores)
     _same_as_definition(x, scores, np.full((2, W), 2, np.int32), 1.0)  # quotients by 3 round together what totals do not
+
+
+# --------------------------------------------------------------- the log-sum-exp in totals
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,scale", [(3000, 1.0), (32001, 1.2), (131072, 1.5), (2000000, 1.5)])
+def test_log_sum_exps_are_close_to_fp64(dt, V, scale):
+    """A live beam's best total is set 2^-21 above or below an ended beam's score (through a live score of some 1e-6, in
+    whose fp32 steps nothing is lost), and comes out on that side.  An exponential is off by 2^-22 of itself
+    at most, at worst all in one direction; the roundings of its argument, of products and of partial sums, 2^-19 of it
+    together, differ from term to term, and the sum is spread over 64 terms or more, which leaves an eighth of
+    them: 2^-22 and 2^-22."""
+    rng = np.random.default_rng(V)
+    N = 24
+    x = torch.from_numpy((scale * rng.standard_normal((N, V))).astype(np.float32)).to(dt)
+    xd = x.double().numpy()
+    top = xd.max(1)
+    e = np.exp(xd - top[:, None])
+    best = -np.log(e.sum(1))
+    assert (e.sum(1) ** 2 / (e ** 2).sum(1)).min() > 64
+    ended = best.astype(np.float32)
+    live = x.cuda()[:, None].repeat(1, 2, 1)
+    fin = torch.tensor([0, 1], dtype=torch.uint8, device="cuda").repeat(N, 1)
+    for side in (1, -1):
+        score = (ended - best + side * 1.01 * 2.0 ** -21).astype(np.float32)
+        gap = score.astype(np.float64) + best - ended
+        assert (side * gap > 2.0 ** -21).all() and np.abs(gap).max() < 2.0 ** -20
+        got = B.beam_select(live, dev(np.stack([score, ended], 1)), eos=0, finished=fin)
+        assert (host(got[1])[:, 0] == (0 if side > 0 else 1)).all()
