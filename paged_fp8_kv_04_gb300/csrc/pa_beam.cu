@@ -98,6 +98,13 @@ __device__ __forceinline__ u64 merge32(u64 k, u64 other_reversed, int lane) {
   return k;
 }
 
+// The 32 best of a descending list and 32 keys in any order.  (They take as many instructions as one inserted at its
+// place.)
+__device__ __forceinline__ u64 take32(u64 list, u64 k) {
+  const int lane = threadIdx.x & 31;
+  return merge32(list, __shfl_sync(~0u, sort32(k, lane), 31 - lane), lane);
+}
+
 constexpr int kBeamThreads = 512;
 constexpr int kBeamWarps = kBeamThreads / 32;
 // Vectors cut from two: 1 x 4 x 32001 8.6 us with 3 at a time, 8.9 with 4; 32 x 8 x 131071 fp32 33.3 with 3, 32.3
@@ -470,10 +477,8 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
     return pair_key(x, r.first(jl) + e);
   };
   search([&](const uint4 &v, int jl, unsigned left) {
-    for (; left != 0; left &= left - 1) {
-      const int at = atomicAdd(&sm.cands, 1);
-      if (at < kMaxCands) sm.cand[at] = element(v, jl, left);
-    }
+    if (left == 0) return;
+    for (int at = atomicAdd(&sm.cands, __popc(left)); left != 0 && at < kMaxCands; ++at, left &= left - 1) sm.cand[at] = element(v, jl, left);
   });
   if (wait) pa::cluster_wait();  // the first CTA runs: its shared memory can be written
   __syncthreads();
@@ -489,24 +494,30 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
     }
     if (tid >= cands && tid < kMaxBeams) store_cluster(in_first_cta(&sm.list[slot][tid]), (u64)0);
   } else {
-    // many (long runs of equal or rising values): each warp keeps its best 32 in order, then they are joined
-    u64 mine = 0;
-    search([&](const uint4 &v, int jl, unsigned left) {
-      while (__any_sync(~0u, left != 0)) {
-        const int src = __ffs(__ballot_sync(~0u, left != 0)) - 1;
-        u64 c = 0;
-        if (lane == src) {
-          c = element(v, jl, left);
-          left &= left - 1;
+    // many (long runs of equal or rising values): each warp keeps the best 32 of a share of the vectors in order, then they
+    // are joined (64 x 32 x 1000 bf16: 187 us; 415 with elements counted and inserted one by one)
+    u64 mine = 0, least = 0;
+    const int first = lo + 32 * warp + lane;
+    auto vector = [&](int j) { return j < hi ? r.load(j) : make_uint4(0u, 0u, 0u, 0u); };
+    uint4 v = vector(first), next = vector(first + kBeamThreads);
+    for (int jl = first; jl - lane < hi; jl += kBeamThreads) {
+      const uint4 later = vector(jl + 2 * kBeamThreads);
+      const u64 most = pair_key(Vec<T>::max(v), r.first(jl));
+      if (__any_sync(~0u, jl < hi && most >= tau && most > least)) {
+#pragma unroll 1
+        for (int e = 0; e < E; ++e) {
+          const int at = r.first(jl) + e;
+          u64 k = jl < hi && at < p.V ? pair_key(Vec<T>::get(v, e), at) : 0ull;
+          if (k < tau) k = 0;
+          if (__any_sync(~0u, k > least)) {
+            mine = take32(mine, k);
+            least = __shfl_sync(~0u, mine, 31);
+          }
         }
-        c = __shfl_sync(~0u, c, src);
-        // lanes above it keep theirs, the others shift down by one
-        const int pos = __popc(__ballot_sync(~0u, mine > c));
-        const u64 up = __shfl_up_sync(~0u, mine, 1);
-        if (lane == pos) mine = c;
-        if (lane > pos) mine = up;
       }
-    });
+      v = next;
+      next = later;
+    }
     __syncthreads();  // the owners have been read
     const u64 k = join_warps(mine, sm, warp, lane, kBeamWarps);
     if (warp == 0) store_cluster(in_first_cta(&sm.list[slot][lane]), k);
