@@ -83,8 +83,8 @@ enum { PA_OUT_BF16 = 0, PA_OUT_F32 = 1 };
  *   wait for it to complete before reading q, the caches or the scales, and before
  *   writing anything (before the wait they only ask L2 to prefetch the first pages,
  *   which reads nothing into the kernel).  So with PDL on, the kernel enqueued immediately before pa_decode
- *   must not write those index inputs (copies and host writes are unaffected).  Set
- *   this flag if it does. */
+ *   must not write those index inputs (copies and host writes are unaffected), nor may the one before
+ *   that if it was such a pa_decode.  Set this flag if they do. */
 #define PA_PLAN_NO_PDL 0x1
 /* PA_PLAN_TCGEN05: for an FP8 plan with q_len 1, run the tcgen05 kernel, which feeds the
  *   cache bytes to the tensor core (QK^T and PV as kind::f8f6f4 MMAs with accumulators
@@ -365,8 +365,8 @@ typedef struct pa_attn_mass_args {
   const int32_t *block_table;    /* [num_seqs, block_table_stride] */
   const int32_t *context_lens;   /* [num_seqs]: tokens in each request's cache, own q_len included */
   const int32_t *cu_seqlens_q;   /* [num_seqs + 1]: rows of request r are [cu[r], cu[r+1]) */
-  const float *lse;              /* fp32 [num_rows, num_kv_heads * group_size]: pa_decode's lse of the same step
-                                    (natural log; a row of -inf gives no weight) */
+  const float *lse;              /* fp32 [num_rows, num_kv_heads * group_size]: lse of the same step's pa_decode over
+                                    the whole context (not of a sparse plan; natural log; -inf: no weight) */
   const float *mass;             /* fp32 [num_seqs, num_kv_heads, mass_stride]; may be NULL when decay is 0 */
   float *mass_out;               /* same shape; may be `mass` itself (any other overlap, also with q, lse or the index
                                     inputs, is refused) */
@@ -390,8 +390,9 @@ typedef struct pa_attn_mass_args {
   int32_t reserved;              /* 0 */
 } pa_attn_mass_args_t;
 
-/* Adds one decode step's attention weights to the mass of the cached tokens, the quantity
- * by which pa_evict_select keeps them.  For request r with context L, q_len rows and KV head
+/* Adds one dense decode step's attention weights to the mass of the cached tokens, the quantity
+ * by which pa_evict_select keeps them.  The lse of a decode over selected pages covers those alone, while every
+ * position is weighed here: tokens that nobody attended would gain weight, even above one.  For request r with context L, q_len rows and KV head
  * h, and every position p < L:
  *   w[p] = sum over its rows t and the 16 query heads g of h, where p < L - q_len + t + 1,
  *          of exp(sm_scale * q[t][g] . k[p] * k_scale[p] - lse[t][g]),
@@ -400,8 +401,9 @@ typedef struct pa_attn_mass_args {
  * with decay 0 `mass` is not read.  Positions >= L, and requests without rows, are left as they are
  * (in mass_out).  A position on a bad page gets w = 0.  A request with a bad length is skipped.
  * The mass belongs to the request, not to the page: requests may share pages (a common prefix,
- * beams).  Sums and exponentials are fp32 and always in the same order.  Inputs other than lse's
- * -inf must be finite.  One kernel launch on `stream`; no host synchronisation, no allocation.
+ * beams).  Sums and exponentials are fp32 and always in the same order; with an e4m3 cache a query row is held
+ * as pairs of e4m3 numbers, exactly for elements within 2^-14 of the row's largest and to 2^-22 of that for
+ * smaller ones.  Inputs other than lse's -inf must be finite.  One kernel launch on `stream`; no host synchronisation, no allocation.
  * PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap of mass and
  * mass_out other than equality, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for
  * a shape or mode outside the limits above, PA_ERR_CAPACITY when num_pages * num_kv_heads *
@@ -413,7 +415,9 @@ pa_status_t pa_attn_mass(const pa_attn_mass_args_t *args, void *stream);
 /* A pa_decode on a plan without PA_PLAN_NO_PDL reads its index inputs before the kernel enqueued
  * just before it has completed (see the flag).  pa_evict_select writes new_lens and
  * pa_beam_reorder writes block_table_out, which are such inputs: another kernel has to lie between
- * them and that decode (the write of the step's new tokens does), or the plan has to have the flag. */
+ * them and that decode (the write of the step's new tokens does; a second pa_decode does not, it may let
+ * the next one start before it has waited itself), or the plan has to have the flag.
+ * The indexer's key cache is neither compacted nor reordered by these calls: see pa_kv_compact and pa_beam_reorder. */
 
 #define PA_DEV_BAD_KEEP 0x400u /* pa_kv_compact: new_lens outside [0, keep_stride] or past the tables, or a keep row
                                   that is not ascending positions of the request's cache */
@@ -481,7 +485,9 @@ typedef struct pa_kv_compact_args {
 /* Moves the kept tokens to the front: for every (request r, KV head h) and i < new_lens[r],
  * slot i of r's destination pages takes the K and V rows, the scales and the mass of position
  * keep[r][h][i], bit for bit; afterwards new_lens is the request's context_lens.  Positions
- * keep their order, so causal cutoffs, recency and the indexer's last page stay meaningful.
+ * keep their order, so causal cutoffs and recency stay meaningful.  The indexer's keys and scales are not moved: page
+ * scores of pa_index_topk belong to the tokens that were there before, until the caller has moved its index cache
+ * by the same keep (or written it anew).
  * In place nothing but the request's own first pages is written, and pages all of whose tokens
  * stay are not; slots past new_lens are left as they are.  Pages that another request reads
  * as well (a common prefix, beams) must not be compacted in place: give dst_block_table, whose pages
@@ -520,7 +526,7 @@ typedef struct pa_beam_select_args {
   int32_t vocab;                 /* 1 .. 2^24 */
   int32_t logits_dtype;          /* PA_LOGITS_* */
   int32_t eos_token;             /* the token that ends a beam, or -1: none; needed (>= 0) with finished */
-  float length_penalty;          /* >= 0 */
+  float length_penalty;          /* >= 0; the exponent is this fp32 number (0.6f is 0.60000002384) */
   int32_t reserved;              /* 0 */
 } pa_beam_select_args_t;
 
@@ -531,10 +537,12 @@ typedef struct pa_beam_select_args {
  * then the lower token.  A candidate that does not exist or whose total is NaN (a row of -inf
  * logits, a NaN or +inf among them) counts as -inf and is taken, lowest beam and token first, only
  * where nothing better is left; its scores_out is -inf.  finished_out is set where the parent
- * had ended or the token is eos_token.  Totals and ranks are fp64 (the sum of exponentials is
- * accumulated in fp32 over short runs and joined in fp64; the power of a length is CUDA's pow, within two units
- * of its last place, and with a length_penalty of 1 the length itself), and ranks that round to the same number are
- * equal, also those of different logits; scores_out is rounded once.  One kernel launch on `stream`;
+ * had ended or the token is eos_token.  Totals and ranks are fp64.  The
+ * log-sum-exp in them adds fp32 exponentials, off by 2^-22 of themselves at most, in fp32 over a thread's share of
+ * a row and in steps of 2^-36 across threads; it measures some 1e-7 from fp64's, and totals of two beams that
+ * are closer than that may come in either order unless their rows are equal.  The power of a length is CUDA's pow, within
+ * two units of its last place, and with a length_penalty of 1 the length itself.  Ranks that round to the same number
+ * are equal, also those of different logits.  scores_out is rounded once.  One kernel launch on `stream`;
  * no host synchronisation, no allocation.  Outputs share no byte with each other or an input, but for an output
  * that begins where its own input does.  PA_ERR_INVALID_ARG for a missing pointer, a value out
  * of range or another overlap, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for more than 32 beams,
@@ -580,7 +588,8 @@ typedef struct pa_beam_reorder_args {
  * copied (K, V and scales of all KV heads).  So the partial pages of a request's beams must be its own
  * and distinct before the call, and are afterwards; nothing is allocated.  With parents all 0
  * the call also spreads a prompt, cached once in beam 0's pages, over all beams.  Each state's row j becomes
- * its parent's row (mass, token history).  A flagged request keeps its rows, as if each beam were its
+ * its parent's row (mass, token history).  The indexer's keys are not copied: the page that a further child takes
+ * keeps the childless beam's, and pa_index_topk scores it by them until the caller has copied the parent's.  A flagged request keeps its rows, as if each beam were its
  * own parent.  One kernel launch on `stream`; no host synchronisation, no allocation.
  * PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for
  * a misaligned pointer, PA_ERR_UNSUPPORTED for a shape or mode outside the limits above,

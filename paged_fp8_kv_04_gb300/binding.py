@@ -502,7 +502,9 @@ def attn_mass(q, k_cache, block_table, context_lens, cu_seqlens_q, lse, mass, *,
               stream=None):
     """Adds a decode step's attention weights to the cached tokens' mass (pa_attn_mass).
 
-    q bf16 [rows, Hq, D], k_cache as pa_decode's, lse fp32 [rows, Hq] of the same pa_decode,
+    q bf16 [rows, Hq, D], k_cache as pa_decode's, lse fp32 [rows, Hq] of the same step's pa_decode
+    over the whole context (a sparse decode's lse covers the selected pages alone, and would give
+    weight to tokens that nobody attended),
     mass fp32 [B, Hkv, stride]; updated in place, or into `out` when given (positions past a
     request's context are not written).  max_q_len bounds every request's rows.  Returns
     the updated tensor."""
@@ -516,7 +518,11 @@ def evict_select(mass, context_lens, *, budget, first=0, recent=0, keep=None, ne
     """The positions that stay when every cache is cut to `budget` tokens (pa_evict_select):
     the first `first`, the last `recent` and the largest mass between.  mass fp32
     [B, Hkv, stride], context_lens int32 [B].  Returns (keep int32 [B, Hkv, budget], ascending,
-    -1 after; new_lens int32 [B])."""
+    -1 after; new_lens int32 [B]).
+
+    A decode on a plan with pdl (the default) reads its context lengths while the kernel before it is
+    still running: between this call and a decode that reads new_lens there has to be another kernel that
+    is not a decode, such as kv_compact or the write of the step's new tokens."""
     return (_module or torch_module()).evict_select(
         mass, context_lens, keep, new_lens, status, _handle(stream), budget, first, recent)
 
@@ -526,7 +532,9 @@ def kv_compact(keep, new_lens, block_table, k_cache, v_cache, *, dst_block_table
     """Moves the kept tokens to the front of their own pages, or of dst_block_table's
     (pa_kv_compact).  keep int32 [B, Hkv, n] and new_lens int32 [B] as evict_select gives
     them; mass fp32 [B, Hkv, stride] moves along, in place or, with dst_block_table, into
-    mass_out.  Afterwards new_lens are the context lengths."""
+    mass_out.  Afterwards new_lens are the context lengths.  The indexer's key cache is not moved:
+    index_topk scores pages by the tokens that were there before until the caller has moved its
+    index keys and scales by the same keep."""
     (_module or torch_module()).kv_compact(
         keep, new_lens, block_table, dst_block_table, k_cache, v_cache, k_scale, v_scale, mass, mass_out, status,
         _handle(stream))
@@ -537,7 +545,7 @@ def beam_select(logits, scores, *, eos=-1, finished=None, lengths=None, length_p
     """One step of beam search (pa_beam_select): the W best continuations of each request's W
     beams.  logits bf16 or fp32 [N, W, V] or [N * W, V] (rows may be strided: a padded
     vocabulary), scores fp32 [N, W] (-inf: no such beam yet), finished uint8 and lengths int32
-    [N, W], both optional.  Returns (tokens, parents, scores, finished, lengths), each [N, W];
+    [N, W], both optional; length_penalty is rounded to fp32.  Returns (tokens, parents, scores, finished, lengths), each [N, W];
     the last two are None where their input is and no output is given."""
     return (_module or torch_module()).beam_select(
         logits, scores, finished, lengths, tokens, parents, scores_out, finished_out, lengths_out, _handle(stream),
@@ -548,7 +556,13 @@ def beam_reorder(parents, context_lens, block_table, block_table_out, k_cache, v
                  v_scale=None, states=(), status=None, stream=None) -> None:
     """Lets the beams' histories follow their parents (pa_beam_reorder).  parents int32 [N, W],
     context_lens int32 [N * W], block tables int32 [N * W, stride]; states: up to four
-    (in, out) pairs of tensors with N * W rows, gathered by parent."""
+    (in, out) pairs of tensors with N * W rows, gathered by parent.
+
+    A decode on a plan with pdl (the default) reads its block table while the kernel before it is still
+    running: between this call and a decode that reads block_table_out there has to be another kernel that is
+    not a decode, such as the write of the step's new tokens.  The indexer's key cache is not copied: a
+    further child's partial page keeps the keys of the childless beam it came from, and index_topk scores it by
+    them until the caller has copied the parent's."""
     (_module or torch_module()).beam_reorder(
         parents, context_lens, block_table, block_table_out, k_cache, v_cache, k_scale, v_scale, states, status,
         _handle(stream))
