@@ -35,8 +35,9 @@ constexpr int kMaxReqs = 65535;
 // cluster's first CTA, one cluster barrier follows, and a warp there joins parts and beams.
 //
 // Bound by HBM while the logits stream, then by the chain of joins.  Measured: 32 requests x 8 beams x
-// 131072 bf16, 67 MB (9.9 us at a copy's rate), 22.0 us: 11 to 13 us of streaming (5.5 TB/s), 2 to tau, 2 to
-// the part's list, 2 for the barrier, 2 in the first CTA, 2 of launch; 1 x 4 x 32001 fp32 8.6 us.  One CTA per
+// 131072 bf16, 67 MB (9.9 us at a copy's rate), 21.9 us: 11 to 13 us of streaming (5.5 TB/s), 2 to tau, 2 to
+// the part's list, 2 for the barrier, 2 in the first CTA, 2 of launch; 1 x 4 x 32001 fp32 8.8 us (0.2 of it the checks whether
+// equal ranks are in order; where one fails the launch takes some 12 us more).  One CTA per
 // request and one pass per candidate took 1644 and 152 us.  Lists sent as asynchronous stores that an mbarrier
 // counts, in place of stores and a cluster barrier, cost 0.5 us more: some hundred 8-byte transactions.
 struct BeamParams {
@@ -107,8 +108,8 @@ __device__ __forceinline__ u64 take32(u64 list, u64 k) {
 
 constexpr int kBeamThreads = 512;
 constexpr int kBeamWarps = kBeamThreads / 32;
-// Vectors cut from two: 1 x 4 x 32001 8.6 us with 3 at a time, 8.9 with 4; 32 x 8 x 131071 fp32 33.3 with 3, 32.3
-// with 4, 36.5 with 2 (30.9 where rows of other alignment were other vectors).
+// Vectors cut from two: 1 x 4 x 32001 8.8 us with 3 at a time, 9.3 with 4; 32 x 8 x 131071 fp32 33.7 with 3, 34.2
+// with 4, 36.8 with 2 (30.9 where rows of other alignment were other vectors).
 constexpr int kCutUnroll = 3;
 constexpr int kUnroll = 4;  // 16-byte loads in flight per thread: 32 KB per CTA, two CTAs per SM
 
@@ -429,7 +430,7 @@ __device__ void beam_part(const BeamParams &p, BeamShared &sm, int64_t row, int 
 
   // ---- tau: the W-th of the best elements of every 16 threads, so at least W elements reach it.  With more
   // beams of every 8: the fewer groups there are to spare, the lower tau lies and the more elements reach it
-  // (1 x 32 x 131072: 32.6 us with 8 against 61.6 with 16; 1 x 4 x 32001: 9.6 against 8.6)
+  // (1 x 32 x 131072: 31.6 us with 8 against 60.3 with 16; 1 x 4 x 32001: 9.8 against 8.8)
   float top;
   const u64 tau = p.W <= 16 ? lower_bound<16>(key, sm, p.W, tid, top) : lower_bound<8>(key, sm, p.W, tid, top);
   // the threads whose best reaches it
@@ -860,7 +861,7 @@ __device__ void copy_row(const uint8_t *src, uint8_t *dst, int64_t n, int64_t i,
 // Row j = blockIdx.y of a request: its table row (CTA x = 0), its share of the copy of the partial
 // page, its share of the states.  Every CTA works the request's parents out by itself, a lane per beam,
 // so that nothing has to be exchanged.  Copies only, bound by latency at the sizes of a step: 32 x 8 beams
-// with 32 KB of mass each (20 MB, 2.9 us at a copy's rate) take 6.6 us, a request of four beams 3.0 us.
+// with 32 KB of mass each (20 MB, 2.9 us at a copy's rate) take 6.2 us, a request of four beams 2.6 us.
 __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const ReorderParams p) {
   pa::pdl_wait();
   const int n = blockIdx.y / p.W, j = blockIdx.y % p.W, tid = threadIdx.x, lane = tid & 31;
@@ -1009,8 +1010,8 @@ extern "C" pa_status_t pa_beam_select(const pa_beam_select_args_t *a, void *stre
   const int sms = beam_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per request: as many as keep one wave (two CTAs per SM) and have a beam or 16 KB of logits each.
-  // 32 x 8 x 131072: 22.0 us with 8, +12.7 with 16, +8 with 4; 1 x 4 x 32001 fp32: 8.6 us with 16, +15 with
-  // 1; 1 x 8 x 1000: 9.0 us with 8, 33.6 with 1; 64 x 4 x 32000: 10.6 with 4, 18.2 with 8.
+  // 32 x 8 x 131072: 21.9 us with 8, 33.4 with 16, 28.7 with 4; 1 x 4 x 32001 fp32: 8.8 us with 16, 24.2 with
+  // 1; 1 x 8 x 1000: 9.3 us with 8, 33.1 with 1; 64 x 4 x 32000: 10.9 with 4, 18.9 with 8.
   const int64_t bytes = (int64_t)a->num_beams * a->vocab * (f32 ? 4 : 2);
   int C = 1;
   while (C < kMaxCluster && (int64_t)a->num_reqs * C <= sms &&

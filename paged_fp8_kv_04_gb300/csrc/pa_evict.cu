@@ -2,11 +2,11 @@
 // pa_kv_compact moves them to the front of their pages.  See include/pa.h for the contract.
 //
 // The selection has little to read (4 B per position) and is bound by its dependent steps:
-// measured on 16 rows x 131072 (8.4 MB, 1.3 us at HBM rate) 17.4 us, of which the masses take 2.5, a
+// measured on 16 rows x 131072 (8.4 MB, 1.3 us at HBM rate) 17.3 us, of which the masses take 2.5, a
 // counting step 3 (counting, two exchanges of 0.5 to 0.7 each, the pick; two or three steps as a rule), counting
-// and writing 3; some SMs have CTAs of two rows (8 rows: 13.8 us).  One CTA per row, bit by bit, took 475 us.
+// and writing 3; some SMs have CTAs of two rows (8 rows: 13.9 us).  One CTA per row, bit by bit, took 475 us.
 // The compaction is bound by HBM: 528 B and more per kept token.  32 x 8192 tokens into other pages, 142 MB,
-// take 27.2 us (5.2 TB/s, 0.77 of a copy's rate); 8 x 4095 in place 6.5 us.  One CTA per row
+// take 26.8 us (5.3 TB/s, 0.78 of a copy's rate); 8 x 4095 in place 6.1 us.  One CTA per row
 // took 203 and 70 us; rows carried in registers 33 and 10 us.
 #include <cuda_runtime.h>
 
@@ -577,8 +577,8 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   const int sms = evict_device();
   if (sms < 1) return sms == 0 ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
   // CTAs per row: more while each keeps 2048 positions and all run at once (two per SM), or
-  // while a row's keys do not fit their registers.  16 rows x 131072: 17.4 us with 8 CTAs per row; 4 rows x
-  // 1000: 4.0 us with one CTA; 1 x 4096 6.5 with two, 1 x 2048 4.4 with one and 6.3 with two.
+  // while a row's keys do not fit their registers.  16 rows x 131072: 17.3 us with 8 CTAs per row; 4 rows x
+  // 1000: 4.0 us with one CTA; 1 x 4096 6.5 with two, 1 x 2048 4.2 with one and 6.3 with two.
   const int64_t rows = (int64_t)a->num_seqs * a->num_kv_heads;
   auto fits = [&](int ctas) { return a->mass_stride <= (int64_t)ctas * kSelThreads * kMaxKeys; };
   int C = 1;
@@ -588,7 +588,7 @@ extern "C" pa_status_t pa_evict_select(const pa_evict_select_args_t *a, void *st
   if (C == kMaxCluster && a->mass_stride / (2 * C) >= 2048 && (rows * 2 * C <= sms || (!fits(C) && fits(2 * C)))) C *= 2;
   // The keys a warp's stretch of the longest row gives each lane.  The loops are unrolled over the keys a
   // lane can have, so fewer is faster for short rows (4 x 1000: +1.9 us with 16, +4.4 with 32), and keeping
-  // them beats reading them again (16 x 131072: 17.4 us with 32, twice that re-read).
+  // them beats reading them again (16 x 131072: 17.3 us with 32, twice that re-read).
   const int64_t warps = (int64_t)C * kSelWarps;
   const int64_t keys = (((int64_t)a->mass_stride + warps - 1) / warps + 31) / 32;
   const pa_host::Launch run(dim3((unsigned)(rows * C)), dim3(kSelThreads), 0, stream, C);
