@@ -715,7 +715,11 @@ __device__ __noinline__ void lowest_tokens(const BeamParams &p, BeamShared &sm, 
     while (from < kBeamWarps && k >= (int)sm.wsum[from]) k -= (int)sm.wsum[from++];
     if (from < kBeamWarps) {
       const int token = (int)sm.buf[from][k];
-      const float y = sizeof(T) == 4 ? __uint_as_float((uint32_t)x[token]) : __uint_as_float((uint32_t)x[token] << 16);
+      float y;
+      if constexpr (sizeof(T) == 4)
+        y = x[token];
+      else
+        y = __uint_as_float((uint32_t)x[token] << 16);
       sm.token[b][higher + lane] = token;
       sm.total[b][higher + lane] = (float)total_of(c, y, lse);
     }

@@ -147,6 +147,31 @@ def test_totals_that_round_together(dt, score, unit, base, W, V, cells):
     _same_as_definition(x, scores, np.full((2, W), 2, np.int32), 1.0)  # quotients by 3 round together what totals do not
 
 
+@pytest.mark.parametrize("dt,cell", [(torch.float32, 2.0 ** -16), (torch.bfloat16, 2.0 ** -15)])
+def test_scores_of_the_lower_tokens_of_equal_rank(dt, cell):
+    """Totals just past the middle of two fp32 numbers: -2^40 - 2^16 + x (fp32) or -2^44 - 2^20 + x (bf16), x some 2^-9 or
+    2^-7 below 0, where fp64 numbers lie 2^-12 or 2^-8 apart and the logits closer.  A score taken without its
+    token's logit rounds to the beam's."""
+    x = torch.full((1, 3, 70), -1e6)
+    x[..., 40] = 65536.0
+    base = 8 * 2.0 ** -12 if dt == torch.float32 else 8 * 2.0 ** -10
+    x[..., 10:17] = -base + cell * torch.arange(-3, 4)         # rising: the highest logit is the highest token's
+    x = x.to(dt).cuda()
+    assert len(x[0, 0, 10:17].unique()) >= (7 if dt == torch.float32 else 3)
+    score = np.full((1, 3), -2.0 ** 40 if dt == torch.float32 else -2.0 ** 44, np.float32)
+    if dt == torch.bfloat16:
+        x[..., 40] = 2.0 ** 20
+    got = B.beam_select(x, dev(score))
+    want = C.beam_select(x.double().cpu().numpy(), score)
+    assert host(got[1]).tolist() == want[1].tolist() == [[0, 1, 2]] and host(got[0]).tolist() == want[0].tolist() == [[40, 40, 40]]
+    score[:, 1:] = -np.inf
+    got = B.beam_select(x, dev(score))
+    want = C.beam_select(x.double().cpu().numpy(), score)
+    assert np.array_equal(host(got[0]), want[0]) and want[0].tolist() == [[40, 10, 11]]
+    assert np.array_equal(host(got[2]), want[2].astype(np.float32))
+    assert host(got[2])[0, 1] < score[0, 0]                       # and not the score itself
+
+
 # --------------------------------------------------------------- the log-sum-exp in totals
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
