@@ -677,7 +677,7 @@ __device__ __noinline__ void lowest_tokens(const BeamParams &p, BeamShared &sm, 
       lo += 31 * step + 1;
     }
   }
-  if (lo == last) return;  // one logit only, whose lowest tokens the list has
+  if (lo == top) return;  // one logit only, whose lowest tokens the list has
   const T *x = static_cast<const T *>(p.logits) + row * p.stride;
   const RowView<T> r(x, p.V);
   const int begin = (int)((int64_t)r.nv * warp / kBeamWarps), end = (int)((int64_t)r.nv * (warp + 1) / kBeamWarps);

@@ -172,6 +172,16 @@ def test_scores_of_the_lower_tokens_of_equal_rank(dt, cell):
     assert host(got[2])[0, 1] < score[0, 0]                       # and not the score itself
 
 
+def test_more_tokens_of_the_lowest_logit_of_a_rank_than_the_list_holds():
+    """-2^40 - 200 - 2^-13 lies in the middle of two fp64 numbers and rounds to -2^40 - 200, which is even: the
+    lowest logit of that rank is -200 - 2^-13, of which the three best by logit hold one token of two."""
+    x = torch.full((1, 3, 40), -1e6)
+    x[..., 30], x[..., 33], x[..., 10], x[..., 20] = 0.0, -200.0, -200.0 - 2.0 ** -13, -200.0 - 2.0 ** -13
+    score = np.array([[-2.0 ** 40, -np.inf, -np.inf]], np.float32)
+    got, want = B.beam_select(x.cuda(), dev(score)), C.beam_select(x.double().numpy(), score)
+    assert host(got[0]).tolist() == want[0].tolist() == [[30, 10, 20]] and (host(got[1]) == 0).all()
+
+
 # --------------------------------------------------------------- the log-sum-exp in totals
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
