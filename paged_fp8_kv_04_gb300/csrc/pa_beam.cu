@@ -27,8 +27,8 @@ constexpr int kMaxReqs = 65535;
 // into parts where there are more CTAs than beams.  Each part is read once: a thread keeps the
 // running maximum and sum of exponentials of its elements, and the vector its maximum came from.
 //   lse = m + log sum exp(x - m),  total = score + (x - lse).
-// Within a row the order of the totals is the order of the logits, so the W best of a part are
-// found without its lse: of the best elements of every 16 (or 8) threads the W-th, tau, bounds them
+// Within a row the order of the totals is the order of the logits but for their rounding, so the W best of a
+// part are found without its lse: of the best elements of every 16 (or 8) threads the W-th, tau, bounds them
 // from below, and elements at or above tau lie with the few threads whose best does.  Only those threads'
 // elements are looked at again (from L2), whatever the values: keys are (value, index) pairs,
 // all different.  Every CTA leaves its list, maximum and sum in the shared memory of the
@@ -275,6 +275,8 @@ __device__ __noinline__ double length_power(int len, float penalty) {
 // Ranks of different lengths this many steps of a double apart (2^-28 of their size or more) are
 // in the right order however the tables' 1e-10 fell.
 constexpr u64 kClearSteps = 1ull << 24;
+// Ranks of one length within this many steps may be equal once divided by the power itself, or be so only by the tables.
+constexpr u64 kSameSteps = 8;
 constexpr double kSmallInverse = 1e-200;  // below this products may underflow
 
 // This shared-memory address in the cluster's first CTA.
@@ -628,9 +630,7 @@ __device__ __forceinline__ int write_choice(const BeamParams &p, const BeamShare
 
 // The order of totals is that of the logits unless their rounding makes one of several logits, as with scores
 // of -1e9 for beams that hardly exist: then the lower token comes first, which may not even be in the list.
-// The first place of beam b's list from which that can be so (32: nowhere), for a warp.  Ranks within
-// kSameSteps steps of a double may be equal once divided by the power itself.
-constexpr u64 kSameSteps = 8;
+// The first place of beam b's list from which that can be so (32: nowhere), for a warp.
 template <typename T>
 __device__ int open_from(const BeamParams &p, const BeamShared &sm, int b, float c) {
   const int lane = threadIdx.x & 31, n = min(p.W, p.V), i = min(lane + 1, 31);
@@ -815,15 +815,20 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __gr
     const int from_len = write_choice(p, sm, x, me, done, len);
     // The chosen are in the order of their computed ranks, so two of different lengths have neighbours of different
     // lengths between them; what is left of a beam comes after its next candidate, which each lane compares with
-    // the last of the chosen.
+    // the last of the chosen.  Two beams of one length are in the order of their totals, unless quotients round together
+    // what the products do not, or the other way round.
     bool unsure = false;
     if (p.penalty != 0.f) {
       const u64 lowest = rank_key(-INFINITY);
-      const int next_len = __shfl_down_sync(~0u, from_len, 1), last_len = __shfl_sync(~0u, from_len, p.W - 1);
+      auto close = [&](int b, int n, u64 r, int b2, int n2, u64 r2) {  // r >= r2
+        return b != b2 && r > lowest && r - r2 <= (n != n2 ? kClearSteps : kSameSteps);
+      };
       const u64 next = __shfl_down_sync(~0u, x.rank, 1), last = __shfl_sync(~0u, x.rank, p.W - 1);
+      const int next_from = __shfl_down_sync(~0u, x.from, 1), last_from = __shfl_sync(~0u, x.from, p.W - 1);
+      const int next_len = __shfl_down_sync(~0u, from_len, 1), last_len = __shfl_sync(~0u, from_len, p.W - 1);
       unsure = mine && (sm.inv[lane] < kSmallInverse ||
-                        (lane + 1 < p.W && next_len != from_len && x.rank > lowest && x.rank - next < kClearSteps) ||
-                        (x.left != 0 && len != last_len && last > lowest && last - x.left < kClearSteps));
+                        (lane + 1 < p.W && close(x.from, from_len, x.rank, next_from, next_len, next)) ||
+                        (x.left != 0 && close(last_from, last_len, last, lane, len, x.left)));
     }
     unsure = __any_sync(~0u, unsure);
     if (lane == 0) sm.unsure = unsure;

@@ -172,6 +172,23 @@ def test_scores_of_the_lower_tokens_of_equal_rank(dt, cell):
     assert host(got[2])[0, 1] < score[0, 0]                       # and not the score itself
 
 
+@pytest.mark.parametrize("penalty", [0.0, 1.0])
+def test_quotients_of_two_beams_that_round_together(penalty):
+    """Second tokens of two beams of one length, with totals up to three fp64 steps (2^-13 at 10^12) apart: where their
+    quotients are one number the lower beam comes first, and else the larger total's."""
+    rng = np.random.default_rng(31)
+    n = 4000
+    x = torch.zeros(n, 3, 2)
+    x[..., 1] = torch.from_numpy(-(200 + 2.0 ** -13 * rng.integers(0, 4, size=(n, 3)))).float()
+    score = np.tile(np.array([-1e12, -1e12, -np.inf], np.float32), (n, 1))
+    lengths = rng.integers(2, 40, size=(n, 1)).repeat(3, 1).astype(np.int32)
+    got = B.beam_select(x.cuda(), dev(score), lengths=dev(lengths), length_penalty=penalty)
+    want = C.beam_select(x.double().numpy(), score, -1, None, lengths, penalty)
+    assert np.array_equal(host(got[0]), want[0]) and np.array_equal(host(got[1]), want[1])
+    equal = x[:, 0, 1] < x[:, 1, 1]                                # the larger total is beam 1's
+    assert (host(got[1])[:, 2][equal.numpy()] == 0).any() == (penalty == 1.0)
+
+
 def test_more_tokens_of_the_lowest_logit_of_a_rank_than_the_list_holds():
     """-2^40 - 200 - 2^-13 lies in the middle of two fp64 numbers and rounds to -2^40 - 200, which is even: the
     lowest logit of that rank is -200 - 2^-13, of which the three best by logit hold one token of two."""
