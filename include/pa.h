@@ -8,7 +8,9 @@
  * variant's pages (pa_index_topk); the log-sum-exp merge that combines the parts of a
  * context split across GPUs (pa_lse_merge); and what happens to the cache between two
  * decode steps: eviction by accumulated attention weight (pa_attn_mass, pa_evict_select,
- * pa_kv_compact) and beam search (pa_beam_select, pa_beam_reorder).  sm_103a (GB300).
+ * pa_kv_compact) and beam search (pa_beam_select, pa_beam_reorder); and a prompt's way into the
+ * cache: pages and slots for its tokens (pa_page_assign, pa_page_release), rotary positions (pa_rope)
+ * and causal attention over whole packed prompts (pa_prompt_attn).  sm_103a (GB300).
  *
  * Sources of the operation (the pages are pull-request threads):
  *  - ROCm/ATOM PR 2614, "Change": dense max-q-len-1 per-token FP8 decode and sparse
@@ -596,6 +598,150 @@ typedef struct pa_beam_reorder_args {
  * PA_ERR_CAPACITY when num_pages * num_kv_heads * page_size passes 2^31 - 1, PA_ERR_CUDA when the
  * launch fails. */
 pa_status_t pa_beam_reorder(const pa_beam_reorder_args_t *args, void *stream);
+
+/* ---- a prompt's way into the cache: pages and slots, rotary positions, attention ---- */
+
+#define PA_DEV_PAGE_POOL 0x1000u /* pa_page_assign: a request needed more pages than were left; pa_page_release: the
+                                    stack has no room for a request's pages */
+
+/* Arguments of pa_page_assign.  All pointers are device pointers. */
+typedef struct pa_page_assign_args {
+  const int32_t *context_lens;   /* [num_seqs]: tokens in each request's cache before the step */
+  const int32_t *cu_seqlens_q;   /* [num_seqs + 1]: the new tokens of request r are rows [cu[r], cu[r+1]) */
+  int32_t *block_table;          /* [num_seqs, block_table_stride]: the new pages are entered */
+  const int32_t *free_pages;     /* [free_capacity]: a stack of free pages, its top at num_free - 1 */
+  const int32_t *num_free;       /* [1] */
+  int32_t *num_free_out;         /* [1]; may be num_free */
+  int32_t *new_lens;             /* out: [num_seqs] context lengths with the new tokens; may be context_lens */
+  int64_t *slot_mapping;         /* out: [num_rows] slot of every row, -1 where it has none (pa_kv_quantize_write's) */
+  int32_t *positions;            /* nullable out: [num_rows] position of every row in its request (pa_rope's) */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT, PA_DEV_BAD_QLEN, PA_DEV_BAD_PAGE, PA_DEV_PAGE_POOL */
+  int64_t num_pages;             /* 1 .. 2^31 - 1: pages of the cache */
+  int32_t num_seqs;              /* >= 0 */
+  int32_t num_rows;              /* >= 0: rows of the step, padding behind the last request's among them */
+  int32_t block_table_stride;
+  int32_t page_size;             /* 16, 32, 64 or 128 */
+  int32_t free_capacity;         /* >= 1 */
+  int32_t reserved;              /* 0 */
+} pa_page_assign_args_t;
+
+/* Gives requests that grow their pages, and their new tokens slots and positions.  With L = context_lens[r] and
+ * q = cu[r+1] - cu[r], request r needs ceil((L + q) / page_size) - ceil(L / page_size) pages.  In the order of the
+ * requests each takes its pages off the top of the stack, lower positions first, as long as the pool lasts: from
+ * the first request on that needs more than is left, those that need a page are not served (PA_DEV_PAGE_POOL), and
+ * those that need none still are.  A served request's row of position p gets the slot
+ * block_table[r][p / page_size] * page_size + p % page_size, and new_lens[r] = L + q; one that is not served gets no
+ * page, slots of -1 and new_lens[r] = L.  positions are L + row - cu[r] for both.  Rows of no request (before cu[0], behind
+ * cu[num_seqs]) get slot -1 and position 0.  Entries of the block table other than the new pages', and the
+ * stack, are left as they are; num_free_out is what is left.  So the table's partial pages must be the request's own, as they are
+ * after pa_beam_reorder.  A request with a negative context or one whose tokens pass the table or 2^31 - 1 is not served
+ * (PA_DEV_BAD_CONTEXT).  If cu does not ascend from 0 or more to num_rows or fewer, no request is served and every position
+ * is 0 (PA_DEV_BAD_QLEN).  num_free is taken as within 0 .. free_capacity.  A page outside [0, num_pages), off the stack or in
+ * the table, gives its rows slot -1 (PA_DEV_BAD_PAGE); off the stack it is entered as it stands, and the decode flags it again.
+ * Outputs share no byte with each other or with an input, but for the two pairs above at the same address.
+ * One kernel launch on `stream`, none where there is nothing to write (no requests, no rows, num_free_out at num_free; pointers to
+ * nothing may be NULL); no host synchronisation, no allocation.  A pa_decode on a plan without PA_PLAN_NO_PDL
+ * reads new_lens and block_table before the kernel enqueued just before it has completed: another kernel that is no decode
+ * has to lie between (pa_rope and pa_kv_quantize_write do).  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap,
+ * PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for another page size, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_page_assign(const pa_page_assign_args_t *args, void *stream);
+
+/* Arguments of pa_page_release.  All pointers are device pointers. */
+typedef struct pa_page_release_args {
+  const int32_t *context_lens;   /* [num_seqs]: tokens that the request's pages were taken for */
+  const int32_t *new_lens;       /* [num_seqs]: tokens that stay; 0 for a request that has ended */
+  const int32_t *block_table;    /* [num_seqs, block_table_stride] */
+  int32_t *free_pages;           /* [free_capacity]: the stack, its top at num_free - 1 */
+  const int32_t *num_free;       /* [1] */
+  int32_t *num_free_out;         /* [1]; may be num_free */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT, PA_DEV_BAD_PAGE, PA_DEV_PAGE_POOL */
+  int64_t num_pages;             /* 1 .. 2^31 - 1 */
+  int32_t num_seqs;              /* >= 0 */
+  int32_t block_table_stride;
+  int32_t page_size;             /* 16, 32, 64 or 128 */
+  int32_t free_capacity;         /* >= 1 */
+  int32_t reserved;              /* 0 */
+} pa_page_release_args_t;
+
+/* Takes pages back: entries [ceil(new_lens[r] / page_size), ceil(context_lens[r] / page_size)) of row r of the block
+ * table go on top of the stack, request by request, lower positions first.  A request that does not shrink gives none.  The
+ * table is left as it is (what lies behind a context length is not read).  Pages that another request reads as well (a
+ * common prefix, beams) must not be given back: who counts references is the caller.  From the first request on whose pages
+ * pass free_capacity, those that have pages to give back keep them (PA_DEV_PAGE_POOL: such a pool has been given a page twice).  A request with a
+ * negative length or a context beyond the table gives none back (PA_DEV_BAD_CONTEXT).  A page outside [0, num_pages) goes on
+ * the stack as it stands and is flagged (PA_DEV_BAD_PAGE).  num_free is taken as within 0 .. free_capacity.  Outputs share no byte with each
+ * other or with an input, but for num_free_out at num_free.  One kernel launch on `stream`, none without requests and with
+ * num_free_out at num_free; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer,
+ * PA_ERR_UNSUPPORTED for another page size, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_page_release(const pa_page_release_args_t *args, void *stream);
+
+enum { PA_ROPE_BF16 = 0, PA_ROPE_F32 = 1 };
+enum { PA_ROPE_HALF = 0, PA_ROPE_PAIRS = 1 };
+
+/* Arguments of pa_rope.  All pointers are device pointers; strides are elements between tokens, and a token's heads lie
+ * one behind the other, so that views of one projection's output can be given. */
+typedef struct pa_rope_args {
+  const void *q;                 /* [num_tokens, num_q_heads, head_dim], aligned to its element */
+  const void *k;                 /* [num_tokens, num_kv_heads, head_dim]; NULL with num_kv_heads 0 */
+  const int32_t *positions;      /* [num_tokens], of either sign */
+  const int64_t *freqs;          /* [rot_dim / 2]: turns per position of each pair, times 2^64, modulo 2^64 */
+  void *q_out;                   /* as q; may be q with q's stride */
+  void *k_out;                   /* as k; may be k with k's stride */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  /* >= heads * head_dim */
+  int32_t num_tokens;            /* >= 0; 0 enqueues nothing */
+  int32_t num_q_heads;           /* >= 1 */
+  int32_t num_kv_heads;          /* >= 0 */
+  int32_t head_dim;              /* 128 */
+  int32_t rot_dim;               /* even, 2 .. 128: the head's first rot_dim elements turn, the others are carried over */
+  int32_t dtype;                 /* PA_ROPE_* */
+  int32_t layout;                /* PA_ROPE_HALF: pair i is elements (i, i + rot_dim / 2); PA_ROPE_PAIRS: (2i, 2i + 1) */
+  int32_t inverse;               /* 1 turns back: the gradient of the rotation, or a key that is to be moved; else 0 */
+  float scale;                   /* finite; what the turned elements are multiplied by (1, or that of a stretched context) */
+  int32_t reserved;              /* 0 */
+} pa_rope_args_t;
+
+/* Rotary positions: pair i = (a, b) of every head of a token at position p becomes
+ *   (a cos t - b sin t, b cos t + a sin t) * scale,   t = 2 pi p freqs[i] / 2^64   (-t with inverse),
+ * in fp32, rounded once to the type.  The angle is reduced in 64-bit integers: p * freqs[i] modulo 2^64 is the fraction of
+ * a turn, exactly, however far the position, so far positions are as exact as near ones.  One kernel launch on `stream`; no host
+ * synchronisation, no allocation.  Outputs share no byte with each other or another input (rows of one buffer interleave only
+ * with equal strides).  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for
+ * head_dim other than 128, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_rope(const pa_rope_args_t *args, void *stream);
+
+/* Arguments of pa_prompt_attn.  All pointers are device pointers; strides are elements between tokens, and a token's heads
+ * lie one behind the other, so that views of one projection's output can be given. */
+typedef struct pa_prompt_attn_args {
+  const void *q;                 /* bf16 [num_rows, num_kv_heads * group_size, head_dim], 16-B aligned */
+  const void *k;                 /* bf16 [num_rows, num_kv_heads, head_dim], 16-B aligned */
+  const void *v;                 /* as k */
+  const int32_t *cu_seqlens;     /* [num_seqs + 1]: sequence s is rows [cu[s], cu[s+1]) */
+  void *out;                     /* [num_rows, num_kv_heads * group_size, head_dim], bf16 or fp32 per out_dtype, dense, 16-B aligned */
+  float *lse;                    /* nullable: fp32 [num_rows, num_kv_heads * group_size], natural log */
+  uint32_t *status;              /* nullable: PA_DEV_BAD_QLEN, PA_DEV_TIMEOUT are OR-ed in */
+  int64_t q_stride, k_stride, v_stride;  /* multiples of 8, >= heads * head_dim */
+  int32_t num_seqs;              /* 0 .. 4096; 0 enqueues nothing */
+  int32_t num_rows;              /* 0 .. 2^24; 0 enqueues nothing */
+  int32_t num_kv_heads;          /* 1 .. 64 */
+  int32_t group_size;            /* 1 .. 64 */
+  int32_t head_dim;              /* 128 */
+  int32_t out_dtype;             /* PA_OUT_BF16 or PA_OUT_F32 */
+  float sm_scale;                /* > 0 */
+  int32_t reserved;              /* 0 */
+} pa_prompt_attn_args_t;
+
+/* Causal attention over whole prompts, packed one behind the other: row t of sequence s (its t-th token) and query head j
+ * of KV head h = j / group_size attend the sequence's tokens 0 .. t,
+ *   out[t][j] = sum_i softmax_i(sm_scale * q[t][j] . k[i][h]) v[i][h],   lse[t][j] = log sum_i exp(sm_scale * q[t][j] . k[i][h]).
+ * Scores, maxima, sums and accumulators are fp32; the softmax weights are rounded to bf16 for the second product (their sum is
+ * taken before), so an fp32 output is good to 2^-9 of its terms and serves pa_lse_merge, which joins it with the part of a context
+ * that is already cached (a decode over the cached pages with an fp32 output and lse).  What a row does not attend has no effect on it,
+ * infinities and NaN included: later tokens, other sequences, rows of no sequence; rows of no sequence are left as they are.
+ * A sequence whose cu does not lie in order within 0 .. num_rows is left out (PA_DEV_BAD_QLEN).  One kernel launch on
+ * `stream`; no host synchronisation, no allocation.  out and lse share no byte with each other or an input.  PA_ERR_INVALID_ARG
+ * for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer or stride, PA_ERR_UNSUPPORTED for a shape outside the limits
+ * above, PA_ERR_CUDA when the launch fails. */
+pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *args, void *stream);
 
 /* ---- test hooks: exact integer / byte outputs of the row map and the page gather ---- */
 

@@ -81,6 +81,9 @@ DEV_BAD_SLOT = 0x100
 DEV_BAD_INDEX_ROW = 0x200
 DEV_BAD_KEEP = 0x400
 DEV_BAD_BEAM = 0x800
+DEV_PAGE_POOL = 0x1000
+ROPE_BF16, ROPE_F32 = 0, 1
+ROPE_HALF, ROPE_PAIRS = 0, 1
 LOGITS_BF16, LOGITS_F32 = 0, 1
 MAX_BEAM_STATES = 4
 
@@ -141,6 +144,20 @@ class BeamReorderArgs(ctypes.Structure):
             "scale_mode", "block_table_stride", "reserved")]
 
 
+PageAssignArgs = _struct(
+    "PageAssignArgs", "context_lens cu_seqlens_q block_table free_pages num_free num_free_out new_lens slot_mapping positions "
+    "status", "num_pages", "num_seqs num_rows block_table_stride page_size free_capacity")
+PageReleaseArgs = _struct(
+    "PageReleaseArgs", "context_lens new_lens block_table free_pages num_free num_free_out status", "num_pages",
+    "num_seqs block_table_stride page_size free_capacity")
+RopeArgs = _struct(
+    "RopeArgs", "q k positions freqs q_out k_out", "q_stride k_stride q_out_stride k_out_stride",
+    "num_tokens num_q_heads num_kv_heads head_dim rot_dim dtype layout inverse", "scale")
+PromptAttnArgs = _struct(
+    "PromptAttnArgs", "q k v cu_seqlens out lse status", "q_stride k_stride v_stride",
+    "num_seqs num_rows num_kv_heads group_size head_dim out_dtype", "sm_scale")
+
+
 _lib = None
 P = ctypes.c_void_p
 
@@ -196,7 +213,8 @@ def lib(path: Optional[str] = None):
     L.pa_lse_merge.restype = ctypes.c_int
     for name, args in (("pa_attn_mass", AttnMassArgs), ("pa_evict_select", EvictSelectArgs),
                        ("pa_kv_compact", KvCompactArgs), ("pa_beam_select", BeamSelectArgs),
-                       ("pa_beam_reorder", BeamReorderArgs)):
+                       ("pa_beam_reorder", BeamReorderArgs), ("pa_page_assign", PageAssignArgs),
+                       ("pa_page_release", PageReleaseArgs), ("pa_rope", RopeArgs), ("pa_prompt_attn", PromptAttnArgs)):
         f = getattr(L, name)
         f.argtypes = [ctypes.POINTER(args), P]
         f.restype = ctypes.c_int
@@ -488,7 +506,8 @@ def torch_module():
         loader.exec_module(m)
         L = lib()
         m.bind(PaError, *(ctypes.cast(f, P).value for f in (
-            L.pa_attn_mass, L.pa_evict_select, L.pa_kv_compact, L.pa_beam_select, L.pa_beam_reorder)))
+            L.pa_attn_mass, L.pa_evict_select, L.pa_kv_compact, L.pa_beam_select, L.pa_beam_reorder, L.pa_page_assign,
+            L.pa_page_release, L.pa_rope, L.pa_prompt_attn)))
         _module = m
     return _module
 
@@ -566,3 +585,100 @@ def beam_reorder(parents, context_lens, block_table, block_table_out, k_cache, v
     (_module or torch_module()).beam_reorder(
         parents, context_lens, block_table, block_table_out, k_cache, v_cache, k_scale, v_scale, states, status,
         _handle(stream))
+
+
+# ----------------------------------------------------- a prompt's way into the cache
+
+def page_assign(context_lens, cu_seqlens_q, block_table, free_pages, num_free, *, page_size, num_pages, num_rows=None,
+                num_free_out=None, new_lens=None, slot_mapping=None, positions=None, status=None, stream=None):
+    """Gives requests that grow their pages, and their new tokens slots and positions (pa_page_assign).
+
+    context_lens int32 [B], cu_seqlens_q int32 [B + 1], block_table int32 [B, stride] (updated in place), free_pages
+    int32 [capacity] a stack of which num_free (int32 [1]) pages are left, updated in place or into num_free_out.
+    num_rows rows in all, padding behind the last request's among them, unless slot_mapping is given.  Returns
+    (new_lens int32 [B], slot_mapping int64 [rows] as kv_quantize_write takes it, positions int32 [rows] as rope
+    does); new_lens may be context_lens.  A request that the pool has no pages for keeps its length and
+    gets slots of -1 (DEV_PAGE_POOL in status).
+
+    A decode on a plan with pdl (the default) reads its context lengths and block table while the kernel before it is still
+    running: between this call and that decode there has to be another kernel that is not a decode, such as rope
+    or the write of the step's new tokens."""
+    return (_module or torch_module()).page_assign(
+        context_lens, cu_seqlens_q, block_table, free_pages, num_free, num_free_out, new_lens, slot_mapping, positions, status,
+        _handle(stream), page_size, num_pages, num_rows)
+
+
+def page_release(context_lens, new_lens, block_table, free_pages, num_free, *, page_size, num_pages, num_free_out=None,
+                 status=None, stream=None) -> None:
+    """Takes back the pages behind the requests' new lengths (pa_page_release): 0 for a request that has ended, evict_select's
+    for one that was cut.  They go on top of free_pages; num_free int32 [1] is updated in place or into
+    num_free_out.  The block table is left as it is.  Pages that another request reads too (a common prefix, beams) must not
+    be given back by this call: who counts references is the caller."""
+    (_module or torch_module()).page_release(
+        context_lens, new_lens, block_table, free_pages, num_free, num_free_out, status, _handle(stream), page_size, num_pages)
+
+
+def rope_frequencies(rot_dim, *, base=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0,
+                     device="cuda"):
+    """The frequencies that rope takes, and the scale that belongs to them: (int64 [rot_dim / 2], float).
+
+    Pair i turns by base ** (-2 i / rot_dim) radians per position.  For contexts `factor` times as long as the
+    original_len that a model was trained on, scaling is "linear" (all pairs slower by factor), "ntk" (a larger base, so that the
+    slowest pair is slower by factor) or "yarn" (pairs that turn more than beta_fast times within original_len stay, those
+    that turn less than beta_slow times are slower by factor, a ramp between; queries and keys scaled by
+    0.1 ln(factor) + 1 each).  Kept in units of 2^-64 turns, modulo one: a program makes them once."""
+    import math
+
+    import torch
+    if rot_dim < 2 or rot_dim % 2 or rot_dim > 128:
+        raise ValueError(f"rot_dim: {rot_dim}, expected an even number of 2 .. 128")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling: {scaling!r}, expected None, 'linear', 'ntk' or 'yarn'")
+    if not (base > 1.0 and math.isfinite(base)) or (scaling is not None and not (factor >= 1.0 and math.isfinite(factor))):
+        raise ValueError(f"base {base} and factor {factor}: expected finite, above 1 and at least 1")
+    half, scale = rot_dim // 2, 1.0
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2.0))
+    elif scaling == "ntk":
+        base = base * factor
+    w = [base ** (-2.0 * i / rot_dim) for i in range(half)]
+    if scaling == "linear":
+        w = [x / factor for x in w]
+    elif scaling == "yarn":
+        if not (original_len > 0 and beta_fast > beta_slow > 0):
+            raise ValueError("original_len, beta_fast and beta_slow: expected beta_fast > beta_slow > 0")
+        # the pair that turns so many times within original_len
+        pair = lambda turns: rot_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rot_dim - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(half)]
+        w = [x / factor * r + x * (1.0 - r) for x, r in zip(w, ramp)]
+        scale = 0.1 * math.log(factor) + 1.0
+    turns = [round(x / (2.0 * math.pi) * 2.0 ** 64) % 2 ** 64 for x in w]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device), scale
+
+
+def rope(q, k, positions, freqs, *, layout="half", inverse=False, scale=1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions (pa_rope).  q bf16 or fp32 [T, Hq, 128] and k [T, Hkv, 128] (or None), views of one projection's output
+    among them; positions int32 [T]; freqs and scale from rope_frequencies.  Pair i is elements (i, i + rot / 2) with layout
+    "half", (2 i, 2 i + 1) with "pairs"; elements past rot are carried over.  inverse turns back, which is also the
+    rotation's gradient.  In place, or into q_out and k_out; returns (q_out, k_out)."""
+    kinds = {"half": ROPE_HALF, "pairs": ROPE_PAIRS}
+    if layout not in kinds:
+        raise ValueError(f"layout: {layout!r}, expected 'half' or 'pairs'")
+    return (_module or torch_module()).rope(
+        q, k, positions, freqs, q_out, k_out, _handle(stream), kinds[layout], 1 if inverse else 0, scale)
+
+
+def prompt_attn(q, k, v, cu_seqlens, *, sm_scale=None, out=None, lse=None, out_dtype="bf16", want_lse=False, status=None,
+                stream=None):
+    """Causal attention over whole prompts packed one behind the other (pa_prompt_attn).
+
+    q bf16 [T, Hq, 128], k and v bf16 [T, Hkv, 128], views of one projection's output among them; cu_seqlens int32 [S + 1].
+    Returns (out [T, Hq, 128], bf16 or, with out_dtype "f32" or a given fp32 `out`, fp32; lse fp32 [T, Hq], or None unless
+    it is given or wanted).  Rows of no sequence are not written.  With an fp32 output and an lse the result joins, by
+    lse_merge, with that of a decode over what is already cached of the same requests."""
+    if out_dtype not in ("bf16", "f32"):
+        raise ValueError(f"out_dtype: {out_dtype!r}, expected 'bf16' or 'f32'")
+    return (_module or torch_module()).prompt_attn(
+        q, k, v, cu_seqlens, out, lse, status, _handle(stream), sm_scale, OUT_F32 if out_dtype == "f32" else OUT_BF16,
+        1 if want_lse else 0)

@@ -85,4 +85,28 @@ inline bool overlaps(const Span &out, std::initializer_list<Span> others) {
   return false;
 }
 
+// `count` rows of `bytes` bytes, `stride` bytes apart (at least `bytes`).
+struct Rows {
+  const void *p;
+  int64_t count, bytes, stride;
+};
+// Whether two such tensors share a byte.  Rows of the same stride may interleave, as views of one buffer do; with
+// different strides the whole extents are compared.
+inline bool rows_overlap(const Rows &a, const Rows &b) {
+  if (a.p == nullptr || b.p == nullptr || a.count < 1 || b.count < 1 || a.bytes < 1 || b.bytes < 1) return false;
+  const uint64_t na = (uint64_t)((a.count - 1) * a.stride + a.bytes), nb = (uint64_t)((b.count - 1) * b.stride + b.bytes);
+  if (!overlap(a.p, na, b.p, nb)) return false;
+  if (a.stride != b.stride) return true;
+  // row i of a and row i + k of b lie delta + k stride apart: the shifts that bring them next to each other, as far
+  // as there are such rows
+  const int64_t delta = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  const int64_t s = a.stride, near = -delta / s;
+  for (int64_t k = near - 1; k <= near + 1; ++k) {
+    if (k > b.count - 1 || k < -(a.count - 1)) continue;
+    const int64_t at = delta + k * s;
+    if (at < a.bytes && -at < b.bytes) return true;
+  }
+  return false;
+}
+
 }  // namespace pa_host

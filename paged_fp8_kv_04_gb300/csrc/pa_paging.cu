@@ -1,0 +1,392 @@
+// pa_paging.cu -- pages of the cache for requests that grow and back from those that shrink:
+// pa_page_assign and pa_page_release.  See include/pa.h for the contract.
+//
+// Both are a prefix sum over the requests' pages followed by work per row (a slot, a position and, where the
+// row opens a page, a table entry) or per page.  Each runs as one cluster: every CTA scans all the
+// requests by itself, which costs less than an exchange, and takes its share of the rows.  A single cluster, since
+// the lengths and the count of free pages may be updated in place: every CTA has read them once the
+// cluster's barrier is through, and only then are they written.  More clusters would need a counter in
+// memory, which the caller would have to keep.
+//
+// Bound by latency: 12 bytes per row, and a chain of lengths -> scan -> page -> slot.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "pa.h"
+#include "pa_host.cuh"
+#include "pa_ptx.cuh"
+
+namespace {
+
+using pa_host::aligned;
+
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxCluster = 16;
+
+struct AssignParams {
+  const int32_t *L, *cu, *free_pages, *num_free;
+  int32_t *bt, *num_free_out, *new_lens, *pos;
+  int64_t *slots;
+  uint32_t *status;
+  int32_t num_pages, B, rows, bt_stride, shift, capacity;
+};
+
+struct ReleaseParams {
+  const int32_t *L, *new_lens, *bt, *num_free;
+  int32_t *free_pages, *num_free_out;
+  uint32_t *status;
+  int32_t num_pages, B, bt_stride, shift, capacity;
+};
+
+__device__ __forceinline__ void raise(uint32_t *status, uint32_t flags) {
+  if (flags != 0 && status != nullptr) atomicOr(status, flags);
+}
+
+__device__ __forceinline__ int64_t pages_of(int64_t tokens, int shift) { return (tokens + (1 << shift) - 1) >> shift; }
+
+// Inclusive sum over the CTA's threads (a multiple of 32 of them); `all` becomes the total.
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t *sums, int64_t &all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the sums of the chunk before have been read
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int64_t before = 0;
+  all = 0;
+  for (int w = 0; w < warps; ++w) {
+    const int64_t v = sums[w];
+    before += w < warp ? v : 0;
+    all += v;
+  }
+  return x + before;
+}
+
+// The last of at[0 .. n] that is not above x (ascending), or -1.
+__device__ __forceinline__ int find(const int32_t *at, int n, int x) {
+  int lo = -1, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// R rows per thread and step, 32 apart: R independent chains in flight.
+template <int R>
+__global__ void __launch_bounds__(kMaxThreads) page_assign_kernel(const __grid_constant__ AssignParams p) {
+  __shared__ int64_t sums[kMaxThreads / 32];
+  __shared__ int32_t cu_s[kMaxThreads + 1], len_s[kMaxThreads], have_s[kMaxThreads], base_s[kMaxThreads];
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+  const int ranks = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
+  pa::pdl_wait();
+  pa::pdl_launch_dependents();
+  const int stack = min(max(*p.num_free, 0), p.capacity);
+  uint32_t flags = 0;
+  // Ascending within 0 .. rows, or nobody is served: then every row has one owner at most.
+  bool bad = false;
+  for (int r = tid; r < p.B; r += threads) {
+    const int a = p.cu[r], b = p.cu[r + 1];
+    bad |= a < 0 || b < a || b > p.rows;
+  }
+  const bool ascends = __syncthreads_or(bad) == 0;
+  if (!ascends) flags |= PA_DEV_BAD_QLEN;
+
+  int64_t run = 0;  // pages that the requests so far have asked for
+  int taken = 0;    // and what was taken
+  int r0 = 0;
+  do {
+    const int n = min(threads, p.B - r0), r = r0 + tid;
+    int L = 0, have = 0;
+    int64_t need = 0;
+    bool good = false;
+    if (tid < n) {
+      const int a = p.cu[r], b = p.cu[r + 1];
+      L = p.L[r];
+      if (ascends) {
+        const int64_t end = (int64_t)L + (b - a);
+        good = L >= 0 && end <= INT_MAX && pages_of(end, p.shift) <= p.bt_stride;
+        if (!good) flags |= PA_DEV_BAD_CONTEXT;
+        if (good) {
+          have = (int)pages_of(L, p.shift);
+          need = pages_of(end, p.shift) - have;
+        }
+      }
+      cu_s[tid] = a;
+      if (tid == n - 1) cu_s[n] = b;
+      len_s[tid] = L;
+      have_s[tid] = have;
+    }
+    int64_t all;
+    const int64_t upto = run + scan(need, sums, all);  // synchronises the CTA
+    const bool served = good && (need == 0 || upto <= stack);
+    if (good && !served) flags |= PA_DEV_PAGE_POOL;
+    if (tid < n) base_s[tid] = served ? (need == 0 ? 0 : (int)(upto - need)) : -1;
+    pa::cluster_arrive();  // this chunk's lengths have been read
+    // what was taken: the last of those served (they are the first of those that asked)
+    taken = max(taken, __reduce_max_sync(~0u, served && need > 0 ? (int)upto : 0));
+    run += all;
+    __syncthreads();
+
+    const bool last = r0 + threads >= p.B;
+    const int lo = r0 == 0 || !ascends ? 0 : cu_s[0], hi = last || !ascends ? p.rows : cu_s[n];
+    const int strip = 32 * R, warps = ranks * (threads >> 5);
+    // (64 bits: the last strip may pass 2^31)
+    for (int64_t s = lo + (int64_t)strip * (rank * (threads >> 5) + (tid >> 5)); s < hi && (ascends || r0 == 0);
+         s += (int64_t)strip * warps) {
+      int j[R], id[R], at[R];
+      bool opens[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int64_t row = s + 32 * k + lane;
+        j[k] = -1;
+        id[k] = -1;
+        at[k] = 0;
+        opens[k] = false;
+        if (row < hi && ascends && p.B > 0) {
+          j[k] = find(cu_s, n, (int)row);
+          if (j[k] >= n) j[k] = -1;
+        }
+        if (j[k] >= 0) {
+          at[k] = (int)((uint32_t)len_s[j[k]] + (uint32_t)((int)row - cu_s[j[k]]));
+          const int base = base_s[j[k]];
+          if (base >= 0) {
+            const int col = at[k] >> p.shift, more = col - have_s[j[k]];
+            opens[k] = more >= 0 && (at[k] & ((1 << p.shift) - 1)) == 0;
+            id[k] = more >= 0 ? p.free_pages[stack - 1 - (base + more)] : p.bt[(int64_t)(r0 + j[k]) * p.bt_stride + col];
+          } else {
+            j[k] = -1;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int64_t row = s + 32 * k + lane;
+        if (row >= hi) continue;
+        if (opens[k]) p.bt[(int64_t)(r0 + j[k]) * p.bt_stride + (at[k] >> p.shift)] = id[k];
+        const bool page = id[k] >= 0 && id[k] < p.num_pages;
+        if (j[k] >= 0 && !page) flags |= PA_DEV_BAD_PAGE;
+        p.slots[row] = !page ? -1 : ((int64_t)id[k] << p.shift) + (at[k] & ((1 << p.shift) - 1));
+        if (p.pos != nullptr) p.pos[row] = at[k];
+      }
+    }
+    pa::cluster_wait();  // every CTA has read this chunk's lengths (and the count of free pages)
+    if (rank == 0 && tid < n) p.new_lens[r] = served ? L + (cu_s[tid + 1] - cu_s[tid]) : L;
+    __syncthreads();  // the chunk's arrays have been read
+    r0 += threads;
+  } while (r0 < p.B);
+
+  if (rank == 0) {
+    __shared__ int32_t most;
+    if (tid == 0) most = 0;
+    __syncthreads();
+    if (lane == 0 && taken > 0) atomicMax(&most, taken);
+    __syncthreads();
+    if (tid == 0) *p.num_free_out = stack - most;
+  }
+  flags = __reduce_or_sync(~0u, flags);
+  if (lane == 0) raise(p.status, flags);
+}
+
+template <int R>
+__global__ void __launch_bounds__(kMaxThreads) page_release_kernel(const __grid_constant__ ReleaseParams p) {
+  __shared__ int64_t sums[kMaxThreads / 32];
+  __shared__ int32_t from_s[kMaxThreads + 1], col_s[kMaxThreads];
+  __shared__ int32_t most;
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
+  const int ranks = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
+  pa::pdl_wait();
+  pa::pdl_launch_dependents();
+  const int stack = min(max(*p.num_free, 0), p.capacity), room = p.capacity - stack;
+  pa::cluster_arrive();
+  uint32_t flags = 0;
+  int64_t run = 0;  // pages of the requests so far
+  int given = 0;
+  for (int r0 = 0; r0 < p.B; r0 += threads) {
+    const int n = min(threads, p.B - r0), r = r0 + tid;
+    int64_t back = 0;
+    int col = 0;
+    if (tid < n) {
+      const int L = p.L[r], m = p.new_lens[r];
+      if (L < 0 || m < 0 || pages_of(L, p.shift) > p.bt_stride) {
+        flags |= PA_DEV_BAD_CONTEXT;
+      } else if (m < L) {
+        col = (int)pages_of(m, p.shift);
+        back = pages_of(L, p.shift) - col;
+      }
+    }
+    int64_t all;
+    const int64_t upto = run + scan(back, sums, all);
+    const bool fits = upto <= room;
+    if (!fits && back > 0) flags |= PA_DEV_PAGE_POOL;
+    // the page, of all that are given back, with which the request's begin; past the end of those that fit: none
+    if (tid == 0) most = given;
+    __syncthreads();
+    const int mine = __reduce_max_sync(~0u, fits ? (int)upto : 0);
+    if (lane == 0) atomicMax(&most, mine);
+    if (tid < n) {
+      from_s[tid] = (int)min(upto - back, (int64_t)INT_MAX);
+      col_s[tid] = col;
+    }
+    __syncthreads();
+    const int end = most;
+    const int strip = 32 * R, warps = ranks * (threads >> 5);
+    for (int64_t s = given + (int64_t)strip * (rank * (threads >> 5) + (tid >> 5)); s < end; s += (int64_t)strip * warps) {
+      int id[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int64_t f = s + 32 * k + lane;
+        if (f < end) {
+          const int j = find(from_s, n - 1, (int)f);
+          id[k] = p.bt[(int64_t)(r0 + j) * p.bt_stride + col_s[j] + ((int)f - from_s[j])];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int64_t f = s + 32 * k + lane;
+        if (f >= end) continue;
+        if (id[k] < 0 || id[k] >= p.num_pages) flags |= PA_DEV_BAD_PAGE;
+        p.free_pages[stack + f] = id[k];
+      }
+    }
+    given = end;
+    run += all;
+    __syncthreads();  // the chunk's arrays have been read
+  }
+  pa::cluster_wait();  // every CTA has read the count of free pages
+  if (rank == 0 && tid == 0) *p.num_free_out = stack + given;
+  flags = __reduce_or_sync(~0u, flags);
+  if (lane == 0) raise(p.status, flags);
+}
+
+// The kernels' opt-in to clusters of 16, once per device.
+bool paging_device() {
+  static int8_t known[pa_host::kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= pa_host::kMaxDevices) return false;
+  if (known[dev]) return true;
+  for (const void *f : {(const void *)page_assign_kernel<1>, (const void *)page_assign_kernel<4>,
+                        (const void *)page_release_kernel<1>, (const void *)page_release_kernel<4>})
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+  known[dev] = 1;
+  return true;
+}
+
+// Threads per CTA, CTAs per cluster and items per thread for `items` rows or pages of `seqs` requests.
+struct Shape {
+  int threads, ctas, each;
+};
+Shape shape_of(int64_t items, int64_t seqs) {
+  Shape s{kMaxThreads, 1, 1};
+  const int64_t most = items > seqs ? items : seqs;
+  if (most <= 512) {
+    s.threads = most <= 128 ? 128 : 512;
+    return s;
+  }
+  while (s.ctas < kMaxCluster && (int64_t)s.ctas * kMaxThreads < items) s.ctas *= 2;
+  if (items > (int64_t)s.ctas * kMaxThreads) s.each = 4;
+  return s;
+}
+
+}  // namespace
+
+extern "C" pa_status_t pa_page_assign(const pa_page_assign_args_t *a, void *stream) {
+  if (a == nullptr) return PA_ERR_INVALID_ARG;
+  if (a->num_seqs < 0 || a->num_rows < 0 || a->block_table_stride < 1 || a->free_capacity < 1 || a->num_pages < 1 ||
+      a->num_pages > INT_MAX || a->reserved != 0)
+    return PA_ERR_INVALID_ARG;
+  if (pa_host::log2_page(a->page_size) < 0) return PA_ERR_UNSUPPORTED;
+  if (a->cu_seqlens_q == nullptr || a->free_pages == nullptr || a->num_free == nullptr || a->num_free_out == nullptr ||
+      (a->num_seqs > 0 && (a->context_lens == nullptr || a->block_table == nullptr || a->new_lens == nullptr)) ||
+      (a->num_rows > 0 && a->slot_mapping == nullptr))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned(a->context_lens, 4) || !aligned(a->cu_seqlens_q, 4) || !aligned(a->block_table, 4) || !aligned(a->free_pages, 4) ||
+      !aligned(a->num_free, 4) || !aligned(a->num_free_out, 4) || !aligned(a->new_lens, 4) || !aligned(a->slot_mapping, 8) ||
+      !aligned(a->positions, 4) || !aligned(a->status, 4))
+    return PA_ERR_ALIGN;
+  using pa_host::Span;
+  const uint64_t lens = (uint64_t)a->num_seqs * 4, rows = (uint64_t)a->num_rows;
+  const Span L{a->context_lens, lens}, cu{a->cu_seqlens_q, lens + 4}, table{a->block_table, lens * a->block_table_stride},
+      pages{a->free_pages, (uint64_t)a->free_capacity * 4}, count{a->num_free, 4}, left{a->num_free_out, 4}, grown{a->new_lens, lens},
+      slots{a->slot_mapping, rows * 8}, pos{a->positions, rows * 4}, none{nullptr, 0};
+  if (pa_host::overlaps(table, {L, cu, pages, count, left, grown, slots, pos}) ||
+      pa_host::overlaps(left, {a->num_free_out == a->num_free ? none : count, L, cu, pages, grown, slots, pos}) ||
+      pa_host::overlaps(grown, {a->new_lens == a->context_lens ? none : L, cu, pages, count, slots, pos}) ||
+      pa_host::overlaps(slots, {L, cu, pages, count, pos}) || pa_host::overlaps(pos, {L, cu, pages, count}))
+    return PA_ERR_INVALID_ARG;
+  if (a->num_seqs == 0 && a->num_rows == 0 && a->num_free_out == a->num_free) return PA_OK;
+  if (!paging_device()) return PA_ERR_CUDA;
+  AssignParams p;
+  p.L = a->context_lens;
+  p.cu = a->cu_seqlens_q;
+  p.free_pages = a->free_pages;
+  p.num_free = a->num_free;
+  p.bt = a->block_table;
+  p.num_free_out = a->num_free_out;
+  p.new_lens = a->new_lens;
+  p.pos = a->positions;
+  p.slots = a->slot_mapping;
+  p.status = a->status;
+  p.num_pages = (int32_t)a->num_pages;
+  p.B = a->num_seqs;
+  p.rows = a->num_rows;
+  p.bt_stride = a->block_table_stride;
+  p.shift = pa_host::log2_page(a->page_size);
+  p.capacity = a->free_capacity;
+  const Shape s = shape_of(a->num_rows, a->num_seqs);
+  const pa_host::Launch run(dim3((unsigned)s.ctas), dim3((unsigned)s.threads), 0, stream, s.ctas);
+  const cudaError_t e = s.each == 1 ? cudaLaunchKernelEx(run.cfg(), page_assign_kernel<1>, p)
+                                    : cudaLaunchKernelEx(run.cfg(), page_assign_kernel<4>, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" pa_status_t pa_page_release(const pa_page_release_args_t *a, void *stream) {
+  if (a == nullptr) return PA_ERR_INVALID_ARG;
+  if (a->num_seqs < 0 || a->block_table_stride < 1 || a->free_capacity < 1 || a->num_pages < 1 || a->num_pages > INT_MAX ||
+      a->reserved != 0)
+    return PA_ERR_INVALID_ARG;
+  if (pa_host::log2_page(a->page_size) < 0) return PA_ERR_UNSUPPORTED;
+  if (a->free_pages == nullptr || a->num_free == nullptr || a->num_free_out == nullptr ||
+      (a->num_seqs > 0 && (a->context_lens == nullptr || a->new_lens == nullptr || a->block_table == nullptr)))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned(a->context_lens, 4) || !aligned(a->new_lens, 4) || !aligned(a->block_table, 4) || !aligned(a->free_pages, 4) ||
+      !aligned(a->num_free, 4) || !aligned(a->num_free_out, 4) || !aligned(a->status, 4))
+    return PA_ERR_ALIGN;
+  using pa_host::Span;
+  const uint64_t lens = (uint64_t)a->num_seqs * 4;
+  const Span L{a->context_lens, lens}, grown{a->new_lens, lens}, table{a->block_table, lens * a->block_table_stride},
+      pages{a->free_pages, (uint64_t)a->free_capacity * 4}, count{a->num_free, 4}, left{a->num_free_out, 4}, none{nullptr, 0};
+  if (pa_host::overlaps(pages, {L, grown, table, count, left}) ||
+      pa_host::overlaps(left, {a->num_free_out == a->num_free ? none : count, L, grown, table}))
+    return PA_ERR_INVALID_ARG;
+  if (a->num_seqs == 0 && a->num_free_out == a->num_free) return PA_OK;
+  if (!paging_device()) return PA_ERR_CUDA;
+  ReleaseParams p;
+  p.L = a->context_lens;
+  p.new_lens = a->new_lens;
+  p.bt = a->block_table;
+  p.num_free = a->num_free;
+  p.free_pages = a->free_pages;
+  p.num_free_out = a->num_free_out;
+  p.status = a->status;
+  p.num_pages = (int32_t)a->num_pages;
+  p.B = a->num_seqs;
+  p.bt_stride = a->block_table_stride;
+  p.shift = pa_host::log2_page(a->page_size);
+  p.capacity = a->free_capacity;
+  // how many pages come back is not known here: what the tables and the stack can hold
+  const int64_t table_pages = (int64_t)a->num_seqs * a->block_table_stride;
+  const Shape s = shape_of(table_pages < a->free_capacity ? table_pages : a->free_capacity, a->num_seqs);
+  const pa_host::Launch run(dim3((unsigned)s.ctas), dim3((unsigned)s.threads), 0, stream, s.ctas);
+  const cudaError_t e = s.each == 1 ? cudaLaunchKernelEx(run.cfg(), page_release_kernel<1>, p)
+                                    : cudaLaunchKernelEx(run.cfg(), page_release_kernel<4>, p);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}

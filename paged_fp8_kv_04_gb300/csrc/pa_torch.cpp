@@ -4,8 +4,9 @@
 // These calls come several times per decode step, and their kernels take a few microseconds.  Checked
 // and marshalled in Python they cost 11 to 23 us each on the host, more than most of the kernels;
 // here 3 to 9.  The functions take their arguments by position, as binding.py passes them; None stands
-// for what is absent.  Tensors have to be dense, of the documented type and shape, and all on one
-// CUDA device, on which the call runs whatever the current device is.
+// for what is absent.  Tensors have to be dense (queries, keys and values of a prompt may be views of one projection's
+// output), of the documented type and shape, and all on one CUDA device, on which the call runs whatever the current
+// device is.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -37,6 +38,10 @@ struct Library {
   pa_status_t (*kv_compact)(const pa_kv_compact_args_t *, void *) = nullptr;
   pa_status_t (*beam_select)(const pa_beam_select_args_t *, void *) = nullptr;
   pa_status_t (*beam_reorder)(const pa_beam_reorder_args_t *, void *) = nullptr;
+  pa_status_t (*page_assign)(const pa_page_assign_args_t *, void *) = nullptr;
+  pa_status_t (*page_release)(const pa_page_release_args_t *, void *) = nullptr;
+  pa_status_t (*rope)(const pa_rope_args_t *, void *) = nullptr;
+  pa_status_t (*prompt_attn)(const pa_prompt_attn_args_t *, void *) = nullptr;
   PyObject *error = nullptr;
 } g_lib;
 
@@ -103,6 +108,22 @@ void *need(PyObject *o, const char *name, ScalarType type, IntArrayRef shape, in
 }
 void *need_or_null(PyObject *o, const char *name, ScalarType type, IntArrayRef shape, int dev) {
   return o == Py_None ? nullptr : need(o, name, type, shape, dev);
+}
+
+// The pointer of a [tokens, heads, head_dim] tensor whose tokens may lie apart (a view of a projection's output), and the
+// elements between tokens.
+void *token_rows(const Tensor &t, const char *name, ScalarType type, IntArrayRef shape, int dev, int64_t &stride) {
+  if (t.scalar_type() != type)
+    type_error(std::string(name) + ": " + toString(t.scalar_type()) + ", expected " + toString(type));
+  if (t.sizes() != shape) value_error(std::string(name) + ": shape " + shape_text(t.sizes()) + ", expected " + shape_text(shape));
+  const IntArrayRef st = t.strides();
+  const int64_t row = shape[1] * shape[2];
+  stride = shape[0] > 1 ? st[0] : row;  // the stride of a dimension of size 1 means nothing
+  if ((shape[2] > 1 && st[2] != 1) || (shape[1] > 1 && st[1] != shape[2]) || stride < row)
+    value_error(std::string(name) + ": a token's heads must lie one behind the other, and its tokens apart");
+  if (!t.is_cuda() || t.get_device() != dev)
+    value_error(std::string(name) + ": on " + t.device().str() + ", expected cuda:" + std::to_string(dev) + " like the rest of the call");
+  return t.data_ptr();
 }
 
 int cuda_device(const Tensor &t) {
@@ -459,11 +480,156 @@ PyObject *beam_reorder(PyObject *, PyObject *const *x, Py_ssize_t n) {
   });
 }
 
-// error class, then the addresses of the five entry points in the order of the calls above
+// context_lens, cu_seqlens_q, block_table, free_pages, num_free, num_free_out, new_lens, slot_mapping, positions, status,
+// stream, page_size, num_pages, num_rows or None -> (new_lens, slot_mapping, positions)
+PyObject *page_assign(PyObject *, PyObject *const *x, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject * {
+    const Tensor &table = tensor(x[2], "block_table");
+    const int dev = cuda_device(table);
+    const IntArrayRef ts = rank(table, 2, "block_table"), fs = rank(tensor(x[3], "free_pages"), 1, "free_pages");
+    const auto stream = stream_arg(x[10], dev);
+    const bool own = x[10] != Py_None;
+    const int64_t B = ts[0], B1 = B + 1, one = 1;
+    pa_page_assign_args_t a = {};
+    a.context_lens = static_cast<int32_t *>(need(x[0], "context_lens", ScalarType::Int, B, dev));
+    a.cu_seqlens_q = static_cast<int32_t *>(need(x[1], "cu_seqlens_q", ScalarType::Int, B1, dev));
+    a.block_table = static_cast<int32_t *>(need(table, "block_table", ScalarType::Int, ts, dev));
+    a.free_pages = static_cast<int32_t *>(need(x[3], "free_pages", ScalarType::Int, fs, dev));
+    a.num_free = static_cast<int32_t *>(need(x[4], "num_free", ScalarType::Int, one, dev));
+    a.num_free_out = static_cast<int32_t *>(need(x[5] == Py_None ? x[4] : x[5], "num_free_out", ScalarType::Int, one, dev));
+    a.status = status_word(x[9], dev);
+    a.page_size = int_arg(x[11], "page_size");
+    a.num_pages = int_arg(x[12], "num_pages");
+    int64_t rows = 0;
+    if (x[13] != Py_None)
+      rows = int_arg(x[13], "num_rows");
+    else if (x[7] != Py_None)
+      rows = rank(tensor(x[7], "slot_mapping"), 1, "slot_mapping")[0];
+    else
+      type_error("num_rows: needed without slot_mapping");
+    if (rows < 0) value_error("num_rows: negative");
+    a.num_seqs = int_of(B, "block_table");
+    a.num_rows = int_of(rows, "slot_mapping");
+    a.block_table_stride = int_of(ts[1], "block_table");
+    a.free_capacity = int_of(fs[0], "free_pages");
+    Output lens(x[6], "new_lens", ScalarType::Int, B, dev, stream, own), slots(x[7], "slot_mapping", ScalarType::Long, rows, dev, stream, own),
+        pos(x[8], "positions", ScalarType::Int, rows, dev, stream, own);
+    a.new_lens = lens.as<int32_t>();
+    a.slot_mapping = slots.as<int64_t>();
+    a.positions = pos.as<int32_t>();
+    enqueue("pa_page_assign", g_lib.page_assign, a, false, dev, stream);
+    return Py_BuildValue("(NNN)", lens.release(), slots.release(), pos.release());
+  });
+}
+
+// context_lens, new_lens, block_table, free_pages, num_free, num_free_out, status, stream, page_size, num_pages -> None
+PyObject *page_release(PyObject *, PyObject *const *x, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject * {
+    const Tensor &table = tensor(x[2], "block_table");
+    const int dev = cuda_device(table);
+    const IntArrayRef ts = rank(table, 2, "block_table"), fs = rank(tensor(x[3], "free_pages"), 1, "free_pages");
+    const int64_t B = ts[0], one = 1;
+    pa_page_release_args_t a = {};
+    a.context_lens = static_cast<int32_t *>(need(x[0], "context_lens", ScalarType::Int, B, dev));
+    a.new_lens = static_cast<int32_t *>(need(x[1], "new_lens", ScalarType::Int, B, dev));
+    a.block_table = static_cast<int32_t *>(need(table, "block_table", ScalarType::Int, ts, dev));
+    a.free_pages = static_cast<int32_t *>(need(x[3], "free_pages", ScalarType::Int, fs, dev));
+    a.num_free = static_cast<int32_t *>(need(x[4], "num_free", ScalarType::Int, one, dev));
+    a.num_free_out = static_cast<int32_t *>(need(x[5] == Py_None ? x[4] : x[5], "num_free_out", ScalarType::Int, one, dev));
+    a.status = status_word(x[6], dev);
+    a.page_size = int_arg(x[8], "page_size");
+    a.num_pages = int_arg(x[9], "num_pages");
+    a.num_seqs = int_of(B, "block_table");
+    a.block_table_stride = int_of(ts[1], "block_table");
+    a.free_capacity = int_of(fs[0], "free_pages");
+    enqueue("pa_page_release", g_lib.page_release, a, false, dev, stream_arg(x[7], dev));
+    Py_RETURN_NONE;
+  });
+}
+
+// q, k or None, positions, freqs, q_out, k_out, stream, layout, inverse, scale -> (q_out, k_out or None); without an
+// output its input is turned in place
+PyObject *rope(PyObject *, PyObject *const *x, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject * {
+    const Tensor &q = tensor(x[0], "q");
+    const int dev = cuda_device(q);
+    const IntArrayRef qs = rank(q, 3, "q"), fs = rank(tensor(x[3], "freqs"), 1, "freqs");
+    const ScalarType t = q.scalar_type();
+    if (t != ScalarType::BFloat16 && t != ScalarType::Float)
+      type_error(std::string("q: ") + toString(t) + ", expected bfloat16 or float32");
+    pa_rope_args_t a = {};
+    a.q = token_rows(q, "q", t, qs, dev, a.q_stride);
+    PyObject *qo = x[4] == Py_None ? x[0] : x[4], *ko = x[5] == Py_None ? x[1] : x[5];
+    a.q_out = token_rows(tensor(qo, "q_out"), "q_out", t, qs, dev, a.q_out_stride);
+    a.num_tokens = int_of(qs[0], "q");
+    a.num_q_heads = int_of(qs[1], "q");
+    a.head_dim = int_of(qs[2], "q");
+    if (x[1] != Py_None) {
+      const Tensor &k = tensor(x[1], "k");
+      const IntArrayRef ks = rank(k, 3, "k");
+      if (ks[0] != qs[0] || ks[2] != qs[2] || ks[1] < 1) value_error("k " + shape_text(ks) + " for q " + shape_text(qs));
+      a.k = token_rows(k, "k", t, ks, dev, a.k_stride);
+      a.k_out = token_rows(tensor(ko, "k_out"), "k_out", t, ks, dev, a.k_out_stride);
+      a.num_kv_heads = int_of(ks[1], "k");
+    } else if (x[5] != Py_None) {
+      value_error("k_out: without k");
+    }
+    a.positions = static_cast<int32_t *>(need(x[2], "positions", ScalarType::Int, qs[0], dev));
+    a.freqs = static_cast<int64_t *>(need(x[3], "freqs", ScalarType::Long, fs, dev));
+    if (fs[0] > 64) value_error("freqs: more than 64 pairs");
+    a.rot_dim = (int32_t)(2 * fs[0]);
+    a.dtype = t == ScalarType::Float ? PA_ROPE_F32 : PA_ROPE_BF16;
+    a.layout = int_arg(x[7], "layout");
+    a.inverse = int_arg(x[8], "inverse");
+    a.scale = float_arg(x[9]);
+    enqueue("pa_rope", g_lib.rope, a, qs[0] == 0, dev, stream_arg(x[6], dev));
+    return Py_BuildValue("(OO)", qo, x[1] == Py_None ? Py_None : ko);
+  });
+}
+
+// q, k, v, cu_seqlens, out, lse, status, stream, sm_scale or None, out_f32, want_lse -> (out, lse or None)
+PyObject *prompt_attn(PyObject *, PyObject *const *x, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject * {
+    const Tensor &q = tensor(x[0], "q"), &k = tensor(x[1], "k"), &v = tensor(x[2], "v");
+    const int dev = cuda_device(q);
+    const IntArrayRef qs = rank(q, 3, "q"), ks = rank(k, 3, "k"), cs = rank(tensor(x[3], "cu_seqlens"), 1, "cu_seqlens");
+    if (ks[0] != qs[0] || ks[2] != qs[2] || ks[1] < 1 || qs[1] < 1 || qs[1] % ks[1] != 0 || cs[0] < 1)
+      value_error("q " + shape_text(qs) + ", k " + shape_text(ks) + " and cu_seqlens " + shape_text(cs));
+    const auto stream = stream_arg(x[7], dev);
+    const bool own = x[7] != Py_None;
+    const ScalarType bf = ScalarType::BFloat16;
+    pa_prompt_attn_args_t a = {};
+    a.q = token_rows(q, "q", bf, qs, dev, a.q_stride);
+    a.k = token_rows(k, "k", bf, ks, dev, a.k_stride);
+    a.v = token_rows(v, "v", bf, ks, dev, a.v_stride);
+    a.cu_seqlens = static_cast<int32_t *>(need(x[3], "cu_seqlens", ScalarType::Int, cs, dev));
+    a.status = status_word(x[6], dev);
+    const ScalarType ot = x[4] != Py_None ? tensor(x[4], "out").scalar_type() : int_arg(x[9], "out_dtype") != 0 ? ScalarType::Float : bf;
+    if (ot != bf && ot != ScalarType::Float) type_error(std::string("out: ") + toString(ot) + ", expected bfloat16 or float32");
+    Output out(x[4], "out", ot, qs, dev, stream, own);
+    std::optional<Output> lse;
+    if (x[5] != Py_None || int_arg(x[10], "want_lse") != 0) lse.emplace(x[5], "lse", ScalarType::Float, qs.slice(0, 2), dev, stream, own);
+    a.out = out.as<void>();
+    if (lse) a.lse = lse->as<float>();
+    a.num_seqs = int_of(cs[0] - 1, "cu_seqlens");
+    a.num_rows = int_of(qs[0], "q");
+    a.num_kv_heads = int_of(ks[1], "k");
+    a.group_size = int_of(qs[1] / ks[1], "q");
+    a.head_dim = int_of(qs[2], "q");
+    a.out_dtype = ot == ScalarType::Float ? PA_OUT_F32 : PA_OUT_BF16;
+    a.sm_scale = x[8] == Py_None ? (float)(1.0 / std::sqrt((double)qs[2])) : float_arg(x[8]);
+    enqueue("pa_prompt_attn", g_lib.prompt_attn, a, qs[0] == 0, dev, stream);
+    Output none;
+    return Py_BuildValue("(NN)", out.release(), lse ? lse->release() : none.release());
+  });
+}
+
+// error class, then the addresses of the entry points in the order of the calls above
 PyObject *bind(PyObject *, PyObject *const *x, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject * {
-    void *at[5];
-    for (int i = 0; i < 5; ++i) {
+  constexpr int kEntries = 9;
+  return guarded(n, 1 + kEntries, [&]() -> PyObject * {
+    void *at[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
       at[i] = PyLong_AsVoidPtr(x[i + 1]);
       if (at[i] == nullptr) throw Refusal(PyErr_Occurred() ? nullptr : PyExc_ValueError, "a null entry point");
     }
@@ -472,6 +638,10 @@ PyObject *bind(PyObject *, PyObject *const *x, Py_ssize_t n) {
     g_lib.kv_compact = reinterpret_cast<decltype(g_lib.kv_compact)>(at[2]);
     g_lib.beam_select = reinterpret_cast<decltype(g_lib.beam_select)>(at[3]);
     g_lib.beam_reorder = reinterpret_cast<decltype(g_lib.beam_reorder)>(at[4]);
+    g_lib.page_assign = reinterpret_cast<decltype(g_lib.page_assign)>(at[5]);
+    g_lib.page_release = reinterpret_cast<decltype(g_lib.page_release)>(at[6]);
+    g_lib.rope = reinterpret_cast<decltype(g_lib.rope)>(at[7]);
+    g_lib.prompt_attn = reinterpret_cast<decltype(g_lib.prompt_attn)>(at[8]);
     Py_INCREF(x[0]);
     Py_XDECREF(g_lib.error);
     g_lib.error = x[0];
@@ -480,8 +650,9 @@ PyObject *bind(PyObject *, PyObject *const *x, Py_ssize_t n) {
 }
 
 #define PA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {PA_METHOD(bind),       PA_METHOD(attn_mass),   PA_METHOD(evict_select), PA_METHOD(kv_compact),
-                           PA_METHOD(beam_select), PA_METHOD(beam_reorder), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {PA_METHOD(bind),        PA_METHOD(attn_mass),   PA_METHOD(evict_select), PA_METHOD(kv_compact), PA_METHOD(beam_select),
+                           PA_METHOD(beam_reorder), PA_METHOD(page_assign), PA_METHOD(page_release), PA_METHOD(rope),       PA_METHOD(prompt_attn),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "pa_torch", "Torch side of the cache operators.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
