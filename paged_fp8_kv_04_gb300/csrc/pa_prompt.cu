@@ -13,8 +13,8 @@
 // share its keys, short prompts fill a tile as well as long ones do, and the diagonal cuts few tokens.  A CTA has two tiles, so that the
 // tensor core works on one while the other's weights are computed: S0 S1 | PV0 S0' PV1 S1' | ...
 //
-// Warp roles (384 threads): warps 0-3 and 4-7 are the softmax of tiles 0 and 1; warp 8 fetches tiles by TMA; warp 9
-// issues the MMAs; warps 10 and 11 look through the values of the blocks that the diagonal or the sequence's end cuts: an
+// Warp roles (384 threads): warps 0-3 and 4-7 are the softmax of tiles 0 and 1; warp 8 fetches tiles by TMA; one lane
+// of warp 9 issues the MMAs; warps 10 and 11 look through the values of the blocks that the diagonal or the sequence's end cuts: an
 // infinity or NaN there must not reach rows that do not attend it (0 * inf), so it is replaced by 0, and rows that do attend it
 // get it in the epilogue.  Every wait is bounded; TMEM is released on every path.
 #include <cuda.h>
@@ -46,11 +46,13 @@ constexpr int kMaxGroup = 64;
 constexpr int kMaxRows = 1 << 24;
 constexpr int kOperand = kM * kD * 2;  // bytes of a tile or block: two halves of 64 elements a row
 constexpr int kStages = 5;
+constexpr int kMinSplit = 3;      // blocks that a unit has more than to be split into its tiles
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;     // log2 of what the weights may exceed 1 by
 
 struct PromptParams {
-  CUtensorMap tm_q, tm_k, tm_v;
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;  // tm_o: a bf16 output, in boxes like the queries'
+
   const int32_t *cu;
   const uint16_t *v;  // for the epilogue of values that are not finite
   void *out;
@@ -59,6 +61,7 @@ struct PromptParams {
   int64_t v_stride;
   int32_t B, T, Hkv, G, tokens;  // tokens of a tile
   int32_t out_f32;
+  int32_t sms;
   float fold;  // sm_scale * log2 e
 };
 
@@ -70,8 +73,8 @@ enum {
   B_FULL = 2,                       // [kStages]
   B_EMPTY = B_FULL + kStages,       // [kStages]
   B_S = B_EMPTY + kStages,          // [2] S is complete
-  B_P = B_S + 2,                    // [2] P is in TMEM (and O scaled)
-  B_O = B_P + 2,                    // [2] PV is complete
+  B_P = B_S + 2,                    // [2][2] half of P is in TMEM (and O scaled)
+  B_O = B_P + 4,                    // [2] PV is complete
   B_CLEAN = B_O + 2,                // [2] the values have been looked through: of the first and second cut block
   B_CUT = B_CLEAN + 2,              // [2] the values of a cut block, in place of B_FULL
   B_DONE = B_CUT + 2,               // the softmax warps are done with TMEM
@@ -80,9 +83,12 @@ enum {
 };
 constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM address, dirty blocks, sequence, padding
 constexpr int kRed = kMisc + 16;             // [2][warps] of the schedule's sums
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int kSmem = kRed + 2 * 4 * (kThreads / 32) + 1024;
+// Both slots' maxima and sums of a tile that has two, over the second tile's queries: [2][128] each.
+constexpr int kBothM = kOperand, kBothL = kBothM + 2 * kM * 4;
 
-// TMEM columns: S of tile t at 128 t, O at 256 + 128 t; P over S.
+// TMEM columns: S of tile t at 128 t, O at 256 + 128 t; P over S.  The CTA has all of them, so they begin at 0.
 constexpr uint32_t kTmemCols = 512;
 
 __host__ __device__ constexpr uint32_t idesc(int b_mn) {
@@ -121,12 +127,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, K = 16.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(accumulate));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
@@ -134,6 +138,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// This thread's stores are complete.
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 __device__ __forceinline__ void raise(const PromptParams &p, uint32_t flag) {
@@ -145,12 +164,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(~0u, pa::mbar_wait_bounded(bar, parity)) != 0;
 }
 
-// A CTA's share: two tiles of one sequence and KV head.
+// A CTA's share, all keys of up to two tiles of a sequence and KV head.  It has two slots, each with its softmax warps and its
+// columns of TMEM: one for either tile, or (solo) both for one tile, with the even and the odd blocks of its keys.
 struct Unit {
-  int row0, len, tok0, h;  // the sequence's first row and length, the unit's first token
-  // Key blocks of each tile (0: no tokens) and of both, and the first that the diagonal cuts: two of them at most, since a
-  // unit has 256 tokens and begins with a block, or has 128 or fewer.
-  int nb[2], blocks, cut;
+  int row0, len, h;        // the sequence's first row and length, the KV head
+  int tok0, tok1;          // the first token of either slot's tile
+  int nb0, nb1;            // either slot's key blocks (0: no tokens)
+  int blocks, cut;         // key blocks in all, and the first that the diagonal cuts: two of them at most, since a unit has
+                           // 256 tokens and begins with a block, or has 128 or fewer
+  bool solo;
+  __device__ __forceinline__ int nb(int t) const { return t ? nb1 : nb0; }
+  __device__ __forceinline__ int tok(int t) const { return t ? tok1 : tok0; }
+  __device__ __forceinline__ int block(int t, int j) const { return solo ? 2 * j + t : j; }  // a slot's j-th
 };
 
 // ---------------------------------------------------------------------------- schedule
@@ -173,44 +198,68 @@ __device__ __forceinline__ int reduce_all(int v, bool most, int *red, int turn) 
 // The x-th unit of the call for one KV head, the units with the most keys first: unit j of a sequence has j + 1 times the
 // keys of its first, and the GPU's last CTAs should be short ones.  Units of index c or more number N(c), the sum
 // of max(0, n_s - c) over the sequences: the unit's index is the largest c with N(c) > x, and it belongs to the
-// (x - N(c + 1))-th of the sequences that have such a unit.  Synchronises the CTA; false if there are fewer units.
+// (x - N(c + 1))-th of the sequences that have such a unit.  False if there are fewer units.
+// KS 0: up to 32 sequences, a lane each, every warp by itself.  Else KS sequences per thread of the CTA, which is synchronised.
+// While there are SMs without a unit the longest units are split into their two tiles, a CTA each, which takes half the time: its
+// keys are dealt to both slots (2048 tokens x 16 heads: SOLO us, 26.3 without; 1024: SOLO2, 15.8).
 template <int KS>
-__device__ bool locate(const PromptParams &p, int x, uint8_t *smem, Unit &u) {
-  const int tid = threadIdx.x, span = 2 * p.tokens;
+__device__ bool locate(const PromptParams &p, uint8_t *smem, Unit &u) {
+  constexpr int kOwn = KS > 0 ? KS : 1;
+  const int tid = threadIdx.x, lane = tid & 31, span = 2 * p.tokens;
   int *red = reinterpret_cast<int *>(smem + kRed);
-  volatile int *found = reinterpret_cast<volatile int *>(smem + kMisc + 8);
-  int n[KS], sum = 0, top = 0;
+  int n[kOwn], row0 = 0, len = 0, sum = 0, top = 0;
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    const int s = tid + i * kThreads;
+  for (int i = 0; i < kOwn; ++i) {
+    const int s = KS > 0 ? tid + i * kThreads : lane;
     n[i] = 0;
     if (s < p.B) {
       const int a = p.cu[s], b = p.cu[s + 1];
-      if (a < 0 || b < a || b > p.T)
+      if (a < 0 || b < a || b > p.T) {
         bad = true;
-      else
+      } else {
         n[i] = (b - a + span - 1) / span;
+        row0 = a;
+        len = b - a;
+      }
     }
     sum += n[i];
     top = max(top, n[i]);
   }
-  if (bad && blockIdx.x == 0) raise(p, PA_DEV_BAD_QLEN);
-  const int total = reduce_all(sum, false, red, 0);
-  if (x >= total) return false;
+  if (bad && blockIdx.x == 0 && (KS > 0 || tid < 32)) raise(p, PA_DEV_BAD_QLEN);
+  int turn = 0;
+  auto reduce = [&](int v, bool most) {
+    if constexpr (KS == 0) return most ? __reduce_max_sync(~0u, v) : __reduce_add_sync(~0u, v);
+    turn ^= 1;
+    return reduce_all(v, most, red, turn);
+  };
+  const int total = reduce(sum, false);
+  const int units = total * p.Hkv;
+  int x = (int)blockIdx.x, tile = -1;
+  if (units < p.sms) {
+    const int first = (kMinSplit * kN + span - 1) / span;  // units with more than kMinSplit blocks
+    int longer = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) longer += max(0, n[i] - first);
+    const int splits = min(reduce(longer, false) * p.Hkv, p.sms - units);
+    tile = x < 2 * splits ? x & 1 : -1;
+    x = x < 2 * splits ? x >> 1 : x - splits;
+  }
+  if (x >= units) return false;
+  u.h = p.Hkv == 1 ? 0 : x % p.Hkv;
+  x = p.Hkv == 1 ? x : x / p.Hkv;
   int lo = 0, above = 0;  // N(lo) > x >= above = N(hi)
   if (p.B == 1) {
     lo = total - 1 - x;
     above = x;
   } else {
-    int hi = reduce_all(top, true, red, 1), turn = 0;
+    int hi = reduce(top, true);
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       int v = 0;
 #pragma unroll
-      for (int i = 0; i < KS; ++i) v += max(0, n[i] - mid);
-      const int count = reduce_all(v, false, red, turn);
-      turn ^= 1;
+      for (int i = 0; i < kOwn; ++i) v += max(0, n[i] - mid);
+      const int count = reduce(v, false);
       if (count > x) {
         lo = mid;
       } else {
@@ -219,38 +268,54 @@ __device__ bool locate(const PromptParams &p, int x, uint8_t *smem, Unit &u) {
       }
     }
   }
-  // the (x - above)-th of those with more than lo units, thread by thread
-  int mine = 0;
+  // the (x - above)-th of those with more than lo units
+  if constexpr (KS == 0) {
+    const uint32_t have = __ballot_sync(~0u, n[0] > lo);
+    const int owner = __fns(have, 0, x - above + 1) & 31;
+    u.row0 = __shfl_sync(~0u, row0, owner);
+    u.len = __shfl_sync(~0u, len, owner);
+  } else {  // thread by thread
+    volatile int *found = reinterpret_cast<volatile int *>(smem + kMisc + 8);
+    int mine = 0;
 #pragma unroll
-  for (int i = 0; i < KS; ++i) mine += n[i] > lo;
-  int upto = mine;
+    for (int i = 0; i < kOwn; ++i) mine += n[i] > lo;
+    int upto = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, upto, o);
-    if ((tid & 31) >= o) upto += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    __syncthreads();  // the last sum has been read
+    if (lane == 31) red[tid >> 5] = upto;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 5); ++w) upto += red[w];
+    int at = x - above - (upto - mine);
+    if (at >= 0 && at < mine) {
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i)
+        if (n[i] > lo && at-- == 0) *found = tid + i * kThreads;
+    }
+    __syncthreads();
+    const int s = *found;
+    u.row0 = p.cu[s];
+    u.len = p.cu[s + 1] - u.row0;
   }
-  __syncthreads();  // the last sum has been read
-  if ((tid & 31) == 31) red[tid >> 5] = upto;
-  __syncthreads();
-  for (int w = 0; w < (tid >> 5); ++w) upto += red[w];
-  int at = x - above - (upto - mine);
-  if (at >= 0 && at < mine) {
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-      if (n[i] > lo && at-- == 0) *found = tid + i * kThreads;
+  auto blocks_of = [&](int first) { return first < u.len ? (min(u.len, first + p.tokens) + kN - 1) / kN : 0; };
+  u.cut = lo * span / kN;
+  u.solo = tile >= 0;
+  if (u.solo) {
+    u.tok0 = u.tok1 = lo * span + tile * p.tokens;
+    u.blocks = blocks_of(u.tok0);
+    u.nb0 = (u.blocks + 1) >> 1;
+    u.nb1 = u.blocks >> 1;
+    if (u.blocks == 0) return false;  // (a sequence's last unit may have but one tile)
+  } else {
+    u.tok0 = lo * span;
+    u.tok1 = u.tok0 + p.tokens;
+    u.nb0 = blocks_of(u.tok0);
+    u.nb1 = blocks_of(u.tok1);
+    u.blocks = max(u.nb0, u.nb1);
   }
-  __syncthreads();
-  const int s = *found;
-  u.row0 = p.cu[s];
-  u.len = p.cu[s + 1] - u.row0;
-  u.tok0 = lo * span;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = u.tok0 + t * p.tokens;
-    u.nb[t] = first < u.len ? (min(u.len, first + p.tokens) + kN - 1) / kN : 0;
-  }
-  u.blocks = max(u.nb[0], u.nb[1]);
-  u.cut = u.tok0 / kN;
   return true;
 }
 
@@ -269,37 +334,43 @@ __device__ __forceinline__ bool landed(const Unit &u, uint32_t bars, int i) {
   return warp_wait(bar, parity);
 }
 
+__device__ __forceinline__ void load_block(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars, int i) {
+  uint32_t parity;
+  const uint32_t bar = bar_landed(u, bars, i, parity), dst = base + kRing + (i % kStages) * kOperand;
+  pa::mbar_arrive_expect_tx(bar, kOperand);
+  for (int x = 0; x < 2; ++x)
+    tma_load_3d(dst + x * (kOperand / 2), i & 1 ? &p.tm_v : &p.tm_k, 64 * x, u.h, u.row0 + (i >> 1) * kN, bar);
+}
+
+// The queries and as many blocks as the ring holds, by one thread.
+__device__ void first_loads(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars) {
+  const uint32_t qbytes = (uint32_t)p.G * p.tokens * kD * 2;
+  for (int t = 0; t < (u.solo ? 1 : 2); ++t) {
+    if (u.nb(t) == 0) continue;
+    pa::mbar_arrive_expect_tx(bars + 8 * (B_QFULL + t), qbytes);
+    for (int x = 0; x < 2; ++x)
+      tma_load_3d(base + t * kOperand + x * (kOperand / 2), &p.tm_q, 64 * x, u.h * p.G, u.row0 + u.tok(t), bars + 8 * (B_QFULL + t));
+    if (t == 0) load_block(p, u, base, bars, 0);
+  }
+  for (int i = 1; i < min(kStages, 2 * u.blocks); ++i) load_block(p, u, base, bars, i);
+}
+
 __device__ void run_producer(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars) {
   const int lane = threadIdx.x & 31;
-  const uint32_t qbytes = (uint32_t)p.G * p.tokens * kD * 2;
-  if (lane == 0) {
-    for (int t = 0; t < 2; ++t) {
-      if (u.nb[t] == 0) continue;
-      pa::mbar_arrive_expect_tx(bars + 8 * (B_QFULL + t), qbytes);
-      for (int x = 0; x < 2; ++x)
-        tma_load_3d(base + t * kOperand + x * (kOperand / 2), &p.tm_q, 64 * x, u.h * p.G, u.row0 + u.tok0 + t * p.tokens,
-                    bars + 8 * (B_QFULL + t));
-    }
-  }
+  if (lane == 0) first_loads(p, u, base, bars);
+  __syncwarp();
   bool ok = true;
-  int i = 0;
-  for (; i < 2 * u.blocks && ok; ++i) {
-    const int st = i % kStages, use = i / kStages;
-    if (use > 0) ok = warp_wait(bars + 8 * (B_EMPTY + st), (use - 1) & 1);
+  int i = min(kStages, 2 * u.blocks);
+  for (; i < 2 * u.blocks; ++i) {
+    ok = warp_wait(bars + 8 * (B_EMPTY + i % kStages), (i / kStages - 1) & 1);
     if (!ok) break;
-    if (lane == 0) {
-      uint32_t parity;
-      const uint32_t bar = bar_landed(u, bars, i, parity), dst = base + kRing + st * kOperand;
-      pa::mbar_arrive_expect_tx(bar, kOperand);
-      for (int x = 0; x < 2; ++x)
-        tma_load_3d(dst + x * (kOperand / 2), i & 1 ? &p.tm_v : &p.tm_k, 64 * x, u.h, u.row0 + (i >> 1) * kN, bar);
-    }
+    if (lane == 0) load_block(p, u, base, bars, i);
     __syncwarp();
   }
   if (!ok && lane == 0) {
     raise(p, PA_DEV_TIMEOUT);
-    for (int t = 0; t < 2; ++t)  // copies in flight land before the CTA can exit
-      if (u.nb[t] > 0) pa::mbar_wait_bounded(bars + 8 * (B_QFULL + t), 0);
+    for (int t = 0; t < (u.solo ? 1 : 2); ++t)  // copies in flight land before the CTA can exit
+      if (u.nb(t) > 0) pa::mbar_wait_bounded(bars + 8 * (B_QFULL + t), 0);
     for (int k = max(0, i - kStages); k < i; ++k) {
       uint32_t parity;
       const uint32_t bar = bar_landed(u, bars, k, parity);
@@ -308,92 +379,162 @@ __device__ void run_producer(const PromptParams &p, const Unit &u, uint32_t base
   }
 }
 
-__device__ void run_mma(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars, uint32_t tm) {
-  const int lane = threadIdx.x & 31;
-  bool ok = true;
-  auto stage = [&](int i) { return base + kRing + (i % kStages) * kOperand; };
-  auto scores = [&](int t, int j, bool last) {  // S_t of block j; `last`: nobody else reads its keys
+// A bounded wait of a whole warp whose control flow stays uniform: what the MMAs' operands are computed from then stays
+// in uniform registers, where the instructions want them.
+__device__ __forceinline__ bool uniform_wait(uint32_t bar, uint32_t parity) {
+  if (__all_sync(~0u, pa::mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(~0u, pa::mbar_try_wait(bar, parity)))
+    if (__any_sync(~0u, clock64() - t0 > pa::kWaitCycles)) return false;
+  return true;
+}
+
+// D (+)= A B with the low words of the shared-memory descriptors, whose high words are the same for all: 1024 bytes between
+// groups of 8 rows, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__host__ __device__ constexpr uint32_t desc_low(uint32_t lead) { return (lead >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate), "r"(kDescHigh));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate), "r"(kDescHigh));
+}
+
+// The MMAs of both slots: PV0 S0' PV1 S1' of every block, S' being the slot's next one's.  The waits for what the next product
+// reads come half way through the one before, where the tensor core has MMAs left (before them instead: 620 us, not 613, for
+// 16384 tokens x 16 heads).
+__device__ bool issue_mmas(const Unit &u, uint32_t base, uint32_t bars) {
+  const int nb0 = __reduce_max_sync(~0u, u.nb0), nb1 = __reduce_max_sync(~0u, u.nb1), cut = __reduce_max_sync(~0u, u.cut);
+  const bool solo = __any_sync(~0u, u.solo);
+  // (14 bits of the address)
+  const uint32_t q_at = (base >> 4) & 0x3FFFu, ring_at = q_at + (kRing >> 4);
+  const uint32_t q_low = q_at | desc_low(1024), k_low = ring_at | desc_low(1024), v_low = ring_at | desc_low(kOperand / 2);
+  auto block = [&](int t, int j) { return solo ? 2 * j + t : j; };
+  auto last_of = [&](int t, int j) { return solo || t == 1 || j >= nb1; };  // the slot that reads a block last
+  auto arrived = [&](int bar, uint32_t parity) { return uniform_wait(bars + 8 * bar, parity); };
+  auto fetched = [&](int i) {
+    const bool own = (i & 1) != 0 && (i >> 1) >= cut;
+    return own ? arrived(B_CUT + (i >> 1) - cut, 0) && arrived(B_CLEAN + (i >> 1) - cut, 0) : arrived(B_FULL + i % kStages, (i / kStages) & 1);
+  };
+  auto scores = [&](int t, int j, bool values) {  // S of the slot's j-th block; `values`: half way through, those have landed
+    const int i = 2 * block(t, j);
+    const uint32_t q = q_low + (solo ? 0 : t) * (kOperand >> 4), k = k_low + (i % kStages) * (kOperand >> 4);
     if (pa::elect_one()) {
-      const uint32_t q = base + t * kOperand, k = stage(2 * j);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const uint32_t off = (x >> 2) * (kOperand / 2) + 32 * (x & 3);
-        pa::umma_f16(tm + 128 * t, pa::umma_sdesc(q + off, 1024, 1024, 2), pa::umma_sdesc(k + off, 1024, 1024, 2), idesc(0), x > 0);
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t off = (32 * x) >> 4;
+        mma_ss(128 * t, q + off, k + off, idesc(0), x > 0);
       }
-      pa::umma_commit(bars + 8 * (B_S + t));
-      if (last) pa::umma_commit(bars + 8 * (B_EMPTY + (2 * j) % kStages));
     }
     __syncwarp();
-  };
-  // the tile that reads a block last: 1 if it has the block
-  auto last_of = [&](int j) { return j < u.nb[1] ? 1 : 0; };
-  for (int t = 0; t < 2 && ok; ++t)
-    if (u.nb[t] > 0) {
-      ok = warp_wait(bars + 8 * (B_QFULL + t), 0) && landed(u, bars, 0);
-      if (!ok) break;
-      pa::tc_fence_after();
-      scores(t, 0, t == last_of(0));
-    }
-  for (int j = 0; j < u.blocks && ok; ++j) {
-    ok = landed(u, bars, 2 * j + 1);
-    if (ok && j >= u.cut) ok = warp_wait(bars + 8 * (B_CLEAN + j - u.cut), 0);
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (j >= u.nb[t]) continue;
-      ok = warp_wait(bars + 8 * (B_P + t), j & 1);
-      if (!ok) break;
-      pa::tc_fence_after();
-      if (pa::elect_one()) {
-        const uint32_t v = stage(2 * j + 1);
+    const bool ok = !values || fetched(i + 1);
+    if (pa::elect_one()) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x)  // 16 keys: two groups of 8 rows; the two halves of head_dim 16 KB apart
-          umma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * x, pa::umma_sdesc(v + 2048 * x, kOperand / 2, 1024, 2), idesc(1), j > 0 || x > 0);
-        pa::umma_commit(bars + 8 * (B_O + t));
-        if (t == last_of(j)) pa::umma_commit(bars + 8 * (B_EMPTY + (2 * j + 1) % kStages));
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t off = (kOperand / 2 + 32 * x) >> 4;
+        mma_ss(128 * t, q + off, k + off, idesc(0), 1);
       }
-      __syncwarp();
-      if (j + 1 < u.nb[t]) {  // over P of this block, which the product before reads: MMAs run in order
-        ok = landed(u, bars, 2 * j + 2);
-        if (!ok) break;
-        scores(t, j + 1, t == last_of(j + 1));
+      pa::umma_commit(bars + 8 * (B_S + t));
+      if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + i % kStages));
+    }
+    __syncwarp();
+    return ok;
+  };
+  if (nb0 > 0) {
+    if (!arrived(B_QFULL, 0) || !fetched(0)) return false;
+    pa::tc_fence_after();
+    scores(0, 0, false);
+  }
+  if (nb1 > 0) {
+    if (solo ? !fetched(2) : !arrived(B_QFULL + 1, 0)) return false;
+    pa::tc_fence_after();
+    scores(1, 0, false);
+  }
+  if (!fetched(1) || (solo && nb1 > 0 && !fetched(3))) return false;
+  for (int j = 0; j < max(nb0, nb1); ++j) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int nb = t ? nb1 : nb0, i = 2 * block(t, j) + 1;
+      if (j >= nb) continue;
+      const uint32_t v = v_low + (i % kStages) * (kOperand >> 4);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!arrived(B_P + 2 * t + half, j & 1)) return false;
+        pa::tc_fence_after();
+        if (pa::elect_one()) {
+#pragma unroll
+          for (int x = 4 * half; x < 4 * half + 4; ++x)  // 16 keys: two groups of 8 rows; the two halves of head_dim 16 KB apart
+            mma_ts(256 + 128 * t, 128 * t + 8 * x, v + x * (2048 >> 4), idesc(1), j > 0 || x > 0);
+          if (half == 1) {
+            pa::umma_commit(bars + 8 * (B_O + t));
+            if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + i % kStages));
+          }
+        }
+        __syncwarp();
+        // the next block's keys: of either slot's, or the same for both
+        const bool next = solo || t == 1 ? j + 1 < nb : j + 1 < max(nb0, nb1);
+        if (half == 0 && next && (solo || t == 0 || j >= nb0) && !fetched(2 * block(t, j + 1))) return false;
       }
+      // over P of this block, which the product before reads: a thread's MMAs run in order
+      if (j + 1 < nb && !scores(t, j + 1, last_of(t, j + 1))) return false;
     }
   }
-  if (!ok && lane == 0) raise(p, PA_DEV_TIMEOUT);
-  __syncwarp();
+  return true;
+}
+
+__device__ void run_mma(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars) {
+  const int lane = threadIdx.x & 31;
+  pa::tc_fence_after();
+  const bool ok = issue_mmas(u, base, bars);
   if (pa::elect_one()) pa::umma_commit(bars + 8 * B_MMA);
   __syncwarp();
-  if (!warp_wait(bars + 8 * B_MMA, 0) && lane == 0) raise(p, PA_DEV_TIMEOUT);
-  if (!warp_wait(bars + 8 * B_DONE, 0) && lane == 0) raise(p, PA_DEV_TIMEOUT);
-  pa::tc_fence_after();
-  pa::tmem_dealloc(tm, kTmemCols);
+  if (!(warp_wait(bars + 8 * B_MMA, 0) & ok) && lane == 0) raise(p, PA_DEV_TIMEOUT);
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
 
-// Values of the blocks that the diagonal or the sequence's end cuts, by two warps.
-__device__ void run_clean(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars, uint8_t *smem) {
-  const int tid = threadIdx.x & 63, lane = tid & 31;
+// Whether one of the eight bf16 values of w is an infinity or NaN: an exponent of ones carries into the sign's place.
+__device__ __forceinline__ uint32_t any_not_finite(const uint4 &w) {
+  constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+  return (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) & 0x80008000u;
+}
+
+// Values of the blocks that the diagonal or the sequence's end cuts.
+__device__ void run_clean(const PromptParams &p, const Unit &u, uint32_t bars, uint8_t *smem) {
+  constexpr int kBatch = 8;
+  const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - kCleanWarp;
   for (int j = u.cut; j < u.blocks; ++j) {
     const int i = 2 * j + 1, st = i % kStages;
     if (!landed(u, bars, i)) {
       if (lane == 0) raise(p, PA_DEV_TIMEOUT);
       return;
     }
-    const uint32_t at = base + kRing + st * kOperand;
+    uint4 *at = reinterpret_cast<uint4 *>(smem + kRing + st * kOperand + half * (kOperand / 2)) + lane;
     bool own = false;  // one of the sequence's own
-    for (int c = tid; c < kOperand / 16; c += 64) {
-      uint4 w = pa::lds128(at + 16 * c);
-      uint32_t v[4] = {w.x, w.y, w.z, w.w};
-      bool any = false;
+#pragma unroll 1
+    for (int c0 = 0; c0 < kOperand / 32; c0 += 32 * kBatch) {  // pieces of this half
+      uint4 w[kBatch];
+      uint32_t any = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool lo = not_finite(v[e]), hi = not_finite(v[e] >> 16);
-        any |= lo || hi;
-        v[e] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
-      }
-      if (any) {
-        pa::sts128(at + 16 * c, make_uint4(v[0], v[1], v[2], v[3]));
-        own |= j * kN + ((c & (kOperand / 32 - 1)) >> 3) < u.len;  // 8 pieces a row, in each half
+      for (int b = 0; b < kBatch; ++b) w[b] = at[c0 + 32 * b];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) any |= any_not_finite(w[b]);
+      if (any == 0) continue;
+#pragma unroll 1
+      for (int b = 0; b < kBatch; ++b) {
+        uint32_t *v = reinterpret_cast<uint32_t *>(at + c0 + 32 * b);
+        for (int e = 0; e < 4; ++e) {
+          const bool lo = not_finite(v[e]), hi = not_finite(v[e] >> 16);
+          if (!lo && !hi) continue;
+          v[e] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+          own |= j * kN + ((c0 + 32 * b + lane) >> 3) < u.len;  // 8 pieces a row
+        }
       }
     }
     if (own) atomicOr(reinterpret_cast<unsigned *>(smem + kMisc + 4), 1u << (j - u.cut));
@@ -403,35 +544,101 @@ __device__ void run_clean(const PromptParams &p, const Unit &u, uint32_t base, u
   }
 }
 
-__device__ void run_softmax(const PromptParams &p, const Unit &u, uint32_t bars, uint32_t tm, const uint8_t *smem) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2;
-  const int row = 32 * (warp & 3) + lane;
-  const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16), s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
-  const int first = u.tok0 + t * p.tokens, tk = row / p.G, token = first + tk, nb = u.nb[t];
-  const bool live = tk < p.tokens && token < u.len;
+// The infinities and NaN among the values that a row attends and that were replaced by 0: into its output, which this
+// thread has written.
+__device__ __noinline__ void add_not_finite(const uint16_t *v, int64_t v_stride, void *out, bool out_f32, uint32_t dirty, int cut, int token) {
+  for (int i = cut * kN; i <= token; ++i) {
+    if (!(dirty >> (i / kN - cut) & 1u)) continue;
+    for (int d = 0; d < kD; ++d) {
+      const uint16_t bits = v[i * v_stride + d];
+      if (!not_finite(bits)) continue;
+      const float x = __uint_as_float((uint32_t)bits << 16);
+      if (out_f32) {
+        static_cast<float *>(out)[d] += x;
+      } else {
+        uint16_t *o = static_cast<uint16_t *>(out) + d;
+        *o = (uint16_t)(pa::pack_bf16x2(__uint_as_float((uint32_t)*o << 16) + x, 0.f) & 0xFFFFu);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float peak_of(const uint32_t (&s)[kN]) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < kN; k += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[k + 2 * e]), __uint_as_float(s[k + 2 * e + 1]));
+  return max3(fmaxf(top[0], top[1]), top[2], top[3]);
+}
+
+// 2^(c s - m) of half a block as bf16 pairs; their sum, before the rounding.
+__device__ __forceinline__ float weights(const uint32_t *s, float c, float m, uint32_t (&w)[32]) {
+  const pa::f32x2 c2 = pa::pack2(c, c), m2 = pa::pack2(-m, -m);
+  pa::f32x2 part[2] = {pa::pack2(0.f, 0.f), pa::pack2(0.f, 0.f)};
+#pragma unroll
+  for (int e = 0; e < kN / 2; e += 2) {
+    float a, b;
+    pa::unpack2(pa::fma2(pa::pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, m2), a, b);
+    a = pa::fast_exp2(a);
+    b = pa::fast_exp2(b);
+    part[(e >> 1) & 1] = pa::add2(part[(e >> 1) & 1], pa::pack2(a, b));
+    w[e >> 1] = pa::pack_bf16x2(a, b);
+  }
+  float x, y;
+  pa::unpack2(pa::add2(part[0], part[1]), x, y);
+  return x + y;
+}
+
+__device__ __forceinline__ void publish(uint32_t at, const uint32_t (&w)[32], uint32_t bar) {
+  tmem_st32(at, w);
+  tmem_wait_st();
+  pa::tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) pa::mbar_arrive(bar);
+}
+
+// A row of a tile: TMEM lane and thread.
+struct Row {
+  int row, tk, token;  // of the tile, its token of the tile and of the sequence
+  bool live;
+  uint32_t lanes;      // of the warp, in a TMEM address
+};
+__device__ __forceinline__ Row row_of(const PromptParams &p, const Unit &u) {
+  const int warp = threadIdx.x >> 5;
+  Row r;
+  r.row = 32 * (warp & 3) + (threadIdx.x & 31);
+  r.tk = r.row / p.G;
+  r.token = u.tok(warp >> 2) + r.tk;
+  r.live = r.tk < p.tokens && r.token < u.len;
+  r.lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  return r;
+}
+
+// The weights of all blocks; m: what is subtracted from the scaled scores, in units of log2, l: the weights' sum.
+__device__ bool run_softmax(const PromptParams &p, const Unit &u, const Row &r, uint32_t bars, float &m, float &l) {
+  const int t = threadIdx.x >> 7, nb = u.nb(t);
+  const uint32_t s_at = r.lanes + 128 * t, o_at = r.lanes + 256 + 128 * t;
+  const int first = u.tok(t);
   const float c = p.fold;
-  float m = 0.f, l = 0.f;  // m: what is subtracted, in units of log2
-  bool ok = true;
+  m = -INFINITY;
+  l = 0.f;
   for (int j = 0; j < nb; ++j) {
-    ok = warp_wait(bars + 8 * (B_S + t), j & 1);
-    if (!ok) break;
+    if (!warp_wait(bars + 8 * (B_S + t), j & 1)) return false;
     pa::tc_fence_after();
     uint32_t s[kN];
 #pragma unroll
     for (int k = 0; k < kN; k += 32) tmem_ld32(s_at + k, s + k);
 #pragma unroll
     for (int k = 0; k < kN; k += 32) tmem_wait32(s + k);
-    if ((j + 1) * kN > first) {  // the diagonal may cut this block
-      const int seen = token - j * kN;
+    const int key0 = u.block(t, j) * kN;
+    if (key0 + kN > first) {  // the diagonal may cut this block
+      const int seen = r.token - key0;
 #pragma unroll
       for (int k = 0; k < kN; ++k) s[k] = k <= seen ? s[k] : 0xFF800000u;
     }
-    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int k = 0; k < kN; k += 4)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[k + e]));
-    const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+    uint32_t w[32];
+    const float peak = peak_of(s) * c;
     if (j == 0) {
       m = peak;
     } else {
@@ -440,89 +647,143 @@ __device__ void run_softmax(const PromptParams &p, const Unit &u, uint32_t bars,
         const float alpha = grown ? pa::fast_exp2(m - peak) : 1.f;
         if (grown) m = peak;
         l *= alpha;
-        ok = warp_wait(bars + 8 * (B_O + t), (j - 1) & 1);
-        if (!ok) break;
+        if (!warp_wait(bars + 8 * (B_O + t), (j - 1) & 1)) return false;
         pa::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kD; k += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_at + k, o);
-          tmem_wait32(o);
+          tmem_ld32(o_at + k, w);
+          tmem_wait32(w);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(o_at + k, o);
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+          tmem_st32(o_at + k, w);
         }
       }
     }
-    const pa::f32x2 c2 = pa::pack2(c, c), m2 = pa::pack2(-m, -m);
-    pa::f32x2 part[2] = {pa::pack2(0.f, 0.f), pa::pack2(0.f, 0.f)};
-#pragma unroll
-    for (int k = 0; k < kN; k += 64) {
-      uint32_t w[32];
-#pragma unroll
-      for (int e = 0; e < 64; e += 2) {
-        float a, b;
-        pa::unpack2(pa::fma2(pa::pack2(__uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1])), c2, m2), a, b);
-        a = pa::fast_exp2(a);
-        b = pa::fast_exp2(b);
-        part[(e >> 1) & 1] = pa::add2(part[(e >> 1) & 1], pa::pack2(a, b));
-        w[e >> 1] = pa::pack_bf16x2(a, b);
-      }
-      tmem_st32(s_at + (k >> 1), w);
-    }
-    float x0, x1;
-    pa::unpack2(pa::add2(part[0], part[1]), x0, x1);
-    l += x0 + x1;
-    tmem_wait_st();
-    pa::tc_fence_before();
-    __syncwarp();
-    if (lane == 0) pa::mbar_arrive(bars + 8 * (B_P + t));
+    l += weights(s, c, m, w);
+    publish(s_at, w, bars + 8 * (B_P + 2 * t));  // its product begins while the second half is worked out
+    l += weights(s + kN / 2, c, m, w);
+    publish(s_at + kN / 4, w, bars + 8 * (B_P + 2 * t + 1));
   }
-  if (ok && nb > 0) ok = warp_wait(bars + 8 * (B_O + t), (nb - 1) & 1);
-  if (ok && nb > 0) {
+  if (nb > 0 && !warp_wait(bars + 8 * (B_O + t), (nb - 1) & 1)) return false;
+  pa::tc_fence_after();
+  return true;
+}
+
+// The tile's rows: O / l and the log-sum-exp.  A solo tile's O is the sum of both slots', which lie in the same lanes of TMEM: each
+// slot's warps join half of its columns.
+__device__ void write_tile(const PromptParams &p, const Unit &u, const Row &r, float m, float l, uint8_t *smem) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = warp >> 2, hq = p.Hkv * p.G;
+  const int first = u.tok(t);
+  const uint32_t o_at = r.lanes + 256 + (u.solo ? 0 : 128 * t);
+  float mine = 1.f, others = 0.f;  // what O of slot 0 (or of the tile's own) and that of slot 1 count
+  if (u.solo) {
+    float *ms = reinterpret_cast<float *>(smem + kBothM), *ls = reinterpret_cast<float *>(smem + kBothL);
+    ms[t * kM + r.row] = m;
+    ls[t * kM + r.row] = l;
+    asm volatile("bar.sync 4, 256;" ::: "memory");
     pa::tc_fence_after();
-    const uint32_t dirty = *reinterpret_cast<const volatile uint32_t *>(smem + kMisc + 4);
-    const int64_t at = (int64_t)(u.row0 + token) * (p.Hkv * p.G) + u.h * p.G + (row - tk * p.G);
-    const float inv = 1.f / l;
-    if (live && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
-#pragma unroll
-    for (int k = 0; k < kD; k += 32) {
+    const float m0 = ms[r.row], m1 = ms[kM + r.row];
+    m = fmaxf(m0, m1);
+    mine = pa::fast_exp2(m0 - m);
+    others = pa::fast_exp2(m1 - m);
+    l = ls[r.row] * mine + ls[kM + r.row] * others;
+  }
+  const uint32_t dirty = *reinterpret_cast<const volatile uint32_t *>(smem + kMisc + 4);
+  const int64_t at = (int64_t)(u.row0 + r.token) * hq + u.h * p.G + (r.row - r.tk * p.G);
+  const bool writes = r.live && !(u.solo && t == 1);  // a row's lse, and what else is one thread's
+  if (writes && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
+  mine /= l;
+  others /= l;
+  // Through the tile's queries' place in shared memory (its last S is complete), as the tensor map has it: two halves of 128
+  // bytes a row, in 128-byte swizzle.  Stored from the lanes, row by row, each store took 32 cycles and a tile 4000.
+  uint8_t *rows = smem + (u.solo ? 0 : t * kOperand);
+  const bool whole = !p.out_f32 && first + p.tokens <= u.len;  // else the tile's box reaches past the sequence
+  const int size = p.out_f32 ? 4 : 2, cols = 256 / size;
+  auto together = [&]() {  // the warps that write the tile
+    if (u.solo)
+      asm volatile("bar.sync 4, 256;" ::: "memory");
+    else
+      asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
+  };
+#pragma unroll 1
+  for (int k0 = 0; k0 < kD; k0 += cols) {
+    const int from = u.solo ? k0 + t * (cols / 2) : k0, to = u.solo ? from + cols / 2 : k0 + cols;
+#pragma unroll 1
+    for (int k = from; k < to; k += 32) {
       uint32_t o[32];
       tmem_ld32(o_at + k, o);
-      tmem_wait32(o);
+      if (u.solo) {
+        uint32_t x[32];
+        tmem_ld32(o_at + 128 + k, x);
+        tmem_wait32(x);
+        tmem_wait32(o);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-      if (dirty != 0 && live) {  // infinities and NaN among the values that were replaced by 0
-        for (int j = u.cut; j < nb; ++j) {
-          if (!(dirty >> (j - u.cut) & 1u)) continue;
-          for (int i = j * kN; i <= token && i < (j + 1) * kN; ++i) {
-            const uint16_t *v = p.v + (int64_t)(u.row0 + i) * p.v_stride + u.h * kD + k;
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), mine, __uint_as_float(x[e]) * others));
+      } else {
+        tmem_wait32(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (not_finite(v[e])) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float((uint32_t)v[e] << 16));
-          }
-        }
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mine);
       }
-      if (live) {
-        if (p.out_f32) {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at * kD + k);
+      const int piece = (k - k0) * size / 16;  // of the row's 16
+      if (p.out_f32) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else {
-          uint32_t w[16];
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4 *>(rows + (piece >> 3) * (kOperand / 2) + r.row * 128 + ((e ^ (r.row & 7)) << 4)) =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = pa::pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at * kD + k);
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          for (int i = 0; i < 4; ++i) w[i] = pa::pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]), __uint_as_float(o[8 * e + 2 * i + 1]));
+          *reinterpret_cast<uint4 *>(rows + (piece >> 3) * (kOperand / 2) + r.row * 128 + ((((piece & 7) + e) ^ (r.row & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
+    if (whole) {
+      pa::fence_async_smem();
+      together();
+      if (warp == (u.solo ? 0 : 4 * t) && pa::elect_one()) {
+        for (int x = 0; x < 2; ++x) tma_store_3d(&p.tm_o, pa::smem_u32(rows) + x * (kOperand / 2), 64 * x, u.h * p.G, u.row0 + first);
+        bulk_store_wait();
+      }
+    } else {  // whole rows to half a warp: of the warp's own 32, or (solo) half of them, which both slots have written
+      const int where = r.live ? r.tk * hq + r.row - r.tk * p.G : -1;  // from the tile's first row and head
+      const int64_t origin = (int64_t)(u.row0 + first) * hq + u.h * p.G;
+      const int begin = u.solo ? 16 * t : 0, end = u.solo ? begin + 16 : 32;
+      if (u.solo)
+        together();
+      else
+        __syncwarp();
+#pragma unroll 4
+      for (int q0 = begin; q0 < end; q0 += 2) {
+        const int q = q0 + (lane >> 4), dst = __shfl_sync(~0u, where, q), row = 32 * (warp & 3) + q, l16 = lane & 15;
+        const uint4 v = *reinterpret_cast<const uint4 *>(rows + (l16 >> 3) * (kOperand / 2) + row * 128 + (((l16 & 7) ^ (row & 7)) << 4));
+        if (dst >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + ((origin + dst) * kD + k0) * size + l16 * 16) = v;
+      }
+      if (u.solo)
+        together();
+      else
+        __syncwarp();
+    }
   }
-  if (!ok && lane == 0) raise(p, PA_DEV_TIMEOUT);
-  pa::tc_fence_before();
-  __syncwarp();
-  if (lane == 0) pa::mbar_arrive(bars + 8 * B_DONE);
+  if (dirty != 0) {
+    together();  // the tile has been written
+    if (writes)
+      add_not_finite(p.v + u.row0 * p.v_stride + u.h * kD, p.v_stride, static_cast<uint8_t *>(p.out) + at * kD * size, p.out_f32, dirty,
+                     u.cut, r.token);
+  }
+}
+
+// Whether none of the warps that write a tile together gave up: they write it, or none of them does.
+__device__ __forceinline__ bool agreed(bool ok, bool solo, int t) {
+  int r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"((int)ok), "r"(solo ? 4 : 2 + t), "r"(solo ? 256 : 128)
+               : "memory");
+  return r != 0;
 }
 
 // KS: sequences per thread in the schedule.
@@ -531,43 +792,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t *smem = raw + ((1024u - (pa::smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = pa::smem_u32(smem), bars = base + kBars;
-  const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
+  // (from lane 0, so that the roles' control flow and the MMAs' operands are known to be uniform: 650 us, else 620, for
+  // 16384 tokens x 16 heads)
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  if (warp == kLoadWarp && (threadIdx.x & 31) == 0) {
+    prefetch_map(&p.tm_q);
+    prefetch_map(&p.tm_k);
+    prefetch_map(&p.tm_v);
     for (int i = 0; i < kNumBars; ++i) {
-      const bool soft = i == B_P || i == B_P + 1;
-      pa::mbar_init(bars + 8 * i, soft ? 4 : i == B_CLEAN || i == B_CLEAN + 1 ? 2 : i == B_DONE ? kSoftWarps : 1);
+      pa::mbar_init(bars + 8 * i, i >= B_P && i < B_P + 4 ? 4 : i == B_DONE ? kSoftWarps : i >= B_CLEAN && i < B_CLEAN + 2 ? 2 : 1);
     }
     *reinterpret_cast<uint32_t *>(smem + kMisc + 4) = 0;
     pa::fence_barrier_init();
   }
+  if (warp == kMmaWarp) pa::tmem_alloc(base + kMisc, kTmemCols);
   pa::pdl_wait();
   pa::pdl_launch_dependents();
   Unit u;
-  const int x = p.Hkv == 1 ? blockIdx.x : blockIdx.x / p.Hkv;
-  if (!locate<KS>(p, x, smem, u)) return;
-  u.h = (int)blockIdx.x - x * p.Hkv;
-  if (warp == 9) pa::tmem_alloc(base + kMisc, kTmemCols);
+  const bool some = locate<KS>(p, smem, u);
+  // The load warp, which initialised the barriers and needs nothing of the others, goes ahead.
   pa::tc_fence_before();
-  __syncthreads();
+  if (warp == kLoadWarp)
+    asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+  else
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
   pa::tc_fence_after();
-  const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(smem + kMisc);
+  if (!some) {
+    if (warp == kMmaWarp) pa::tmem_dealloc(0, kTmemCols);
+    return;
+  }
   if (warp < kSoftWarps) {
     pa::regs_inc<216>();
-    run_softmax(p, u, bars, tm, smem);
+    const Row r = row_of(p, u);
+    const int t = warp >> 2;
+    float m, l;
+    const bool ok = run_softmax(p, u, r, bars, m, l);
+    if (!ok && (threadIdx.x & 31) == 0) raise(p, PA_DEV_TIMEOUT);
+    if (agreed(ok, u.solo, t) && u.nb(t) > 0) write_tile(p, u, r, m, l, smem);
+    pa::tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) pa::mbar_arrive(bars + 8 * B_DONE);
   } else {
     pa::regs_dec<72>();
-    if (warp == 8)
+    if (warp == kLoadWarp)
       run_producer(p, u, base, bars);
-    else if (warp == 9)
-      run_mma(p, u, base, bars, tm);
+    else if (warp == kMmaWarp)
+      run_mma(p, u, base, bars);
     else
-      run_clean(p, u, base, bars, smem);
+      run_clean(p, u, bars, smem);
+    if (warp == kMmaWarp) {
+      if (!warp_wait(bars + 8 * B_DONE, 0) && (threadIdx.x & 31) == 0) raise(p, PA_DEV_TIMEOUT);
+      pa::tc_fence_after();
+      pa::tmem_dealloc(0, kTmemCols);
+    }
   }
 }
 
 // ------------------------------------------------------------------------------- host
 
 struct PromptDevice {
+  int sms = 0;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
@@ -582,7 +866,8 @@ const PromptDevice *prompt_device() {
     PromptDevice d;
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult res;
-    for (const void *f : {(const void *)prompt_attn_kernel<1>, (const void *)prompt_attn_kernel<11>}) {
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return;
+    for (const void *f : {(const void *)prompt_attn_kernel<0>, (const void *)prompt_attn_kernel<1>, (const void *)prompt_attn_kernel<11>}) {
       cudaFuncAttributes at;
       if (cudaFuncGetAttributes(&at, f) != cudaSuccess || at.numRegs != kRegs ||
           cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
@@ -652,14 +937,19 @@ extern "C" pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *a, void *stre
   p.tokens = kM / a->group_size;
   p.out_f32 = a->out_dtype == PA_OUT_F32;
   p.fold = (float)((double)a->sm_scale * 1.4426950408889634);
+  p.sms = dev->sms;
   if (!encode_rows(dev, &p.tm_q, a->q, a->num_rows, heads, a->q_stride, p.G, p.tokens) ||
       !encode_rows(dev, &p.tm_k, a->k, a->num_rows, a->num_kv_heads, a->k_stride, 1, kN) ||
-      !encode_rows(dev, &p.tm_v, a->v, a->num_rows, a->num_kv_heads, a->v_stride, 1, kN))
+      !encode_rows(dev, &p.tm_v, a->v, a->num_rows, a->num_kv_heads, a->v_stride, 1, kN) ||
+      !encode_rows(dev, &p.tm_o, a->out, a->num_rows, heads, q_row, p.G, p.tokens))
     return PA_ERR_CUDA;
-  // as many CTAs as there can be units: those without one exit
-  const int64_t span = 2 * p.tokens, units = (n + a->num_seqs * (span - 1)) / span;
-  const pa_host::Launch run(dim3((unsigned)(units * a->num_kv_heads)), dim3(kThreads), kSmem, stream);
-  const cudaError_t e = a->num_seqs <= kThreads ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1>, p)
-                                                : cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<11>, p);
+  // As many CTAs as there can be units, and where that is fewer than SMs as many as they may be split into: those without
+  // a share exit.
+  const int64_t span = 2 * p.tokens, units = (n + a->num_seqs * (span - 1)) / span * a->num_kv_heads;
+  const int64_t grid = units >= dev->sms ? units : std::min<int64_t>(2 * units, dev->sms);
+  const pa_host::Launch run(dim3((unsigned)grid), dim3(kThreads), kSmem, stream);
+  const cudaError_t e = a->num_seqs <= 32         ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<0>, p)
+                        : a->num_seqs <= kThreads ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1>, p)
+                                                  : cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<11>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
