@@ -46,7 +46,7 @@ constexpr int kMaxGroup = 64;
 constexpr int kMaxRows = 1 << 24;
 constexpr int kOperand = kM * kD * 2;  // bytes of a tile or block: two halves of 64 elements a row
 constexpr int kStages = 5;
-constexpr int kMinSplit = 3;      // blocks that a unit has more than to be split into its tiles
+constexpr int kMinSplit = 1;      // blocks that a unit has more than to be split into its tiles (3: 512 tokens x 16 heads 9.9 us, not 8.9)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;     // log2 of what the weights may exceed 1 by
 
@@ -201,7 +201,10 @@ __device__ __forceinline__ int reduce_all(int v, bool most, int *red, int turn) 
 // (x - N(c + 1))-th of the sequences that have such a unit.  False if there are fewer units.
 // KS 0: up to 32 sequences, a lane each, every warp by itself.  Else KS sequences per thread of the CTA, which is synchronised.
 // While there are SMs without a unit the longest units are split into their two tiles, a CTA each, which takes half the time: its
-// keys are dealt to both slots (2048 tokens x 16 heads: SOLO us, 26.3 without; 1024: SOLO2, 15.8).
+// keys are dealt to both slots.  So many more may be split that the shortest units come last, to the SMs that are done first: of units
+// of 1, 2, ... n times the same keys, s = (2 SMs - units - what a CTA takes beside its keys, about 4 blocks) / 3 makes the longest
+// whole one and two short ones in turn take the same time.  Not more of them than there are units below a third of the longest's
+// index.  (2048 tokens x 16 heads: 22.6 us, 24.1 with as many as there are idle SMs, 26.5 without; 1024: 12.5, 15.8 without.)
 template <int KS>
 __device__ bool locate(const PromptParams &p, uint8_t *smem, Unit &u) {
   constexpr int kOwn = KS > 0 ? KS : 1;
@@ -236,12 +239,18 @@ __device__ bool locate(const PromptParams &p, uint8_t *smem, Unit &u) {
   const int total = reduce(sum, false);
   const int units = total * p.Hkv;
   int x = (int)blockIdx.x, tile = -1;
-  if (units < p.sms) {
-    const int first = (kMinSplit * kN + span - 1) / span;  // units with more than kMinSplit blocks
-    int longer = 0;
+  if (units < 2 * p.sms) {
+    const int first = (kMinSplit * kN + span - 1) / span, few = reduce(top, true) / 3;
+    int longer = 0, rest = 0;  // units that may be split; all but the shortest
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) longer += max(0, n[i] - first);
-    const int splits = min(reduce(longer, false) * p.Hkv, p.sms - units);
+    for (int i = 0; i < kOwn; ++i) {
+      longer += max(0, n[i] - first);
+      rest += max(0, n[i] - few);
+    }
+    longer = reduce(longer, false) * p.Hkv;
+    rest = reduce(rest, false) * p.Hkv;
+    const int idle = p.sms - units, even = (p.sms + idle - 4 * kN * p.Hkv / span) / 3;
+    const int splits = max(0, min(min(longer, max(idle, min(even, p.sms - rest))), (int)gridDim.x - units));
     tile = x < 2 * splits ? x & 1 : -1;
     x = x < 2 * splits ? x >> 1 : x - splits;
   }
@@ -943,10 +952,9 @@ extern "C" pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *a, void *stre
       !encode_rows(dev, &p.tm_v, a->v, a->num_rows, a->num_kv_heads, a->v_stride, 1, kN) ||
       !encode_rows(dev, &p.tm_o, a->out, a->num_rows, heads, q_row, p.G, p.tokens))
     return PA_ERR_CUDA;
-  // As many CTAs as there can be units, and where that is fewer than SMs as many as they may be split into: those without
-  // a share exit.
+  // As many CTAs as there can be units, and where those are few as they may be split into: those without a share exit.
   const int64_t span = 2 * p.tokens, units = (n + a->num_seqs * (span - 1)) / span * a->num_kv_heads;
-  const int64_t grid = units >= dev->sms ? units : std::min<int64_t>(2 * units, dev->sms);
+  const int64_t grid = units < 2 * dev->sms ? 2 * units : units;
   const pa_host::Launch run(dim3((unsigned)grid), dim3(kThreads), kSmem, stream);
   const cudaError_t e = a->num_seqs <= 32         ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<0>, p)
                         : a->num_seqs <= kThreads ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1>, p)
