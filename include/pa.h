@@ -639,8 +639,8 @@ typedef struct pa_page_assign_args {
  * is 0 (PA_DEV_BAD_QLEN).  num_free is taken as within 0 .. free_capacity.  A page outside [0, num_pages), off the stack or in
  * the table, gives its rows slot -1 (PA_DEV_BAD_PAGE); off the stack it is entered as it stands, and the decode flags it again.
  * Outputs share no byte with each other or with an input, but for the two pairs above at the same address.
- * One kernel launch on `stream`, none where there is nothing to write (no requests, no rows, num_free_out at num_free; pointers to
- * nothing may be NULL); no host synchronisation, no allocation.  A pa_decode on a plan without PA_PLAN_NO_PDL
+ * One kernel launch on `stream`, two for more than 16384 rows with lengths or count updated in place, none where there is nothing to
+ * write (no requests, no rows, num_free_out at num_free; pointers to nothing may be NULL); no host synchronisation, no allocation.  A pa_decode on a plan without PA_PLAN_NO_PDL
  * reads new_lens and block_table before the kernel enqueued just before it has completed: another kernel that is no decode
  * has to lie between (pa_rope and pa_kv_quantize_write do).  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap,
  * PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for another page size, PA_ERR_CUDA when the launch fails. */
@@ -670,8 +670,8 @@ typedef struct pa_page_release_args {
  * pass free_capacity, those that have pages to give back keep them (PA_DEV_PAGE_POOL: such a pool has been given a page twice).  A request with a
  * negative length or a context beyond the table gives none back (PA_DEV_BAD_CONTEXT).  A page outside [0, num_pages) goes on
  * the stack as it stands and is flagged (PA_DEV_BAD_PAGE).  num_free is taken as within 0 .. free_capacity.  Outputs share no byte with each
- * other or with an input, but for num_free_out at num_free.  One kernel launch on `stream`, none without requests and with
- * num_free_out at num_free; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer,
+ * other or with an input, but for num_free_out at num_free.  One kernel launch on `stream`, two where more than 16384 pages could be
+ * given back (by the table's and the stack's sizes) and num_free_out is num_free, none without requests and with num_free_out at num_free; no host synchronisation, no allocation.  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer,
  * PA_ERR_UNSUPPORTED for another page size, PA_ERR_CUDA when the launch fails. */
 pa_status_t pa_page_release(const pa_page_release_args_t *args, void *stream);
 

@@ -2,11 +2,10 @@
 // pa_page_assign and pa_page_release.  See include/pa.h for the contract.
 //
 // Both are a prefix sum over the requests' pages followed by work per row (a slot, a position and, where the
-// row opens a page, a table entry) or per page.  Each runs as one cluster: every CTA scans all the
-// requests by itself, which costs less than an exchange, and takes its share of the rows.  A single cluster, since
-// the lengths and the count of free pages may be updated in place: every CTA has read them once the
-// cluster's barrier is through, and only then are they written.  More clusters would need a counter in
-// memory, which the caller would have to keep.
+// row opens a page, a table entry) or per page.  Every CTA scans all the requests by itself, which costs less than an
+// exchange, and takes its share of the rows.  The lengths and the count of free pages may be updated in place, so no CTA may write
+// them before all have read them.  Few rows: one cluster, whose barrier tells.  Many rows: CTAs all over the GPU, and a second
+// launch of one CTA for what is updated in place (WIDE: 32 x 8192 tokens 16.2 us in one cluster, WIDE_US here).
 //
 // Bound by latency: 12 bytes per row, and a chain of lengths -> scan -> page -> slot.
 #include <cuda_runtime.h>
@@ -31,6 +30,7 @@ struct AssignParams {
   int64_t *slots;
   uint32_t *status;
   int32_t num_pages, B, rows, bt_stride, shift, capacity;
+  int32_t write_rows;  // 0: lengths and count alone; those are left to another launch where new_lens is NULL
 };
 
 struct ReleaseParams {
@@ -38,6 +38,20 @@ struct ReleaseParams {
   int32_t *free_pages, *num_free_out;
   uint32_t *status;
   int32_t num_pages, B, bt_stride, shift, capacity;
+  int32_t write_pages;  // 0: the count alone, which is left to another launch where num_free_out is NULL
+};
+
+// This CTA's place among those that share the work: of a cluster, whose barrier they pass when they have read what may be
+// updated in place, or of the grid.
+template <bool WIDE>
+struct Team {
+  int rank = (int)blockIdx.x, ranks = (int)gridDim.x;  // (a cluster is the whole grid)
+  __device__ __forceinline__ void have_read() {
+    if constexpr (!WIDE) pa::cluster_arrive();
+  }
+  __device__ __forceinline__ void all_have_read() {
+    if constexpr (!WIDE) pa::cluster_wait();
+  }
 };
 
 __device__ __forceinline__ void raise(uint32_t *status, uint32_t flags) {
@@ -81,12 +95,12 @@ __device__ __forceinline__ int find(const int32_t *at, int n, int x) {
 }
 
 // R rows per thread and step, 32 apart: R independent chains in flight.
-template <int R>
+template <int R, bool WIDE>
 __global__ void __launch_bounds__(kMaxThreads) page_assign_kernel(const __grid_constant__ AssignParams p) {
   __shared__ int64_t sums[kMaxThreads / 32];
   __shared__ int32_t cu_s[kMaxThreads + 1], len_s[kMaxThreads], have_s[kMaxThreads], base_s[kMaxThreads];
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
-  const int ranks = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
+  Team<WIDE> team;
   pa::pdl_wait();
   pa::pdl_launch_dependents();
   const int stack = min(max(*p.num_free, 0), p.capacity);
@@ -130,17 +144,17 @@ __global__ void __launch_bounds__(kMaxThreads) page_assign_kernel(const __grid_c
     const bool served = good && (need == 0 || upto <= stack);
     if (good && !served) flags |= PA_DEV_PAGE_POOL;
     if (tid < n) base_s[tid] = served ? (need == 0 ? 0 : (int)(upto - need)) : -1;
-    pa::cluster_arrive();  // this chunk's lengths have been read
+    team.have_read();  // this chunk's lengths
     // what was taken: the last of those served (they are the first of those that asked)
     taken = max(taken, __reduce_max_sync(~0u, served && need > 0 ? (int)upto : 0));
     run += all;
     __syncthreads();
 
     const bool last = r0 + threads >= p.B;
-    const int lo = r0 == 0 || !ascends ? 0 : cu_s[0], hi = last || !ascends ? p.rows : cu_s[n];
-    const int strip = 32 * R, warps = ranks * (threads >> 5);
+    const int lo = r0 == 0 || !ascends ? 0 : cu_s[0], hi = p.write_rows == 0 ? 0 : last || !ascends ? p.rows : cu_s[n];
+    const int strip = 32 * R, warps = team.ranks * (threads >> 5);
     // (64 bits: the last strip may pass 2^31)
-    for (int64_t s = lo + (int64_t)strip * (rank * (threads >> 5) + (tid >> 5)); s < hi && (ascends || r0 == 0);
+    for (int64_t s = lo + (int64_t)strip * (team.rank * (threads >> 5) + (tid >> 5)); s < hi && (ascends || r0 == 0);
          s += (int64_t)strip * warps) {
       int j[R], id[R], at[R];
       bool opens[R];
@@ -178,13 +192,13 @@ __global__ void __launch_bounds__(kMaxThreads) page_assign_kernel(const __grid_c
         if (p.pos != nullptr) p.pos[row] = at[k];
       }
     }
-    pa::cluster_wait();  // every CTA has read this chunk's lengths (and the count of free pages)
-    if (rank == 0 && tid < n) p.new_lens[r] = served ? L + (cu_s[tid + 1] - cu_s[tid]) : L;
+    team.all_have_read();  // this chunk's lengths, and the count of free pages
+    if (team.rank == 0 && tid < n && p.new_lens != nullptr) p.new_lens[r] = served ? L + (cu_s[tid + 1] - cu_s[tid]) : L;
     __syncthreads();  // the chunk's arrays have been read
     r0 += threads;
   } while (r0 < p.B);
 
-  if (rank == 0) {
+  if (team.rank == 0 && p.num_free_out != nullptr) {
     __shared__ int32_t most;
     if (tid == 0) most = 0;
     __syncthreads();
@@ -196,17 +210,17 @@ __global__ void __launch_bounds__(kMaxThreads) page_assign_kernel(const __grid_c
   if (lane == 0) raise(p.status, flags);
 }
 
-template <int R>
+template <int R, bool WIDE>
 __global__ void __launch_bounds__(kMaxThreads) page_release_kernel(const __grid_constant__ ReleaseParams p) {
   __shared__ int64_t sums[kMaxThreads / 32];
   __shared__ int32_t from_s[kMaxThreads + 1], col_s[kMaxThreads];
   __shared__ int32_t most;
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
-  const int ranks = (int)pa::cluster_ctas(), rank = (int)pa::cluster_rank();
+  Team<WIDE> team;
   pa::pdl_wait();
   pa::pdl_launch_dependents();
   const int stack = min(max(*p.num_free, 0), p.capacity), room = p.capacity - stack;
-  pa::cluster_arrive();
+  team.have_read();
   uint32_t flags = 0;
   int64_t run = 0;  // pages of the requests so far
   int given = 0;
@@ -237,9 +251,9 @@ __global__ void __launch_bounds__(kMaxThreads) page_release_kernel(const __grid_
       col_s[tid] = col;
     }
     __syncthreads();
-    const int end = most;
-    const int strip = 32 * R, warps = ranks * (threads >> 5);
-    for (int64_t s = given + (int64_t)strip * (rank * (threads >> 5) + (tid >> 5)); s < end; s += (int64_t)strip * warps) {
+    const int end = most;  // (in pages; those of this chunk begin at `given`)
+    const int strip = 32 * R, warps = team.ranks * (threads >> 5);
+    for (int64_t s = given + (int64_t)strip * (team.rank * (threads >> 5) + (tid >> 5)); s < end && p.write_pages != 0; s += (int64_t)strip * warps) {
       int id[R];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
@@ -261,31 +275,38 @@ __global__ void __launch_bounds__(kMaxThreads) page_release_kernel(const __grid_
     run += all;
     __syncthreads();  // the chunk's arrays have been read
   }
-  pa::cluster_wait();  // every CTA has read the count of free pages
-  if (rank == 0 && tid == 0) *p.num_free_out = stack + given;
+  team.all_have_read();  // the count of free pages
+  if (team.rank == 0 && tid == 0 && p.num_free_out != nullptr) *p.num_free_out = stack + given;
   flags = __reduce_or_sync(~0u, flags);
   if (lane == 0) raise(p.status, flags);
 }
 
-// The kernels' opt-in to clusters of 16, once per device.
-bool paging_device() {
-  static int8_t known[pa_host::kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= pa_host::kMaxDevices) return false;
-  if (known[dev]) return true;
-  for (const void *f : {(const void *)page_assign_kernel<1>, (const void *)page_assign_kernel<4>,
-                        (const void *)page_release_kernel<1>, (const void *)page_release_kernel<4>})
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
-  known[dev] = 1;
-  return true;
+// The current device's SM count, looked up with the kernels' opt-in to clusters of 16 once per device; 0 if a call fails.
+int paging_device() {
+  static int known[pa_host::kMaxDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= pa_host::kMaxDevices) return 0;
+  if (known[dev] > 0) return known[dev];
+  for (const void *f : {(const void *)page_assign_kernel<1, false>, (const void *)page_assign_kernel<4, false>,
+                        (const void *)page_release_kernel<1, false>, (const void *)page_release_kernel<4, false>})
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  known[dev] = sms;
+  return sms;
 }
 
-// Threads per CTA, CTAs per cluster and items per thread for `items` rows or pages of `seqs` requests.
+// CTAs, threads of each and items per thread for `items` rows or pages of `seqs` requests.
 struct Shape {
-  int threads, ctas, each;
+  int ctas, threads, each;
+  bool wide;
 };
-Shape shape_of(int64_t items, int64_t seqs) {
-  Shape s{kMaxThreads, 1, 1};
+constexpr int64_t kWide = 16384;  // more items than this go to the whole GPU
+Shape shape_of(int64_t items, int64_t seqs, int sms) {
+  Shape s{1, kMaxThreads, 1, false};
+  if (items > kWide) {
+    const int64_t ctas = (items + 2047) / 2048;
+    return Shape{(int)(ctas < 2 * sms ? ctas : 2 * sms), 512, 4, true};
+  }
   const int64_t most = items > seqs ? items : seqs;
   if (most <= 512) {
     s.threads = most <= 128 ? 128 : 512;
@@ -294,6 +315,12 @@ Shape shape_of(int64_t items, int64_t seqs) {
   while (s.ctas < kMaxCluster && (int64_t)s.ctas * kMaxThreads < items) s.ctas *= 2;
   if (items > (int64_t)s.ctas * kMaxThreads) s.each = 4;
   return s;
+}
+
+template <typename P>
+cudaError_t launch(void (*one)(P), void (*four)(P), void (*wide)(P), const Shape &s, const P &p, void *stream) {
+  const pa_host::Launch run(dim3((unsigned)s.ctas), dim3((unsigned)s.threads), 0, stream, s.wide ? 0 : s.ctas);
+  return cudaLaunchKernelEx(run.cfg(), s.wide ? wide : s.each == 1 ? one : four, p);
 }
 
 }  // namespace
@@ -323,7 +350,8 @@ extern "C" pa_status_t pa_page_assign(const pa_page_assign_args_t *a, void *stre
       pa_host::overlaps(slots, {L, cu, pages, count, pos}) || pa_host::overlaps(pos, {L, cu, pages, count}))
     return PA_ERR_INVALID_ARG;
   if (a->num_seqs == 0 && a->num_rows == 0 && a->num_free_out == a->num_free) return PA_OK;
-  if (!paging_device()) return PA_ERR_CUDA;
+  const int sms = paging_device();
+  if (sms < 1) return PA_ERR_CUDA;
   AssignParams p;
   p.L = a->context_lens;
   p.cu = a->cu_seqlens_q;
@@ -341,10 +369,20 @@ extern "C" pa_status_t pa_page_assign(const pa_page_assign_args_t *a, void *stre
   p.bt_stride = a->block_table_stride;
   p.shift = pa_host::log2_page(a->page_size);
   p.capacity = a->free_capacity;
-  const Shape s = shape_of(a->num_rows, a->num_seqs);
-  const pa_host::Launch run(dim3((unsigned)s.ctas), dim3((unsigned)s.threads), 0, stream, s.ctas);
-  const cudaError_t e = s.each == 1 ? cudaLaunchKernelEx(run.cfg(), page_assign_kernel<1>, p)
-                                    : cudaLaunchKernelEx(run.cfg(), page_assign_kernel<4>, p);
+  p.write_rows = 1;
+  const Shape s = shape_of(a->num_rows, a->num_seqs, sms);
+  const bool later = s.wide && (a->num_free_out == a->num_free || a->new_lens == a->context_lens);  // no cluster: a launch of its own
+  if (later) {
+    p.new_lens = nullptr;
+    p.num_free_out = nullptr;
+  }
+  cudaError_t e = launch(page_assign_kernel<1, false>, page_assign_kernel<4, false>, page_assign_kernel<4, true>, s, p, stream);
+  if (later && e == cudaSuccess) {
+    p.new_lens = a->new_lens;
+    p.num_free_out = a->num_free_out;
+    p.write_rows = 0;
+    e = launch(page_assign_kernel<1, false>, page_assign_kernel<4, false>, page_assign_kernel<4, true>, shape_of(0, a->num_seqs, sms), p, stream);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -368,7 +406,8 @@ extern "C" pa_status_t pa_page_release(const pa_page_release_args_t *a, void *st
       pa_host::overlaps(left, {a->num_free_out == a->num_free ? none : count, L, grown, table}))
     return PA_ERR_INVALID_ARG;
   if (a->num_seqs == 0 && a->num_free_out == a->num_free) return PA_OK;
-  if (!paging_device()) return PA_ERR_CUDA;
+  const int sms = paging_device();
+  if (sms < 1) return PA_ERR_CUDA;
   ReleaseParams p;
   p.L = a->context_lens;
   p.new_lens = a->new_lens;
@@ -384,9 +423,15 @@ extern "C" pa_status_t pa_page_release(const pa_page_release_args_t *a, void *st
   p.capacity = a->free_capacity;
   // how many pages come back is not known here: what the tables and the stack can hold
   const int64_t table_pages = (int64_t)a->num_seqs * a->block_table_stride;
-  const Shape s = shape_of(table_pages < a->free_capacity ? table_pages : a->free_capacity, a->num_seqs);
-  const pa_host::Launch run(dim3((unsigned)s.ctas), dim3((unsigned)s.threads), 0, stream, s.ctas);
-  const cudaError_t e = s.each == 1 ? cudaLaunchKernelEx(run.cfg(), page_release_kernel<1>, p)
-                                    : cudaLaunchKernelEx(run.cfg(), page_release_kernel<4>, p);
+  p.write_pages = 1;
+  const Shape s = shape_of(table_pages < a->free_capacity ? table_pages : a->free_capacity, a->num_seqs, sms);
+  const bool later = s.wide && a->num_free_out == a->num_free;
+  if (later) p.num_free_out = nullptr;
+  cudaError_t e = launch(page_release_kernel<1, false>, page_release_kernel<4, false>, page_release_kernel<4, true>, s, p, stream);
+  if (later && e == cudaSuccess) {
+    p.num_free_out = a->num_free_out;
+    p.write_pages = 0;
+    e = launch(page_release_kernel<1, false>, page_release_kernel<4, false>, page_release_kernel<4, true>, shape_of(0, a->num_seqs, sms), p, stream);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

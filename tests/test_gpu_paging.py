@@ -80,6 +80,24 @@ def test_assign_prompts(reqs, q, page):
         _assign(*_case(rng, lens, ql, page, room, 5), page)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("reqs,q,page", [(1, 16384, 16), (1, 16385, 16), (700, 24, 64), (2500, 11, 16), (5, 60001, 128)])
+def test_assign_about_the_rows_of_one_cluster(reqs, q, page, in_place):
+    rng = np.random.default_rng(q + page)
+    lens = rng.integers(0, 70, size=reqs)
+    ql = np.full(reqs, q) if reqs == 1 else q + rng.integers(-10, 11, size=reqs)
+    for room in (None, 0.6):
+        _assign(*_case(rng, lens, ql, page, room, 3), page, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_assign_many_rows_of_which_none_is_served(in_place):
+    rng = np.random.default_rng(12)
+    lens, cu, table, free, left, pages, rows = _case(rng, [3, 5], [20000, 9000], 16, None, 2)
+    cu[1] = 31000
+    assert _assign(lens, cu, table, free, left, pages, rows, 16, in_place) == 0x4
+
+
 def test_assign_takes_lower_positions_from_the_top():
     lens, cu, table, free = np.array([15], np.int32), np.array([0, 40], np.int32), np.full((1, 4), 0, np.int32), np.array([4, 5, 6, 1], np.int32)
     d = dev(table)
