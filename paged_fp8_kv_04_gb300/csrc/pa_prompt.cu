@@ -45,7 +45,11 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxRows = 1 << 24;
 constexpr int kOperand = kM * kD * 2;  // bytes of a tile or block: two halves of 64 elements a row
-constexpr int kStages = 5;
+constexpr int kMaxStages = 5;     // blocks of keys and values in flight
+// One unit to a CTA: five.  CTAs that go on with further units: four, and room for outputs on their way while the next unit's
+// queries come in.
+template <bool LOOP>
+constexpr int kStages = LOOP ? 4 : kMaxStages;
 constexpr int kMinSplit = 1;      // blocks that a unit has more than to be split into its tiles (3: 512 tokens x 16 heads 9.9 us, not 8.9)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;     // log2 of what the weights may exceed 1 by
@@ -65,28 +69,37 @@ struct PromptParams {
   float fold;  // sm_scale * log2 e
 };
 
-// Shared memory: two query tiles, the ring of K and V blocks, barriers and the schedule's scratch.
-constexpr int kRing = 2 * kOperand;
-constexpr int kBars = kRing + kStages * kOperand;
+// Shared memory: two query tiles, the ring of K and V blocks (and with LOOP 16 KB of either tile's output), barriers and the
+// schedule's scratch.
+constexpr int kRing = 2 * kOperand, kOut = kRing + kStages<true> * kOperand;
+constexpr int kBars = kRing + kMaxStages * kOperand;
+static_assert(kOut + kOperand <= kBars, "the outputs on their way lie in place of a stage");
 enum {
-  B_QFULL = 0,                      // [2] the tile's queries
-  B_FULL = 2,                       // [kStages]
-  B_EMPTY = B_FULL + kStages,       // [kStages]
-  B_S = B_EMPTY + kStages,          // [2] S is complete
+  B_QFULL = 0,                      // [2] the tile's queries have landed
+  B_QFREE = B_QFULL + 2,            // [2] the tile's last S is complete
+  B_FULL = B_QFREE + 2,             // [stages]
+  B_EMPTY = B_FULL + kMaxStages,    // [stages]
+  B_S = B_EMPTY + kMaxStages,       // [2] S is complete
   B_P = B_S + 2,                    // [2][2] half of P is in TMEM (and O scaled)
   B_O = B_P + 4,                    // [2] PV is complete
-  B_CLEAN = B_O + 2,                // [2] the values have been looked through: of the first and second cut block
-  B_CUT = B_CLEAN + 2,              // [2] the values of a cut block, in place of B_FULL
-  B_DONE = B_CUT + 2,               // the softmax warps are done with TMEM
+  B_CUT = B_O + 2,                  // [2] the values of the unit's first or second cut block have landed
+  B_CLEAN = B_CUT + 2,              // [2] and been looked through
+  B_UNIT = B_CLEAN + 2,             // [4] the unit has been found
+  B_CLAIM = B_UNIT + 4,             // the answer of the launch queue
+  B_DONE = B_CLAIM + 1,             // the softmax warps are done with TMEM
   B_MMA = B_DONE + 1,               // every MMA is complete
   kNumBars = B_MMA + 1
 };
-constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM address, dirty blocks, sequence, padding
-constexpr int kRed = kMisc + 16;             // [2][warps] of the schedule's sums
+constexpr int kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;  // TMEM address, padding, a sequence
+constexpr int kDirty = kMisc + 16;           // [2 units][2 warps] dirty blocks
+constexpr int kClaim = kDirty + 16;          // the launch queue's answer
+constexpr int kPosted = kClaim + 16;         // [4] units
+constexpr int kRed = kPosted + 4 * 48;       // [2][warps] of the schedule's sums
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int kSmem = kRed + 2 * 4 * (kThreads / 32) + 1024;
-// Both slots' maxima and sums of a tile that has two, over the second tile's queries: [2][128] each.
-constexpr int kBothM = kOperand, kBothL = kBothM + 2 * kM * 4;
+// Both slots' maxima and sums of a tile that has two, [2][128] each: over the second tile's queries, or (LOOP) the outputs.
+template <bool LOOP>
+constexpr int kBoth = LOOP ? kOut : kOperand;
 
 // TMEM columns: S of tile t at 128 t, O at 256 + 128 t; P over S.  The CTA has all of them, so they begin at 0.
 constexpr uint32_t kTmemCols = 512;
@@ -145,11 +158,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
                "r"(src), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
-// This thread's stores are complete.
-__device__ __forceinline__ void bulk_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's stores have read their rows, or are complete.
+__device__ __forceinline__ void bulk_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_write_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -178,6 +190,25 @@ struct Unit {
   __device__ __forceinline__ int block(int t, int j) const { return solo ? 2 * j + t : j; }  // a slot's j-th
 };
 
+// What the units before this one have used, in phases of the barriers.
+struct Past {
+  int ring = 0;              // blocks of keys and values
+  int units = 0, q0 = 0, q1 = 0, b0 = 0, b1 = 0;  // units, and of either slot units and key blocks
+  int cut1 = 0;              // units with a second cut block (all have a first one)
+  __device__ __forceinline__ int q(int t) const { return t ? q1 : q0; }
+  __device__ __forceinline__ int b(int t) const { return t ? b1 : b0; }
+  __device__ __forceinline__ int cut(int k) const { return k ? cut1 : units; }
+  __device__ __forceinline__ void add(const Unit &u) {
+    ring += 2 * u.blocks;
+    units += 1;
+    q0 += u.nb0 > 0;
+    q1 += u.nb1 > 0;
+    b0 += u.nb0;
+    b1 += u.nb1;
+    cut1 += u.blocks > u.cut + 1;
+  }
+};
+
 // ---------------------------------------------------------------------------- schedule
 
 // The sum over the CTA's threads, or their maximum, in all of them.  `turn` alternates between calls.
@@ -195,197 +226,241 @@ __device__ __forceinline__ int reduce_all(int v, bool most, int *red, int turn) 
   return all;
 }
 
-// The x-th unit of the call for one KV head, the units with the most keys first: unit j of a sequence has j + 1 times the
-// keys of its first, and the GPU's last CTAs should be short ones.  Units of index c or more number N(c), the sum
-// of max(0, n_s - c) over the sequences: the unit's index is the largest c with N(c) > x, and it belongs to the
-// (x - N(c + 1))-th of the sequences that have such a unit.  False if there are fewer units.
-// KS 0: up to 32 sequences, a lane each, every warp by itself.  Else KS sequences per thread of the CTA, which is synchronised.
+// The units of the call, those with the most keys first: unit j of a sequence has j + 1 times the keys of its first, and the GPU's
+// last CTAs should be short ones.  Units of index c or more number N(c) for one KV head, the sum of max(0, n_s - c) over the
+// sequences: the x-th unit's index is the largest c with N(c) > x, and it belongs to the (x - N(c + 1))-th of the sequences that
+// have such a unit.
+// OWN sequences to each thread: of a warp by itself, up to 32 OWN sequences, or (ALL) of the CTA, which every call synchronises.
+//
 // While there are SMs without a unit the longest units are split into their two tiles, a CTA each, which takes half the time: its
 // keys are dealt to both slots.  So many more may be split that the shortest units come last, to the SMs that are done first: of units
 // of 1, 2, ... n times the same keys, s = (2 SMs - units - what a CTA takes beside its keys, about 4 blocks) / 3 makes the longest
 // whole one and two short ones in turn take the same time.  Not more of them than there are units below a third of the longest's
 // index.  (2048 tokens x 16 heads: 22.6 us, 24.1 with as many as there are idle SMs, 26.5 without; 1024: 12.5, 15.8 without.)
-template <int KS>
-__device__ bool locate(const PromptParams &p, uint8_t *smem, Unit &u) {
-  constexpr int kOwn = KS > 0 ? KS : 1;
-  const int tid = threadIdx.x, lane = tid & 31, span = 2 * p.tokens;
-  int *red = reinterpret_cast<int *>(smem + kRed);
-  int n[kOwn], row0 = 0, len = 0, sum = 0, top = 0;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int s = KS > 0 ? tid + i * kThreads : lane;
-    n[i] = 0;
-    if (s < p.B) {
-      const int a = p.cu[s], b = p.cu[s + 1];
-      if (a < 0 || b < a || b > p.T) {
-        bad = true;
-      } else {
-        n[i] = (b - a + span - 1) / span;
-        row0 = a;
-        len = b - a;
-      }
-    }
-    sum += n[i];
-    top = max(top, n[i]);
-  }
-  if (bad && blockIdx.x == 0 && (KS > 0 || tid < 32)) raise(p, PA_DEV_BAD_QLEN);
-  int turn = 0;
-  auto reduce = [&](int v, bool most) {
-    if constexpr (KS == 0) return most ? __reduce_max_sync(~0u, v) : __reduce_add_sync(~0u, v);
+template <int OWN, bool ALL>
+struct Schedule {
+  const PromptParams &p;
+  uint8_t *smem;
+  int n[OWN];  // units of each sequence
+  int total, units, splits = 0, turn = 0;  // units for one head and for all
+
+  __device__ __forceinline__ Schedule(const PromptParams &params, uint8_t *shared) : p(params), smem(shared) {}
+
+  __device__ __forceinline__ int reduce(int v, bool most) {
+    if constexpr (!ALL) return most ? __reduce_max_sync(~0u, v) : __reduce_add_sync(~0u, v);
     turn ^= 1;
-    return reduce_all(v, most, red, turn);
-  };
-  const int total = reduce(sum, false);
-  const int units = total * p.Hkv;
-  int x = (int)blockIdx.x, tile = -1;
-  if (units < 2 * p.sms) {
-    const int first = (kMinSplit * kN + span - 1) / span, few = reduce(top, true) / 3;
-    int longer = 0, rest = 0;  // units that may be split; all but the shortest
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      longer += max(0, n[i] - first);
-      rest += max(0, n[i] - few);
-    }
-    longer = reduce(longer, false) * p.Hkv;
-    rest = reduce(rest, false) * p.Hkv;
-    const int idle = p.sms - units, even = (p.sms + idle - 4 * kN * p.Hkv / span) / 3;
-    const int splits = max(0, min(min(longer, max(idle, min(even, p.sms - rest))), (int)gridDim.x - units));
-    tile = x < 2 * splits ? x & 1 : -1;
-    x = x < 2 * splits ? x >> 1 : x - splits;
+    return reduce_all(v, most, reinterpret_cast<int *>(smem + kRed), turn);
   }
-  if (x >= units) return false;
-  u.h = p.Hkv == 1 ? 0 : x % p.Hkv;
-  x = p.Hkv == 1 ? x : x / p.Hkv;
-  int lo = 0, above = 0;  // N(lo) > x >= above = N(hi)
-  if (p.B == 1) {
-    lo = total - 1 - x;
-    above = x;
-  } else {
-    int hi = reduce(top, true);
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      int v = 0;
+  // N(c), for one head
+  __device__ __forceinline__ int from(int c) {
+    int v = 0;
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) v += max(0, n[i] - mid);
-      const int count = reduce(v, false);
-      if (count > x) {
-        lo = mid;
-      } else {
-        hi = mid;
-        above = count;
+    for (int i = 0; i < OWN; ++i) v += max(0, n[i] - c);
+    return reduce(v, false);
+  }
+  __device__ __forceinline__ int longest() {
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) top = max(top, n[i]);
+    return reduce(top, true);
+  }
+
+  __device__ __forceinline__ void start() {
+    const int tid = threadIdx.x, lane = tid & 31, span = 2 * p.tokens;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      const int s = ALL ? tid + i * kThreads : lane + 32 * i;
+      n[i] = 0;
+      if (s < p.B) {
+        const int a = p.cu[s], b = p.cu[s + 1];
+        if (a < 0 || b < a || b > p.T)
+          bad = true;
+        else
+          n[i] = (b - a + span - 1) / span;
       }
     }
+    if (bad && blockIdx.x == 0) raise(p, PA_DEV_BAD_QLEN);
+    total = from(0);
+    units = total * p.Hkv;
+    if (units > 0 && units < 2 * p.sms) {
+      const int few = longest() / 3;
+      const int longer = from((kMinSplit * kN + span - 1) / span) * p.Hkv, rest = from(few) * p.Hkv;  // that may be split; but the shortest
+      const int idle = p.sms - units, even = (p.sms + idle - 4 * kN * p.Hkv / span) / 3;
+      splits = max(0, min(longer, max(idle, min(even, p.sms - rest))));
+    }
   }
-  // the (x - above)-th of those with more than lo units
-  if constexpr (KS == 0) {
-    const uint32_t have = __ballot_sync(~0u, n[0] > lo);
-    const int owner = __fns(have, 0, x - above + 1) & 31;
-    u.row0 = __shfl_sync(~0u, row0, owner);
-    u.len = __shfl_sync(~0u, len, owner);
-  } else {  // thread by thread
-    volatile int *found = reinterpret_cast<volatile int *>(smem + kMisc + 8);
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) mine += n[i] > lo;
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(~0u, upto, o);
-      if (lane >= o) upto += y;
+
+  // The x-th share: false if there are fewer, or it is an empty tile.
+  __device__ __forceinline__ bool find(int x, Unit &u) {
+    const int tid = threadIdx.x, lane = tid & 31, span = 2 * p.tokens;
+    const int tile = x < 2 * splits ? x & 1 : -1;
+    x = x < 2 * splits ? x >> 1 : x - splits;
+    if (x >= units) return false;
+    u.h = p.Hkv == 1 ? 0 : x % p.Hkv;
+    x = p.Hkv == 1 ? x : x / p.Hkv;
+    int lo = 0, above = 0;  // N(lo) > x >= above = N(hi)
+    if (p.B == 1) {
+      lo = total - 1 - x;
+      above = x;
+    } else {
+      int hi = longest();
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1, count = from(mid);
+        if (count > x) {
+          lo = mid;
+        } else {
+          hi = mid;
+          above = count;
+        }
+      }
     }
-    __syncthreads();  // the last sum has been read
-    if (lane == 31) red[tid >> 5] = upto;
-    __syncthreads();
-    for (int w = 0; w < (tid >> 5); ++w) upto += red[w];
-    int at = x - above - (upto - mine);
-    if (at >= 0 && at < mine) {
+    // the (x - above)-th of those with more than lo units
+    int s = 0;
+    if constexpr (!ALL) {
+      int k = x - above;
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-        if (n[i] > lo && at-- == 0) *found = tid + i * kThreads;
+      for (int i = 0; i < OWN; ++i) {
+        const uint32_t have = __ballot_sync(~0u, n[i] > lo);
+        const uint32_t it = __ballot_sync(~0u, n[i] > lo && __popc(have & ((1u << lane) - 1u)) == k);
+        if (it != 0) s = 32 * i + __ffs(it) - 1;
+        k -= __popc(have);
+      }
+    } else {  // thread by thread
+      int *red = reinterpret_cast<int *>(smem + kRed);
+      volatile int *found = reinterpret_cast<volatile int *>(smem + kMisc + 8);
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) mine += n[i] > lo;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += y;
+      }
+      __syncthreads();  // the last sum has been read
+      if (lane == 31) red[tid >> 5] = upto;
+      __syncthreads();
+      for (int w = 0; w < (tid >> 5); ++w) upto += red[w];
+      int at = x - above - (upto - mine);
+      if (at >= 0 && at < mine) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+          if (n[i] > lo && at-- == 0) *found = tid + i * kThreads;
+      }
+      __syncthreads();
+      s = *found;
     }
-    __syncthreads();
-    const int s = *found;
     u.row0 = p.cu[s];
     u.len = p.cu[s + 1] - u.row0;
+    auto blocks_of = [&](int first) { return first < u.len ? (min(u.len, first + p.tokens) + kN - 1) / kN : 0; };
+    u.cut = lo * span / kN;
+    u.solo = tile >= 0;
+    if (u.solo) {
+      u.tok0 = u.tok1 = lo * span + tile * p.tokens;
+      u.blocks = blocks_of(u.tok0);
+      u.nb0 = (u.blocks + 1) >> 1;
+      u.nb1 = u.blocks >> 1;
+    } else {
+      u.tok0 = lo * span;
+      u.tok1 = u.tok0 + p.tokens;
+      u.nb0 = blocks_of(u.tok0);
+      u.nb1 = blocks_of(u.tok1);
+      u.blocks = max(u.nb0, u.nb1);
+    }
+    return u.blocks > 0;  // (a sequence's last unit may have but one tile)
   }
-  auto blocks_of = [&](int first) { return first < u.len ? (min(u.len, first + p.tokens) + kN - 1) / kN : 0; };
-  u.cut = lo * span / kN;
-  u.solo = tile >= 0;
-  if (u.solo) {
-    u.tok0 = u.tok1 = lo * span + tile * p.tokens;
-    u.blocks = blocks_of(u.tok0);
-    u.nb0 = (u.blocks + 1) >> 1;
-    u.nb1 = u.blocks >> 1;
-    if (u.blocks == 0) return false;  // (a sequence's last unit may have but one tile)
-  } else {
-    u.tok0 = lo * span;
-    u.tok1 = u.tok0 + p.tokens;
-    u.nb0 = blocks_of(u.tok0);
-    u.nb1 = blocks_of(u.tok1);
-    u.blocks = max(u.nb0, u.nb1);
-  }
-  return true;
+};
+
+// The next CTA of the grid that has not been launched yet, to be run by this one in its place: asked for by one thread, the answer
+// is there when the barrier's phase is complete.  Its index, or -1 if there is none left.
+__device__ __forceinline__ void claim_next(uint32_t answer, uint32_t bar) {
+  pa::mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer), "r"(bar) : "memory");
+}
+__device__ __forceinline__ int claimed(uint32_t answer) {
+  uint32_t x, any;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\tld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tselp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=r"(x), "=r"(any)
+      : "r"(answer)
+      : "memory");
+  return any ? (int)x : -1;
+}
+
+// The units that the load warp has found for the others: a place for each of the last four (it is ahead of them by less than
+// three), and a barrier for each.
+struct Slot {
+  int row0, len, h, tok0, tok1, nb0, nb1, blocks, cut, solo, pad[2];
+};
+constexpr int kUnits = 4;
+__device__ __forceinline__ void post_unit(uint8_t *smem, int round, const Unit &u, bool some) {
+  Slot *s = reinterpret_cast<Slot *>(smem + kPosted) + (round & (kUnits - 1));
+  *s = Slot{u.row0, u.len, u.h, u.tok0, u.tok1, u.nb0, u.nb1, some ? u.blocks : 0, u.cut, (int)u.solo, {0, 0}};
+}
+__device__ __forceinline__ bool posted_unit(const uint8_t *smem, int round, Unit &u) {
+  const Slot s = reinterpret_cast<const Slot *>(smem + kPosted)[round & (kUnits - 1)];
+  u = Unit{s.row0, s.len, s.h, s.tok0, s.tok1, s.nb0, s.nb1, s.blocks, s.cut, s.solo != 0};
+  return s.blocks > 0;
 }
 
 // ------------------------------------------------------------------------------- roles
 
-// The barrier that block i of the ring (keys and values in turn) lands on.  Values of cut blocks have one of their own,
-// since the warps that look through them follow no others; nothing comes after them in their stages.
-__device__ __forceinline__ uint32_t bar_landed(const Unit &u, uint32_t bars, int i, uint32_t &parity) {
-  const bool cut = (i & 1) != 0 && (i >> 1) >= u.cut;
-  parity = cut ? 0 : (i / kStages) & 1;
-  return bars + 8 * (cut ? B_CUT + (i >> 1) - u.cut : B_FULL + i % kStages);
-}
-__device__ __forceinline__ bool landed(const Unit &u, uint32_t bars, int i) {
-  uint32_t parity;
-  const uint32_t bar = bar_landed(u, bars, i, parity);
-  return warp_wait(bar, parity);
-}
+__device__ __forceinline__ uint32_t bar_full(uint32_t bars, int stage) { return bars + 8 * (B_FULL + stage); }
 
-__device__ __forceinline__ void load_block(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars, int i) {
-  uint32_t parity;
-  const uint32_t bar = bar_landed(u, bars, i, parity), dst = base + kRing + (i % kStages) * kOperand;
+// Block i of the unit (keys and values in turn) into its place of the ring, by one thread.
+template <int STAGES>
+__device__ __forceinline__ void load_block(const PromptParams &p, const Unit &u, int ring, uint32_t base, uint32_t bars, int i) {
+  const int stage = (ring + i) % STAGES;
+  const uint32_t bar = bar_full(bars, stage), dst = base + kRing + stage * kOperand;
   pa::mbar_arrive_expect_tx(bar, kOperand);
   for (int x = 0; x < 2; ++x)
     tma_load_3d(dst + x * (kOperand / 2), i & 1 ? &p.tm_v : &p.tm_k, 64 * x, u.h, u.row0 + (i >> 1) * kN, bar);
 }
-
-// The queries and as many blocks as the ring holds, by one thread.
-__device__ void first_loads(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars) {
-  const uint32_t qbytes = (uint32_t)p.G * p.tokens * kD * 2;
-  for (int t = 0; t < (u.solo ? 1 : 2); ++t) {
-    if (u.nb(t) == 0) continue;
-    pa::mbar_arrive_expect_tx(bars + 8 * (B_QFULL + t), qbytes);
-    for (int x = 0; x < 2; ++x)
-      tma_load_3d(base + t * kOperand + x * (kOperand / 2), &p.tm_q, 64 * x, u.h * p.G, u.row0 + u.tok(t), bars + 8 * (B_QFULL + t));
-    if (t == 0) load_block(p, u, base, bars, 0);
-  }
-  for (int i = 1; i < min(kStages, 2 * u.blocks); ++i) load_block(p, u, base, bars, i);
+__device__ __forceinline__ void load_queries(const PromptParams &p, const Unit &u, int t, uint32_t base, uint32_t bars) {
+  pa::mbar_arrive_expect_tx(bars + 8 * (B_QFULL + t), (uint32_t)p.G * p.tokens * kD * 2);
+  for (int x = 0; x < 2; ++x)
+    tma_load_3d(base + t * kOperand + x * (kOperand / 2), &p.tm_q, 64 * x, u.h * p.G, u.row0 + u.tok(t), bars + 8 * (B_QFULL + t));
 }
 
-__device__ void run_producer(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars) {
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) first_loads(p, u, base, bars);
-  __syncwarp();
-  bool ok = true;
-  int i = min(kStages, 2 * u.blocks);
-  for (; i < 2 * u.blocks; ++i) {
-    ok = warp_wait(bars + 8 * (B_EMPTY + i % kStages), (i / kStages - 1) & 1);
-    if (!ok) break;
-    if (lane == 0) load_block(p, u, base, bars, i);
+// The loads of a unit, in the order of their use: as many blocks as the ring holds do not wait for anything in the first unit.
+// `done` counts what has been asked for.
+struct Loads {
+  int blocks = 0, q0 = 0, q1 = 0;
+};
+template <int STAGES>
+__device__ bool load_unit(const PromptParams &p, const Unit &u, const Past &past, uint32_t base, uint32_t bars, Loads &done) {
+  const int lane = threadIdx.x & 31, tiles = u.solo ? 1 : 2;
+  auto block = [&](int i) {
+    const int e = past.ring + i;
+    if (e >= STAGES && !warp_wait(bars + 8 * (B_EMPTY + e % STAGES), (e / STAGES - 1) & 1)) return false;
+    if (lane == 0) load_block<STAGES>(p, u, past.ring, base, bars, i);
     __syncwarp();
-  }
-  if (!ok && lane == 0) {
-    raise(p, PA_DEV_TIMEOUT);
-    for (int t = 0; t < (u.solo ? 1 : 2); ++t)  // copies in flight land before the CTA can exit
-      if (u.nb(t) > 0) pa::mbar_wait_bounded(bars + 8 * (B_QFULL + t), 0);
-    for (int k = max(0, i - kStages); k < i; ++k) {
-      uint32_t parity;
-      const uint32_t bar = bar_landed(u, bars, k, parity);
-      pa::mbar_wait_bounded(bar, parity);
+    ++done.blocks;
+    return true;
+  };
+  for (int t = 0; t < tiles; ++t) {
+    if (u.nb(t) > 0) {
+      if (past.q(t) > 0 && !warp_wait(bars + 8 * (B_QFREE + t), (past.q(t) - 1) & 1)) return false;
+      if (lane == 0) load_queries(p, u, t, base, bars);
+      __syncwarp();
+      ++(t ? done.q1 : done.q0);
     }
+    if (t == 0 && !block(0)) return false;
   }
+  for (int i = 1; i < 2 * u.blocks; ++i)
+    if (!block(i)) return false;
+  return true;
+}
+
+// Copies in flight land before the CTA can exit: what a load warp that gave up may have left.
+template <int STAGES>
+__device__ void drain(uint32_t bars, const Loads &done) {
+  for (int e = max(0, done.blocks - STAGES); e < done.blocks; ++e) pa::mbar_wait_bounded(bar_full(bars, e % STAGES), (e / STAGES) & 1);
+  if (done.q0 > 0) pa::mbar_wait_bounded(bars + 8 * B_QFULL, (done.q0 - 1) & 1);
+  if (done.q1 > 0) pa::mbar_wait_bounded(bars + 8 * (B_QFULL + 1), (done.q1 - 1) & 1);
 }
 
 // A bounded wait of a whole warp whose control flow stays uniform: what the MMAs' operands are computed from then stays
@@ -415,25 +490,35 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(id), "r"(accumulate), "r"(kDescHigh));
 }
 
-// The MMAs of both slots: PV0 S0' PV1 S1' of every block, S' being the slot's next one's.  The waits for what the next product
-// reads come half way through the one before, where the tensor core has MMAs left (before them instead: 620 us, not 613, for
-// 16384 tokens x 16 heads).
-__device__ bool issue_mmas(const Unit &u, uint32_t base, uint32_t bars) {
+// The MMAs of a unit, both slots: PV0 S0' PV1 S1' of every block, S' being the slot's next one's.  The waits for what the next
+// product reads come half way through the one before, where the tensor core has MMAs left (before them instead: 620 us, not 613,
+// for 16384 tokens x 16 heads).
+template <int STAGES>
+__device__ bool issue_mmas(const Unit &u, const Past &past, uint32_t base, uint32_t bars) {
   const int nb0 = __reduce_max_sync(~0u, u.nb0), nb1 = __reduce_max_sync(~0u, u.nb1), cut = __reduce_max_sync(~0u, u.cut);
+  const int ring = __reduce_max_sync(~0u, past.ring), units = __reduce_max_sync(~0u, past.units);
+  const int uses[4] = {__reduce_max_sync(~0u, past.q0), __reduce_max_sync(~0u, past.q1), __reduce_max_sync(~0u, past.b0), __reduce_max_sync(~0u, past.b1)};
+  const int cut1 = __reduce_max_sync(~0u, past.cut1);
   const bool solo = __any_sync(~0u, u.solo);
   // (14 bits of the address)
   const uint32_t q_at = (base >> 4) & 0x3FFFu, ring_at = q_at + (kRing >> 4);
   const uint32_t q_low = q_at | desc_low(1024), k_low = ring_at | desc_low(1024), v_low = ring_at | desc_low(kOperand / 2);
   auto block = [&](int t, int j) { return solo ? 2 * j + t : j; };
   auto last_of = [&](int t, int j) { return solo || t == 1 || j >= nb1; };  // the slot that reads a block last
-  auto arrived = [&](int bar, uint32_t parity) { return uniform_wait(bars + 8 * bar, parity); };
-  auto fetched = [&](int i) {
-    const bool own = (i & 1) != 0 && (i >> 1) >= cut;
-    return own ? arrived(B_CUT + (i >> 1) - cut, 0) && arrived(B_CLEAN + (i >> 1) - cut, 0) : arrived(B_FULL + i % kStages, (i / kStages) & 1);
+  auto arrived = [&](int bar, int phase) { return uniform_wait(bars + 8 * bar, (uint32_t)phase & 1u); };
+  auto fetched = [&](int i) {  // block i of the unit's (keys and values in turn) has landed
+    const int e = ring + i;
+    if (!arrived(B_FULL + e % STAGES, e / STAGES)) return false;
+    const int k = (i >> 1) - cut;
+    if ((i & 1) != 0 && k >= 0) {  // values to be looked through
+      if (pa::elect_one()) pa::mbar_arrive(bars + 8 * (B_CUT + k));
+      __syncwarp();
+    }
+    return true;
   };
   auto scores = [&](int t, int j, bool values) {  // S of the slot's j-th block; `values`: half way through, those have landed
-    const int i = 2 * block(t, j);
-    const uint32_t q = q_low + (solo ? 0 : t) * (kOperand >> 4), k = k_low + (i % kStages) * (kOperand >> 4);
+    const int i = 2 * block(t, j), stage = (ring + i) % STAGES;
+    const uint32_t q = q_low + (solo ? 0 : t) * (kOperand >> 4), k = k_low + stage * (kOperand >> 4);
     if (pa::elect_one()) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -450,18 +535,19 @@ __device__ bool issue_mmas(const Unit &u, uint32_t base, uint32_t bars) {
         mma_ss(128 * t, q + off, k + off, idesc(0), 1);
       }
       pa::umma_commit(bars + 8 * (B_S + t));
-      if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + i % kStages));
+      if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
+      if (j + 1 == (t ? nb1 : nb0)) pa::umma_commit(bars + 8 * (B_QFREE + t));
     }
     __syncwarp();
     return ok;
   };
   if (nb0 > 0) {
-    if (!arrived(B_QFULL, 0) || !fetched(0)) return false;
+    if (!arrived(B_QFULL, uses[0]) || !fetched(0)) return false;
     pa::tc_fence_after();
     scores(0, 0, false);
   }
   if (nb1 > 0) {
-    if (solo ? !fetched(2) : !arrived(B_QFULL + 1, 0)) return false;
+    if (solo ? !fetched(2) : !arrived(B_QFULL + 1, uses[1])) return false;
     pa::tc_fence_after();
     scores(1, 0, false);
   }
@@ -469,12 +555,13 @@ __device__ bool issue_mmas(const Unit &u, uint32_t base, uint32_t bars) {
   for (int j = 0; j < max(nb0, nb1); ++j) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int nb = t ? nb1 : nb0, i = 2 * block(t, j) + 1;
+      const int nb = t ? nb1 : nb0, b = block(t, j), stage = (ring + 2 * b + 1) % STAGES;
       if (j >= nb) continue;
-      const uint32_t v = v_low + (i % kStages) * (kOperand >> 4);
+      if (b >= cut && (solo || t == 0 || j >= nb0) && !arrived(B_CLEAN + b - cut, b > cut ? cut1 : units)) return false;
+      const uint32_t v = v_low + stage * (kOperand >> 4);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!arrived(B_P + 2 * t + half, j & 1)) return false;
+        if (!arrived(B_P + 2 * t + half, uses[2 + t] + j)) return false;
         pa::tc_fence_after();
         if (pa::elect_one()) {
 #pragma unroll
@@ -482,7 +569,7 @@ __device__ bool issue_mmas(const Unit &u, uint32_t base, uint32_t bars) {
             mma_ts(256 + 128 * t, 128 * t + 8 * x, v + x * (2048 >> 4), idesc(1), j > 0 || x > 0);
           if (half == 1) {
             pa::umma_commit(bars + 8 * (B_O + t));
-            if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + i % kStages));
+            if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
           }
         }
         __syncwarp();
@@ -497,15 +584,6 @@ __device__ bool issue_mmas(const Unit &u, uint32_t base, uint32_t bars) {
   return true;
 }
 
-__device__ void run_mma(const PromptParams &p, const Unit &u, uint32_t base, uint32_t bars) {
-  const int lane = threadIdx.x & 31;
-  pa::tc_fence_after();
-  const bool ok = issue_mmas(u, base, bars);
-  if (pa::elect_one()) pa::umma_commit(bars + 8 * B_MMA);
-  __syncwarp();
-  if (!(warp_wait(bars + 8 * B_MMA, 0) & ok) && lane == 0) raise(p, PA_DEV_TIMEOUT);
-}
-
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
 
 // Whether one of the eight bf16 values of w is an infinity or NaN: an exponent of ones carries into the sign's place.
@@ -514,17 +592,15 @@ __device__ __forceinline__ uint32_t any_not_finite(const uint4 &w) {
   return (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) & 0x80008000u;
 }
 
-// Values of the blocks that the diagonal or the sequence's end cuts.
-__device__ void run_clean(const PromptParams &p, const Unit &u, uint32_t bars, uint8_t *smem) {
+// Values of the unit's blocks that the diagonal or the sequence's end cuts.
+template <int STAGES>
+__device__ bool clean_unit(const Unit &u, const Past &past, uint32_t bars, uint8_t *smem) {
   constexpr int kBatch = 8;
   const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - kCleanWarp;
+  uint32_t dirty = 0;
   for (int j = u.cut; j < u.blocks; ++j) {
-    const int i = 2 * j + 1, st = i % kStages;
-    if (!landed(u, bars, i)) {
-      if (lane == 0) raise(p, PA_DEV_TIMEOUT);
-      return;
-    }
-    uint4 *at = reinterpret_cast<uint4 *>(smem + kRing + st * kOperand + half * (kOperand / 2)) + lane;
+    if (!warp_wait(bars + 8 * (B_CUT + j - u.cut), past.cut(j - u.cut) & 1)) return false;
+    uint4 *at = reinterpret_cast<uint4 *>(smem + kRing + ((past.ring + 2 * j + 1) % STAGES) * kOperand + half * (kOperand / 2)) + lane;
     bool own = false;  // one of the sequence's own
 #pragma unroll 1
     for (int c0 = 0; c0 < kOperand / 32; c0 += 32 * kBatch) {  // pieces of this half
@@ -546,11 +622,14 @@ __device__ void run_clean(const PromptParams &p, const Unit &u, uint32_t bars, u
         }
       }
     }
-    if (own) atomicOr(reinterpret_cast<unsigned *>(smem + kMisc + 4), 1u << (j - u.cut));
+    dirty |= __any_sync(~0u, own) ? 1u << (j - u.cut) : 0u;
+    // (the unit's word, read by the softmax warps once its last product is complete: those of the unit before have read theirs)
+    if (lane == 0) reinterpret_cast<volatile uint32_t *>(smem + kDirty)[2 * (past.units & 1) + half] = dirty;
     pa::fence_async_smem();
     __syncwarp();
     if (lane == 0) pa::mbar_arrive(bars + 8 * (B_CLEAN + j - u.cut));
   }
+  return true;
 }
 
 // The infinities and NaN among the values that a row attends and that were replaced by 0: into its output, which this
@@ -625,15 +704,15 @@ __device__ __forceinline__ Row row_of(const PromptParams &p, const Unit &u) {
 }
 
 // The weights of all blocks; m: what is subtracted from the scaled scores, in units of log2, l: the weights' sum.
-__device__ bool run_softmax(const PromptParams &p, const Unit &u, const Row &r, uint32_t bars, float &m, float &l) {
-  const int t = threadIdx.x >> 7, nb = u.nb(t);
+__device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &past, const Row &r, uint32_t bars, float &m, float &l) {
+  const int t = threadIdx.x >> 7, nb = u.nb(t), before = past.b(t);
   const uint32_t s_at = r.lanes + 128 * t, o_at = r.lanes + 256 + 128 * t;
   const int first = u.tok(t);
   const float c = p.fold;
   m = -INFINITY;
   l = 0.f;
   for (int j = 0; j < nb; ++j) {
-    if (!warp_wait(bars + 8 * (B_S + t), j & 1)) return false;
+    if (!warp_wait(bars + 8 * (B_S + t), (before + j) & 1)) return false;
     pa::tc_fence_after();
     uint32_t s[kN];
 #pragma unroll
@@ -656,7 +735,7 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Row &r, 
         const float alpha = grown ? pa::fast_exp2(m - peak) : 1.f;
         if (grown) m = peak;
         l *= alpha;
-        if (!warp_wait(bars + 8 * (B_O + t), (j - 1) & 1)) return false;
+        if (!warp_wait(bars + 8 * (B_O + t), (before + j - 1) & 1)) return false;
         pa::tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < kD; k += 32) {
@@ -673,52 +752,60 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Row &r, 
     l += weights(s + kN / 2, c, m, w);
     publish(s_at + kN / 4, w, bars + 8 * (B_P + 2 * t + 1));
   }
-  if (nb > 0 && !warp_wait(bars + 8 * (B_O + t), (nb - 1) & 1)) return false;
-  pa::tc_fence_after();
   return true;
 }
 
 // The tile's rows: O / l and the log-sum-exp.  A solo tile's O is the sum of both slots', which lie in the same lanes of TMEM: each
 // slot's warps join half of its columns.
-__device__ void write_tile(const PromptParams &p, const Unit &u, const Row &r, float m, float l, uint8_t *smem) {
+// The rows go through shared memory, 128 bytes of each at a time, as the tensor map has them (128-byte swizzle): in place of the
+// tile's queries, whose last S is complete, or (LOOP) where the next unit's queries are not.  Stored from the lanes, row by row, each
+// store took 32 cycles and a tile 4000.
+template <bool LOOP>
+__device__ void write_tile(const PromptParams &p, const Unit &u, const Past &past, const Row &r, float m, float l, uint8_t *smem) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = warp >> 2, hq = p.Hkv * p.G;
   const int first = u.tok(t);
   const uint32_t o_at = r.lanes + 256 + (u.solo ? 0 : 128 * t);
   float mine = 1.f, others = 0.f;  // what O of slot 0 (or of the tile's own) and that of slot 1 count
+  const bool leader = warp == 4 * t && lane == 0;  // the tile's stores are this thread's
+  auto together = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory"); };  // the slot's four warps
+  auto both = [&]() { asm volatile("bar.sync 4, 256;" ::: "memory"); };
   if (u.solo) {
-    float *ms = reinterpret_cast<float *>(smem + kBothM), *ls = reinterpret_cast<float *>(smem + kBothL);
+    float *ms = reinterpret_cast<float *>(smem + kBoth<LOOP>), *ls = ms + 2 * kM;
+    if (LOOP) {  // (the stores of the unit before have read that place)
+      if (leader) bulk_read_wait();
+      both();
+    }
     ms[t * kM + r.row] = m;
     ls[t * kM + r.row] = l;
-    asm volatile("bar.sync 4, 256;" ::: "memory");
+    both();
     pa::tc_fence_after();
-    const float m0 = ms[r.row], m1 = ms[kM + r.row];
+    const float m0 = ms[r.row], m1 = ms[kM + r.row], l0 = ls[r.row], l1 = ls[kM + r.row];
+    if (LOOP) both();  // read by both before rows are written there
     m = fmaxf(m0, m1);
     mine = pa::fast_exp2(m0 - m);
     others = pa::fast_exp2(m1 - m);
-    l = ls[r.row] * mine + ls[kM + r.row] * others;
+    l = l0 * mine + l1 * others;
   }
-  const uint32_t dirty = *reinterpret_cast<const volatile uint32_t *>(smem + kMisc + 4);
+  const volatile uint32_t *dirt = reinterpret_cast<const volatile uint32_t *>(smem + kDirty) + 2 * (past.units & 1);
+  const uint32_t dirty = dirt[0] | dirt[1];
   const int64_t at = (int64_t)(u.row0 + r.token) * hq + u.h * p.G + (r.row - r.tk * p.G);
   const bool writes = r.live && !(u.solo && t == 1);  // a row's lse, and what else is one thread's
   if (writes && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
   mine /= l;
   others /= l;
-  // Through the tile's queries' place in shared memory (its last S is complete), as the tensor map has it: two halves of 128
-  // bytes a row, in 128-byte swizzle.  Stored from the lanes, row by row, each store took 32 cycles and a tile 4000.
-  uint8_t *rows = smem + (u.solo ? 0 : t * kOperand);
   const bool whole = !p.out_f32 && first + p.tokens <= u.len;  // else the tile's box reaches past the sequence
-  const int size = p.out_f32 ? 4 : 2, cols = 256 / size;
-  auto together = [&]() {  // the warps that write the tile
-    if (u.solo)
-      asm volatile("bar.sync 4, 256;" ::: "memory");
-    else
-      asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
-  };
+  const int size = p.out_f32 ? 4 : 2, cols = 128 / size;
+  int pass = 0;
 #pragma unroll 1
-  for (int k0 = 0; k0 < kD; k0 += cols) {
-    const int from = u.solo ? k0 + t * (cols / 2) : k0, to = u.solo ? from + cols / 2 : k0 + cols;
+  for (int k0 = u.solo ? t * cols : 0; k0 < kD; k0 += u.solo ? 2 * cols : cols, ++pass) {
+    // (solo: the slots' passes take turns, and so do the two places)
+    uint8_t *rows = LOOP ? smem + kOut + t * (kOperand / 2) : smem + (u.solo ? 0 : t * kOperand) + ((u.solo ? t : pass) & 1) * (kOperand / 2);
+    if (LOOP) {  // the store before, of this unit or the last one, has read its rows
+      if (leader) bulk_read_wait();
+      together();
+    }
 #pragma unroll 1
-    for (int k = from; k < to; k += 32) {
+    for (int k = k0; k < k0 + cols; k += 32) {
       uint32_t o[32];
       tmem_ld32(o_at + k, o);
       if (u.solo) {
@@ -733,52 +820,47 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Row &r, f
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mine);
       }
-      const int piece = (k - k0) * size / 16;  // of the row's 16
+      uint4 *row = reinterpret_cast<uint4 *>(rows + r.row * 128);
       if (p.out_f32) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4 *>(rows + (piece >> 3) * (kOperand / 2) + r.row * 128 + ((e ^ (r.row & 7)) << 4)) =
-              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int e = 0; e < 8; ++e) row[e ^ (r.row & 7)] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       } else {
+        const int piece = (k - k0) >> 3;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = pa::pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]), __uint_as_float(o[8 * e + 2 * i + 1]));
-          *reinterpret_cast<uint4 *>(rows + (piece >> 3) * (kOperand / 2) + r.row * 128 + ((((piece & 7) + e) ^ (r.row & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          row[(piece + e) ^ (r.row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
     if (whole) {
       pa::fence_async_smem();
       together();
-      if (warp == (u.solo ? 0 : 4 * t) && pa::elect_one()) {
-        for (int x = 0; x < 2; ++x) tma_store_3d(&p.tm_o, pa::smem_u32(rows) + x * (kOperand / 2), 64 * x, u.h * p.G, u.row0 + first);
-        bulk_store_wait();
+      if (leader) {
+        tma_store_3d(&p.tm_o, pa::smem_u32(rows), k0, u.h * p.G, u.row0 + first);
+        bulk_commit();
       }
-    } else {  // whole rows to half a warp: of the warp's own 32, or (solo) half of them, which both slots have written
+    } else {  // 128 bytes of a row to 8 lanes; a warp's rows are its own
       const int where = r.live ? r.tk * hq + r.row - r.tk * p.G : -1;  // from the tile's first row and head
       const int64_t origin = (int64_t)(u.row0 + first) * hq + u.h * p.G;
-      const int begin = u.solo ? 16 * t : 0, end = u.solo ? begin + 16 : 32;
-      if (u.solo)
-        together();
-      else
-        __syncwarp();
+      __syncwarp();
 #pragma unroll 4
-      for (int q0 = begin; q0 < end; q0 += 2) {
-        const int q = q0 + (lane >> 4), dst = __shfl_sync(~0u, where, q), row = 32 * (warp & 3) + q, l16 = lane & 15;
-        const uint4 v = *reinterpret_cast<const uint4 *>(rows + (l16 >> 3) * (kOperand / 2) + row * 128 + (((l16 & 7) ^ (row & 7)) << 4));
-        if (dst >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + ((origin + dst) * kD + k0) * size + l16 * 16) = v;
+      for (int i = 0; i < 8; ++i) {
+        const int q = 4 * i + (lane >> 3), dst = __shfl_sync(~0u, where, q), row = 32 * (warp & 3) + q;
+        const uint4 v = *reinterpret_cast<const uint4 *>(rows + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+        if (dst >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + ((origin + dst) * kD + k0) * size + (lane & 7) * 16) = v;
       }
-      if (u.solo)
-        together();
-      else
-        __syncwarp();
+      __syncwarp();
     }
   }
-  if (dirty != 0) {
-    together();  // the tile has been written
+  if (dirty != 0) {  // (the same for both slots of a solo tile)
+    if (leader) bulk_write_wait();
+    if (u.solo)
+      both();
+    else
+      together();  // the tile has been written
     if (writes)
       add_not_finite(p.v + u.row0 * p.v_stride + u.h * kD, p.v_stride, static_cast<uint8_t *>(p.out) + at * kD * size, p.out_f32, dirty,
                      u.cut, r.token);
@@ -795,66 +877,126 @@ __device__ __forceinline__ bool agreed(bool ok, bool solo, int t) {
   return r != 0;
 }
 
-// KS: sequences per thread in the schedule.
-template <int KS>
+// OWN, ALL: how the schedule is worked out.  LOOP: CTAs go on with further units, whose first scores are there when the rows of
+// the one before have been written; else a CTA for each.
+template <int OWN, bool ALL, bool LOOP>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptParams p) {
+  constexpr int STAGES = kStages<LOOP>;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t *smem = raw + ((1024u - (pa::smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = pa::smem_u32(smem), bars = base + kBars;
   // (from lane 0, so that the roles' control flow and the MMAs' operands are known to be uniform: 650 us, else 620, for
   // 16384 tokens x 16 heads)
-  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  if (warp == kLoadWarp && (threadIdx.x & 31) == 0) {
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (warp == kLoadWarp && lane == 0) {
     prefetch_map(&p.tm_q);
     prefetch_map(&p.tm_k);
     prefetch_map(&p.tm_v);
-    for (int i = 0; i < kNumBars; ++i) {
+    for (int i = 0; i < kNumBars; ++i)
       pa::mbar_init(bars + 8 * i, i >= B_P && i < B_P + 4 ? 4 : i == B_DONE ? kSoftWarps : i >= B_CLEAN && i < B_CLEAN + 2 ? 2 : 1);
-    }
-    *reinterpret_cast<uint32_t *>(smem + kMisc + 4) = 0;
     pa::fence_barrier_init();
   }
   if (warp == kMmaWarp) pa::tmem_alloc(base + kMisc, kTmemCols);
   pa::pdl_wait();
   pa::pdl_launch_dependents();
+  // The load warp finds the CTA's units, the first one before the others need anything of it.  The units come in descending order.
   Unit u;
-  const bool some = locate<KS>(p, smem, u);
-  // The load warp, which initialised the barriers and needs nothing of the others, goes ahead.
+  Past past;
+  bool ok = true, more = false;
+  int round = 0;
+  Schedule<OWN, ALL> schedule(p, smem);
+  auto post = [&]() {
+    if (lane == 0) {
+      post_unit(smem, round, u, more);
+      pa::mbar_arrive(bars + 8 * (B_UNIT + (round & (kUnits - 1))));
+    }
+    __syncwarp();
+  };
+  if (ALL || warp == kLoadWarp) {
+    schedule.start();
+    more = schedule.find((int)blockIdx.x, u);
+    if (!ALL) post();
+  }
   pa::tc_fence_before();
-  if (warp == kLoadWarp)
+  if (warp == kLoadWarp)  // (it needs nothing of the others)
     asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
   else
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
   pa::tc_fence_after();
-  if (!some) {
+  if (!ALL && warp != kLoadWarp) more = posted_unit(smem, 0, u);
+  if (!more) {
     if (warp == kMmaWarp) pa::tmem_dealloc(0, kTmemCols);
     return;
   }
+  auto next = [&]() {  // the unit after this one, if there is one
+    past.add(u);
+    ++round;
+    more = false;
+    if (LOOP) {
+      ok = warp_wait(bars + 8 * (B_UNIT + (round & (kUnits - 1))), (round / kUnits) & 1);
+      more = ok && posted_unit(smem, round, u);
+    }
+  };
   if (warp < kSoftWarps) {
     pa::regs_inc<216>();
-    const Row r = row_of(p, u);
     const int t = warp >> 2;
-    float m, l;
-    const bool ok = run_softmax(p, u, r, bars, m, l);
-    if (!ok && (threadIdx.x & 31) == 0) raise(p, PA_DEV_TIMEOUT);
-    if (agreed(ok, u.solo, t) && u.nb(t) > 0) write_tile(p, u, r, m, l, smem);
-    pa::tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) pa::mbar_arrive(bars + 8 * B_DONE);
+    while (more) {
+      const Row r = row_of(p, u);
+      float m, l;
+      ok = run_softmax(p, u, past, r, bars, m, l);
+      if (ok && u.nb(t) > 0) ok = warp_wait(bars + 8 * (B_O + t), (past.b(t) + u.nb(t) - 1) & 1);
+      pa::tc_fence_after();
+      ok = agreed(ok, u.solo, t);
+      if (!ok) break;
+      if (u.nb(t) > 0) write_tile<LOOP>(p, u, past, r, m, l, smem);
+      pa::tc_fence_before();  // O has been read before the next unit's weights are published
+      next();
+    }
+    if (lane == 0) {
+      bulk_write_wait();
+      pa::mbar_arrive(bars + 8 * B_DONE);
+    }
   } else {
     pa::regs_dec<72>();
-    if (warp == kLoadWarp)
-      run_producer(p, u, base, bars);
-    else if (warp == kMmaWarp)
-      run_mma(p, u, base, bars);
-    else
-      run_clean(p, u, bars, smem);
-    if (warp == kMmaWarp) {
-      if (!warp_wait(bars + 8 * B_DONE, 0) && (threadIdx.x & 31) == 0) raise(p, PA_DEV_TIMEOUT);
+    if (warp == kLoadWarp) {
+      Loads done;
+      while (more) {
+        ok = load_unit<STAGES>(p, u, past, base, bars, done);
+        if (!ok || !LOOP) break;
+        // The CTA that would come next: asked for when the last loads of this unit have been (some two blocks before its end).
+        if (lane == 0) claim_next(base + kClaim, bars + 8 * B_CLAIM);
+        __syncwarp();
+        past.add(u);
+        ok = warp_wait(bars + 8 * B_CLAIM, round & 1);
+        if (!ok) break;
+        const int x = claimed(base + kClaim);
+        __syncwarp();
+        ++round;
+        more = x >= 0 && schedule.find(x, u);
+        pa::fence_async_smem();  // the answer has been read
+        post();
+      }
+      if (!ok && lane == 0) drain<STAGES>(bars, done);
+    } else if (warp == kMmaWarp) {
+      pa::tc_fence_after();
+      while (ok && more) {
+        ok = issue_mmas<STAGES>(u, past, base, bars);
+        if (ok) next();
+      }
+      if (pa::elect_one()) pa::umma_commit(bars + 8 * B_MMA);
+      __syncwarp();
+      ok = warp_wait(bars + 8 * B_MMA, 0) & ok;
+      ok = warp_wait(bars + 8 * B_DONE, 0) & ok;
       pa::tc_fence_after();
       pa::tmem_dealloc(0, kTmemCols);
+    } else {
+      while (ok && more) {
+        ok = clean_unit<STAGES>(u, past, bars, smem);
+        if (ok) next();
+      }
     }
   }
+  if (!ok && lane == 0) raise(p, PA_DEV_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------------- host
@@ -876,7 +1018,9 @@ const PromptDevice *prompt_device() {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult res;
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return;
-    for (const void *f : {(const void *)prompt_attn_kernel<0>, (const void *)prompt_attn_kernel<1>, (const void *)prompt_attn_kernel<11>}) {
+    for (const void *f : {(const void *)prompt_attn_kernel<1, false, false>, (const void *)prompt_attn_kernel<1, true, false>,
+                          (const void *)prompt_attn_kernel<11, true, false>, (const void *)prompt_attn_kernel<1, false, true>,
+                          (const void *)prompt_attn_kernel<4, false, true>, (const void *)prompt_attn_kernel<32, false, true>}) {
       cudaFuncAttributes at;
       if (cudaFuncGetAttributes(&at, f) != cudaSuccess || at.numRegs != kRegs ||
           cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
@@ -952,12 +1096,22 @@ extern "C" pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *a, void *stre
       !encode_rows(dev, &p.tm_v, a->v, a->num_rows, a->num_kv_heads, a->v_stride, 1, kN) ||
       !encode_rows(dev, &p.tm_o, a->out, a->num_rows, heads, q_row, p.G, p.tokens))
     return PA_ERR_CUDA;
-  // As many CTAs as there can be units, and where those are few as they may be split into: those without a share exit.
+  // A CTA for every unit there can be, and for those that may be split (while there are fewer units than twice the SMs).  CTAs
+  // without a share exit.  Of many short ones a CTA takes several in turn (16 x 2048 tokens x 16 heads 213 us, 251 without, 8 x 4096
+  // 369 and 393, 5 x 6000 473 and 479; but 4 x 8192 681 and 671).  Their load warps work out the schedule alone, which holds for up to
+  // 1024 sequences.
   const int64_t span = 2 * p.tokens, units = (n + a->num_seqs * (span - 1)) / span * a->num_kv_heads;
-  const int64_t grid = units < 2 * dev->sms ? 2 * units : units;
+  const bool loop = units >= 2 * dev->sms && a->num_seqs <= 1024 && n <= 5120 * (int64_t)a->num_seqs;
+  const int64_t grid = std::max(units, std::min<int64_t>(2 * units, 4 * dev->sms));
   const pa_host::Launch run(dim3((unsigned)grid), dim3(kThreads), kSmem, stream);
-  const cudaError_t e = a->num_seqs <= 32         ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<0>, p)
-                        : a->num_seqs <= kThreads ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1>, p)
-                                                  : cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<11>, p);
+  cudaError_t e;
+  if (loop)
+    e = a->num_seqs <= 32    ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1, false, true>, p)
+        : a->num_seqs <= 128 ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<4, false, true>, p)
+                             : cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<32, false, true>, p);
+  else
+    e = a->num_seqs <= 32         ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1, false, false>, p)
+        : a->num_seqs <= kThreads ? cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<1, true, false>, p)
+                                  : cudaLaunchKernelEx(run.cfg(), prompt_attn_kernel<11, true, false>, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -189,6 +189,85 @@ def test_prompt_many_sequences():
         _compare(*_call(q, k, v, cu), q, k, v, cu)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("count,lo,hi,heads,group", [(20, 0, 420, 4, 8), (32, 100, 300, 2, 16), (33, 1, 350, 3, 8), (128, 1, 90, 1, 33), (129, 0, 150, 2, 12), (600, 1, 40, 1, 16)])
+def test_prompt_many_units(count, lo, hi, heads, group, f32):
+    """More units than CTAs run at once, so that they come one after the other: ragged ends, empty sequences, odd groups."""
+    rng = np.random.default_rng(count + f32)
+    g = torch.Generator(device="cuda").manual_seed(count)
+    cu = _cu(rng.integers(lo, hi + 1, size=count), 4)
+    q, k, v = _inputs(g, int(cu[-1]) + 40, heads, group)
+    _compare(*_call(q, k, v, cu, f32=f32), q, k, v, cu, f32=f32)
+
+
+def test_prompt_many_units_and_what_they_do_not_attend():
+    """Infinities and NaN of one sequence, of later tokens and of no sequence, among units that follow one another in a CTA; and where
+    rows attend them."""
+    rng = np.random.default_rng(21)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    cu = _cu(rng.integers(60, 500, size=24), 7)
+    T = int(cu[-1]) + 60
+    q, k, v = _inputs(g, T, 4, 8)
+    want, wl = _call(q, k, v, cu)
+    for bad in (math.inf, math.nan):
+        q2, k2, v2 = q.clone(), k.clone(), v.clone()
+        same = torch.ones(T, dtype=torch.bool, device="cuda")
+        for s in range(0, 24, 2):
+            a, b = int(cu[s]), int(cu[s + 1])
+            at = a + (b - a) // 2
+            for x in (k2, v2):
+                x[at:b, :, 1::5] = bad
+            q2[at:b], same[at:b] = bad, False
+        for x in (q2, k2, v2):
+            x[:7], x[int(cu[-1]):] = bad, bad
+        out, lse = _call(q2, k2, v2, cu)
+        assert torch.equal(out[same], want[same]) and torch.equal(lse[same], wl[same])
+    v2, clean = v.clone(), torch.ones_like(want, dtype=torch.bool)
+    for s in range(24):
+        a, b = int(cu[s]), int(cu[s + 1])
+        at = b - 1 - s
+        v2[at, 3, 2 * s] = math.inf
+        clean[at:b, 24:, 2 * s] = False
+    out, lse = _call(q, k, v2, cu)
+    assert torch.equal(out[clean], want[clean]) and torch.equal(lse, wl) and bool((out[~clean] == math.inf).all())
+
+
+def test_prompt_many_units_running_maximum():
+    g = torch.Generator(device="cuda").manual_seed(22)
+    cu = _cu([700] * 12)
+    n = int(cu[-1])
+    q, k, v = _inputs(g, n, 2, 16)
+    along = torch.nn.functional.normalize(torch.randn(128, generator=g, device="cuda"), dim=0)
+    size = (torch.arange(n, device="cuda") % 700 // 100) * 40.0
+    k = (k.float() * 0.2 + size[:, None, None] * along).bfloat16()
+    q = (q.float() * 0.2 + (torch.rand(n, 32, 1, generator=g, device="cuda") * 12) * along).bfloat16()
+    _compare(*_call(q, k, v, cu), q, k, v, cu)
+
+
+def test_prompt_many_units_captured_with_new_lengths():
+    """One graph, whose lengths change between replays from many units to few."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    q, k, v = _inputs(g, 9000, 2, 16)
+    cu = torch.zeros(41, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        B.prompt_attn(q, k, v, cu, out=out, lse=lse)
+        B.prompt_attn(q, k, v, cu, out=out, lse=lse)
+    for lens in ([200] * 40, [9000] + [0] * 39, [0] * 40, [1] * 40, list(range(100, 300, 5)), [0] * 39 + [300]):
+        c = _cu(lens)
+        cu.copy_(torch.from_numpy(c))
+        out.fill_(SENTINEL)
+        lse.fill_(SENTINEL)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wl = _call(q, k, v, c)
+        assert torch.equal(out, want) and torch.equal(lse, wl), lens[:3]
+        if sum(lens) < 3000:
+            _compare(out, lse, q, k, v, c)
+
+
 def test_prompt_is_the_same_packed_or_alone_dense_or_a_view():
     g = torch.Generator(device="cuda").manual_seed(17)
     lens, heads, group = [333, 128, 1, 700], 2, 6
