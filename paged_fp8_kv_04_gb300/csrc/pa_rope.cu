@@ -4,8 +4,8 @@
 // copy's); 32 tokens 1.6 us.  A thread's first elements asked for before the angles are worked out: no faster (registers, so fewer
 // threads).  A CTA takes kTokens tokens (one where there
 // are few): first a thread per (token, pair) works out cosine and sine into shared memory, then a
-// thread per 32 bytes of a head turns them, with 16-byte accesses where sizes and alignment allow
-// it and element by element where not.  A token's cosines serve all its heads.
+// thread per two accesses of a head turns them, of 16 bytes where alignment and the number of turning pairs allow
+// it and of 8, 4 or 2 where not (half layout: 8 elements at a time need a multiple of 16 turning ones).  A token's cosines serve all its heads.
 //
 // The angle of pair i at position p is p * freqs[i] / 2^64 turns: the 64-bit product modulo 2^64 is the
 // fraction of a turn without any rounding.  The nearest quarter turn is taken off it as an integer, and what is
@@ -39,21 +39,39 @@ struct RopeParams {
   float scale, sign;
 };
 
-// E consecutive elements as floats: 16 bytes, or one element.
+// E consecutive elements as floats: 16, 8, 4 or 2 bytes in one access.
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> {
+  using type = uint4;
+};
+template <>
+struct Raw<8> {
+  using type = uint2;
+};
+template <>
+struct Raw<4> {
+  using type = uint32_t;
+};
+template <>
+struct Raw<2> {
+  using type = uint16_t;
+};
+
 template <typename T, int E>
 struct Vec {
+  using R = typename Raw<E * sizeof(T)>::type;
   float x[E];
   __device__ __forceinline__ void load(const T *p) {
-    if constexpr (E == 1) {
-      if constexpr (sizeof(T) == 2)
-        x[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16);
-      else
-        x[0] = *reinterpret_cast<const float *>(p);
+    const R w = *reinterpret_cast<const R *>(p);
+    if constexpr (sizeof(R) == 2) {
+      x[0] = __uint_as_float((uint32_t)w << 16);
     } else {
-      const uint4 w = *reinterpret_cast<const uint4 *>(p);
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      alignas(16) uint32_t v[sizeof(R) / 4];
+      *reinterpret_cast<R *>(v) = w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < (int)sizeof(R) / 4; ++i) {
         if constexpr (sizeof(T) == 2) {
           x[2 * i] = pa::bf16lo(v[i]);
           x[2 * i + 1] = pa::bf16hi(v[i]);
@@ -64,32 +82,26 @@ struct Vec {
     }
   }
   __device__ __forceinline__ void store(T *p) const {
-    if constexpr (E == 1) {
-      if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(x[0]);
-      else
-        *reinterpret_cast<float *>(p) = x[0];
+    if constexpr (sizeof(R) == 2) {
+      *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(x[0]);
     } else {
-      uint32_t v[4];
+      alignas(16) uint32_t v[sizeof(R) / 4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < (int)sizeof(R) / 4; ++i) {
         if constexpr (sizeof(T) == 2)
           v[i] = pa::pack_bf16x2(x[2 * i], x[2 * i + 1]);
         else
           v[i] = __float_as_uint(x[i]);
       }
-      *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<R *>(p) = *reinterpret_cast<const R *>(v);
     }
   }
 };
 
-// T: uint16_t (bf16) or float; E: elements per access; HALF: the layout; TOK: tokens per CTA.
-template <typename T, int E, bool HALF, int TOK>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ __align__(16) float cs[TOK][kD / 2], sn[TOK][kD / 2];
-  const int tid = threadIdx.x, t0 = blockIdx.x * TOK, half = p.rot >> 1;
-  pa::pdl_wait();
-  pa::pdl_launch_dependents();
+// Cosine and sine of the CTA's tokens, a thread to a pair.
+template <int TOK>
+__device__ __forceinline__ void angles(const RopeParams &p, int t0, float (*cs)[kD / 2], float (*sn)[kD / 2]) {
+  const int tid = threadIdx.x, half = p.rot >> 1;
   for (int u = tid; u < TOK * (kD / 2); u += kThreads) {
     const int t = u / (kD / 2), i = u % (kD / 2);
     if (t0 + t >= p.T || i >= half) continue;
@@ -101,6 +113,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     cs[t][i] = (quarter == 1 || quarter == 2 ? -a : a) * p.scale;
     sn[t][i] = (quarter >= 2 ? -b : b) * p.scale * p.sign;
   }
+}
+
+// T: uint16_t (bf16) or float; E: elements per access; HALF: the layout; TOK: tokens per CTA.
+template <typename T, int E, bool HALF, int TOK>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ __align__(16) float cs[TOK][kD / 2], sn[TOK][kD / 2];
+  const int tid = threadIdx.x, t0 = blockIdx.x * TOK, half = p.rot >> 1;
+  pa::pdl_wait();
+  pa::pdl_launch_dependents();
+  angles<TOK>(p, t0, cs, sn);
   __syncthreads();
   // units of two accesses, of all heads of all the CTA's tokens
   constexpr int kUnits = kD / E / 2;
@@ -115,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                   : static_cast<T *>(p.k_out) + token * p.k_out_stride + (h - p.hq) * kD;
     if constexpr (HALF) {
       const bool turns = i * E < half;
-      const int a = turns ? i * E : p.rot + 2 * (i * E - half), b = turns ? half + i * E : a + E;
+      const int a = turns ? i * E : i * E + half, b = turns ? half + i * E : i * E + kD / 2;  // what does not turn: in halves too
       if (!turns && src == dst) continue;
       Vec<T, E> x, y;
       x.load(src + a);
@@ -144,15 +166,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       x.store(dst + 2 * i);
       y.store(dst + 2 * i + 1);
     } else {
+      // half a head apart, so that neighbours read neighbouring accesses (next to each other: 15.4 us, not 10.2, for 4096 tokens x 17
+      // heads, fp32)
       Vec<T, E> x[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[j].load(src + (2 * i + j) * E);
+      for (int j = 0; j < 2; ++j) x[j].load(src + j * (kD / 2) + i * E);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int a = (2 * i + j) * E;
+        const int a = j * (kD / 2) + i * E;
         if (a < p.rot) {
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
+            if (a + e >= p.rot) break;
             const float c = cs[t][(a + e) >> 1], s = sn[t][(a + e) >> 1], xa = x[j].x[e], xb = x[j].x[e + 1];
             x[j].x[e] = fmaf(xa, c, -(xb * s));
             x[j].x[e + 1] = fmaf(xb, c, xa * s);
@@ -164,6 +189,47 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
 }
 
+// Half layout with an odd number of turning pairs, not in place: the sides of a pair lie in accesses of their own.  A thread
+// takes 16 bytes of a head and reads the elements' other sides one by one, from L1 (8192 tokens x 17 heads, 34 elements turning,
+// bf16: 21 us; element by element throughout 33).
+template <typename T, int TOK>
+__global__ void __launch_bounds__(kThreads) rope_odd_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int E = 16 / sizeof(T), kUnits = kD / E;
+  __shared__ __align__(16) float cs[TOK][kD / 2], sn[TOK][kD / 2];
+  const int tid = threadIdx.x, t0 = blockIdx.x * TOK, half = p.rot >> 1;
+  pa::pdl_wait();
+  pa::pdl_launch_dependents();
+  angles<TOK>(p, t0, cs, sn);
+  __syncthreads();
+  const int per_token = p.heads * kUnits, left = min(TOK, p.T - t0) * per_token;
+  for (int u = tid; u < left; u += kThreads) {
+    const int t = TOK == 1 ? 0 : u / per_token, v = u - t * per_token, h = v / kUnits, a = v % kUnits * E;
+    const bool is_q = h < p.hq;
+    const int64_t token = t0 + t;
+    const T *src = is_q ? static_cast<const T *>(p.q) + token * p.q_stride + h * kD
+                        : static_cast<const T *>(p.k) + token * p.k_stride + (h - p.hq) * kD;
+    T *dst = is_q ? static_cast<T *>(p.q_out) + token * p.q_out_stride + h * kD
+                  : static_cast<T *>(p.k_out) + token * p.k_out_stride + (h - p.hq) * kD;
+    Vec<T, E> x;
+    x.load(src + a);
+    if (a < p.rot) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int j = a + e;
+        if (j < p.rot) {
+          const bool first = j < half;
+          const int i = first ? j : j - half;
+          Vec<T, 1> other;
+          other.load(src + (first ? j + half : i));
+          const float c = cs[t][i], s = sn[t][i];
+          x.x[e] = fmaf(x.x[e], c, first ? -(other.x[0] * s) : other.x[0] * s);
+        }
+      }
+    }
+    x.store(dst + a);
+  }
+}
+
 template <typename T, int E, bool HALF>
 cudaError_t launch(const RopeParams &p, bool few, void *stream) {
   const int tokens = few ? 1 : kTokens;
@@ -172,9 +238,22 @@ cudaError_t launch(const RopeParams &p, bool few, void *stream) {
              : cudaLaunchKernelEx(run.cfg(), rope_kernel<T, E, HALF, kTokens>, p);
 }
 
-template <typename T, int E>
-cudaError_t launch(const RopeParams &p, bool half, bool few, void *stream) {
-  return half ? launch<T, E, true>(p, few, stream) : launch<T, E, false>(p, few, stream);
+// `bytes`: what every row is aligned to, at most 16.
+template <typename T>
+cudaError_t launch(const RopeParams &p, bool half, int bytes, bool few, bool in_place, void *stream) {
+  constexpr int kWide = 16 / sizeof(T);
+  int e = bytes / (int)sizeof(T);
+  if (!half) return e == kWide ? launch<T, kWide, false>(p, few, stream) : launch<T, 1, false>(p, few, stream);
+  if (e == kWide && p.rot % 4 != 0 && !in_place) {
+    const pa_host::Launch run(dim3((unsigned)((p.T + (few ? 1 : kTokens) - 1) / (few ? 1 : kTokens))), dim3(kThreads), 0, stream);
+    return few ? cudaLaunchKernelEx(run.cfg(), rope_odd_kernel<T, 1>, p) : cudaLaunchKernelEx(run.cfg(), rope_odd_kernel<T, kTokens>, p);
+  }
+  while (e > 1 && (p.rot / 2) % e != 0) e /= 2;  // whole accesses on either side of the pairs
+  if constexpr (sizeof(T) == 2)
+    if (e == 8) return launch<T, 8, true>(p, few, stream);
+  return e == 4   ? launch<T, 4, true>(p, few, stream)
+         : e == 2 ? launch<T, 2, true>(p, few, stream)
+                  : launch<T, 1, true>(p, few, stream);
 }
 
 }  // namespace
@@ -231,16 +310,14 @@ extern "C" pa_status_t pa_rope(const pa_rope_args_t *a, void *stream) {
   p.scale = a->scale;
   p.sign = a->inverse ? -1.f : 1.f;
   const bool half = a->layout == PA_ROPE_HALF;
-  // 16-byte accesses: every row on a 16-byte boundary, and what turns in whole accesses
-  const int e = 16 / size;
-  const bool wide = a->rot_dim % (half ? 2 * e : e) == 0 && aligned(a->q, 16) && aligned(a->q_out, 16) && a->q_stride % e == 0 &&
-                    a->q_out_stride % e == 0 && (!keys || (aligned(a->k, 16) && aligned(a->k_out, 16) && a->k_stride % e == 0 && a->k_out_stride % e == 0));
+  // the widest accesses that every row's place allows
+  int bytes = 16;
+  for (const Rows &r : {q, qo, k, ko})
+    if (r.p != nullptr && r.bytes > 0)
+      while (!aligned(r.p, bytes) || r.stride % bytes != 0) bytes /= 2;
   // a CTA for every token while they would not fill the GPU otherwise (32 tokens: 1.6 us, 2.7 in fours; 16384: 38 us, 26 in fours)
   const bool few = n <= 2048;
-  cudaError_t st;
-  if (size == 2)
-    st = wide ? launch<uint16_t, 8>(p, half, few, stream) : launch<uint16_t, 1>(p, half, few, stream);
-  else
-    st = wide ? launch<float, 4>(p, half, few, stream) : launch<float, 1>(p, half, few, stream);
+  const bool in_place = a->q_out == a->q || (keys && a->k_out == a->k);
+  const cudaError_t st = size == 2 ? launch<uint16_t>(p, half, bytes, few, in_place, stream) : launch<float>(p, half, bytes, few, in_place, stream);
   return st == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

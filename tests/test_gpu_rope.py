@@ -68,6 +68,24 @@ def test_rope(rot, layout, dtype):
         assert a is inplace and b is None and torch.equal(inplace, qo)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_rope_every_number_of_pairs(layout, dtype):
+    """All accesses' widths: every rotation dimension, in place and not, at rows that are 16, 8, 4 and 2 bytes aligned."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    T, hq = 9, 3
+    pos = torch.randint(-500, 70000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    for rot in range(2, 130, 2):
+        freqs, _ = B.rope_frequencies(rot)
+        for shift in (0, 4, 2, 1):
+            buf = torch.randn(T, hq * 128 + 8, generator=g, device="cuda").to(dtype)
+            q = buf[:, shift:shift + hq * 128].unflatten(1, (-1, 128))
+            out, _ = B.rope(q, None, pos, freqs, layout=layout, q_out=torch.full((T, hq, 128), math.nan, dtype=dtype, device="cuda"))
+            _check(out, q, pos.cpu().numpy(), freqs, layout == "half")
+            B.rope(q, None, pos, freqs, layout=layout)
+            assert torch.equal(q, out), (rot, shift)
+
+
 @pytest.mark.parametrize("scaling", ["linear", "ntk", "yarn"])
 def test_rope_of_stretched_contexts(scaling):
     g = torch.Generator(device="cuda").manual_seed(1)
