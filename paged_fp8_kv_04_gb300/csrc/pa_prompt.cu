@@ -193,7 +193,7 @@ struct Unit {
 // What the units before this one have used, in phases of the barriers.
 struct Past {
   int ring = 0;              // blocks of keys and values
-  int units = 0, q0 = 0, q1 = 0, b0 = 0, b1 = 0;  // units, and of either slot units and key blocks
+  int units = 0, q0 = 0, q1 = 0, b0 = 0, b1 = 0;  // units, of either tile units with queries of it, of either slot key blocks
   int cut1 = 0;              // units with a second cut block (all have a first one)
   __device__ __forceinline__ int q(int t) const { return t ? q1 : q0; }
   __device__ __forceinline__ int b(int t) const { return t ? b1 : b0; }
@@ -202,7 +202,7 @@ struct Past {
     ring += 2 * u.blocks;
     units += 1;
     q0 += u.nb0 > 0;
-    q1 += u.nb1 > 0;
+    q1 += u.nb1 > 0 && !u.solo;
     b0 += u.nb0;
     b1 += u.nb1;
     cut1 += u.blocks > u.cut + 1;
@@ -536,7 +536,8 @@ __device__ bool issue_mmas(const Unit &u, const Past &past, uint32_t base, uint3
       }
       pa::umma_commit(bars + 8 * (B_S + t));
       if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
-      if (j + 1 == (t ? nb1 : nb0)) pa::umma_commit(bars + 8 * (B_QFREE + t));
+      // the last S that reads a tile's queries: either slot's own, or (solo) the last block's of both
+      if (solo ? i + 2 == 2 * (nb0 + nb1) : j + 1 == (t ? nb1 : nb0)) pa::umma_commit(bars + 8 * (B_QFREE + (solo ? 0 : t)));
     }
     __syncwarp();
     return ok;

@@ -268,6 +268,40 @@ def test_prompt_many_units_captured_with_new_lengths():
             _compare(out, lse, q, k, v, c)
 
 
+@pytest.mark.parametrize("heads,group", [(2, 16), (3, 8), (1, 33)])
+def test_prompt_units_that_are_split_and_in_turn(heads, group):
+    """Buffers for many sequences that hold few tokens: CTAs take units in turn, and the longest are split.  The same as with
+    buffers of their size, where every unit has a CTA of its own."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    q, k, v = _inputs(g, 9000, heads, group)
+    tokens = 128 // group * 2
+    for units in (100, 153, 170, 200, 250, 290):
+        n = units * tokens // heads
+        for lens in ([n], [n // 2, n - n // 2 - 9, 9], [n // 3, 0, n // 3, n // 4]):
+            cu = _cu(lens + [0] * (32 - len(lens)))
+            out, lse = _call(q, k, v, cu)
+            t = int(cu[-1])
+            small, sl = _call(q[:t], k[:t], v[:t], _cu(lens))
+            assert torch.equal(out[:t], small) and torch.equal(lse[:t], sl), (units, lens)
+            assert bool((out[t:] == SENTINEL).all())
+            if units == 170:
+                _compare(out, lse, q, k, v, cu)
+
+
+def test_prompt_infinities_in_fp32_outputs():
+    g = torch.Generator(device="cuda").manual_seed(25)
+    for lens, heads, group in (([300, 41], 1, 16), ([90] * 30, 4, 8)):
+        cu = _cu(lens)
+        q, k, v = _inputs(g, int(cu[-1]), heads, group)
+        want, wl = _call(q, k, v, cu, f32=True)
+        v2, clean = v.clone(), torch.ones_like(want, dtype=torch.bool)
+        for s, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+            v2[b - 20, 0, 100 - s] = -math.inf
+            clean[b - 20:b, :group, 100 - s] = False
+        out, lse = _call(q, k, v2, cu, f32=True)
+        assert torch.equal(out[clean], want[clean]) and torch.equal(lse, wl) and bool((out[~clean] == -math.inf).all())
+
+
 def test_prompt_is_the_same_packed_or_alone_dense_or_a_view():
     g = torch.Generator(device="cuda").manual_seed(17)
     lens, heads, group = [333, 128, 1, 700], 2, 6
