@@ -66,6 +66,8 @@ struct PromptParams {
   int32_t B, T, Hkv, G, tokens;  // tokens of a tile
   int32_t out_f32;
   int32_t sms;
+  int32_t first_split, aside;  // the first unit index that may be split; blocks' worth of units that a CTA takes beside its keys
+  uint64_t per_span;           // ceil(2^40 / (2 tokens)): x / (2 tokens) = x per_span / 2^40 for x < 2^25
   float fold;  // sm_scale * log2 e
 };
 
@@ -277,7 +279,7 @@ struct Schedule {
         if (a < 0 || b < a || b > p.T)
           bad = true;
         else
-          n[i] = (b - a + span - 1) / span;
+          n[i] = (int)(((uint64_t)(b - a + span - 1) * p.per_span) >> 40);
       }
     }
     if (bad && blockIdx.x == 0) raise(p, PA_DEV_BAD_QLEN);
@@ -285,8 +287,8 @@ struct Schedule {
     units = total * p.Hkv;
     if (units > 0 && units < 2 * p.sms) {
       const int few = longest() / 3;
-      const int longer = from((kMinSplit * kN + span - 1) / span) * p.Hkv, rest = from(few) * p.Hkv;  // that may be split; but the shortest
-      const int idle = p.sms - units, even = (p.sms + idle - 4 * kN * p.Hkv / span) / 3;
+      const int longer = from(p.first_split) * p.Hkv, rest = from(few) * p.Hkv;  // that may be split; but the shortest
+      const int idle = p.sms - units, even = (p.sms + idle - p.aside) / 3;
       splits = max(0, min(longer, max(idle, min(even, p.sms - rest))));
     }
   }
@@ -600,8 +602,13 @@ __device__ bool clean_unit(const Unit &u, const Past &past, uint32_t bars, uint8
   const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - kCleanWarp;
   uint32_t dirty = 0;
   for (int j = u.cut; j < u.blocks; ++j) {
-    if (!warp_wait(bars + 8 * (B_CUT + j - u.cut), past.cut(j - u.cut) & 1)) return false;
-    uint4 *at = reinterpret_cast<uint4 *>(smem + kRing + ((past.ring + 2 * j + 1) % STAGES) * kOperand + half * (kOperand / 2)) + lane;
+    // In the first unit a stage's first use: its barrier has one phase until these values have been looked through.  Else the
+    // MMA warp tells; and it is waited for there too, afterwards, since a wait knows a phase from the next one alone.
+    const int e = past.ring + 2 * j + 1;
+    const bool first = past.units == 0 && e < STAGES;
+    const uint32_t told = bars + 8 * (B_CUT + j - u.cut), phase = past.cut(j - u.cut) & 1;
+    if (!(first ? warp_wait(bar_full(bars, e), 0) : warp_wait(told, phase))) return false;
+    uint4 *at = reinterpret_cast<uint4 *>(smem + kRing + (e % STAGES) * kOperand + half * (kOperand / 2)) + lane;
     bool own = false;  // one of the sequence's own
 #pragma unroll 1
     for (int c0 = 0; c0 < kOperand / 32; c0 += 32 * kBatch) {  // pieces of this half
@@ -629,6 +636,7 @@ __device__ bool clean_unit(const Unit &u, const Past &past, uint32_t bars, uint8
     pa::fence_async_smem();
     __syncwarp();
     if (lane == 0) pa::mbar_arrive(bars + 8 * (B_CLEAN + j - u.cut));
+    if (first && !warp_wait(told, phase)) return false;
   }
   return true;
 }
@@ -898,8 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     pa::fence_barrier_init();
   }
   if (warp == kMmaWarp) pa::tmem_alloc(base + kMisc, kTmemCols);
-  pa::pdl_wait();
-  pa::pdl_launch_dependents();
+  __syncwarp();  // (before the register split, which whole warps take)
   // The load warp finds the CTA's units, the first one before the others need anything of it.  The units come in descending order.
   Unit u;
   Past past;
@@ -913,22 +920,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     }
     __syncwarp();
   };
-  if (ALL || warp == kLoadWarp) {
-    schedule.start();
-    more = schedule.find((int)blockIdx.x, u);
-    if (!ALL) post();
-  }
-  pa::tc_fence_before();
-  if (warp == kLoadWarp)  // (it needs nothing of the others)
-    asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
-  else
-    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-  pa::tc_fence_after();
-  if (!ALL && warp != kLoadWarp) more = posted_unit(smem, 0, u);
-  if (!more) {
-    if (warp == kMmaWarp) pa::tmem_dealloc(0, kTmemCols);
-    return;
-  }
+  auto begin = [&]() {
+    pa::pdl_wait();
+    pa::pdl_launch_dependents();
+    if (ALL || warp == kLoadWarp) {
+      schedule.start();
+      more = schedule.find((int)blockIdx.x, u);
+      if (!ALL) post();
+    }
+    pa::tc_fence_before();
+    if (warp == kLoadWarp)  // (it needs nothing of the others)
+      asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+    else
+      asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    pa::tc_fence_after();
+    if (!ALL && warp != kLoadWarp) more = posted_unit(smem, 0, u);
+  };
   auto next = [&]() {  // the unit after this one, if there is one
     past.add(u);
     ++round;
@@ -940,6 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   };
   if (warp < kSoftWarps) {
     pa::regs_inc<216>();
+    begin();
+    if (!more) return;
     const int t = warp >> 2;
     while (more) {
       const Row r = row_of(p, u);
@@ -954,11 +963,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       next();
     }
     if (lane == 0) {
-      bulk_write_wait();
+      bulk_read_wait();
       pa::mbar_arrive(bars + 8 * B_DONE);
     }
   } else {
     pa::regs_dec<72>();
+    begin();
+    if (!more) {
+      if (warp == kMmaWarp) pa::tmem_dealloc(0, kTmemCols);
+      return;
+    }
     if (warp == kLoadWarp) {
       Loads done;
       while (more) {
@@ -1092,6 +1106,10 @@ extern "C" pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *a, void *stre
   p.out_f32 = a->out_dtype == PA_OUT_F32;
   p.fold = (float)((double)a->sm_scale * 1.4426950408889634);
   p.sms = dev->sms;
+  const int64_t span = 2 * p.tokens;
+  p.first_split = (int)((kMinSplit * kN + span - 1) / span);
+  p.aside = (int)(4 * kN * a->num_kv_heads / span);
+  p.per_span = ((1ull << 40) + span - 1) / span;
   if (!encode_rows(dev, &p.tm_q, a->q, a->num_rows, heads, a->q_stride, p.G, p.tokens) ||
       !encode_rows(dev, &p.tm_k, a->k, a->num_rows, a->num_kv_heads, a->k_stride, 1, kN) ||
       !encode_rows(dev, &p.tm_v, a->v, a->num_rows, a->num_kv_heads, a->v_stride, 1, kN) ||
@@ -1101,7 +1119,7 @@ extern "C" pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *a, void *stre
   // without a share exit.  Of many short ones a CTA takes several in turn (16 x 2048 tokens x 16 heads 213 us, 251 without, 8 x 4096
   // 369 and 393, 5 x 6000 473 and 479; but 4 x 8192 681 and 671).  Their load warps work out the schedule alone, which holds for up to
   // 1024 sequences.
-  const int64_t span = 2 * p.tokens, units = (n + a->num_seqs * (span - 1)) / span * a->num_kv_heads;
+  const int64_t units = (n + a->num_seqs * (span - 1)) / span * a->num_kv_heads;
   const bool loop = units >= 2 * dev->sms && a->num_seqs <= 1024 && n <= 5120 * (int64_t)a->num_seqs;
   const int64_t grid = std::max(units, std::min<int64_t>(2 * units, 4 * dev->sms));
   const pa_host::Launch run(dim3((unsigned)grid), dim3(kThreads), kSmem, stream);
