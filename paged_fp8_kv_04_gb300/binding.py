@@ -3,8 +3,8 @@
 Every step of the attention runs in the library's CUDA kernels; this module checks
 tensor dtypes and devices, passes data pointers and the current torch stream, and
 raises on a non-OK status.  It fails loudly when the shared library is missing.
-The cache operators between two decode steps are marshalled by a compiled module
-(csrc/pa_torch.cpp), since their kernels are shorter than the same checks in Python.
+The cache operators between two decode steps and those on a prompt's way into the cache are marshalled
+by a compiled module (csrc/pa_torch.cpp), since most of their kernels are shorter than the same checks in Python.
 """
 from __future__ import annotations
 

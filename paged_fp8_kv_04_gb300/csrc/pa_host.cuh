@@ -1,5 +1,5 @@
 // pa_host.cuh -- host-side argument checks shared by the cache operators (pa_mass.cu,
-// pa_evict.cu, pa_beam.cu).
+// pa_evict.cu, pa_beam.cu) and those on a prompt's way into the cache (pa_paging.cu, pa_rope.cu, pa_prompt.cu).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -10,13 +10,24 @@
 //                    rounding of 2^-9 per weight, as that of the output), V as the B operand, MN-major, as TMA left it
 //
 // Rows of a tile are (token, head of the group) pairs, 128 / group_size tokens with all query heads of a KV head: they
-// share its keys, short prompts fill a tile as well as long ones do, and the diagonal cuts few tokens.  A CTA has two tiles, so that the
-// tensor core works on one while the other's weights are computed: S0 S1 | PV0 S0' PV1 S1' | ...
+// share its keys, short prompts fill a tile as well as long ones do, and the diagonal cuts few tokens.  A CTA has two tiles (a unit),
+// so that the tensor core works on one while the other's weights are computed: PV0 S0' | PV1 S1' | ...  Where there are fewer units
+// than SMs a unit's tiles go to a CTA each, and its two slots take the even and the odd blocks of keys.  Of many short sequences
+// a CTA takes several units, claimed from the launch queue, whose first scores are there when the rows of the one before are written.
 //
-// Warp roles (384 threads): warps 0-3 and 4-7 are the softmax of tiles 0 and 1; warp 8 fetches tiles by TMA; one lane
-// of warp 9 issues the MMAs; warps 10 and 11 look through the values of the blocks that the diagonal or the sequence's end cuts: an
+// Warp roles (384 threads): warps 0-3 and 4-7 are the softmax of slots 0 and 1; warp 8 finds the units and fetches tiles by TMA; one
+// lane of warp 9 issues the MMAs; warps 10 and 11 look through the values of the blocks that the diagonal or the sequence's end cuts: an
 // infinity or NaN there must not reach rows that do not attend it (0 * inf), so it is replaced by 0, and rows that do attend it
 // get it in the epilogue.  Every wait is bounded; TMEM is released on every path.
+//
+// Bound by the tensor core at what its power allows: 2600 cycles for two tiles and a block (16.8 MFLOP), of 2054 that the MMAs take
+// on constant data, hardly fewer with the softmax left out (2520), and a cuBLAS product of 8192^3 comes to the same rate.  32768
+// tokens x 16 heads 2370 us (1.86 PFLOP/s, 0.98 of cuBLAS' 1887), 16384 615 us; shorter ones by what a CTA takes beside its blocks (some
+// 5 us alone, 2.7 between units of one CTA) and by SMs that are done early: 2048 tokens 21 us, 13 prompts of 200 .. 4001 tokens x 4 KV
+// heads 213 us (0.74 of the rate), 16 tokens 6.4 us.
+// Measured on the way: one warp per tile to issue the MMAs 821 us, not 738, for 16384 tokens (both tiles' softmax at once); weights
+// worked out with the maximum so far while the block's own is found 637, not 597; keys split over a cluster of two CTAs and joined
+// through shared memory 23.4 us, not 21, for 2048 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -729,10 +740,14 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &pa
 #pragma unroll
     for (int k = 0; k < kN; k += 32) tmem_wait32(s + k);
     const int key0 = u.block(t, j) * kN;
-    if (key0 + kN > first) {  // the diagonal may cut this block
+    if (key0 + kN > first) {  // the diagonal may cut this block (a bit for each column: 0.1 us less than comparisons, for 128 tokens)
       const int seen = r.token - key0;
 #pragma unroll
-      for (int k = 0; k < kN; ++k) s[k] = k <= seen ? s[k] : 0xFF800000u;
+      for (int k0 = 0; k0 < kN; k0 += 32) {
+        const uint32_t bits = seen >= k0 + 31 ? ~0u : seen < k0 ? 0u : (2u << (seen - k0)) - 1u;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k0 + k] = (bits >> k) & 1u ? s[k0 + k] : 0xFF800000u;
+      }
     }
     uint32_t w[32];
     const float peak = peak_of(s) * c;
@@ -762,6 +777,29 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &pa
     publish(s_at + kN / 4, w, bars + 8 * (B_P + 2 * t + 1));
   }
   return true;
+}
+
+// N columns of a tile's O, scaled; of a solo tile, whose other slot's lie 128 columns on, the sum of both.
+template <int N>
+__device__ __forceinline__ void o_columns(uint32_t at, bool solo, float mine, float others, uint32_t *o) {
+#pragma unroll
+  for (int k = 0; k < N; k += 32) tmem_ld32(at + k, o + k);
+  if (solo) {
+    uint32_t x[N];
+#pragma unroll
+    for (int k = 0; k < N; k += 32) tmem_ld32(at + 128 + k, x + k);
+#pragma unroll
+    for (int k = 0; k < N; k += 32) tmem_wait32(o + k);
+#pragma unroll
+    for (int k = 0; k < N; k += 32) tmem_wait32(x + k);
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), mine, __uint_as_float(x[e]) * others));
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k += 32) tmem_wait32(o + k);
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mine);
+  }
 }
 
 // The tile's rows: O / l and the log-sum-exp.  A solo tile's O is the sum of both slots', which lie in the same lanes of TMEM: each
@@ -800,8 +838,9 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
   const int64_t at = (int64_t)(u.row0 + r.token) * hq + u.h * p.G + (r.row - r.tk * p.G);
   const bool writes = r.live && !(u.solo && t == 1);  // a row's lse, and what else is one thread's
   if (writes && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
-  mine /= l;
-  others /= l;
+  const float inv = 1.f / l;
+  mine *= inv;
+  others *= inv;
   const bool whole = !p.out_f32 && first + p.tokens <= u.len;  // else the tile's box reaches past the sequence
   const int size = p.out_f32 ? 4 : 2, cols = 128 / size;
   int pass = 0;
@@ -813,35 +852,21 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
       if (leader) bulk_read_wait();
       together();
     }
-#pragma unroll 1
-    for (int k = k0; k < k0 + cols; k += 32) {
+    uint4 *row = reinterpret_cast<uint4 *>(rows + r.row * 128);
+    if (p.out_f32) {
       uint32_t o[32];
-      tmem_ld32(o_at + k, o);
-      if (u.solo) {
-        uint32_t x[32];
-        tmem_ld32(o_at + 128 + k, x);
-        tmem_wait32(x);
-        tmem_wait32(o);
+      o_columns<32>(o_at + k0, u.solo, mine, others, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), mine, __uint_as_float(x[e]) * others));
-      } else {
-        tmem_wait32(o);
+      for (int e = 0; e < 8; ++e) row[e ^ (r.row & 7)] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+    } else {
+      uint32_t o[64];
+      o_columns<64>(o_at + k0, u.solo, mine, others, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mine);
-      }
-      uint4 *row = reinterpret_cast<uint4 *>(rows + r.row * 128);
-      if (p.out_f32) {
+      for (int e = 0; e < 8; ++e) {
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) row[e ^ (r.row & 7)] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-      } else {
-        const int piece = (k - k0) >> 3;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pa::pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]), __uint_as_float(o[8 * e + 2 * i + 1]));
-          row[(piece + e) ^ (r.row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int i = 0; i < 4; ++i) w[i] = pa::pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]), __uint_as_float(o[8 * e + 2 * i + 1]));
+        row[e ^ (r.row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     if (whole) {

@@ -1,4 +1,4 @@
-// pa_torch.cpp -- the torch side of the cache operators: checks of the tensors (the library sees only
+// pa_torch.cpp -- the torch side of the cache operators and of a prompt's way into the cache: checks of the tensors (the library sees only
 // pointers), allocation of the outputs that are not given, and the call into libpagedfp8.
 //
 // These calls come several times per decode step, and their kernels take a few microseconds.  Checked
