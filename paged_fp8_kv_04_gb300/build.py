@@ -98,7 +98,7 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False) -> st
         return out
     os.makedirs(BUILD_DIR, exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [nvcc(), ARCH, "--threads=0", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
            "-I" + INCLUDE, "-I" + CSRC, "-o", tmp] + (["-DPA_TRACE"] if trace else []) + sources()
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
