@@ -617,7 +617,7 @@ typedef struct pa_page_assign_args {
   int32_t *positions;            /* nullable out: [num_rows] position of every row in its request (pa_rope's) */
   uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT, PA_DEV_BAD_QLEN, PA_DEV_BAD_PAGE, PA_DEV_PAGE_POOL */
   int64_t num_pages;             /* 1 .. 2^31 - 1: pages of the cache */
-  int32_t num_seqs;              /* >= 0 */
+  int32_t num_seqs;              /* 0 .. 2^30 */
   int32_t num_rows;              /* >= 0: rows of the step, padding behind the last request's among them */
   int32_t block_table_stride;
   int32_t page_size;             /* 16, 32, 64 or 128 */
@@ -656,7 +656,7 @@ typedef struct pa_page_release_args {
   int32_t *num_free_out;         /* [1]; may be num_free */
   uint32_t *status;              /* nullable: PA_DEV_BAD_CONTEXT, PA_DEV_BAD_PAGE, PA_DEV_PAGE_POOL */
   int64_t num_pages;             /* 1 .. 2^31 - 1 */
-  int32_t num_seqs;              /* >= 0 */
+  int32_t num_seqs;              /* 0 .. 2^30 */
   int32_t block_table_stride;
   int32_t page_size;             /* 16, 32, 64 or 128 */
   int32_t free_capacity;         /* >= 1 */
@@ -737,7 +737,8 @@ typedef struct pa_prompt_attn_args {
  * taken before), so an fp32 output is good to 2^-9 of its terms and serves pa_lse_merge, which joins it with the part of a context
  * that is already cached (a decode over the cached pages with an fp32 output and lse).  What a row does not attend has no effect on it,
  * infinities and NaN included: later tokens, other sequences, rows of no sequence; rows of no sequence are left as they are.
- * A sequence whose cu does not lie in order within 0 .. num_rows is left out (PA_DEV_BAD_QLEN).  One kernel launch on
+ * A sequence whose cu does not lie in order within 0 .. num_rows is left out (PA_DEV_BAD_QLEN); where others then overlap, rows may be left
+ * unwritten.  A sequence's last bits may depend on how many rows the call has besides: equal calls give equal bits.  One kernel launch on
  * `stream`; no host synchronisation, no allocation.  out and lse share no byte with each other or an input.  PA_ERR_INVALID_ARG
  * for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer or stride, PA_ERR_UNSUPPORTED for a shape outside the limits
  * above, PA_ERR_CUDA when the launch fails. */

@@ -11,6 +11,7 @@
 // pages given back 3.5 us (back to back; an empty kernel 1.5).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -24,6 +25,7 @@ using pa_host::aligned;
 
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxCluster = 16;
+constexpr int kMaxSeqs = 1 << 30;  // requests are counted in 32 bits, chunks of them ahead
 
 struct AssignParams {
   const int32_t *L, *cu, *free_pages, *num_free;
@@ -298,15 +300,15 @@ __global__ void __launch_bounds__(kMaxThreads) page_release_kernel(const __grid_
 
 // The current device's SM count, looked up with the kernels' opt-in to clusters of 16 once per device; 0 if a call fails.
 int paging_device() {
-  static int known[pa_host::kMaxDevices];
+  static std::atomic<int> known[pa_host::kMaxDevices];
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= pa_host::kMaxDevices) return 0;
-  if (known[dev] > 0) return known[dev];
+  if ((sms = known[dev].load(std::memory_order_acquire)) > 0) return sms;
   for (const void *f : {(const void *)page_assign_kernel<1, false>, (const void *)page_assign_kernel<4, false>,
                         (const void *)page_release_kernel<1, false>, (const void *)page_release_kernel<4, false>})
     if (cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  known[dev] = sms;
+  known[dev].store(sms, std::memory_order_release);
   return sms;
 }
 
@@ -342,7 +344,7 @@ cudaError_t launch(void (*one)(P), void (*four)(P), void (*wide)(P), const Shape
 
 extern "C" pa_status_t pa_page_assign(const pa_page_assign_args_t *a, void *stream) {
   if (a == nullptr) return PA_ERR_INVALID_ARG;
-  if (a->num_seqs < 0 || a->num_rows < 0 || a->block_table_stride < 1 || a->free_capacity < 1 || a->num_pages < 1 ||
+  if (a->num_seqs < 0 || a->num_seqs > kMaxSeqs || a->num_rows < 0 || a->block_table_stride < 1 || a->free_capacity < 1 || a->num_pages < 1 ||
       a->num_pages > INT_MAX || a->reserved != 0)
     return PA_ERR_INVALID_ARG;
   if (pa_host::log2_page(a->page_size) < 0) return PA_ERR_UNSUPPORTED;
@@ -403,7 +405,7 @@ extern "C" pa_status_t pa_page_assign(const pa_page_assign_args_t *a, void *stre
 
 extern "C" pa_status_t pa_page_release(const pa_page_release_args_t *a, void *stream) {
   if (a == nullptr) return PA_ERR_INVALID_ARG;
-  if (a->num_seqs < 0 || a->block_table_stride < 1 || a->free_capacity < 1 || a->num_pages < 1 || a->num_pages > INT_MAX ||
+  if (a->num_seqs < 0 || a->num_seqs > kMaxSeqs || a->block_table_stride < 1 || a->free_capacity < 1 || a->num_pages < 1 || a->num_pages > INT_MAX ||
       a->reserved != 0)
     return PA_ERR_INVALID_ARG;
   if (pa_host::log2_page(a->page_size) < 0) return PA_ERR_UNSUPPORTED;

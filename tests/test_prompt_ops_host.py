@@ -63,6 +63,16 @@ def test_page_release_refusals(lib, over, want):
     assert lib.pa_page_release(None, None) == INVALID
 
 
+FAR = {f: i << 44 for i, f in enumerate(("context_lens", "cu_seqlens_q", "block_table", "new_lens", "free_pages"), 1)}
+
+
+@pytest.mark.parametrize("seqs", [2**30 + 1, 2**31 - 1])
+def test_paging_of_more_requests_than_the_kernels_count(lib, seqs):
+    assert lib.pa_page_assign(ctypes.byref(_fill(B.PageAssignArgs, ASSIGN, dict(FAR, num_seqs=seqs))), None) == INVALID
+    far = {f: at for f, at in FAR.items() if f != "cu_seqlens_q"}
+    assert lib.pa_page_release(ctypes.byref(_fill(B.PageReleaseArgs, RELEASE, dict(far, num_seqs=seqs))), None) == INVALID
+
+
 ROPE = dict(q_stride=2048, k_stride=128, q_out_stride=2048, k_out_stride=128, num_tokens=0, num_q_heads=16, num_kv_heads=1, head_dim=128,
             rot_dim=128, dtype=0, layout=0, inverse=0, scale=1.0)
 # one buffer of 18 heads: 16 queries, a key, a value
