@@ -737,6 +737,7 @@ typedef struct pa_prompt_attn_args {
  * taken before), so an fp32 output is good to 2^-9 of its terms and serves pa_lse_merge, which joins it with the part of a context
  * that is already cached (a decode over the cached pages with an fp32 output and lse).  What a row does not attend has no effect on it,
  * infinities and NaN included: later tokens, other sequences, rows of no sequence; rows of no sequence are left as they are.
+ * A row whose scores are all -inf has an output of NaN (0 / 0) and an lse of -inf.
  * A sequence whose cu does not lie in order within 0 .. num_rows is left out (PA_DEV_BAD_QLEN); where others then overlap, rows may be left
  * unwritten.  A sequence's last bits may depend on how many rows the call has besides: equal calls give equal bits.  One kernel launch on
  * `stream`; no host synchronisation, no allocation.  out and lse share no byte with each other or an input.  PA_ERR_INVALID_ARG

@@ -33,6 +33,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -752,7 +753,7 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &pa
     uint32_t w[32];
     const float peak = peak_of(s) * c;
     if (j == 0) {
-      m = peak;
+      m = fmaxf(peak, -FLT_MAX);  // (scores of -inf alone: weights of 0, not of 2^(inf - inf), so that a later block counts)
     } else {
       const bool grown = peak > m + kSlack;
       if (__any_sync(~0u, grown)) {

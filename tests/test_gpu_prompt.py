@@ -92,6 +92,23 @@ def test_prompt_of_many_blocks(lens, heads, group):
     _compare(*_call(q, k, v, cu, f32=True), q, k, v, cu, f32=True)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("count,dead,n,heads,group", [(1, 1, 2, 1, 16), (1, 200, 700, 1, 16), (2, 128, 390, 1, 3), (1, 300, 1100, 2, 1), (90, 200, 400, 2, 16), (90, 130, 260, 4, 7)])
+def test_prompt_scores_of_minus_infinity(count, dead, n, heads, group, f32):
+    """The first keys of each sequence score -inf: weights of 0 for a row that attends others too, which is then as if they were
+    not there; no row's else (0 / 0, and an lse of -inf)."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    cu = _cu([n] * count)
+    q, k, v = _inputs(g, n * count, heads, group)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k.view(count, n, heads, 128)[:, :dead, :, 0] = -math.inf
+    out, lse = _call(q, k, v, cu, f32=f32)
+    for a in cu[:-1][:: max(1, count // 3)].tolist():
+        assert bool(out[a : a + dead].isnan().all()) and bool((lse[a : a + dead] == -math.inf).all())
+        at = slice(a + dead, a + n)
+        _compare(out[at], lse[at], q[at], k[at], v[at], _cu([n - dead]), f32=f32)
+
+
 @pytest.mark.parametrize("sm", [0.001, 0.5, 2.0])
 def test_prompt_scales(sm):
     g = torch.Generator(device="cuda").manual_seed(11)
