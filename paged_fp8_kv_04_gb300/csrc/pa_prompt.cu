@@ -99,14 +99,15 @@ enum {
   B_CUT = B_O + 2,                  // [2] the values of the unit's first or second cut block have landed
   B_CLEAN = B_CUT + 2,              // [2] and been looked through
   B_UNIT = B_CLEAN + 2,             // [4] the unit has been found
-  B_CLAIM = B_UNIT + 4,             // the answer of the launch queue
+  B_LEFT = B_UNIT + 4,              // [4] every warp that the unit was found for is done with it
+  B_CLAIM = B_LEFT + 4,             // the answer of the launch queue
   B_DONE = B_CLAIM + 1,             // the softmax warps are done with TMEM
   B_MMA = B_DONE + 1,               // every MMA is complete
   kNumBars = B_MMA + 1
 };
 constexpr int kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;  // TMEM address, padding, a sequence
-constexpr int kDirty = kMisc + 16;           // [2 units][2 warps] dirty blocks
-constexpr int kClaim = kDirty + 16;          // the launch queue's answer
+constexpr int kDirty = kMisc + 16;           // [4 units][2 warps] dirty blocks
+constexpr int kClaim = kDirty + 32;          // the launch queue's answer
 constexpr int kPosted = kClaim + 16;         // [4] units
 constexpr int kRed = kPosted + 4 * 48;       // [2][warps] of the schedule's sums
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
@@ -404,8 +405,8 @@ __device__ __forceinline__ int claimed(uint32_t answer) {
   return any ? (int)x : -1;
 }
 
-// The units that the load warp has found for the others: a place for each of the last four (it is ahead of them by less than
-// three), and a barrier for each.
+// The units that the load warp has found for the others: a place for each of the last four, and two barriers: found, and left by all.
+// (A slot without a tile of its own runs ahead of the other, or lags behind it, by any number of units.)
 struct Slot {
   int row0, len, h, tok0, tok1, nb0, nb1, blocks, cut, solo, pad[2];
 };
@@ -643,8 +644,8 @@ __device__ bool clean_unit(const Unit &u, const Past &past, uint32_t bars, uint8
       }
     }
     dirty |= __any_sync(~0u, own) ? 1u << (j - u.cut) : 0u;
-    // (the unit's word, read by the softmax warps once its last product is complete: those of the unit before have read theirs)
-    if (lane == 0) reinterpret_cast<volatile uint32_t *>(smem + kDirty)[2 * (past.units & 1) + half] = dirty;
+    // (the unit's word, read by the softmax warps once its last product is complete)
+    if (lane == 0) reinterpret_cast<volatile uint32_t *>(smem + kDirty)[2 * (past.units & (kUnits - 1)) + half] = dirty;
     pa::fence_async_smem();
     __syncwarp();
     if (lane == 0) pa::mbar_arrive(bars + 8 * (B_CLEAN + j - u.cut));
@@ -834,7 +835,7 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
     others = pa::fast_exp2(m1 - m);
     l = l0 * mine + l1 * others;
   }
-  const volatile uint32_t *dirt = reinterpret_cast<const volatile uint32_t *>(smem + kDirty) + 2 * (past.units & 1);
+  const volatile uint32_t *dirt = reinterpret_cast<const volatile uint32_t *>(smem + kDirty) + 2 * (past.units & (kUnits - 1));
   const uint32_t dirty = dirt[0] | dirt[1];
   const int64_t at = (int64_t)(u.row0 + r.token) * hq + u.h * p.G + (r.row - r.tk * p.G);
   const bool writes = r.live && !(u.solo && t == 1);  // a row's lse, and what else is one thread's
@@ -928,7 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     prefetch_map(&p.tm_k);
     prefetch_map(&p.tm_v);
     for (int i = 0; i < kNumBars; ++i)
-      pa::mbar_init(bars + 8 * i, i >= B_P && i < B_P + 4 ? 4 : i == B_DONE ? kSoftWarps : i >= B_CLEAN && i < B_CLEAN + 2 ? 2 : 1);
+      pa::mbar_init(bars + 8 * i, i >= B_P && i < B_P + 4 ? 4 : i == B_DONE ? kSoftWarps : i >= B_CLEAN && i < B_CLEAN + 2 ? 2
+                                                              : i >= B_LEFT && i < B_LEFT + 4 ? kThreads / 32 - 1 : 1);
     pa::fence_barrier_init();
   }
   if (warp == kMmaWarp) pa::tmem_alloc(base + kMisc, kTmemCols);
@@ -963,6 +965,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     if (!ALL && warp != kLoadWarp) more = posted_unit(smem, 0, u);
   };
   auto next = [&]() {  // the unit after this one, if there is one
+    if (LOOP) {
+      __syncwarp();
+      if (lane == 0) pa::mbar_arrive(bars + 8 * (B_LEFT + (round & (kUnits - 1))));
+    }
     past.add(u);
     ++round;
     more = false;
@@ -1013,6 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         const int x = claimed(base + kClaim);
         __syncwarp();
         ++round;
+        if (round >= kUnits) ok = warp_wait(bars + 8 * (B_LEFT + (round & (kUnits - 1))), (round / kUnits - 1) & 1);
+        if (!ok) break;
         more = x >= 0 && schedule.find(x, u);
         pa::fence_async_smem();  // the answer has been read
         post();
