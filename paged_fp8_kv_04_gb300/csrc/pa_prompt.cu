@@ -153,6 +153,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
       : "memory");
 }
+// 16 columns
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -673,62 +681,104 @@ __device__ __noinline__ void add_not_finite(const uint16_t *v, int64_t v_stride,
   }
 }
 
-__device__ __forceinline__ float peak_of(const uint32_t (&s)[kN]) {
+template <int N>
+__device__ __forceinline__ float peak_of(const uint32_t *s) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < kN; k += 8)
+  for (int k = 0; k < N; k += 8)
 #pragma unroll
     for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[k + 2 * e]), __uint_as_float(s[k + 2 * e + 1]));
   return max3(fmaxf(top[0], top[1]), top[2], top[3]);
 }
 
-// 2^(c s - m) of half a block as bf16 pairs; their sum, before the rounding.
-__device__ __forceinline__ float weights(const uint32_t *s, float c, float m, uint32_t (&w)[32]) {
-  const pa::f32x2 c2 = pa::pack2(c, c), m2 = pa::pack2(-m, -m);
+// 2^(c s - m) of N columns as bf16 pairs; they are added, before the rounding, to the half block's sums.
+struct Sums {
   pa::f32x2 part[2] = {pa::pack2(0.f, 0.f), pa::pack2(0.f, 0.f)};
+  __device__ __forceinline__ float all() const {
+    float x, y;
+    pa::unpack2(pa::add2(part[0], part[1]), x, y);
+    return x + y;
+  }
+};
+template <int N>
+__device__ __forceinline__ void weights(const uint32_t *s, float c, float m, uint32_t *w, Sums &sums) {
+  const pa::f32x2 c2 = pa::pack2(c, c), m2 = pa::pack2(-m, -m);
 #pragma unroll
-  for (int e = 0; e < kN / 2; e += 2) {
+  for (int e = 0; e < N; e += 2) {
     float a, b;
     pa::unpack2(pa::fma2(pa::pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, m2), a, b);
     a = pa::fast_exp2(a);
     b = pa::fast_exp2(b);
-    part[(e >> 1) & 1] = pa::add2(part[(e >> 1) & 1], pa::pack2(a, b));
+    sums.part[(e >> 1) & 1] = pa::add2(sums.part[(e >> 1) & 1], pa::pack2(a, b));
     w[e >> 1] = pa::pack_bf16x2(a, b);
   }
-  float x, y;
-  pa::unpack2(pa::add2(part[0], part[1]), x, y);
-  return x + y;
 }
 
-__device__ __forceinline__ void publish(uint32_t at, const uint32_t (&w)[32], uint32_t bar) {
-  tmem_st32(at, w);
+__device__ __forceinline__ void published(uint32_t bar) {
   tmem_wait_st();
   pa::tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) pa::mbar_arrive(bar);
 }
 
-// A row of a tile: TMEM lane and thread.
+// A row of a tile: TMEM lane and thread.  A warp's rows are in the order of their tokens.
 struct Row {
   int row, tk, token;  // of the tile, its token of the tile and of the sequence
   bool live;
+  int first, last;     // tokens of the sequence: of the warp's first row, and of its last one that is live (or less)
   uint32_t lanes;      // of the warp, in a TMEM address
 };
-__device__ __forceinline__ Row row_of(const PromptParams &p, const Unit &u) {
+__device__ __forceinline__ Row row_of(const PromptParams &p, const Unit &u, int tk, int tk0, int tk1) {  // tk0, tk1: of the warp's first and last row
   const int warp = threadIdx.x >> 5;
   Row r;
   r.row = 32 * (warp & 3) + (threadIdx.x & 31);
-  r.tk = r.row / p.G;
+  r.tk = tk;
   r.token = u.tok(warp >> 2) + r.tk;
   r.live = r.tk < p.tokens && r.token < u.len;
+  r.first = u.tok(warp >> 2) + tk0;
+  r.last = tk0 < p.tokens ? min(u.tok(warp >> 2) + min(tk1, p.tokens - 1), u.len - 1) : -1;
   r.lanes = (uint32_t)(32 * (warp & 3)) << 16;
   return r;
 }
 
+// 32 columns of S from the g-th, -inf where a row does not attend.
+__device__ __forceinline__ void cut_scores(const Row &r, int key0, int g, uint32_t s_at, uint32_t (&s)[32]) {
+  tmem_ld32(s_at + 32 * g, s);
+  tmem_wait32(s);
+  key0 += 32 * g;
+  if (r.first - key0 >= 31) return;
+  const int seen = r.token - key0;  // a bit for each column (0.1 us less than comparisons, for 128 tokens)
+  const uint32_t bits = seen >= 31 ? ~0u : seen < 0 ? 0u : (2u << seen) - 1u;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) s[k] = (bits >> k) & 1u ? s[k] : 0xFF800000u;
+}
+
+// Where a row's scores grew by more than the slack: O and l are scaled.
+__device__ __forceinline__ bool raise_max(float peak, uint32_t o_at, uint32_t bar_o, uint32_t phase_o, float &m, float &l) {
+  const bool grown = peak > m + kSlack;
+  if (!__any_sync(~0u, grown)) return true;
+  const float alpha = grown ? pa::fast_exp2(m - peak) : 1.f;
+  if (grown) m = peak;
+  l *= alpha;
+  if (!warp_wait(bar_o, phase_o)) return false;
+  pa::tc_fence_after();
+  uint32_t w[32];
+#pragma unroll 1
+  for (int k = 0; k < kD; k += 32) {
+    tmem_ld32(o_at + k, w);
+    tmem_wait32(w);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+    tmem_st32(o_at + k, w);
+  }
+  return true;
+}
+
 // The weights of all blocks; m: what is subtracted from the scaled scores, in units of log2, l: the weights' sum.
+template <bool LOOP>
 __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &past, const Row &r, uint32_t bars, float &m, float &l) {
   const int t = threadIdx.x >> 7, nb = u.nb(t), before = past.b(t);
-  const uint32_t s_at = r.lanes + 128 * t, o_at = r.lanes + 256 + 128 * t;
+  const uint32_t s_at = r.lanes + 128 * t, o_at = r.lanes + 256 + 128 * t, bar_o = bars + 8 * (B_O + t), bar_p = bars + 8 * (B_P + 2 * t);
   const int first = u.tok(t);
   const float c = p.fold;
   m = -INFINITY;
@@ -736,13 +786,51 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &pa
   for (int j = 0; j < nb; ++j) {
     if (!warp_wait(bars + 8 * (B_S + t), (before + j) & 1)) return false;
     pa::tc_fence_after();
-    uint32_t s[kN];
+    const int key0 = u.block(t, j) * kN;
+    const uint32_t phase_o = (before + j - 1) & 1;
+    // The diagonal may cut it.  LOOP, whose units are many and short: 32 columns at a time, read twice, and those that no row of the
+    // warp attends cost nothing (300 x 100 tokens x 16 heads 65 us, 73 as below; one prompt of 512 8.6 us, not 8.3).
+    if (LOOP && key0 + kN > first) {
+      const int groups = min(max(r.last - key0 + 32, 0) >> 5, kN / 32);
+      float peak = -INFINITY;
+#pragma unroll 1
+      for (int g = 0; g < groups; ++g) {
+        uint32_t s[32];
+        cut_scores(r, key0, g, s_at, s);
+        peak = fmaxf(peak, peak_of<32>(s));
+      }
+      peak *= c;
+      if (j == 0)
+        m = fmaxf(peak, -FLT_MAX);  // (scores of -inf alone: weights of 0, not of 2^(inf - inf), so that a later block counts)
+      else if (!raise_max(peak, o_at, bar_o, phase_o, m, l))
+        return false;
+      Sums sums;
+#pragma unroll 1
+      for (int g = 0; g < kN / 32; ++g) {  // over S of columns that have been read twice
+        uint32_t w[16];
+        if (g < groups) {
+          uint32_t s[32];
+          cut_scores(r, key0, g, s_at, s);
+          weights<32>(s, c, m, w, sums);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = 0u;
+        }
+        tmem_st16(s_at + 16 * g, w);
+        if (g & 1) {
+          published(bar_p + 4 * (g - 1));
+          l += sums.all();  // (in the order of whole blocks: the same bits)
+          sums = Sums();
+        }
+      }
+      continue;
+    }
+    uint32_t s[kN], w[32];
 #pragma unroll
     for (int k = 0; k < kN; k += 32) tmem_ld32(s_at + k, s + k);
 #pragma unroll
     for (int k = 0; k < kN; k += 32) tmem_wait32(s + k);
-    const int key0 = u.block(t, j) * kN;
-    if (key0 + kN > first) {  // the diagonal may cut this block (a bit for each column: 0.1 us less than comparisons, for 128 tokens)
+    if (!LOOP && key0 + kN > first) {  // the diagonal may cut this block (a bit for each column: 0.1 us less than comparisons, for 128 tokens)
       const int seen = r.token - key0;
 #pragma unroll
       for (int k0 = 0; k0 < kN; k0 += 32) {
@@ -751,32 +839,20 @@ __device__ bool run_softmax(const PromptParams &p, const Unit &u, const Past &pa
         for (int k = 0; k < 32; ++k) s[k0 + k] = (bits >> k) & 1u ? s[k0 + k] : 0xFF800000u;
       }
     }
-    uint32_t w[32];
-    const float peak = peak_of(s) * c;
-    if (j == 0) {
-      m = fmaxf(peak, -FLT_MAX);  // (scores of -inf alone: weights of 0, not of 2^(inf - inf), so that a later block counts)
-    } else {
-      const bool grown = peak > m + kSlack;
-      if (__any_sync(~0u, grown)) {
-        const float alpha = grown ? pa::fast_exp2(m - peak) : 1.f;
-        if (grown) m = peak;
-        l *= alpha;
-        if (!warp_wait(bars + 8 * (B_O + t), (before + j - 1) & 1)) return false;
-        pa::tc_fence_after();
-#pragma unroll 1
-        for (int k = 0; k < kD; k += 32) {
-          tmem_ld32(o_at + k, w);
-          tmem_wait32(w);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-          tmem_st32(o_at + k, w);
-        }
-      }
-    }
-    l += weights(s, c, m, w);
-    publish(s_at, w, bars + 8 * (B_P + 2 * t));  // its product begins while the second half is worked out
-    l += weights(s + kN / 2, c, m, w);
-    publish(s_at + kN / 4, w, bars + 8 * (B_P + 2 * t + 1));
+    const float peak = peak_of<kN>(s) * c;
+    if (j == 0)
+      m = fmaxf(peak, -FLT_MAX);
+    else if (!raise_max(peak, o_at, bar_o, phase_o, m, l))
+      return false;
+    Sums first_half, second_half;
+    weights<kN / 2>(s, c, m, w, first_half);
+    l += first_half.all();
+    tmem_st32(s_at, w);
+    published(bar_p);  // its product begins while the second half is worked out
+    weights<kN / 2>(s + kN / 2, c, m, w, second_half);
+    l += second_half.all();
+    tmem_st32(s_at + kN / 4, w);
+    published(bar_p + 8);
   }
   return true;
 }
@@ -840,7 +916,8 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
   const int64_t at = (int64_t)(u.row0 + r.token) * hq + u.h * p.G + (r.row - r.tk * p.G);
   const bool writes = r.live && !(u.solo && t == 1);  // a row's lse, and what else is one thread's
   if (writes && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
-  const float inv = 1.f / l;
+  float inv;  // (to 1 unit of the last place; a division 0.7 us more for 300 x 100 tokens x 16 heads)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(l));
   mine *= inv;
   others *= inv;
   const bool whole = !p.out_f32 && first + p.tokens <= u.len;  // else the tile's box reaches past the sequence
@@ -850,25 +927,35 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
   for (int k0 = u.solo ? t * cols : 0; k0 < kD; k0 += u.solo ? 2 * cols : cols, ++pass) {
     // (solo: the slots' passes take turns, and so do the two places)
     uint8_t *rows = LOOP ? smem + kOut + t * (kOperand / 2) : smem + (u.solo ? 0 : t * kOperand) + ((u.solo ? t : pass) & 1) * (kOperand / 2);
-    if (LOOP) {  // the store before, of this unit or the last one, has read its rows
-      if (leader) bulk_read_wait();
-      together();
-    }
     uint4 *row = reinterpret_cast<uint4 *>(rows + r.row * 128);
+    auto ready = [&]() {
+      if (LOOP) {  // the store before, of this unit or the last one, has read its rows
+        if (leader) bulk_read_wait();
+        together();
+      }
+    };
     if (p.out_f32) {
       uint32_t o[32];
       o_columns<32>(o_at + k0, u.solo, mine, others, o);
+      ready();
 #pragma unroll
       for (int e = 0; e < 8; ++e) row[e ^ (r.row & 7)] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
     } else {
-      uint32_t o[64];
-      o_columns<64>(o_at + k0, u.solo, mine, others, o);
+      // (LOOP: short code, since many units are short ones; 600 x 60 tokens x 16 heads 84 us, 87 with 64 at a time; but a prompt of
+      // 1024 11.4 us, not 11.2)
+      constexpr int kCols = LOOP ? 32 : 64;
+#pragma unroll 1
+      for (int k = 0; k < 64; k += kCols) {
+        uint32_t o[kCols];
+        o_columns<kCols>(o_at + k0 + k, u.solo, mine, others, o);
+        if (k == 0) ready();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t w[4];
+        for (int e = 0; e < kCols / 8; ++e) {
+          uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pa::pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]), __uint_as_float(o[8 * e + 2 * i + 1]));
-        row[e ^ (r.row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) w[i] = pa::pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]), __uint_as_float(o[8 * e + 2 * i + 1]));
+          row[(k / 8 + e) ^ (r.row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
     if (whole) {
@@ -981,11 +1068,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     pa::regs_inc<216>();
     begin();
     if (!more) return;
-    const int t = warp >> 2;
+    const int t = warp >> 2, tk = (threadIdx.x & (kM - 1)) / p.G;
+    const int tk0 = __shfl_sync(~0u, tk, 0), tk1 = __shfl_sync(~0u, tk, 31);
     while (more) {
-      const Row r = row_of(p, u);
+      const Row r = row_of(p, u, tk, tk0, tk1);
       float m, l;
-      ok = run_softmax(p, u, past, r, bars, m, l);
+      ok = run_softmax<LOOP>(p, u, past, r, bars, m, l);
       if (ok && u.nb(t) > 0) ok = warp_wait(bars + 8 * (B_O + t), (past.b(t) + u.nb(t) - 1) & 1);
       pa::tc_fence_after();
       ok = agreed(ok, u.solo, t);
