@@ -513,35 +513,51 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(id), "r"(accumulate), "r"(kDescHigh));
 }
 
+// What the MMA warp needs of a unit, in uniform registers.
+struct Work {
+  int nb0, nb1, cut, ring, units, cut1;
+  int uses[4];  // units before it with queries of either tile, blocks before it of either slot
+  bool solo;
+  __device__ __forceinline__ void set(const Unit &u, const Past &past) {
+    nb0 = __reduce_max_sync(~0u, u.nb0);
+    nb1 = __reduce_max_sync(~0u, u.nb1);
+    cut = __reduce_max_sync(~0u, u.cut);
+    ring = __reduce_max_sync(~0u, past.ring);
+    units = __reduce_max_sync(~0u, past.units);
+    cut1 = __reduce_max_sync(~0u, past.cut1);
+    uses[0] = __reduce_max_sync(~0u, past.q0);
+    uses[1] = __reduce_max_sync(~0u, past.q1);
+    uses[2] = __reduce_max_sync(~0u, past.b0);
+    uses[3] = __reduce_max_sync(~0u, past.b1);
+    solo = __any_sync(~0u, u.solo);
+  }
+  __device__ __forceinline__ int nb(int t) const { return t ? nb1 : nb0; }
+  __device__ __forceinline__ int block(int t, int j) const { return solo ? 2 * j + t : j; }
+  __device__ __forceinline__ bool last_of(int t, int j) const { return solo || t == 1 || j >= nb1; }  // the slot that reads a block last
+};
+
 // The MMAs of a unit, both slots: PV0 S0' PV1 S1' of every block, S' being the slot's next one's.  The waits for what the next
 // product reads come half way through the one before, where the tensor core has MMAs left (before them instead: 620 us, not 613,
 // for 16384 tokens x 16 heads).
 template <int STAGES>
-__device__ bool issue_mmas(const Unit &u, const Past &past, uint32_t base, uint32_t bars) {
-  const int nb0 = __reduce_max_sync(~0u, u.nb0), nb1 = __reduce_max_sync(~0u, u.nb1), cut = __reduce_max_sync(~0u, u.cut);
-  const int ring = __reduce_max_sync(~0u, past.ring), units = __reduce_max_sync(~0u, past.units);
-  const int uses[4] = {__reduce_max_sync(~0u, past.q0), __reduce_max_sync(~0u, past.q1), __reduce_max_sync(~0u, past.b0), __reduce_max_sync(~0u, past.b1)};
-  const int cut1 = __reduce_max_sync(~0u, past.cut1);
-  const bool solo = __any_sync(~0u, u.solo);
+__device__ bool issue_mmas(const Work &w, uint32_t base, uint32_t bars) {
   // (14 bits of the address)
   const uint32_t q_at = (base >> 4) & 0x3FFFu, ring_at = q_at + (kRing >> 4);
   const uint32_t q_low = q_at | desc_low(1024), k_low = ring_at | desc_low(1024), v_low = ring_at | desc_low(kOperand / 2);
-  auto block = [&](int t, int j) { return solo ? 2 * j + t : j; };
-  auto last_of = [&](int t, int j) { return solo || t == 1 || j >= nb1; };  // the slot that reads a block last
   auto arrived = [&](int bar, int phase) { return uniform_wait(bars + 8 * bar, (uint32_t)phase & 1u); };
-  auto fetched = [&](int i) {  // block i of the unit's (keys and values in turn) has landed
-    const int e = ring + i;
+  auto fetched = [&](const Work &w, int i) {  // block i of the unit's (keys and values in turn) has landed
+    const int e = w.ring + i;
     if (!arrived(B_FULL + e % STAGES, e / STAGES)) return false;
-    const int k = (i >> 1) - cut;
+    const int k = (i >> 1) - w.cut;
     if ((i & 1) != 0 && k >= 0) {  // values to be looked through
       if (pa::elect_one()) pa::mbar_arrive(bars + 8 * (B_CUT + k));
       __syncwarp();
     }
     return true;
   };
-  auto scores = [&](int t, int j, bool values) {  // S of the slot's j-th block; `values`: half way through, those have landed
-    const int i = 2 * block(t, j), stage = (ring + i) % STAGES;
-    const uint32_t q = q_low + (solo ? 0 : t) * (kOperand >> 4), k = k_low + stage * (kOperand >> 4);
+  auto scores = [&](const Work &w, int t, int j, bool values) {  // S of the slot's j-th block; `values`: half way through, those have landed
+    const int i = 2 * w.block(t, j), stage = (w.ring + i) % STAGES;
+    const uint32_t q = q_low + (w.solo ? 0 : t) * (kOperand >> 4), k = k_low + stage * (kOperand >> 4);
     if (pa::elect_one()) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -550,7 +566,7 @@ __device__ bool issue_mmas(const Unit &u, const Past &past, uint32_t base, uint3
       }
     }
     __syncwarp();
-    const bool ok = !values || fetched(i + 1);
+    const bool ok = !values || fetched(w, i + 1);
     if (pa::elect_one()) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -558,34 +574,37 @@ __device__ bool issue_mmas(const Unit &u, const Past &past, uint32_t base, uint3
         mma_ss(128 * t, q + off, k + off, idesc(0), 1);
       }
       pa::umma_commit(bars + 8 * (B_S + t));
-      if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
+      if (w.last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
       // the last S that reads a tile's queries: either slot's own, or (solo) the last block's of both
-      if (solo ? i + 2 == 2 * (nb0 + nb1) : j + 1 == (t ? nb1 : nb0)) pa::umma_commit(bars + 8 * (B_QFREE + (solo ? 0 : t)));
+      if (w.solo ? i + 2 == 2 * (w.nb0 + w.nb1) : j + 1 == w.nb(t)) pa::umma_commit(bars + 8 * (B_QFREE + (w.solo ? 0 : t)));
     }
     __syncwarp();
     return ok;
   };
-  if (nb0 > 0) {
-    if (!arrived(B_QFULL, uses[0]) || !fetched(0)) return false;
+  auto begin = [&](const Work &w) {
+    if (!arrived(B_QFULL, w.uses[0]) || !fetched(w, 0)) return false;
     pa::tc_fence_after();
-    scores(0, 0, false);
-  }
-  if (nb1 > 0) {
-    if (solo ? !fetched(2) : !arrived(B_QFULL + 1, uses[1])) return false;
+    scores(w, 0, 0, false);
+    return true;
+  };
+  if (w.nb0 > 0 && !begin(w)) return false;
+  if (w.nb1 > 0) {
+    if (w.solo ? !fetched(w, 2) : !arrived(B_QFULL + 1, w.uses[1])) return false;
     pa::tc_fence_after();
-    scores(1, 0, false);
+    scores(w, 1, 0, false);
   }
-  if (!fetched(1) || (solo && nb1 > 0 && !fetched(3))) return false;
-  for (int j = 0; j < max(nb0, nb1); ++j) {
+  if (!fetched(w, 1) || (w.solo && w.nb1 > 0 && !fetched(w, 3))) return false;
+  const int blocks = max(w.nb0, w.nb1);
+  for (int j = 0; j < blocks; ++j) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int nb = t ? nb1 : nb0, b = block(t, j), stage = (ring + 2 * b + 1) % STAGES;
+      const int nb = w.nb(t), b = w.block(t, j), stage = (w.ring + 2 * b + 1) % STAGES;
       if (j >= nb) continue;
-      if (b >= cut && (solo || t == 0 || j >= nb0) && !arrived(B_CLEAN + b - cut, b > cut ? cut1 : units)) return false;
+      if (b >= w.cut && (w.solo || t == 0 || j >= w.nb0) && !arrived(B_CLEAN + b - w.cut, b > w.cut ? w.cut1 : w.units)) return false;
       const uint32_t v = v_low + stage * (kOperand >> 4);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!arrived(B_P + 2 * t + half, uses[2 + t] + j)) return false;
+        if (!arrived(B_P + 2 * t + half, w.uses[2 + t] + j)) return false;
         pa::tc_fence_after();
         if (pa::elect_one()) {
 #pragma unroll
@@ -593,16 +612,16 @@ __device__ bool issue_mmas(const Unit &u, const Past &past, uint32_t base, uint3
             mma_ts(256 + 128 * t, 128 * t + 8 * x, v + x * (2048 >> 4), idesc(1), j > 0 || x > 0);
           if (half == 1) {
             pa::umma_commit(bars + 8 * (B_O + t));
-            if (last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
+            if (w.last_of(t, j)) pa::umma_commit(bars + 8 * (B_EMPTY + stage));
           }
         }
         __syncwarp();
         // the next block's keys: of either slot's, or the same for both
-        const bool next = solo || t == 1 ? j + 1 < nb : j + 1 < max(nb0, nb1);
-        if (half == 0 && next && (solo || t == 0 || j >= nb0) && !fetched(2 * block(t, j + 1))) return false;
+        const bool another = w.solo || t == 1 ? j + 1 < nb : j + 1 < blocks;
+        if (half == 0 && another && (w.solo || t == 0 || j >= w.nb0) && !fetched(w, 2 * w.block(t, j + 1))) return false;
       }
       // over P of this block, which the product before reads: a thread's MMAs run in order
-      if (j + 1 < nb && !scores(t, j + 1, last_of(t, j + 1))) return false;
+      if (j + 1 < nb && !scores(w, t, j + 1, w.last_of(t, j + 1))) return false;
     }
   }
   return true;
@@ -1117,7 +1136,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     } else if (warp == kMmaWarp) {
       pa::tc_fence_after();
       while (ok && more) {
-        ok = issue_mmas<STAGES>(u, past, base, bars);
+        Work w;
+        w.set(u, past);
+        ok = issue_mmas<STAGES>(w, base, bars);
         if (ok) next();
       }
       if (pa::elect_one()) pa::umma_commit(bars + 8 * B_MMA);
