@@ -1259,11 +1259,13 @@ extern "C" pa_status_t pa_prompt_attn(const pa_prompt_attn_args_t *a, void *stre
       !encode_rows(dev, &p.tm_o, a->out, a->num_rows, heads, q_row, p.G, p.tokens))
     return PA_ERR_CUDA;
   // A CTA for every unit there can be, and for those that may be split (while there are fewer units than twice the SMs).  CTAs
-  // without a share exit.  Of many short ones a CTA takes several in turn (16 x 2048 tokens x 16 heads 213 us, 251 without, 8 x 4096
-  // 369 and 393, 5 x 6000 473 and 479; but 4 x 8192 681 and 671).  Their load warps work out the schedule alone, which holds for up to
-  // 1024 sequences.
+  // without a share exit.  Where CTAs would come to an SM one after the other, a CTA takes several units in turn: as many units as SMs
+  // (16 x 2048 tokens x 16 heads 191 us, 238 without, 16384 600 and 613, 64 x 40 10.6 and 13.2), or of several sequences two thirds of
+  // that (4 x 400 10.7 and 12.8, 2 x 1024 15.4 and 17.5; but 4 x 330 9.2 and 8.5).  Units of one sequence are of all lengths, and the
+  // split ones fill such gaps (1800 tokens 19.8 and 17.2).  The load warps of these CTAs work out the schedule alone, which holds for
+  // up to 1024 sequences.
   const int64_t units = (n + a->num_seqs * (span - 1)) / span * a->num_kv_heads;
-  const bool loop = units >= 2 * dev->sms && a->num_seqs <= 1024 && n <= 5120 * (int64_t)a->num_seqs;
+  const bool loop = a->num_seqs <= 1024 && (units >= dev->sms || (a->num_seqs > 1 && 3 * units >= 2 * dev->sms));
   const int64_t grid = std::max(units, std::min<int64_t>(2 * units, 4 * dev->sms));
   const pa_host::Launch run(dim3((unsigned)grid), dim3(kThreads), kSmem, stream);
   cudaError_t e;
