@@ -22,9 +22,9 @@
 //
 // Bound by the tensor core at what its power allows: 2600 cycles for two tiles and a block (16.8 MFLOP), of 2054 that the MMAs take
 // on constant data, hardly fewer with the softmax left out (2520), and a cuBLAS product of 8192^3 comes to the same rate.  32768
-// tokens x 16 heads 2370 us (1.86 PFLOP/s, 0.98 of cuBLAS' 1887), 16384 615 us; shorter ones by what a CTA takes beside its blocks (some
-// 5 us alone, 2.7 between units of one CTA) and by SMs that are done early: 2048 tokens 21 us, 13 prompts of 200 .. 4001 tokens x 4 KV
-// heads 213 us (0.74 of the rate), 16 tokens 6.4 us.
+// tokens x 16 heads 2357 us (1.87 PFLOP/s, 0.99 of cuBLAS' 1887), 16384 607 us; shorter ones by what a CTA takes beside its blocks (some
+// 5 us alone, 2 to 3 between units of one CTA) and by SMs that are done early: 2048 tokens 21 us, 13 prompts of 200 .. 4001 tokens x 4 KV
+// heads 199 us (0.80 of the rate), 300 of 100 tokens x 16 heads 64 us (36 by its bytes), 16 tokens 6.1 us.
 // Measured on the way: one warp per tile to issue the MMAs 821 us, not 738, for 16384 tokens (both tiles' softmax at once); weights
 // worked out with the maximum so far while the block's own is found 637, not 597; keys split over a cluster of two CTAs and joined
 // through shared memory 23.4 us, not 21, for 2048 tokens.
