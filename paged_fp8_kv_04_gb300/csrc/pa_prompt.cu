@@ -930,8 +930,13 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
     others = pa::fast_exp2(m1 - m);
     l = l0 * mine + l1 * others;
   }
+  // A slot looks at the bits of its own blocks alone: the warps of slot 0 would read that of slot 1's last block before it is set, after,
+  // or some of them either way, and part at the barriers below.  Its own bits are final: they are written before the block's B_CLEAN,
+  // which the MMA warp waits for before the block's product, and this warp has waited for the last of those (B_O).  A solo tile's
+  // blocks are both slots', which both() has joined.
   const volatile uint32_t *dirt = reinterpret_cast<const volatile uint32_t *>(smem + kDirty) + 2 * (past.units & (kUnits - 1));
-  const uint32_t dirty = dirt[0] | dirt[1];
+  uint32_t dirty = dirt[0] | dirt[1];
+  if (!u.solo) dirty &= (1u << (u.nb(t) - u.cut)) - 1u;
   const int64_t at = (int64_t)(u.row0 + r.token) * hq + u.h * p.G + (r.row - r.tk * p.G);
   const bool writes = r.live && !(u.solo && t == 1);  // a row's lse, and what else is one thread's
   if (writes && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;

@@ -319,6 +319,30 @@ def test_prompt_infinities_in_fp32_outputs():
         assert torch.equal(out[clean], want[clean]) and torch.equal(lse, wl) and bool((out[~clean] == -math.inf).all())
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("count", [3, 200])
+@pytest.mark.parametrize("group,n,first,at", [(1, 256, 128, 131), (3, 168, 128, 150), (5, 150, 128, 128)])
+def test_prompt_infinities_in_the_later_tiles_block_alone(group, n, first, at, count, f32):
+    """Of the two tiles that a CTA has at a sequence's end the later one alone reads the block that begins at token `first`, and only
+    that block holds what is not finite: rows before it are bit for bit as without it, those from there on attend it.  A CTA for each unit,
+    and CTAs that take them in turn; several times."""
+    g = torch.Generator(device="cuda").manual_seed(26)
+    cu = _cu([n] * count)
+    q, k, v = _inputs(g, n * count, 1, group)
+    want, wl = _call(q, k, v, cu, f32=f32)
+    v2 = v.clone().view(count, n, 128)
+    v2[:, at, 7], v2[:, n - 2, 70] = math.inf, math.nan
+    assert bool(v2[:, :first].isfinite().all())
+    clean = torch.ones_like(want, dtype=torch.bool).view(count, n, group, 128)
+    clean[:, at:, :, 7], clean[:, n - 2:, :, 70] = False, False
+    clean = clean.view(want.shape)
+    for _ in range(5):
+        out, lse = _call(q, k, v2.view(v.shape), cu, f32=f32)
+        assert torch.equal(out[clean], want[clean]) and torch.equal(lse, wl)
+        assert bool((out.view(count, n, group, 128)[:, at:, :, 7] == math.inf).all())
+        assert bool(out.view(count, n, group, 128)[:, n - 2:, :, 70].isnan().all())
+
+
 def test_prompt_is_the_same_packed_or_alone_dense_or_a_view():
     g = torch.Generator(device="cuda").manual_seed(17)
     lens, heads, group = [333, 128, 1, 700], 2, 6
