@@ -1002,6 +1002,12 @@ __device__ void write_tile(const PromptParams &p, const Unit &u, const Past &pas
       __syncwarp();
     }
   }
+  if (LOOP && u.solo) {
+    // Either slot has read columns of both slots' O: neither publishes weights of the next unit, whose product would be written over
+    // them, before the other has read its own.
+    pa::tc_fence_before();
+    both();
+  }
   if (dirty != 0) {  // (the same for both slots of a solo tile)
     if (leader) bulk_write_wait();
     if (u.solo)

@@ -305,6 +305,25 @@ def test_prompt_units_that_are_split_and_in_turn(heads, group):
                 _compare(out, lse, q, k, v, cu)
 
 
+@pytest.mark.parametrize("heads,group,lens", [(1, 16, [2432]), (1, 16, [4096]), (3, 8, [900, 1700]), (2, 16, [33, 1500])])
+def test_prompt_split_units_before_others_are_the_same_every_time(heads, group, lens):
+    """CTAs that have a split unit first and go on with others: the two slots, which join that unit's columns, go on at their own pace.
+    Equal bits however often."""
+    g = torch.Generator(device="cuda").manual_seed(27)
+    cu = _cu(lens + [0] * 30)
+    q, k, v = _inputs(g, max(int(cu[-1]), 160 * 2 * (128 // group) // heads), heads, group)
+    want, wl = _call(q, k, v, cu)
+    _compare(want, wl, q, k, v, cu)
+    out, lse = torch.empty_like(q), torch.empty_like(wl)
+    dcu, st = torch.from_numpy(cu).cuda(), word()
+    wrong = torch.zeros(1, dtype=torch.int64, device="cuda")
+    n = int(cu[-1])
+    for _ in range(200):
+        B.prompt_attn(q, k, v, dcu, out=out, lse=lse, status=st)
+        wrong += (out[:n] != want[:n]).sum() + (lse[:n] != wl[:n]).sum()
+    assert int(wrong) == 0 and int(st) == 0
+
+
 def test_prompt_infinities_in_fp32_outputs():
     g = torch.Generator(device="cuda").manual_seed(25)
     for lens, heads, group in (([300, 41], 1, 16), ([90] * 30, 4, 8)):
