@@ -18,7 +18,8 @@
 // Warp roles (384 threads): warps 0-3 and 4-7 are the softmax of slots 0 and 1; warp 8 finds the units and fetches tiles by TMA; one
 // lane of warp 9 issues the MMAs; warps 10 and 11 look through the values of the blocks that the diagonal or the sequence's end cuts: an
 // infinity or NaN there must not reach rows that do not attend it (0 * inf), so it is replaced by 0, and rows that do attend it
-// get it in the epilogue.  Every wait is bounded; TMEM is released on every path.
+// get it in the epilogue.  Every wait for a barrier in memory is bounded; warps that gave up still come to the named barriers that they
+// share with others (agreed, unit_comes), so that nobody stays there.  TMEM is released on every path.
 //
 // Bound by the tensor core at what its power allows: 2600 cycles for two tiles and a block (16.8 MFLOP), of 2054 that the MMAs take
 // on constant data, hardly fewer with the softmax left out (2520), and a cuBLAS product of 8192^3 comes to the same rate.  32768
@@ -101,7 +102,8 @@ enum {
   B_UNIT = B_CLEAN + 2,             // [4] the unit has been found
   B_LEFT = B_UNIT + 4,              // [4] every warp that the unit was found for is done with it
   B_CLAIM = B_LEFT + 4,             // the answer of the launch queue
-  B_DONE = B_CLAIM + 1,             // the softmax warps are done with TMEM
+  B_END = B_CLAIM + 1,              // the load warp posts no more units
+  B_DONE = B_END + 1,               // the softmax warps are done with TMEM
   B_MMA = B_DONE + 1,               // every MMA is complete
   kNumBars = B_MMA + 1
 };
@@ -429,6 +431,19 @@ __device__ __forceinline__ bool posted_unit(const uint8_t *smem, int round, Unit
   return s.blocks > 0;
 }
 
+// Whether the load warp posts that unit, for a whole warp that has given up: posted, or the load warp has ended without.  The answer is that
+// of the warps that have seen the unit come: warps of a unit meet at named barriers, which know no time.  All waits of the load warp are
+// bounded, and it fails at the first that others do not serve any more.
+__device__ __forceinline__ bool unit_comes(uint32_t bars, int round) {
+  const long long t0 = clock64();
+  bool ended, comes;
+  do {
+    ended = __all_sync(~0u, pa::mbar_try_wait(bars + 8 * B_END, 0));
+    comes = __all_sync(~0u, pa::mbar_try_wait(bars + 8 * (B_UNIT + (round & (kUnits - 1))), (round / kUnits) & 1));
+  } while (!ended && !comes && !__any_sync(~0u, clock64() - t0 > 8 * pa::kWaitCycles));
+  return comes;
+}
+
 // ------------------------------------------------------------------------------- roles
 
 __device__ __forceinline__ uint32_t bar_full(uint32_t bars, int stage) { return bars + 8 * (B_FULL + stage); }
@@ -451,7 +466,7 @@ __device__ __forceinline__ void load_queries(const PromptParams &p, const Unit &
 // The loads of a unit, in the order of their use: as many blocks as the ring holds do not wait for anything in the first unit.
 // `done` counts what has been asked for.
 struct Loads {
-  int blocks = 0, q0 = 0, q1 = 0;
+  int blocks = 0, q0 = 0, q1 = 0, claims = 0;
 };
 template <int STAGES>
 __device__ bool load_unit(const PromptParams &p, const Unit &u, const Past &past, uint32_t base, uint32_t bars, Loads &done) {
@@ -484,6 +499,7 @@ __device__ void drain(uint32_t bars, const Loads &done) {
   for (int e = max(0, done.blocks - STAGES); e < done.blocks; ++e) pa::mbar_wait_bounded(bar_full(bars, e % STAGES), (e / STAGES) & 1);
   if (done.q0 > 0) pa::mbar_wait_bounded(bars + 8 * B_QFULL, (done.q0 - 1) & 1);
   if (done.q1 > 0) pa::mbar_wait_bounded(bars + 8 * (B_QFULL + 1), (done.q1 - 1) & 1);
+  if (done.claims > 0) pa::mbar_wait_bounded(bars + 8 * B_CLAIM, (done.claims - 1) & 1);
 }
 
 // A bounded wait of a whole warp whose control flow stays uniform: what the MMAs' operands are computed from then stays
@@ -1030,6 +1046,13 @@ __device__ __forceinline__ bool agreed(bool ok, bool solo, int t) {
   return r != 0;
 }
 
+// What a warp that gave up owes to others of its slot, or (solo) of both: it comes to the barriers of the units that are posted still,
+// from this one on.  (As many as there are places for them at most: it leaves none.)
+__device__ __noinline__ void come_to_barriers(uint8_t *smem, uint32_t bars, int round, int t) {
+  Unit u;
+  for (; unit_comes(bars, round) && posted_unit(smem, round, u); ++round) agreed(false, u.solo, t);
+}
+
 // OWN, ALL: how the schedule is worked out.  LOOP: CTAs go on with further units, whose first scores are there when the rows of
 // the one before have been written; else a CTA for each.
 template <int OWN, bool ALL, bool LOOP>
@@ -1112,6 +1135,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       pa::tc_fence_before();  // O has been read before the next unit's weights are published
       next();
     }
+    if (LOOP && !ok)  // with its slot (`more`), or while it waited for a unit
+      come_to_barriers(smem, bars, more ? round + 1 : round, t);
     if (lane == 0) {
       bulk_read_wait();
       pa::mbar_arrive(bars + 8 * B_DONE);
@@ -1131,6 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         // The CTA that would come next: asked for when the last loads of this unit have been (some two blocks before its end).
         if (lane == 0) claim_next(base + kClaim, bars + 8 * B_CLAIM);
         __syncwarp();
+        ++done.claims;
         past.add(u);
         ok = warp_wait(bars + 8 * B_CLAIM, round & 1);
         if (!ok) break;
@@ -1143,6 +1169,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         pa::fence_async_smem();  // the answer has been read
         post();
       }
+      if (LOOP && lane == 0) pa::mbar_arrive(bars + 8 * B_END);
       if (!ok && lane == 0) drain<STAGES>(bars, done);
     } else if (warp == kMmaWarp) {
       pa::tc_fence_after();
