@@ -706,7 +706,7 @@ typedef struct pa_rope_args {
  * a turn, exactly, however far the position, so far positions are as exact as near ones.  One kernel launch on `stream`; no host
  * synchronisation, no allocation.  Outputs share no byte with each other or another input (rows of one buffer interleave only
  * with equal strides).  PA_ERR_INVALID_ARG for a missing pointer, a value out of range or an overlap, PA_ERR_ALIGN for a misaligned pointer, PA_ERR_UNSUPPORTED for
- * head_dim other than 128, PA_ERR_CUDA when the launch fails. */
+ * head_dim other than 128 or more than 65535 heads of both together, PA_ERR_CUDA when the launch fails. */
 pa_status_t pa_rope(const pa_rope_args_t *args, void *stream);
 
 /* Arguments of pa_prompt_attn.  All pointers are device pointers; strides are elements between tokens, and a token's heads
@@ -734,10 +734,14 @@ typedef struct pa_prompt_attn_args {
  * of KV head h = j / group_size attend the sequence's tokens 0 .. t,
  *   out[t][j] = sum_i softmax_i(sm_scale * q[t][j] . k[i][h]) v[i][h],   lse[t][j] = log sum_i exp(sm_scale * q[t][j] . k[i][h]).
  * Scores, maxima, sums and accumulators are fp32; the softmax weights are rounded to bf16 for the second product (their sum is
- * taken before), so an fp32 output is good to 2^-9 of its terms and serves pa_lse_merge, which joins it with the part of a context
+ * taken before), so an fp32 output is good to 2^-8 of its terms and serves pa_lse_merge, which joins it with the part of a context
  * that is already cached (a decode over the cached pages with an fp32 output and lse).  What a row does not attend has no effect on it,
  * infinities and NaN included: later tokens, other sequences, rows of no sequence; rows of no sequence are left as they are.
- * A row whose scores are all -inf has an output of NaN (0 / 0) and an lse of -inf.
+ * A row whose scores are all -inf has an output of NaN (0 / 0) and an lse of -inf; one with a score of +inf or NaN has NaN in both.  An infinite
+ * value whose weight is 0 in fp32 (a score of -inf, or 2^-126 of the row's largest) gives an attending row the infinity or NaN (0 * inf),
+ * and which of them may differ with what else the call has; any other weight counts as in the formula.  Weights exceed 1 by 2^8 at most before
+ * the division, so values beyond 2^120 / (number of tokens) may overflow.  Many values that are not finite are slow: each row adds those
+ * of its last blocks one by one.
  * A sequence whose cu does not lie in order within 0 .. num_rows is left out (PA_DEV_BAD_QLEN); where others then overlap, rows may be left
  * unwritten.  A sequence's last bits may depend on how many rows the call has besides: equal calls give equal bits.  One kernel launch on
  * `stream`; no host synchronisation, no allocation.  out and lse share no byte with each other or an input.  PA_ERR_INVALID_ARG

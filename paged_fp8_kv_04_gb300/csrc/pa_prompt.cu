@@ -7,7 +7,7 @@
 //                    when it has grown by more than 2^8: until then the weights exceed 1 by that much at most, and nothing
 //                    has to be scaled again.  The sum of the weights is fp32, taken before they are rounded
 //   O += P V         kind::f16 with P as the A operand in TMEM, in the columns that S had (bf16 because V is: a
-//                    rounding of 2^-9 per weight, as that of the output), V as the B operand, MN-major, as TMA left it
+//                    rounding of 2^-8 of a weight at most, as that of the output), V as the B operand, MN-major, as TMA left it
 //
 // Rows of a tile are (token, head of the group) pairs, 128 / group_size tokens with all query heads of a KV head: they
 // share its keys, short prompts fill a tile as well as long ones do, and the diagonal cuts few tokens.  A CTA has two tiles (a unit),
@@ -23,9 +23,11 @@
 //
 // Bound by the tensor core at what its power allows: 2600 cycles for two tiles and a block (16.8 MFLOP), of 2054 that the MMAs take
 // on constant data, hardly fewer with the softmax left out (2520), and a cuBLAS product of 8192^3 comes to the same rate.  32768
-// tokens x 16 heads 2357 us (1.87 PFLOP/s, 0.99 of cuBLAS' 1887), 16384 607 us; shorter ones by what a CTA takes beside its blocks (some
-// 5 us alone, 2 to 3 between units of one CTA) and by SMs that are done early: 2048 tokens 21 us, 13 prompts of 200 .. 4001 tokens x 4 KV
-// heads 199 us (0.80 of the rate), 300 of 100 tokens x 16 heads 64 us (36 by its bytes), 16 tokens 6.1 us.
+// tokens x 16 heads 2360 to 2420 us in a few calls (1.81 to 1.86 PFLOP/s; cuBLAS 1.89), 2600 in a loop of seconds (1.69; cuBLAS 1.70),
+// 16384 605 us in a few; shorter ones by what a CTA takes beside its blocks (some 5 us alone, 2 to 3 between units of one CTA) and by SMs
+// that are done early: 2048 tokens 21 us, 13 prompts of 200 .. 4001 tokens x 4 KV heads 200 us in a few calls (0.79 of the rate) and 214
+// to 227 in a loop, 300 of 100 tokens x 16 heads 64 us (36 by its bytes), 16 tokens 6.2 us.
+// These are of the kernel as it stands; comparisons, here and beside the code, of the step that they decided.
 // Measured on the way: one warp per tile to issue the MMAs 821 us, not 738, for 16384 tokens (both tiles' softmax at once); weights
 // worked out with the maximum so far while the block's own is found 637, not 597; keys split over a cluster of two CTAs and joined
 // through shared memory 23.4 us, not 21, for 2048 tokens.
@@ -698,7 +700,8 @@ __device__ bool clean_unit(const Unit &u, const Past &past, uint32_t bars, uint8
 }
 
 // The infinities and NaN among the values that a row attends and that were replaced by 0: into its output, which this
-// thread has written.
+// thread has written.  Rare, so it is simple: a thread walks up to 256 keys x 128 elements, two bytes at a time.  A weight of 0 is not told from
+// others here: the infinity is added (0 * inf would be NaN, as it is in blocks that no row is cut in).
 __device__ __noinline__ void add_not_finite(const uint16_t *v, int64_t v_stride, void *out, bool out_f32, uint32_t dirty, int cut, int token) {
   for (int i = cut * kN; i <= token; ++i) {
     if (!(dirty >> (i / kN - cut) & 1u)) continue;
